@@ -387,11 +387,12 @@ def _exact_norm(s, kind, scale, eps):
 
 
 def _exact_product(x, s, cols):
-    """x: 64 bits.  A row's scale is held in 32 bits: that is part of the definition."""
+    """x: 64 bits.  A row's scale is held in 32 bits, and a quotient is rounded to 32 bits before it is rounded to a
+    whole number: that is part of the definition (a tie is a tie of the 32-bit quotient)."""
     scale = (x.abs().max(1).values / 127).to(torch.float32).to(torch.float64)
     q = torch.zeros_like(x)
     some = scale > 0
-    q[some] = torch.clamp(torch.round(x[some] / scale[some, None]), -127, 127)
+    q[some] = torch.clamp(torch.round((x[some] / scale[some, None]).to(torch.float32)), -127, 127).to(torch.float64)
     sums = torch.mm(q, s["w"][:, :cols].to(torch.float64).t().contiguous())
     out = sums * (scale[:, None] * s["w_scale"].to(torch.float64)[None, :])
     return out if s.get("bias") is None else out + s["bias"].to(torch.float64)
