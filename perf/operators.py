@@ -257,15 +257,15 @@ def _plain_sample(s):
     valid, top = z > -math.inf, z[:, :1]
     greedy = ~(s["temperature"] > 0)[:, None]
     t = torch.where(greedy, torch.ones_like(top), s["temperature"][:, None])
-    zt = z / t
-    e = torch.where(valid, torch.where(z == top, torch.ones_like(z), torch.exp(zt - top / t)), torch.zeros_like(z))
+    d = torch.where(z == top, torch.zeros_like(z), (z - top) / t)
+    e = torch.where(valid, torch.exp(d), torch.zeros_like(z))
     rank = torch.arange(V, device=z.device)[None]
     k, p, m = s["top_k"][:, None], s["top_p"][:, None], s["min_p"][:, None]
     keep = valid & ((k <= 0) | (rank < k))
     mass = torch.where(keep, e, torch.zeros_like(e))
     before = torch.cumsum(mass, 1).roll(1, 1)
     keep = keep & ((p >= 1) | (before < p * mass.sum(1, keepdim=True)) | (rank == 0)) & ((e >= m) | (rank == 0))
-    score = torch.where(keep, zt + s["gumbel"].gather(1, index), torch.full_like(z, -math.inf))
+    score = torch.where(keep, d + s["gumbel"].gather(1, index), torch.full_like(z, -math.inf))
     best = score.amax(1, keepdim=True)
     token = torch.where(keep & (score == best), index, torch.full_like(index, V)).amin(1, keepdim=True)
     token = torch.where(greedy, index[:, :1], token)
@@ -424,7 +424,7 @@ def _exact_sample(s):
                 upto = torch.cumsum(kept, 0)
                 last = 1 + int((upto[:-1] < p * upto[-1]).sum())
             last = max(1, min(last, int((weight >= m).sum())))
-            score = v[:last] / t + s["gumbel"][b][ids[:last]].to(torch.float64)
+            score = (v[:last] - v[0]) / t + s["gumbel"][b][ids[:last]].to(torch.float64)
             at = int(ids[:last][score == score.max()].min())
             pos = int(torch.nonzero(ids == at)[0, 0])
         else:
