@@ -13,7 +13,7 @@ ERRORS = {0: "ok", -1: "invalid argument", -2: "level out of range", -3: "device
           -4: "HIP runtime error", -5: "misaligned pointer", -6: "workspace too small",
           -7: "unsupported parameters", -8: "switching key does not match the context",
           -9: "level tables not prepared"}
-EINVAL, ELEVEL, EALIGN, EWORKSPACE, EKEY, ENOTREADY = -1, -2, -5, -6, -8, -9
+EINVAL, ELEVEL, EALIGN, EWORKSPACE, EUNSUPPORTED, EKEY, ENOTREADY = -1, -2, -5, -6, -7, -8, -9
 
 
 class CkksError(RuntimeError):
@@ -35,6 +35,22 @@ class Swk(C.Structure):
     """ckks_swk (include/ckks_gpu.h): switching-key descriptor."""
     _fields_ = [("data", C.c_void_p), ("n", C.c_uint32), ("L", C.c_uint32), ("K", C.c_uint32),
                 ("dnum", C.c_uint32), ("seeded", C.c_uint32), ("reserved", C.c_uint32), ("seed", C.c_uint64)]
+
+
+class PlainNorm(C.Structure):
+    """ckks_plain_norm (include/ckks_plain.h)."""
+    _fields_ = [("type", C.c_int), ("kind", C.c_int), ("rows", C.c_int64), ("cols", C.c_int64), ("groups", C.c_int64),
+                ("x", C.c_void_p), ("y", C.c_void_p), ("x_stride", C.c_int64), ("y_stride", C.c_int64),
+                ("next_weight", C.c_void_p), ("next_bias", C.c_void_p), ("block_weight", C.c_void_p),
+                ("block_bias", C.c_void_p), ("gate", C.c_void_p), ("scale", C.c_float), ("eps", C.c_float)]
+
+
+class PlainNormGrads(C.Structure):
+    """ckks_plain_norm_grads (include/ckks_plain.h)."""
+    _fields_ = [("dh", C.c_void_p), ("du", C.c_void_p), ("dh_stride", C.c_int64), ("du_stride", C.c_int64),
+                ("dx", C.c_void_p), ("dy", C.c_void_p), ("dx_stride", C.c_int64), ("dy_stride", C.c_int64),
+                ("next_weight", C.c_void_p), ("next_bias", C.c_void_p), ("block_weight", C.c_void_p),
+                ("block_bias", C.c_void_p), ("gate", C.c_void_p)]
 
 
 class KernelStat(C.Structure):
@@ -88,6 +104,23 @@ SIGNATURES = {
     "ckks_profile_end": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.POINTER(C.c_int)]),
     "ckks_fill_uniform": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_uint64, C.c_uint64,
                                     C.c_uint64, C.c_void_p]),
+    "ckks_plain_residual_norm": (C.c_int, [C.POINTER(PlainNorm), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                                           C.c_void_p]),
+    "ckks_plain_residual_norm_i8": (C.c_int, [C.POINTER(PlainNorm), C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                                              C.c_void_p, C.c_void_p]),
+    "ckks_plain_norm_grad_workspace_size": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(C.c_size_t)]),
+    "ckks_plain_residual_norm_grad": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(PlainNormGrads), C.c_void_p,
+                                                C.c_size_t, C.c_void_p]),
+    "ckks_plain_quantize_rows": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                           C.c_int64, C.c_void_p, C.c_void_p]),
+    "ckks_plain_matmul_i8_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "ckks_plain_matmul_i8": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                       C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                       C.c_size_t, C.c_void_p]),
+    "ckks_plain_sample_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "ckks_plain_sample": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
+                                    C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
 }
 
 

@@ -12,6 +12,7 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
+PLAIN = os.path.join(CSRC, "plain")  # the plaintext-side operators
 OUT = os.path.join(PKG, "libckksgpu.so")
 BUILD = os.path.join(PKG, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -30,11 +31,11 @@ CXXFLAGS = ["-O2", "-fPIC", "-std=c++17", "-Wall"]
 
 def sources():
     """HIP sources, and the plain C++ host sources (built with the host compiler)."""
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
+    return sorted(os.path.join(d, f) for d in (CSRC, PLAIN) for f in os.listdir(d) if f.endswith((".hip", ".cpp")))
 
 
 def _compile(src: str) -> str:
-    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+    obj = os.path.join(BUILD, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
     if src.endswith(".cpp"):
         cmd = [CXX, *CXXFLAGS, "-c", src, "-o", obj]
     else:

@@ -1,0 +1,522 @@
+// norm.hip -- residual stream and norms around a gated block: forward, 8-bit
+// output, gradient, and the 8-bit form of rows.
+#include "plain_common.h"
+
+namespace ckks_plain {
+
+// ckks_plain_norm with the column count in 32 bits
+struct NormArgs {
+    const void *x, *y, *nw, *nb, *bw, *bb, *gate;
+    int64_t rows, x_stride, y_stride, rows_per_gate;
+    int cols;
+    bool layer;
+    float scale, eps;
+};
+
+// Mean (0 for rms) and 1 / sqrt(mean square around it + eps) of a row in registers; the mean
+// comes first and the squares are of differences from it, so a large mean costs no digits.
+template <typename R, int NT, int E>
+__device__ __forceinline__ void row_stats(const float (&v)[E], const NormArgs &a, int t, float (*buf)[16], float &mu,
+                                          float &r) {
+    mu = 0;
+    float s = 0;
+    if (a.layer) {
+#pragma unroll
+        for (int i = 0; i < E; i++) s += v[i];
+        mu = row_sum<NT>(s, buf[0]) / (float)a.cols;
+        s = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        const float d = v[i] - mu;
+        if (R::col(i, t) < a.cols) s += d * d;
+    }
+    r = 1.0f / sqrtf(row_sum<NT>(s, buf[1]) / (float)a.cols + a.eps);
+}
+
+// One row for NT threads (four rows a workgroup where NT is one wave).
+template <typename T, int NT, int E, bool VECTOR, bool I8>
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_residual_norm(NormArgs a, T *h_out, int64_t h_stride,
+                                                                      void *u_out, int64_t u_stride, float *q_scale) {
+    typedef Row<T, NT, E, VECTOR> R;
+    __shared__ float buf[5][16];
+    const int t = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= a.rows) return;
+    float x[E], n[E], w[E];
+    R::load((const T *)a.x + row * a.x_stride, a.cols, t, x);
+    R::load((const T *)a.y + row * a.y_stride, a.cols, t, n);
+    float mu, r;
+    if (a.bw) {
+        row_stats<R, NT>(n, a, t, buf, mu, r);
+        R::load((const T *)a.bw, a.cols, t, w);
+#pragma unroll
+        for (int i = 0; i < E; i++) n[i] = (n[i] - mu) * r * w[i];
+        if (a.bb) {
+            R::load((const T *)a.bb, a.cols, t, w);
+#pragma unroll
+            for (int i = 0; i < E; i++) n[i] += w[i];
+        }
+    }
+    if (a.gate) {
+        R::load((const T *)a.gate + row / a.rows_per_gate * a.cols, a.cols, t, w);
+#pragma unroll
+        for (int i = 0; i < E; i++) n[i] *= w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < E; i++) x[i] += a.scale * n[i];
+    R::store(h_out + row * h_stride, a.cols, t, x);
+    row_stats<R, NT>(x, a, t, buf + 2, mu, r);
+    R::load((const T *)a.nw, a.cols, t, w);
+#pragma unroll
+    for (int i = 0; i < E; i++) x[i] = (x[i] - mu) * r * w[i];
+    if (a.nb) {
+        R::load((const T *)a.nb, a.cols, t, w);
+#pragma unroll
+        for (int i = 0; i < E; i++) x[i] += w[i];
+    }
+    if constexpr (!I8) {
+        R::store((T *)u_out + row * u_stride, a.cols, t, x);
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+            const uint32_t b = __float_as_uint(x[i]) & 0x7fffffffu;
+            if (R::col(i, t) < a.cols && b > m) m = b;
+        }
+        const float s = i8_scale(row_max<NT>(m, buf[4]));
+        if (t == 0) q_scale[row] = s;
+        const int padded = (a.cols + CKKS_PLAIN_I8_ROW - 1) / CKKS_PLAIN_I8_ROW * CKKS_PLAIN_I8_ROW;
+        store_i8<R>((int8_t *)u_out + row * u_stride, padded, t, x, s);
+    }
+}
+
+template <typename T, int NT, int E, bool VECTOR>
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_quantize_rows(const T *x, int64_t x_stride, int64_t rows,
+                                                                      int cols, int8_t *q, int64_t q_stride,
+                                                                      float *q_scale) {
+    typedef Row<T, NT, E, VECTOR> R;
+    __shared__ float buf[16];
+    const int t = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    if (row >= rows) return;
+    float v[E];
+    R::load(x + row * x_stride, cols, t, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < E; i++) {
+        const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+        if (b > m) m = b;
+    }
+    const float s = i8_scale(row_max<NT>(m, buf));
+    if (t == 0) q_scale[row] = s;
+    store_i8<R>(q + row * q_stride, (cols + CKKS_PLAIN_I8_ROW - 1) / CKKS_PLAIN_I8_ROW * CKKS_PLAIN_I8_ROW, t, v, s);
+}
+
+// ------------------------------------------------------------------ gradient
+
+// The gradient of v -> hat = (v - mu) r from that of hat: r (g - [mean g] - hat mean(g hat)), the
+// bracketed mean for the layer norm alone.
+//
+// A workgroup walks a range of rows and keeps the weights' sums of its columns in registers; they
+// leave as one row of partial sums for each workgroup, which k_norm_grad_sum adds in a fixed order
+// (no atomics: the same bits on every run).  Ranges never cross from one gate row into part of
+// another: either a workgroup has whole gate groups, whose sums are then complete, or a group has
+// `chunks` workgroups.
+struct GradPlan {
+    int64_t rows_per_gate, groups;  // without a gate: all rows, 1
+    int64_t chunks;                 // workgroups of a group (1: `span` whole groups a workgroup)
+    int64_t span;                   // rows of a workgroup
+    int64_t blocks;
+};
+struct GradArgs {
+    const void *dh, *du;
+    void *dx, *dy;
+    int64_t dh_stride, du_stride, dx_stride, dy_stride;
+    float *gate;      // [groups][cols] (chunks == 1)
+    float *part_gate; // [blocks][cols] (chunks > 1)
+    float *part[4];   // [blocks][cols]: next_weight, next_bias, block_weight, block_bias
+};
+
+template <typename T, int NT, int E, bool VECTOR>
+__global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPlan p) {
+    typedef Row<T, NT, E, VECTOR> R;
+    typedef Row<float, NT, E, false> F;
+    __shared__ float buf[8][16];
+    const int t = threadIdx.x;
+    const int64_t group = p.chunks > 1 ? blockIdx.x / p.chunks : 0;
+    const int64_t first = p.chunks > 1 ? group * p.rows_per_gate + blockIdx.x % p.chunks * p.span
+                                       : (int64_t)blockIdx.x * p.span;
+    const int64_t end = p.chunks > 1 ? (group + 1) * p.rows_per_gate : a.rows;
+    const int64_t last = first + p.span < end ? first + p.span : end;
+    const float inv = 1.0f / (float)a.cols;
+    float acc_nw[E] = {}, acc_nb[E] = {}, acc_bw[E] = {}, acc_bb[E] = {}, acc_g[E] = {};
+    for (int64_t row = first; row < last; row++) {
+        float x[E], y[E], h[E], g[E], w[E], du[E];
+        R::load((const T *)a.x + row * a.x_stride, a.cols, t, x);
+        R::load((const T *)a.y + row * a.y_stride, a.cols, t, y);
+        R::load((const T *)o.du + row * o.du_stride, a.cols, t, du);
+        float mu_y = 0, r_y = 1, mu_h, r_h;
+        if (a.bw) {
+            row_stats<R, NT>(y, a, t, buf, mu_y, r_y);
+            R::load((const T *)a.bw, a.cols, t, w);
+#pragma unroll
+            for (int i = 0; i < E; i++) {
+                y[i] = (y[i] - mu_y) * r_y;  // y is its norm from here on
+                h[i] = y[i] * w[i];
+            }
+            if (a.bb) {
+                R::load((const T *)a.bb, a.cols, t, w);
+#pragma unroll
+                for (int i = 0; i < E; i++) h[i] += w[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i++) h[i] = y[i];
+        }
+        // h = n for now; g = scale times gate
+        if (a.gate) {
+            R::load((const T *)a.gate + row / a.rows_per_gate * a.cols, a.cols, t, g);
+#pragma unroll
+            for (int i = 0; i < E; i++) g[i] *= a.scale;
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i++) g[i] = a.scale;
+        }
+#pragma unroll
+        for (int i = 0; i < E; i++) x[i] += g[i] * h[i];
+        row_stats<R, NT>(x, a, t, buf + 2, mu_h, r_h);
+        R::load((const T *)a.nw, a.cols, t, w);
+        float s1 = 0, s2 = 0;
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+            x[i] = (x[i] - mu_h) * r_h;  // x is the norm of h from here on
+            acc_nw[i] += du[i] * x[i];
+            acc_nb[i] += du[i];
+            du[i] *= w[i];
+            s1 += du[i] * x[i];
+            s2 += du[i];
+        }
+        s1 = row_sum<NT>(s1, buf[4]) * inv;
+        s2 = a.layer ? row_sum<NT>(s2, buf[5]) * inv : 0.0f;
+        R::load((const T *)o.dh + row * o.dh_stride, a.cols, t, w);
+#pragma unroll
+        for (int i = 0; i < E; i++) {
+            w[i] += r_h * (du[i] - s2 - x[i] * s1);  // the gradient of h
+            acc_g[i] += a.scale * w[i] * h[i];
+            g[i] *= w[i];  // the gradient of n
+        }
+        R::store((T *)o.dx + row * o.dx_stride, a.cols, t, w);
+        if (a.bw) {
+            R::load((const T *)a.bw, a.cols, t, w);
+            s1 = 0, s2 = 0;
+#pragma unroll
+            for (int i = 0; i < E; i++) {
+                acc_bw[i] += g[i] * y[i];
+                acc_bb[i] += g[i];
+                g[i] *= w[i];
+                s1 += g[i] * y[i];
+                s2 += g[i];
+            }
+            s1 = row_sum<NT>(s1, buf[6]) * inv;
+            s2 = a.layer ? row_sum<NT>(s2, buf[7]) * inv : 0.0f;
+#pragma unroll
+            for (int i = 0; i < E; i++) g[i] = r_y * (g[i] - s2 - y[i] * s1);
+        }
+        R::store((T *)o.dy + row * o.dy_stride, a.cols, t, g);
+        if (a.gate && p.chunks == 1 && (row + 1) % a.rows_per_gate == 0) {
+            float *q = o.gate + row / a.rows_per_gate * a.cols;
+#pragma unroll
+            for (int i = 0; i < E; i++) {
+                if (R::col(i, t) < a.cols) q[R::col(i, t)] = acc_g[i];
+                acc_g[i] = 0;
+            }
+        }
+    }
+    auto put = [&](float *base, const float (&v)[E]) {
+        if (!base) return;
+        base += (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+        for (int i = 0; i < E; i++)
+            if (R::col(i, t) < a.cols) base[R::col(i, t)] = v[i];
+    };
+    put(o.part[0], acc_nw);
+    put(o.part[1], acc_nb);
+    put(o.part[2], acc_bw);
+    put(o.part[3], acc_bb);
+    put(o.part_gate, acc_g);
+}
+
+// out[c] = sum over b of part[b][c], 64 columns a workgroup, SLICES threads a column.  blockIdx.y:
+// the weights' arrays, then the gate's groups.
+struct GradSums {
+    const float *part[4];
+    float *out[4];
+    const float *part_gate;
+    float *gate;
+    int64_t blocks, chunks;
+};
+constexpr int SLICES = 16;
+__global__ __launch_bounds__(64 * SLICES) void k_norm_grad_sum(GradSums s, int cols) {
+    __shared__ float sh[SLICES][64];
+    const int c = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
+    const float *part;
+    float *out;
+    int64_t n;
+    if (blockIdx.y < 4) {
+        part = s.part[blockIdx.y], out = s.out[blockIdx.y], n = s.blocks;
+    } else {
+        const int64_t g = blockIdx.y - 4;
+        part = s.part_gate + g * s.chunks * cols, out = s.gate + g * cols, n = s.chunks;
+    }
+    if (!out) return;
+    float v = 0;
+    if (c < cols)
+        for (int64_t b = k; b < n; b += SLICES) v += part[b * cols + c];
+    sh[k][threadIdx.x & 63] = v;
+    __syncthreads();
+    if (k == 0 && c < cols) {
+#pragma unroll
+        for (int i = 1; i < SLICES; i++) v += sh[i][threadIdx.x];
+        out[c] = v;
+    }
+}
+
+__global__ void k_zero(float *p, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) p[i] = 0;
+}
+
+// ------------------------------------------------------------------ launches
+
+// f(type tag, threads, elements, vector) for the smallest row shape that holds the columns
+template <int N> struct Int { static constexpr int value = N; };
+template <bool B> struct Flag { static constexpr bool value = B; };
+template <typename T, typename F> int by_shape(int64_t cols, bool vector, F f) {
+    auto go = [&](auto nt, auto e) { return vector ? f(T{}, nt, e, Flag<true>{}) : f(T{}, nt, e, Flag<false>{}); };
+    if (cols <= 512) return go(Int<64>{}, Int<8>{});
+    if (cols <= 1024) return go(Int<128>{}, Int<8>{});
+    if (cols <= 2048) return go(Int<256>{}, Int<8>{});
+    if (cols <= 4096) return go(Int<512>{}, Int<8>{});
+    if (cols <= 8192) return go(Int<1024>{}, Int<8>{});
+    return go(Int<1024>{}, Int<16>{});
+}
+template <typename F> int by_type(int type, int64_t cols, bool vector, F f) {
+    switch (type) {
+        case CKKS_PLAIN_BF16: return by_shape<bf16>(cols, vector, f);
+        case CKKS_PLAIN_F16: return by_shape<f16>(cols, vector, f);
+        default: return by_shape<float>(cols, vector, f);
+    }
+}
+inline bool vector_ok(const void *p, int64_t stride, size_t size) { return !p || (at(p, 16) && stride * size % 16 == 0); }
+
+int check_norm(const ckks_plain_norm *p) {
+    if (!p || !type_ok(p->type) || (p->kind != CKKS_PLAIN_RMS && p->kind != CKKS_PLAIN_LAYER)) return CKKS_EINVAL;
+    if (p->rows < 0 || p->cols < 1 || p->groups < 0 || p->rows >= (int64_t)1 << 31) return CKKS_EINVAL;
+    if (p->cols > CKKS_PLAIN_MAX_COLS) return CKKS_EUNSUPPORTED;
+    if (!p->gate != (p->groups == 0) || (p->groups && p->rows % p->groups)) return CKKS_EINVAL;
+    if (!p->next_weight || (p->block_bias && !p->block_weight) || !(p->eps >= 0)) return CKKS_EINVAL;
+    const size_t z = type_size(p->type);
+    for (const void *v : {p->next_weight, p->next_bias, p->block_weight, p->block_bias, p->gate})
+        if (!at(v, z)) return CKKS_EALIGN;
+    if (p->rows == 0) return CKKS_OK;
+    if (int e = check_matrix(p->x, p->x_stride, p->cols, z)) return e;
+    return check_matrix(p->y, p->y_stride, p->cols, z);
+}
+// an output's range against every input of the call
+bool norm_overlap(const ckks_plain_norm *p, const void *out, size_t bytes, bool x_too) {
+    const size_t z = type_size(p->type), row = p->cols * z;
+    if (x_too && overlap(out, bytes, p->x, span(p->rows, p->x_stride, p->cols, z))) return true;
+    if (overlap(out, bytes, p->y, span(p->rows, p->y_stride, p->cols, z))) return true;
+    for (const void *v : {p->next_weight, p->next_bias, p->block_weight, p->block_bias})
+        if (overlap(out, bytes, v, row)) return true;
+    return overlap(out, bytes, p->gate, row * p->groups);
+}
+NormArgs args_of(const ckks_plain_norm *p) {
+    return NormArgs{p->x, p->y, p->next_weight, p->next_bias, p->block_weight, p->block_bias, p->gate, p->rows,
+                    p->x_stride, p->y_stride, p->groups ? p->rows / p->groups : p->rows, (int)p->cols,
+                    p->kind == CKKS_PLAIN_LAYER, p->scale, p->eps};
+}
+bool norm_vector(const ckks_plain_norm *p) {
+    const size_t z = type_size(p->type);
+    return vector_ok(p->x, p->x_stride, z) && vector_ok(p->y, p->y_stride, z) && vector_ok(p->next_weight, 0, z) &&
+           vector_ok(p->next_bias, 0, z) && vector_ok(p->block_weight, 0, z) && vector_ok(p->block_bias, 0, z) &&
+           vector_ok(p->gate, p->groups > 1 ? p->cols : 0, z);
+}
+
+template <bool I8>
+int residual_norm(const ckks_plain_norm *p, void *h, int64_t h_stride, void *u, int64_t u_stride, float *q_scale,
+                  hipStream_t s) {
+    if (int e = check_norm(p)) return e;
+    if (p->rows == 0) return CKKS_OK;
+    const size_t z = type_size(p->type);
+    if (int e = check_matrix(h, h_stride, p->cols, z)) return e;
+    const int64_t padded = round_up(p->cols, CKKS_PLAIN_I8_ROW);
+    if (I8) {
+        if (!u || !q_scale || u_stride < padded || u_stride % CKKS_PLAIN_I8_ROW) return CKKS_EINVAL;
+        if (!at(u, 16) || !at(q_scale, 4)) return CKKS_EALIGN;
+    } else if (int e = check_matrix(u, u_stride, p->cols, z)) {
+        return e;
+    }
+    const size_t hb = span(p->rows, h_stride, p->cols, z);
+    const size_t ub = I8 ? span(p->rows, u_stride, padded, 1) : span(p->rows, u_stride, p->cols, z);
+    const bool in_place = h == p->x && h_stride == p->x_stride;
+    if (norm_overlap(p, h, hb, !in_place) || norm_overlap(p, u, ub, true) || overlap(h, hb, u, ub)) return CKKS_EINVAL;
+    if (I8) {
+        const size_t sb = p->rows * 4;
+        if (norm_overlap(p, q_scale, sb, true) || overlap(q_scale, sb, u, ub) || overlap(q_scale, sb, h, hb))
+            return CKKS_EINVAL;
+    }
+    const bool vec = norm_vector(p) && vector_ok(h, h_stride, z) && (I8 || vector_ok(u, u_stride, z));
+    const NormArgs a = args_of(p);
+    return by_type(p->type, p->cols, vec, [&](auto ty, auto nt, auto e, auto v) {
+        typedef decltype(ty) T;
+        constexpr int NT = decltype(nt)::value;
+        const int64_t blocks = NT == 64 ? (p->rows + 3) / 4 : p->rows;
+        k_residual_norm<T, NT, decltype(e)::value, decltype(v)::value, I8>
+            <<<dim3((uint32_t)blocks), NT == 64 ? 256 : NT, 0, s>>>(a, (T *)h, h_stride, u, u_stride, q_scale);
+        return launched();
+    });
+}
+
+// Rows of a workgroup: enough workgroups to fill the GPU, few enough that the partial sums stay a
+// small part of the traffic.
+GradPlan grad_plan(const ckks_plain_norm *p) {
+    GradPlan q;
+    const int64_t target = 1024;
+    q.groups = p->groups ? p->groups : 1;
+    q.rows_per_gate = p->rows / q.groups;
+    const int64_t want = p->rows / target > 1 ? p->rows / target : 1;
+    if (q.rows_per_gate <= want) {
+        q.chunks = 1;
+        q.span = q.rows_per_gate ? want / q.rows_per_gate * q.rows_per_gate : 1;
+        q.blocks = (p->rows + q.span - 1) / q.span;
+    } else {
+        q.chunks = (q.rows_per_gate + want - 1) / want;
+        q.span = (q.rows_per_gate + q.chunks - 1) / q.chunks;
+        q.chunks = (q.rows_per_gate + q.span - 1) / q.span;
+        q.blocks = q.groups * q.chunks;
+    }
+    return q;
+}
+// partial sums of next_weight, next_bias, block_weight, block_bias, gate
+void grad_parts(const ckks_plain_norm *p, const GradPlan &q, bool (&has)[5]) {
+    has[0] = true;
+    has[1] = p->next_bias != nullptr;
+    has[2] = p->block_weight != nullptr;
+    has[3] = p->block_bias != nullptr;
+    has[4] = p->gate && q.chunks > 1;
+}
+
+}  // namespace ckks_plain
+
+using namespace ckks_plain;
+
+extern "C" int ckks_plain_residual_norm(const ckks_plain_norm *p, void *h, int64_t h_stride, void *u,
+                                        int64_t u_stride, void *stream) {
+    return residual_norm<false>(p, h, h_stride, u, u_stride, nullptr, (hipStream_t)stream);
+}
+extern "C" int ckks_plain_residual_norm_i8(const ckks_plain_norm *p, void *h, int64_t h_stride, int8_t *q,
+                                           int64_t q_stride, float *q_scale, void *stream) {
+    return residual_norm<true>(p, h, h_stride, q, q_stride, q_scale, (hipStream_t)stream);
+}
+
+extern "C" int ckks_plain_norm_grad_workspace_size(const ckks_plain_norm *p, size_t *bytes) {
+    if (!bytes) return CKKS_EINVAL;
+    if (int e = check_norm(p)) return e;
+    const GradPlan q = grad_plan(p);
+    bool has[5];
+    grad_parts(p, q, has);
+    size_t n = 0;
+    for (bool b : has) n += b;
+    *bytes = n * (size_t)round_up(q.blocks * p->cols * 4, 16);
+    return CKKS_OK;
+}
+
+extern "C" int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckks_plain_norm_grads *g, void *ws,
+                                             size_t ws_bytes, void *stream) {
+    if (!g) return CKKS_EINVAL;
+    size_t need;
+    if (int e = ckks_plain_norm_grad_workspace_size(p, &need)) return e;
+    const size_t z = type_size(p->type), row4 = p->cols * 4;
+    float *const outs[5] = {g->next_weight, g->next_bias, g->block_weight, g->block_bias, g->gate};
+    const void *const ins[5] = {p->next_weight, p->next_bias, p->block_weight, p->block_bias, p->gate};
+    for (int i = 0; i < 5; i++) {
+        if (!outs[i] != !ins[i]) return CKKS_EINVAL;
+        if (!at(outs[i], 4)) return CKKS_EALIGN;
+    }
+    if (p->rows) {
+        if (int e = check_matrix(g->dh, g->dh_stride, p->cols, z)) return e;
+        if (int e = check_matrix(g->du, g->du_stride, p->cols, z)) return e;
+        if (int e = check_matrix(g->dx, g->dx_stride, p->cols, z)) return e;
+        if (int e = check_matrix(g->dy, g->dy_stride, p->cols, z)) return e;
+    }
+    struct { const void *p; size_t n; } w[8] = {{g->dx, span(p->rows, g->dx_stride, p->cols, z)},
+                                                {g->dy, span(p->rows, g->dy_stride, p->cols, z)}, {ws, need}};
+    for (int i = 0; i < 5; i++) w[3 + i] = {outs[i], i < 4 ? row4 : row4 * p->groups};
+    for (int i = 0; i < 8; i++) {
+        if (norm_overlap(p, w[i].p, w[i].n, true) ||
+            overlap(w[i].p, w[i].n, g->dh, span(p->rows, g->dh_stride, p->cols, z)) ||
+            overlap(w[i].p, w[i].n, g->du, span(p->rows, g->du_stride, p->cols, z)))
+            return CKKS_EINVAL;
+        for (int j = 0; j < i; j++)
+            if (overlap(w[i].p, w[i].n, w[j].p, w[j].n)) return CKKS_EINVAL;
+    }
+    if (need && (!ws || ws_bytes < need)) return CKKS_EWORKSPACE;
+    if (!at(ws, 16)) return CKKS_EALIGN;
+    const hipStream_t s = (hipStream_t)stream;
+    const GradPlan q = grad_plan(p);
+    bool has[5];
+    grad_parts(p, q, has);
+    GradArgs o{g->dh, g->du, g->dx, g->dy, g->dh_stride, g->du_stride, g->dx_stride, g->dy_stride, g->gate, nullptr, {}};
+    GradSums sums{};
+    sums.blocks = q.blocks, sums.chunks = q.chunks;
+    char *at_ws = (char *)ws;
+    for (int i = 0; i < 5; i++) {
+        if (!has[i]) continue;
+        (i < 4 ? o.part[i] : o.part_gate) = (float *)at_ws;
+        at_ws += round_up(q.blocks * p->cols * 4, 16);
+    }
+    for (int i = 0; i < 4; i++) sums.part[i] = o.part[i], sums.out[i] = outs[i];
+    sums.part_gate = o.part_gate, sums.gate = g->gate;
+    if (p->rows) {
+        const bool vec = norm_vector(p) && vector_ok(g->dh, g->dh_stride, z) && vector_ok(g->du, g->du_stride, z) &&
+                         vector_ok(g->dx, g->dx_stride, z) && vector_ok(g->dy, g->dy_stride, z);
+        const NormArgs a = args_of(p);
+        int e = by_type(p->type, p->cols, vec, [&](auto ty, auto nt, auto el, auto v) {
+            k_norm_grad<decltype(ty), decltype(nt)::value, decltype(el)::value, decltype(v)::value>
+                <<<dim3((uint32_t)q.blocks), decltype(nt)::value, 0, s>>>(a, o, q);
+            return launched();
+        });
+        if (e) return e;
+    }
+    // without rows there are no partial sums: the sums of nothing are written
+    if (p->gate && !p->rows) {
+        const size_t n = (size_t)p->groups * p->cols;
+        k_zero<<<dim3((uint32_t)(n < 65536 * 256 ? (n + 255) / 256 : 65536)), 256, 0, s>>>(g->gate, n);
+    }
+    const uint32_t gate_sums = has[4] ? (uint32_t)p->groups : 0;  // fewer than `target` of grad_plan
+    k_norm_grad_sum<<<dim3((uint32_t)((p->cols + 63) / 64), 4 + gate_sums), 64 * SLICES, 0, s>>>(sums, (int)p->cols);
+    return launched();
+}
+
+extern "C" int ckks_plain_quantize_rows(int type, const void *x, int64_t x_stride, int64_t rows, int64_t cols,
+                                        int8_t *q, int64_t q_stride, float *q_scale, void *stream) {
+    if (!type_ok(type) || rows < 0 || rows >= (int64_t)1 << 31 || cols < 1) return CKKS_EINVAL;
+    if (cols > CKKS_PLAIN_MAX_COLS) return CKKS_EUNSUPPORTED;
+    if (rows == 0) return CKKS_OK;
+    const size_t z = type_size(type);
+    const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
+    if (int e = check_matrix(x, x_stride, cols, z)) return e;
+    if (!q || !q_scale || q_stride < padded || q_stride % CKKS_PLAIN_I8_ROW) return CKKS_EINVAL;
+    if (!at(q, 16) || !at(q_scale, 4)) return CKKS_EALIGN;
+    const size_t xb = span(rows, x_stride, cols, z), qb = span(rows, q_stride, padded, 1), sb = rows * 4;
+    if (overlap(q, qb, x, xb) || overlap(q_scale, sb, x, xb) || overlap(q, qb, q_scale, sb)) return CKKS_EINVAL;
+    return by_type(type, cols, vector_ok(x, x_stride, z), [&](auto ty, auto nt, auto e, auto v) {
+        typedef decltype(ty) T;
+        constexpr int NT = decltype(nt)::value;
+        k_quantize_rows<T, NT, decltype(e)::value, decltype(v)::value>
+            <<<dim3((uint32_t)(NT == 64 ? (rows + 3) / 4 : rows)), NT == 64 ? 256 : NT, 0, (hipStream_t)stream>>>(
+                (const T *)x, x_stride, rows, (int)cols, q, q_stride, q_scale);
+        return launched();
+    });
+}

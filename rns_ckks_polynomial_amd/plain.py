@@ -1,0 +1,267 @@
+"""The plaintext side of an encrypted decoder (include/ckks_plain.h): residual
+stream and norms around a block, products of 8-bit rows, and token sampling.
+
+Argument checks and marshalling only: every step of the computation runs in
+the HIP library.  Matrices are 2-D device tensors with unit column stride (any
+row stride); calls are enqueued on the current torch stream of the tensors'
+device, outputs and scratch come from torch's allocator.
+"""
+from __future__ import annotations
+
+import ctypes as C
+from collections import namedtuple
+
+import torch
+
+from . import _native as nat
+
+TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+KINDS = {"rms": 0, "layer": 1}
+I8_ROW = 128        # CKKS_PLAIN_I8_ROW
+MAX_COLS = 16384    # CKKS_PLAIN_MAX_COLS
+
+ResidualNormGrads = namedtuple("ResidualNormGrads",
+                               "dx dy next_weight next_bias block_weight block_bias gate")
+
+
+def _call(name, device, *args):
+    """One C call on `device` and its current stream."""
+    f = getattr(nat.lib(), name)
+    s = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        nat.check(f(*args, s), name)
+    else:
+        with torch.cuda.device(device):
+            nat.check(f(*args, s), name)
+
+
+def _matrix(t, what, rows=None, cols=None, dtype=None, device=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what}: expected a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a matrix with unit column stride")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    return t
+
+
+def _vector(t, what, n, dtype, device):
+    """Address of a contiguous vector of n elements (None: null)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype} on {device}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _stride(t):
+    """Row stride; torch leaves that of a matrix with at most one row open."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _type(t, what):
+    if t.dtype not in TYPES:
+        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return TYPES[t.dtype]
+
+
+class Int8Rows:
+    """8-bit rows: row t stands for scale[t] * q[t, :cols].
+
+    q: int8 [rows, >= cols rounded up to I8_ROW] with rows that start at multiples of I8_ROW bytes
+    and zeros behind the columns (at least in one operand of a product) is kept as it is; any other
+    layout is copied into such rows once, here.  scale: float32 [rows]."""
+
+    __slots__ = ("q", "scale", "cols")
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int | None = None):
+        if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != torch.int8 or q.dim() != 2:
+            raise ValueError("q: expected an int8 matrix on the device")
+        cols = q.shape[1] if cols is None else cols
+        if not 1 <= cols <= q.shape[1]:
+            raise ValueError(f"cols: {cols} of {q.shape[1]}")
+        _vector(scale, "scale", q.shape[0], torch.float32, q.device)
+        padded = -(-cols // I8_ROW) * I8_ROW
+        if q.shape[1] < padded or q.stride(1) != 1 or q.stride(0) % I8_ROW or q.data_ptr() % 16:
+            rows = torch.zeros((q.shape[0], padded), dtype=torch.int8, device=q.device)
+            rows[:, :cols] = q[:, :cols]
+            q = rows
+        self.q, self.scale, self.cols = q, scale, cols
+
+    @staticmethod
+    def empty(rows: int, cols: int, device) -> "Int8Rows":
+        self = object.__new__(Int8Rows)
+        self.q = torch.empty((rows, -(-cols // I8_ROW) * I8_ROW), dtype=torch.int8, device=device)
+        self.scale = torch.empty(rows, dtype=torch.float32, device=device)
+        self.cols = cols
+        return self
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[0]
+
+    def dequantize(self, dtype=torch.float32) -> torch.Tensor:
+        return (self.q[:, :self.cols].float() * self.scale[:, None]).to(dtype)
+
+
+def _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind):
+    """ckks_plain_norm of the arguments."""
+    _matrix(x, "x")
+    T, D = x.shape
+    dev, dt = x.device, x.dtype
+    _matrix(y, "y", T, D, dt, dev)
+    if kind not in KINDS:
+        raise ValueError(f"kind: expected 'rms' or 'layer', got {kind!r}")
+    groups, gp = 0, None
+    if gate is not None:
+        if gate.dim() == 1:
+            groups, gp = 1, _vector(gate, "gate", D, dt, dev)
+        else:
+            _matrix(gate, "gate", None, D, dt, dev)
+            if not gate.is_contiguous() or gate.shape[0] < 1 or T % gate.shape[0]:
+                raise ValueError(f"gate: expected contiguous rows, a divisor of {T}, got {tuple(gate.shape)}")
+            groups, gp = gate.shape[0], gate.data_ptr()
+    return nat.PlainNorm(_type(x, "x"), KINDS[kind], T, D, groups, x.data_ptr(), y.data_ptr(), _stride(x), _stride(y),
+                         _vector(next_weight, "next_weight", D, dt, dev), _vector(next_bias, "next_bias", D, dt, dev),
+                         _vector(block_weight, "block_weight", D, dt, dev),
+                         _vector(block_bias, "block_bias", D, dt, dev), gp, scale, eps)
+
+
+def _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind):
+    p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+    h, u = torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    D = x.shape[1]
+    _call("ckks_plain_residual_norm", x.device, C.byref(p), h.data_ptr(), D, u.data_ptr(), D)
+    return h, u
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind):
+        ctx.save_for_backward(x, y, next_weight, next_bias, block_weight, block_bias, gate)
+        ctx.rest = (scale, eps, kind)
+        return _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+
+    @staticmethod
+    def backward(ctx, dh, du):
+        x, y, nw, nb, bw, bb, gate = ctx.saved_tensors
+        scale, eps, kind = ctx.rest
+        g = residual_norm_grad(x, y, dh.contiguous(), du.contiguous(), nw, nb, bw, bb, gate, scale, eps, kind)
+        like = lambda v, p: None if p is None else v.view(p.shape).to(p.dtype)  # noqa: E731
+        return (g.dx, g.dy, like(g.next_weight, nw), like(g.next_bias, nb), like(g.block_weight, bw),
+                like(g.block_bias, bb), like(g.gate, gate), None, None, None)
+
+
+def residual_norm(x, y, next_weight, next_bias=None, block_weight=None, block_bias=None, gate=None,
+                  scale: float = 1.0, eps: float = 1e-6, kind: str = "rms"):
+    """(h, u): the residual stream x takes the block output y, and its norm for the next block
+    (ckks_plain_residual_norm).  n = y, or block_weight norm(y) + block_bias; h = x + scale gate n;
+    u = next_weight norm(h) + next_bias.  x, y [T, D]; weights and biases [D]; gate [D] or [G, D]
+    (a row for T / G tokens each); one type for all.  Differentiable through torch.autograd (gradients of weights are
+    summed in 32 bits, then rounded to their type)."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in
+                                       (x, y, next_weight, next_bias, block_weight, block_bias, gate)):
+        return _ResidualNorm.apply(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+    return _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+
+
+def residual_norm_i8(x, y, next_weight, next_bias=None, block_weight=None, block_bias=None, gate=None,
+                     scale: float = 1.0, eps: float = 1e-6, kind: str = "rms"):
+    """(h, rows): residual_norm with u as 8-bit rows, quantised before any other rounding."""
+    p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+    h, u = torch.empty(x.shape, dtype=x.dtype, device=x.device), Int8Rows.empty(*x.shape, x.device)
+    _call("ckks_plain_residual_norm_i8", x.device, C.byref(p), h.data_ptr(), x.shape[1], u.q.data_ptr(),
+          u.q.shape[1], u.scale.data_ptr())
+    return h, u
+
+
+def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=None, block_bias=None, gate=None,
+                       scale: float = 1.0, eps: float = 1e-6, kind: str = "rms") -> ResidualNormGrads:
+    """Gradients of residual_norm's operands from those of h and u: dx and dy in the type of x, those
+    of weights, biases and gate (of the gate's shape) in float32, None where there is no such operand."""
+    p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
+    T, D = x.shape
+    _matrix(dh, "dh", T, D, x.dtype, x.device)
+    _matrix(du, "du", T, D, x.dtype, x.device)
+    new = lambda v: None if v is None else torch.empty(v.shape, dtype=torch.float32, device=x.device)  # noqa: E731
+    r = ResidualNormGrads(torch.empty((T, D), dtype=x.dtype, device=x.device),
+                          torch.empty((T, D), dtype=x.dtype, device=x.device), new(next_weight), new(next_bias),
+                          new(block_weight), new(block_bias), new(gate))
+    at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
+    g = nat.PlainNormGrads(dh.data_ptr(), du.data_ptr(), _stride(dh), _stride(du), r.dx.data_ptr(), r.dy.data_ptr(),
+                           D, D, at(r.next_weight), at(r.next_bias), at(r.block_weight), at(r.block_bias), at(r.gate))
+    need = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_norm_grad_workspace_size(C.byref(p), C.byref(need)),
+              "ckks_plain_norm_grad_workspace_size")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
+    _call("ckks_plain_residual_norm_grad", x.device, C.byref(p), C.byref(g), ws.data_ptr(), need.value)
+    return r
+
+
+def quantize_rows(x) -> Int8Rows:
+    """8-bit rows of x [T, D] (ckks_plain_quantize_rows): scale = max |x| / 127 of the row."""
+    _matrix(x, "x")
+    r = Int8Rows.empty(x.shape[0], x.shape[1], x.device)
+    _call("ckks_plain_quantize_rows", x.device, _type(x, "x"), x.data_ptr(), _stride(x), x.shape[0], x.shape[1],
+          r.q.data_ptr(), r.q.shape[1], r.scale.data_ptr())
+    return r
+
+
+def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torch.Tensor:
+    """out[t, c] = a.scale[t] w.scale[c] sum_k a.q[t, k] w.q[c, k] + bias[c] (ckks_plain_matmul_i8),
+    sums exact in 32-bit integers.  bias: float32 [channels]."""
+    if not isinstance(a, Int8Rows) or not isinstance(w, Int8Rows):
+        raise ValueError("expected Int8Rows")
+    if a.cols != w.cols or a.q.device != w.q.device:
+        raise ValueError(f"a has {a.cols} columns on {a.q.device}, w {w.cols} on {w.q.device}")
+    if dtype not in TYPES:
+        raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+    M, N, dev = a.rows, w.rows, a.q.device
+    bp = _vector(bias, "bias", N, torch.float32, dev)
+    out = torch.empty((M, N), dtype=dtype, device=dev)
+    need = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_matmul_i8_workspace_size(M, N, a.cols, C.byref(need)),
+              "ckks_plain_matmul_i8_workspace_size")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), max(_stride(a.q), a.q.shape[1]), a.scale.data_ptr(),
+          w.q.data_ptr(), _stride(w.q), w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols,
+          None if ws is None else ws.data_ptr(), need.value)
+    return out
+
+
+def linear_i8(x, w: Int8Rows, bias=None, dtype=None) -> torch.Tensor:
+    """matmul_i8 of x quantised row by row; dtype defaults to that of x."""
+    return matmul_i8(quantize_rows(x), w, bias, x.dtype if dtype is None else dtype)
+
+
+def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allowed=None):
+    """(token int64 [B], logprob float32 [B]) from logits [B, V] (ckks_plain_sample).  gumbel: float32
+    [B, V], -log(-log u) of uniform numbers; temperature, top_p, min_p: float32 [B]; top_k: int32 [B];
+    allowed: bool [B, V].  temperature <= 0: the largest logit.  A row without a possible token:
+    token -1, logprob -infinity."""
+    _matrix(logits, "logits")
+    B, V = logits.shape
+    dev = logits.device
+    _matrix(gumbel, "gumbel", B, V, torch.float32, dev)
+    if temperature is None:
+        raise ValueError("temperature: expected float32 of every row")
+    if allowed is not None:
+        _matrix(allowed, "allowed", B, V, torch.bool, dev)
+    token = torch.empty(B, dtype=torch.int64, device=dev)
+    logprob = torch.empty(B, dtype=torch.float32, device=dev)
+    need = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_sample_workspace_size(B, V, C.byref(need)), "ckks_plain_sample_workspace_size")
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _call("ckks_plain_sample", dev, _type(logits, "logits"), logits.data_ptr(), _stride(logits), gumbel.data_ptr(),
+          _stride(gumbel), _vector(temperature, "temperature", B, torch.float32, dev),
+          _vector(top_k, "top_k", B, torch.int32, dev), _vector(top_p, "top_p", B, torch.float32, dev),
+          _vector(min_p, "min_p", B, torch.float32, dev), None if allowed is None else allowed.data_ptr(),
+          0 if allowed is None else _stride(allowed), B, V, token.data_ptr(), logprob.data_ptr(),
+          None if ws is None else ws.data_ptr(), need.value)
+    return token, logprob
