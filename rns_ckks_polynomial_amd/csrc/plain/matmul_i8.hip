@@ -14,28 +14,25 @@ struct MatmulArgs {
     const float *a_scale, *w_scale, *bias;
     int64_t a_stride, w_stride, out_stride;
     int rows, channels, padded;
-    bool vector_out;  // four channels from a multiple of four on can be stored at once
+    bool vector_out;  // 16 bytes of channels can be stored at once
 };
 
-// Four channels of one token from their sums: float(sum) is exact to half a step of 32 bits, and
-// so is each of the products and the bias.
-template <typename T>
-__device__ __forceinline__ void store4(const MatmulArgs &m, T *out, int t, int c, float a_scale, int s0, int s1, int s2,
-                                       int s3) {
-    typedef T T4 __attribute__((ext_vector_type(4)));
-    const int s[4] = {s0, s1, s2, s3};
+// N channels of one token from their sums: the sum, the two scales, their product and the bias
+// round once each in 32 bits.
+template <typename T, int N>
+__device__ __forceinline__ void store_sums(const MatmulArgs &m, T *out, int t, int c, float a_scale, const int (&s)[N],
+                                           const float (&w_scale)[N], const float (&bias)[N]) {
+    typedef T TN __attribute__((ext_vector_type(N)));
     T *p = out + (int64_t)t * m.out_stride + c;
-    if (m.vector_out && c + 4 <= m.channels) {
-        T4 v;
+    TN v;
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            v[i] = from_f32<T>((float)s[i] * (a_scale * m.w_scale[c + i]) + (m.bias ? m.bias[c + i] : 0.0f));
-        *(T4 *)p = v;
+    for (int i = 0; i < N; i++) v[i] = from_f32<T>((float)s[i] * (a_scale * w_scale[i]) + bias[i]);
+    if (m.vector_out && c + N <= m.channels) {
+        *(TN *)p = v;
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (c + i < m.channels)
-                p[i] = from_f32<T>((float)s[i] * (a_scale * m.w_scale[c + i]) + (m.bias ? m.bias[c + i] : 0.0f));
+        for (int i = 0; i < N; i++)
+            if (c + i < m.channels) p[i] = v[i];
     }
 }
 
@@ -57,126 +54,148 @@ struct TileOrder {
 // ------------------------------------------------------------------ tiles
 //
 // A workgroup of four waves (2 x 2) computes BN channels x BM tokens; a wave has a quarter of
-// them as 32 x 32 tiles in registers.  The contraction goes in steps of 128 bytes, two steps in
-// LDS: while one is multiplied, the other is filled by loads that go from memory to LDS directly.
+// them as 32 x 32 tiles in registers.  The contraction goes in steps of 64 bytes, four of them in
+// LDS: while one is multiplied, the next three are there or on their way, by loads that go from
+// memory to LDS directly.
 //
-// LDS layout: rows of 128 bytes in eight 16-byte pieces; piece p of row r lies at p ^ (r & 7), so
-// the lanes that read one piece of neighbouring rows reach different banks.  The loads write LDS
-// in lane order and permute the pieces on the memory side (within a row's 128 bytes).
-constexpr int STEP = 128;
+// LDS layout: rows of 64 bytes in four 16-byte pieces; piece p of row r lies at p ^ (r / 4 & 3), so
+// the 16 lanes that LDS serves at a time (one piece of 16 rows) reach all 64 banks once.  The
+// loads write LDS in lane order and permute the pieces on the memory side (within a row's 64 bytes).
+constexpr int STEP = 64, STAGES = 4;
 
 // 64 lanes x 16 bytes from base + voff (a lane's offset) to the LDS address `lds` (of the wave) on.
-// The write to LDS is tracked by vmcnt, which the compiler does not see here: tile_wait orders it.
+// The write to LDS is counted by vmcnt, which the compiler does not see here: tile_wait orders it.
 __device__ __forceinline__ void load_to_lds(const int8_t *base, uint32_t voff, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  :
                  : "s"(lds), "v"(voff), "s"(base)
                  : "memory", "m0");
 }
-// All of this wave's reads and writes of LDS are done, and then the other waves'.
-__device__ __forceinline__ void tile_wait() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All of this wave's reads of LDS and all but the last `PENDING` of its loads to LDS are done, and
+// then the other waves' too.
+template <int PENDING> __device__ __forceinline__ void tile_wait() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
+}
 
 template <typename T, int BM, int BN>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(MatmulArgs m, T *out, TileOrder order) {
-    constexpr int TN = BN / 64, TM = BM / 64;      // 32 x 32 tiles of a wave
-    constexpr int LOADS_W = BN / 32, LOADS_A = BM / 32;  // of a wave, per step
-    __shared__ int8_t lds[2][(BN + BM) * STEP];
+    constexpr int TN = BN / 64, TM = BM / 64;               // 32 x 32 tiles of a wave
+    constexpr int LOADS_W = BN / 64, LOADS = LOADS_W + BM / 64;  // of a wave, per step
+    constexpr int STAGE = (BN + BM) * STEP;
+    // the epilogue's: 32 tokens x a wave's channels of sums, rows 16 bytes apart in the banks
+    constexpr int SUMS = BN / 2 + 4;
+    static_assert(4 * 32 * SUMS * 4 <= STAGES * STAGE, "the epilogue fits");
+    __shared__ __attribute__((aligned(16))) int8_t lds[STAGES * STAGE];
     int tile_t, tile_c;
     order.tile(blockIdx.x, tile_t, tile_c);
     const int t0 = tile_t * BM, c0 = tile_c * BN;
-    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int8_t *wp = m.w + (int64_t)c0 * m.w_stride, *ap = m.a + (int64_t)t0 * m.a_stride;
-    // lane's row and piece in a load of 8 rows; rows past the end read the last one (not stored)
-    uint32_t off_w[LOADS_W], off_a[LOADS_A];
+    // lane's row and piece in a load of 16 rows; rows past the end read the last one (not stored)
+    uint32_t off[LOADS];
 #pragma unroll
-    for (int j = 0; j < LOADS_W; j++) {
-        const int r = (j * 4 + wave) * 8 + l / 8, left = m.channels - 1 - c0;
-        off_w[j] = (uint32_t)((r < left ? r : left) * m.w_stride) + ((l % 8) ^ (l / 8)) * 16;
+    for (int j = 0; j < LOADS; j++) {
+        const bool weights = j < LOADS_W;
+        const int r = ((weights ? j : j - LOADS_W) * 4 + wave) * 16 + l / 4;
+        const int left = weights ? m.channels - 1 - c0 : m.rows - 1 - t0;
+        off[j] = (uint32_t)((r < left ? r : left) * (weights ? m.w_stride : m.a_stride)) + ((l % 4) ^ (r / 4 % 4)) * 16;
     }
-#pragma unroll
-    for (int j = 0; j < LOADS_A; j++) {
-        const int r = (j * 4 + wave) * 8 + l / 8, left = m.rows - 1 - t0;
-        off_a[j] = (uint32_t)((r < left ? r : left) * m.a_stride) + ((l % 8) ^ (l / 8)) * 16;
-    }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)&lds[0][0];
-    // load j of this wave's share of the step at k
-    auto fill_one = [&](int buf, int64_t k, int j) {
-        const uint32_t at = __builtin_amdgcn_readfirstlane(lds0 + buf * (BN + BM) * STEP + wave * 1024);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)&lds[0] + wave * 1024;
+    // load j of this wave's share of step s
+    auto fill_one = [&](int s, int j) {
+        const uint32_t at = __builtin_amdgcn_readfirstlane(lds0 + s % STAGES * STAGE);
         if (j < LOADS_W)
-            load_to_lds(wp + k, off_w[j], at + j * 4096);
+            load_to_lds(wp + (int64_t)s * STEP, off[j], at + j * 4096);
         else
-            load_to_lds(ap + k, off_a[j - LOADS_W], at + BN * STEP + (j - LOADS_W) * 4096);
-    };
-    auto fill = [&](int buf, int64_t k) {
-#pragma unroll
-        for (int j = 0; j < LOADS_W + LOADS_A; j++) fill_one(buf, k, j);
+            load_to_lds(ap + (int64_t)s * STEP, off[j], at + BN * STEP + (j - LOADS_W) * 4096);
     };
     // wave's quarter; lane's row in a 32-row tile and its 16-byte piece of slab s: 2 s + l / 32
     const int row_w = (wave & 1) * (BN / 2) + l % 32, row_a = BN + (wave >> 1) * (BM / 2) + l % 32;
     v4i fw[2][TN], fa[2][TM];
     v16i acc[TN][TM] = {};
-    auto read = [&](int buf, int s, v4i (&w)[TN], v4i (&a)[TM]) {
-        const int piece = ((2 * s + l / 32) ^ (l & 7)) * 16;
-#pragma unroll
-        for (int i = 0; i < TN; i++) w[i] = *(const v4i *)&lds[buf][(row_w + 32 * i) * STEP + piece];
-#pragma unroll
-        for (int i = 0; i < TM; i++) a[i] = *(const v4i *)&lds[buf][(row_a + 32 * i) * STEP + piece];
-        __builtin_amdgcn_sched_barrier(0);
+    // read n of half h of step s: the weight tiles' pieces, then the tokens'
+    auto read_one = [&](int s, int h, int n) {
+        const int8_t *at = lds + s % STAGES * STAGE + ((2 * h + l / 32) ^ (l / 4 & 3)) * 16;
+        if (n < TN)
+            fw[h][n] = *(const v4i *)(at + (row_w + 32 * n) * STEP);
+        else
+            fa[h][n - TN] = *(const v4i *)(at + (row_a + 32 * (n - TN)) * STEP);
     };
-    // a slab's products; `other(n)` runs after the n-th of them
-    auto mac = [&](const v4i (&w)[TN], const v4i (&a)[TM], auto other) {
+    // A half step's products; `other(n)` runs after the n-th of them.  Reads and loads are spread
+    // over the products: a wave that issues them together waits for LDS to take them, and the
+    // matrix cores with it.
+    auto mac = [&](int h, auto other) {
 #pragma unroll
         for (int n = 0; n < TN * TM; n++) {
             const int i = n / TM, j = n % TM;
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], a[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
             other(n);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
     };
-    auto nothing = [](int) {};
-    // One step: the reads of each slab are issued before the products of the slab in front of it,
-    // the loads of the step after the next one between the products of the last slab.
-    auto step = [&](int s, auto more, auto fill_more) {
-        const int buf = s & 1;
-        read(buf, 1, fw[1], fa[1]);
-        mac(fw[0], fa[0], nothing);
-        read(buf, 2, fw[0], fa[0]);
-        mac(fw[1], fa[1], nothing);
-        read(buf, 3, fw[1], fa[1]);
-        mac(fw[0], fa[0], nothing);
-        tile_wait();  // the other buffer is full, and nobody reads this one any more
-        if constexpr (decltype(more)::value) read(buf ^ 1, 0, fw[0], fa[0]);
-        mac(fw[1], fa[1], [&](int n) {
-            if constexpr (decltype(fill_more)::value) {
-                constexpr int PER = (LOADS_W + LOADS_A + TN * TM - 1) / (TN * TM);
+    // share n of `count` things over a half step's products
+    auto share = [&](int n, int count, auto f) {
+        const int per = (count + TN * TM - 1) / (TN * TM);
 #pragma unroll
-                for (int j = n * PER; j < (n + 1) * PER && j < LOADS_W + LOADS_A; j++)
-                    fill_one(buf, (int64_t)(s + 2) * STEP, j);
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int j = n * per; j < (n + 1) * per && j < count; j++) f(j);
+    };
+    // One step.  Each half is read during the products of the half in front of it (the last step
+    // reads a stale one that nobody uses).  Half way, the next step has to have arrived and the
+    // waves to have read this one, whose place then takes the step STAGES later.
+    auto step = [&](int s, auto filling) {
+        mac(0, [&](int n) { share(n, TN + TM, [&](int r) { read_one(s, 1, r); }); });
+        tile_wait<decltype(filling)::value ? (STAGES - 2) * LOADS : 0>();
+        mac(1, [&](int n) {
+            share(n, TN + TM, [&](int r) { read_one(s + 1, 0, r); });
+            if constexpr (decltype(filling)::value) share(n, LOADS, [&](int j) { fill_one(s + STAGES, j); });
         });
     };
     const int steps = m.padded / STEP;
-    fill(0, 0);
-    if (steps > 1) fill(1, STEP);
-    tile_wait();
-    read(0, 0, fw[0], fa[0]);
+#pragma unroll
+    for (int s = 0; s < STAGES; s++) {
+        if (s >= steps) break;
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) fill_one(s, j);
+    }
+    tile_wait<0>();
+#pragma unroll
+    for (int n = 0; n < TN + TM; n++) read_one(0, 0, n);
     int s = 0;
-    for (; s < steps - 2; s++) step(s, std::true_type{}, std::true_type{});
-    if (s < steps - 1) step(s++, std::true_type{}, std::false_type{});
-    step(s, std::false_type{}, std::false_type{});
-    // lane: token l % 32 of each tile, channels 8 (v / 4) + 4 (l / 32) + v % 4
+    for (; s < steps - STAGES; s++) step(s, std::true_type{});
+    for (; s < steps; s++) step(s, std::false_type{});
+    // Epilogue: 32 tokens at a time through LDS (a place for each wave), so that a token's channels
+    // leave in whole 16-byte pieces of neighbouring lanes.  A lane holds channels
+    // 8 g + 4 (l / 32) + 0..3 of token l % 32 of each tile.
+    tile_wait<0>();
+    constexpr int PER = sizeof(T) == 4 ? 4 : 8, LANES = BN / 2 / PER;  // channels a lane stores, lanes a token
+    int *sums = (int *)lds + wave * 32 * SUMS;
+    const int c = c0 + (wave & 1) * (BN / 2) + l % LANES * PER;
+    float ws[PER], bias[PER];
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
+        bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < TM; j++) {
-        const int t = t0 + (wave >> 1) * (BM / 2) + 32 * j + l % 32;
-        if (t >= m.rows) continue;
-        const float s = m.a_scale[t];
 #pragma unroll
         for (int i = 0; i < TN; i++)
 #pragma unroll
             for (int g = 0; g < 4; g++)
-                store4(m, out, t, c0 + (wave & 1) * (BN / 2) + 32 * i + 8 * g + 4 * (l / 32), s, acc[i][j][4 * g],
-                       acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+                *(v4i *)(sums + l % 32 * SUMS + 32 * i + 8 * g + 4 * (l / 32)) =
+                    v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        __builtin_amdgcn_wave_barrier();
+        const int tj = t0 + (wave >> 1) * (BM / 2) + 32 * j;
+#pragma unroll
+        for (int r = 0; r < 32; r += 64 / LANES) {
+            const int t = tj + r + l / LANES;
+            if (t >= m.rows) break;
+            int v[PER];
+#pragma unroll
+            for (int i = 0; i < PER; i += 4) *(v4i *)(v + i) = *(const v4i *)(sums + (r + l / LANES) * SUMS + l % LANES * PER + i);
+            store_sums<T, PER>(m, out, t, c, m.a_scale[t], v, ws, bias);
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -201,7 +220,7 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
     const size_t z = type_size(out_type);
     const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
     if (!a || !w || !a_scale || !w_scale || a_stride < padded || w_stride < padded || a_stride % CKKS_PLAIN_I8_ROW ||
-        w_stride % CKKS_PLAIN_I8_ROW)
+        w_stride % CKKS_PLAIN_I8_ROW || a_stride >= 1 << 23 || w_stride >= 1 << 23)
         return CKKS_EINVAL;
     if (!at(a, 16) || !at(w, 16) || !at(a_scale, 4) || !at(w_scale, 4) || !at(bias, 4)) return CKKS_EALIGN;
     if (int e = check_matrix(out, out_stride, channels, z)) return e;
@@ -212,7 +231,7 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
         return CKKS_EINVAL;
     if (need && (!ws || ws_bytes < need)) return CKKS_EWORKSPACE;
     const MatmulArgs m{a, w, a_scale, w_scale, bias, a_stride, w_stride, out_stride, (int)rows, (int)channels,
-                       (int)padded, out_stride % 4 == 0 && at(out, 4 * z)};
+                       (int)padded, out_stride * z % 16 == 0 && at(out, 16)};
     auto go = [&](auto ty) {
         typedef decltype(ty) T;
         auto tiles = [&](int bm, int bn) {
