@@ -1,13 +1,10 @@
 // matmul_i8.hip -- product of 8-bit rows with a scale for each row of both
 // operands (include/ckks_plain.h).
-#include <type_traits>
-
 #include "plain_common.h"
 
 namespace ckks_plain {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
 
 struct MatmulArgs {
     const int8_t *a, *w;
@@ -54,14 +51,22 @@ struct TileOrder {
 // ------------------------------------------------------------------ tiles
 //
 // A workgroup of four waves (2 x 2) computes BN channels x BM tokens; a wave has a quarter of
-// them as 32 x 32 tiles in registers.  The contraction goes in steps of 64 bytes, four of them in
-// LDS: while one is multiplied, the next three are there or on their way, by loads that go from
-// memory to LDS directly.
+// them as 16 x 16 tiles in registers.  (On random values 16x16x64 products alone run at
+// 4.0 POP/s on this GPU, 32x32x32 ones at 3.4: the accumulators move half as often for the same
+// work, and under full load power sets the clock.)  The contraction goes in steps of 64 bytes:
+// one is multiplied from registers, the next is read from LDS, and three more are there or on
+// their way, by loads that go from memory to LDS directly.
 //
-// LDS layout: rows of 64 bytes in four 16-byte pieces; piece p of row r lies at p ^ (r / 4 & 3), so
-// the 16 lanes that LDS serves at a time (one piece of 16 rows) reach all 64 banks once.  The
-// loads write LDS in lane order and permute the pieces on the memory side (within a row's 64 bytes).
+// LDS layout: rows of 64 bytes in four 16-byte pieces; piece p of row r lies at p ^ turn(r).  The
+// lanes that LDS serves at a time then reach all 64 banks once, whether those are 16 neighbours
+// (piece p of rows 0..15) or, as the conflict counter says of this GPU, rows 0..3 and 12..15 of one
+// piece with rows 4..11 of the next (p ^ (r / 4 & 3) serves the former only).  The loads write LDS
+// in lane order and permute the pieces on the memory side (within a row's 64 bytes).
 constexpr int STEP = 64, STAGES = 4;
+__device__ __forceinline__ int turn(int row) {  // 0, 2, 3, 1 for each four rows in turn
+    const int q = row / 4 % 4;
+    return q >> 1 | ((q ^ q >> 1) & 1) << 1;
+}
 
 // 64 lanes x 16 bytes from base + voff (a lane's offset) to the LDS address `lds` (of the wave) on.
 // The write to LDS is counted by vmcnt, which the compiler does not see here: tile_wait orders it.
@@ -77,9 +82,23 @@ template <int PENDING> __device__ __forceinline__ void tile_wait() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
 }
 
+// acc += w x a, tied to one set of accumulation registers: with all 256 of them in use, the
+// compiler's own form lets a result go to other registers and pays for it with copies in the loop
+// (70 in two steps of the 256 x 256 tile).  The compiler does not see a matrix product here:
+// products that follow each other need no wait, results are read after mfma_done.
+__device__ __forceinline__ void mfma_i8(v4i &acc, v4i w, v4i a) {
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(w), "v"(a));
+}
+// Results are there (two times 16 cycles after the last product) and may be read from here on.
+__device__ __forceinline__ void not_before(v4i &acc) { asm volatile("" : "+a"(acc)); }
+template <int TN, int TM> __device__ __forceinline__ void mfma_done(v4i (&acc)[TN][TM]) {
+    asm volatile("s_nop 15\n\ts_nop 15");
+    for_all<TN * TM>([&](auto at) { not_before(acc[decltype(at)::value / TM][decltype(at)::value % TM]); });
+}
+
 template <typename T, int BM, int BN>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(MatmulArgs m, T *out, TileOrder order) {
-    constexpr int TN = BN / 64, TM = BM / 64;               // 32 x 32 tiles of a wave
+    constexpr int TN = BN / 32, TM = BM / 32, TILES = TN * TM;  // 16 x 16 tiles of a wave
     constexpr int LOADS_W = BN / 64, LOADS = LOADS_W + BM / 64;  // of a wave, per step
     constexpr int STAGE = (BN + BM) * STEP;
     // the epilogue's: 32 tokens x a wave's channels of sums, rows 16 bytes apart in the banks
@@ -98,75 +117,67 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
         const bool weights = j < LOADS_W;
         const int r = ((weights ? j : j - LOADS_W) * 4 + wave) * 16 + l / 4;
         const int left = weights ? m.channels - 1 - c0 : m.rows - 1 - t0;
-        off[j] = (uint32_t)((r < left ? r : left) * (weights ? m.w_stride : m.a_stride)) + ((l % 4) ^ (r / 4 % 4)) * 16;
+        off[j] = (uint32_t)((r < left ? r : left) * (weights ? m.w_stride : m.a_stride)) + ((l % 4) ^ turn(r)) * 16;
     }
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)&lds[0] + wave * 1024;
-    // load j of this wave's share of step s
-    auto fill_one = [&](int s, int j) {
-        const uint32_t at = __builtin_amdgcn_readfirstlane(lds0 + s % STAGES * STAGE);
+    // load j of this wave's share of step s, to place `place`
+    auto fill_one = [&](int s, int place, int j) {
+        const uint32_t at = __builtin_amdgcn_readfirstlane(lds0 + place * STAGE);
         if (j < LOADS_W)
             load_to_lds(wp + (int64_t)s * STEP, off[j], at + j * 4096);
         else
             load_to_lds(ap + (int64_t)s * STEP, off[j], at + BN * STEP + (j - LOADS_W) * 4096);
     };
-    // wave's quarter; lane's row in a 32-row tile and its 16-byte piece of slab s: 2 s + l / 32
-    const int row_w = (wave & 1) * (BN / 2) + l % 32, row_a = BN + (wave >> 1) * (BM / 2) + l % 32;
+    const int steps = m.padded / STEP;
+    // wave's quarter; lane's row in a 16-row tile, its 16-byte piece: l / 16
+    const int row_w = (wave & 1) * (BN / 2) + l % 16, row_a = BN + (wave >> 1) * (BM / 2) + l % 16;
     v4i fw[2][TN], fa[2][TM];
-    v16i acc[TN][TM] = {};
-    // read n of half h of step s: the weight tiles' pieces, then the tokens'
+    v4i acc[TN][TM] = {};
+    // read n of step s into set h: the weight tiles' pieces, then the tokens'
     auto read_one = [&](int s, int h, int n) {
-        const int8_t *at = lds + s % STAGES * STAGE + ((2 * h + l / 32) ^ (l / 4 & 3)) * 16;
+        const int8_t *at = lds + s % STAGES * STAGE + ((l / 16) ^ turn(l)) * 16;
         if (n < TN)
-            fw[h][n] = *(const v4i *)(at + (row_w + 32 * n) * STEP);
+            fw[h][n] = *(const v4i *)(at + (row_w + 16 * n) * STEP);
         else
-            fa[h][n - TN] = *(const v4i *)(at + (row_a + 32 * (n - TN)) * STEP);
+            fa[h][n - TN] = *(const v4i *)(at + (row_a + 16 * (n - TN)) * STEP);
     };
-    // A half step's products; `other(n)` runs after the n-th of them.  Reads and loads are spread
-    // over the products: a wave that issues them together waits for LDS to take them, and the
-    // matrix cores with it.
-    auto mac = [&](int h, auto other) {
-#pragma unroll
-        for (int n = 0; n < TN * TM; n++) {
-            const int i = n / TM, j = n % TM;
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[h][i], fa[h][j], acc[i][j], 0, 0, 0);
-            other(n);
+    // One step, from register set h.  First the next step has to have arrived and the waves to have
+    // read this one, whose place in LDS then takes the step STAGES later.  Reads and loads are
+    // spread over the products: a wave that issues them together waits for LDS to take them, and
+    // the matrix cores with it.  The last steps load the last one again and read stale ones, which
+    // nobody uses: so every step is the same code, and the accumulators never move.
+    auto step = [&](int s, auto set) {
+        constexpr int h = decltype(set)::value, HALF = TILES / 2;
+        tile_wait<(STAGES - 2) * LOADS>();
+        const int next = s + STAGES < steps ? s + STAGES : steps - 1;
+        for_all<TILES>([&](auto at) {
+            constexpr int n = decltype(at)::value, i = n / TM, j = n % TM;
+            mfma_i8(acc[i][j], fw[h][i], fa[h][j]);
+            for_all<TN + TM>([&](auto r) {
+                if constexpr (n == decltype(r)::value * HALF / (TN + TM)) read_one(s + 1, h ^ 1, decltype(r)::value);
+            });
+            for_all<LOADS>([&](auto r) {
+                constexpr int load = decltype(r)::value;
+                if constexpr (n == HALF + load * HALF / LOADS) fill_one(next, s % STAGES, load);
+            });
             __builtin_amdgcn_sched_barrier(0);
-        }
-    };
-    // share n of `count` things over a half step's products
-    auto share = [&](int n, int count, auto f) {
-        const int per = (count + TN * TM - 1) / (TN * TM);
-#pragma unroll
-        for (int j = n * per; j < (n + 1) * per && j < count; j++) f(j);
-    };
-    // One step.  Each half is read during the products of the half in front of it (the last step
-    // reads a stale one that nobody uses).  Half way, the next step has to have arrived and the
-    // waves to have read this one, whose place then takes the step STAGES later.
-    auto step = [&](int s, auto filling) {
-        mac(0, [&](int n) { share(n, TN + TM, [&](int r) { read_one(s, 1, r); }); });
-        tile_wait<decltype(filling)::value ? (STAGES - 2) * LOADS : 0>();
-        mac(1, [&](int n) {
-            share(n, TN + TM, [&](int r) { read_one(s + 1, 0, r); });
-            if constexpr (decltype(filling)::value) share(n, LOADS, [&](int j) { fill_one(s + STAGES, j); });
         });
     };
-    const int steps = m.padded / STEP;
 #pragma unroll
-    for (int s = 0; s < STAGES; s++) {
-        if (s >= steps) break;
+    for (int s = 0; s < STAGES; s++)
 #pragma unroll
-        for (int j = 0; j < LOADS; j++) fill_one(s, j);
+        for (int j = 0; j < LOADS; j++) fill_one(s < steps ? s : steps - 1, s, j);
+    tile_wait<(STAGES - 1) * LOADS>();
+    for_all<TN + TM>([&](auto n) { read_one(0, 0, decltype(n)::value); });
+    for (int s = 0; s < steps; s += 2) {  // the number of steps is even
+        step(s, Int<0>{});
+        step(s + 1, Int<1>{});
     }
-    tile_wait<0>();
-#pragma unroll
-    for (int n = 0; n < TN + TM; n++) read_one(0, 0, n);
-    int s = 0;
-    for (; s < steps - STAGES; s++) step(s, std::true_type{});
-    for (; s < steps; s++) step(s, std::false_type{});
     // Epilogue: 32 tokens at a time through LDS (a place for each wave), so that a token's channels
     // leave in whole 16-byte pieces of neighbouring lanes.  A lane holds channels
-    // 8 g + 4 (l / 32) + 0..3 of token l % 32 of each tile.
+    // 4 (l / 16) + 0..3 of token l % 16 of each tile.
     tile_wait<0>();
+    mfma_done(acc);
     constexpr int PER = sizeof(T) == 4 ? 4 : 8, LANES = BN / 2 / PER;  // channels a lane stores, lanes a token
     int *sums = (int *)lds + wave * 32 * SUMS;
     const int c = c0 + (wave & 1) * (BN / 2) + l % LANES * PER;
@@ -176,16 +187,15 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
         ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
         bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < TM; j++) {
-#pragma unroll
-        for (int i = 0; i < TN; i++)
-#pragma unroll
-            for (int g = 0; g < 4; g++)
-                *(v4i *)(sums + l % 32 * SUMS + 32 * i + 8 * g + 4 * (l / 32)) =
-                    v4i{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+    for_all<TM / 2>([&](auto pair) {
+        constexpr int j = 2 * decltype(pair)::value;
+        for_all<TN>([&](auto i) {
+            constexpr int at = decltype(i)::value;
+            *(v4i *)(sums + l % 16 * SUMS + 16 * at + 4 * (l / 16)) = acc[at][j];
+            *(v4i *)(sums + (16 + l % 16) * SUMS + 16 * at + 4 * (l / 16)) = acc[at][j + 1];
+        });
         __builtin_amdgcn_wave_barrier();
-        const int tj = t0 + (wave >> 1) * (BM / 2) + 32 * j;
+        const int tj = t0 + (wave >> 1) * (BM / 2) + 16 * j;
 #pragma unroll
         for (int r = 0; r < 32; r += 64 / LANES) {
             const int t = tj + r + l / LANES;
@@ -196,7 +206,7 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
             store_sums<T, PER>(m, out, t, c, m.a_scale[t], v, ws, bias);
         }
         __builtin_amdgcn_wave_barrier();
-    }
+    });
 }
 
 }  // namespace ckks_plain

@@ -289,8 +289,6 @@ __global__ void k_zero(float *p, size_t n) {
 // ------------------------------------------------------------------ launches
 
 // f(type tag, threads, elements, vector) for the smallest row shape that holds the columns
-template <int N> struct Int { static constexpr int value = N; };
-template <bool B> struct Flag { static constexpr bool value = B; };
 template <typename T, typename F> int by_shape(int64_t cols, bool vector, F f) {
     auto go = [&](auto nt, auto e) { return vector ? f(T{}, nt, e, Flag<true>{}) : f(T{}, nt, e, Flag<false>{}); };
     if (cols <= 512) return go(Int<64>{}, Int<8>{});

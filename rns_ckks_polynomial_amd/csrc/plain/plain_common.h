@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "../../../include/ckks_plain.h"
 
 namespace ckks_plain {
@@ -141,6 +143,17 @@ __device__ __forceinline__ void store_i8(int8_t *__restrict__ q, int padded, int
             }
         }
     }
+}
+
+// Compile-time numbers and flags as arguments.
+template <int N> struct Int { static constexpr int value = N; };
+template <bool B> struct Flag { static constexpr bool value = B; };
+// f(Int<0>), ..., f(Int<N - 1>): a loop whose counter is a constant in its body, also where the
+// body is too long for the compiler to unroll a loop early enough to keep arrays in registers.
+template <typename F, int... I>
+__device__ __forceinline__ void for_all(F f, std::integer_sequence<int, I...>) { (f(Int<I>{}), ...); }
+template <int N, typename F> __device__ __forceinline__ void for_all(F f) {
+    for_all(f, std::make_integer_sequence<int, N>{});
 }
 
 // ------------------------------------------------------------------ host side
