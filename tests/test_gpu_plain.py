@@ -450,6 +450,29 @@ def test_sample_ties(levels, V):
     check_sample(z, noise(V + 1, 12, V), full(12, 0.0), k, p)
 
 
+@pytest.mark.parametrize("V", [5000, 20011, 70000])
+@pytest.mark.parametrize("k,p", [(50, 1.0), (4500, 1.0), (4999, 0.9), (0, 0.5), (0, 0.9999), (3000, 0.8)])
+def test_sample_shapes_of_distributions(V, k, p):
+    """Long and flat, peaked, with outliers and infinities: the kept tokens are more than fit any list,
+    or crowd into a sliver of the range."""
+    r = np.random.default_rng(V + k)
+    z = np.stack([
+        r.standard_normal(V) * 0.01,                       # all alike
+        r.standard_normal(V) * 12,                         # peaked
+        np.where(np.arange(V) == 77, 1e30, r.standard_normal(V)),   # one far above
+        np.where(np.arange(V) % 2 == 0, np.inf, r.standard_normal(V)),
+        np.where(np.arange(V) < 3, np.inf, -np.inf),
+        1.0 + r.integers(0, 40, V) * 2.0 ** -23,           # neighbouring numbers
+        -np.exp(r.uniform(-60, 60, V)),                    # many octaves below zero
+        r.choice([-3e38, 0.0, 3e38], V),
+        np.where(r.random(V) < 0.9, -1e4, r.standard_normal(V)),    # a long flat tail
+        np.round(r.standard_normal(V) * 4) / 4,            # runs of equals
+    ])
+    z = torch.from_numpy(z).float().cuda()
+    B = z.shape[0]
+    check_sample(z, noise(V, B, V), full(B, 0.8), full(B, k, torch.int32), full(B, p))
+
+
 @pytest.mark.parametrize("ty", ["bf16", "f32"])
 def test_sample_masks(ty):
     B, V = 16, 3001
