@@ -17,6 +17,7 @@ __device__ __forceinline__ float logit_of(uint64_t order) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 __device__ __forceinline__ uint32_t index_of(uint64_t order) { return ~(uint32_t)order; }
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 struct SampleArgs {
     const void *logits;
@@ -29,257 +30,411 @@ struct SampleArgs {
     float *logprob;
 };
 
-constexpr int NT = 1024, BINS = 2048, LIST = 4096;
+constexpr int NT = 1024, WAVES = NT / 64, BINS = 2048, LIST = 4096, HELD = LIST / NT;
 constexpr uint64_t NONE = ~(uint64_t)0;
 
-// Reductions over the workgroup's 16 waves; the same tree on every run.
-template <typename V, typename F> __device__ __forceinline__ V block_reduce(V v, V *sh, F f) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v = f(v, __shfl_xor(v, m));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = sh[threadIdx.x & 15];
-#pragma unroll
-    for (int m = 8; m; m >>= 1) v = f(v, __shfl_xor(v, m));
-    return v;
+// The neighbour's value that a cross-lane move brings (`none` where there is no neighbour).
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
 }
-__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
-// Sum over the threads in front of this one; `total` over all.
-__device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *sh, uint64_t &total) {
-    const int l = threadIdx.x & 63, w = threadIdx.x >> 6;
-    uint64_t s = v;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint64_t o = __shfl_up(s, m);
-        if (l >= m) s += o;
-    }
-    __syncthreads();
-    if (l == 63) sh[w] = s;
-    __syncthreads();
-    uint64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 64; i++) {
-        const uint64_t x = sh[i];
-        before += i < w ? x : 0;
-        total += x;
-    }
-    return before + s - v;
+template <int CTRL, int ROWS> __device__ __forceinline__ float moved(float none, float v) {
+    return __uint_as_float(moved<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
 }
+template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t none, uint64_t v) {
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(none >> 32), (uint32_t)(v >> 32)) << 32 |
+           moved<CTRL, ROWS>((uint32_t)none, (uint32_t)v);
+}
+__device__ __forceinline__ uint32_t lane(uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); }
+__device__ __forceinline__ float lane(float v, int l) { return __uint_as_float(lane(__float_as_uint(v), l)); }
+__device__ __forceinline__ uint64_t lane(uint64_t v, int l) {
+    return (uint64_t)lane((uint32_t)(v >> 32), l) << 32 | lane((uint32_t)v, l);
+}
+// Inclusive scans over rows of 16 lanes and over the wave, in a fixed order (moves within the
+// register file: an exchange through LDS takes ten times as long).
+template <typename V, typename F> __device__ __forceinline__ V scan16(V v, V none, F f) {
+    v = f(moved<0x111, 0xf>(none, v), v);
+    v = f(moved<0x112, 0xf>(none, v), v);
+    v = f(moved<0x114, 0xf>(none, v), v);
+    return f(moved<0x118, 0xf>(none, v), v);
+}
+template <typename V, typename F> __device__ __forceinline__ V scan64(V v, V none, F f) {
+    v = scan16(v, none, f);
+    v = f(moved<0x142, 0xa>(none, v), v);
+    return f(moved<0x143, 0xc>(none, v), v);
+}
+struct Larger {
+    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a > b ? a : b; }
+};
+struct Sum {
+    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+};
+
+struct SampleShared {
+    uint64_t slot[8][WAVES];
+    uint64_t pick[3];
+    uint32_t n, cut;
+    union {
+        uint64_t list[LIST];
+        uint64_t bins[BINS];
+        uint32_t counts[BINS];
+    };
+};
 
 // One workgroup a row.  A row is read once for its largest logit and its mass (the sum of
 // e = exp((z - max) / temperature)); a filter then needs the last token that stays:
 //  - Bounds.  A token under the k-th largest of the threads' own maxima is not among the first k.
 //    One with e < (1 - p) mass / count is not in the nucleus: all such together have less than
 //    (1 - p) of the mass, so what comes before any of them has p of it.
-//  - What passes the bound usually fits the list in LDS, where it is sorted: everything else is
-//    decided there, without reading the row again.
-//  - Where it does not fit, the last token is located by counts or masses in bins of equal width
-//    over the logits, and the one bin it falls into is listed and sorted (a bin that does not
-//    fit either is divided again, by the tokens' order).
-// Masses are whole multiples of 2^-mass_bits where they are added by atomics or compared, so
-// results do not depend on the order of anything.
+//  - What passes the bound usually fits the list in LDS: everything else is decided there,
+//    without reading the row again.
+//  - A nucleus that does not fit is counted in bins of equal width over the logits.  A bin's mass
+//    is its count times e of its middle, to half a bin's width; that names a few bins that may hold
+//    the end of the nucleus.  The last read takes the tokens above them, adds up their exact mass
+//    and lists those bins.
+//  - Many tokens by count, or a list that overflows (runs of equal logits): the last token is
+//    located by counts or masses in bins, and the one bin it falls into is listed or, if that does
+//    not fit either, divided again by the tokens' order.
+// Masses that are added by atomics are whole multiples of a power of two and float sums go in a
+// fixed order, so the result does not depend on the order of anything.
 template <typename T> struct Sampler {
     static constexpr int N = 16 / sizeof(T);  // logits of a vector
     typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
     typedef uint8_t Mask __attribute__((ext_vector_type(16 / sizeof(T)), aligned(1)));
+    typedef float Four __attribute__((ext_vector_type(4), aligned(4)));
 
     const SampleArgs &a;
+    SampleShared &m;
     const T *z;
     const uint8_t *ok;
     const float *gumbel;
-    float t, c, top;  // temperature, log2(e) / temperature, the largest logit
+    int wave, slot;
+    float t, c, top;   // temperature, log2(e) / temperature, the largest logit
+    float sum, min_p;  // the mass
 
+    // ---- the workgroup's reductions: one barrier each, in eight places in turn
+    template <typename V, typename F> __device__ __forceinline__ V across(V v, V none, F f) {  // of each wave's v
+        V *at = (V *)m.slot[slot++ & 7];
+        if ((threadIdx.x & 63) == 63) at[wave] = v;
+        __syncthreads();
+        return scan16(at[threadIdx.x & 15], none, f);
+    }
+    template <typename V, typename F> __device__ __forceinline__ V all(V v, V none, F f) {
+        return lane(across(scan64(v, none, f), none, f), 15);
+    }
+    // the sum over the threads in front of this one, and over all
+    template <typename V> __device__ __forceinline__ V in_front(V v, V &total) {
+        const V s = scan64(v, V(0), Sum{}), w = across(s, V(0), Sum{});
+        total = lane(w, 15);
+        return (wave ? lane(w, wave - 1) : V(0)) + s - v;
+    }
+
+    // ---- the row
     // f(first index, logits) for this thread's vectors; a token that is not possible has -infinity.
     // Rows need no alignment beyond their elements'.
-    template <int U = 4, typename F> __device__ __forceinline__ void pass(F f) const {  // U vectors in flight
+    __device__ __forceinline__ void logits(const Vec &r, const Mask &k, float (&x)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            x[i] = fmaxf(to_f32(r[i]), -INFINITY);  // NaN: -infinity
+            if (ok) x[i] = k[i] ? x[i] : -INFINITY;
+        }
+    }
+    template <typename F> __device__ __forceinline__ void rest(F f) const {  // the last, broken vector
         const int whole = a.vocab / N, rest = a.vocab % N;
+        if (!rest || threadIdx.x != whole % NT) return;
+        float x[N];
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const bool there = k < rest && (!ok || ok[whole * N + k]);
+            x[k] = there ? fmaxf(to_f32(z[whole * N + k]), -INFINITY) : -INFINITY;
+        }
+        f(whole * N, x);
+    }
+    template <int U, typename F> __device__ __forceinline__ void pass(F f) const {  // U vectors in flight
+        const int whole = a.vocab / N;
         for (int v = threadIdx.x; v < whole; v += U * NT) {
             Vec r[U];
-            Mask m[U];
+            Mask k[U];
 #pragma unroll
             for (int j = 0; j < U; j++) {
                 const int64_t i = (int64_t)(v + j * NT < whole ? v + j * NT : v) * N;
                 r[j] = *(const Vec *)(z + i);
-                if (ok) m[j] = *(const Mask *)(ok + i);
+                if (ok) k[j] = *(const Mask *)(ok + i);
             }
 #pragma unroll
             for (int j = 0; j < U; j++) {
                 if (v + j * NT >= whole) break;
                 float x[N];
-#pragma unroll
-                for (int k = 0; k < N; k++) {
-                    x[k] = fmaxf(to_f32(r[j][k]), -INFINITY);  // NaN: -infinity
-                    if (ok) x[k] = m[j][k] ? x[k] : -INFINITY;
-                }
+                logits(r[j], k[j], x);
                 f((v + j * NT) * N, x);
             }
         }
-        if (rest && threadIdx.x == whole % NT) {
-            float x[N];
-#pragma unroll
-            for (int k = 0; k < N; k++) {
-                const bool there = k < rest && (!ok || ok[whole * N + k]);
-                x[k] = there ? fmaxf(to_f32(z[whole * N + k]), -INFINITY) : -INFINITY;
-            }
-            f(whole * N, x);
-        }
+        rest(f);
     }
+    static __device__ __forceinline__ float largest(const float (&x)[N]) {
+        float v = x[0];
+#pragma unroll
+        for (int i = 1; i < N; i++) v = fmaxf(v, x[i]);
+        return v;
+    }
+
+    // ---- values
     // e in 32 bits; the quotient as a product, which moves it by about 2^-23 of the exponent
     __device__ __forceinline__ float weight(float v, float from) const {
         return __builtin_amdgcn_exp2f(fminf((v - from) * c, 0.0f));  // infinity - infinity: 1
     }
-    __device__ __forceinline__ uint64_t fixed(float e) const {  // e in [0, 1], cut to a multiple
+    // e in [0, 1] cut to a multiple of 2^-bits
+    static __device__ __forceinline__ uint64_t fixed(float e, int bits) {
         const uint32_t b = __float_as_uint(e);
-        const int x = (int)(b >> 23) - 150 + a.mass_bits;
-        const uint64_t m = (b & 0x7fffff) | 0x800000;
-        return b < 0x800000 || x <= -24 ? 0 : x >= 0 ? m << x : m >> -x;
+        const int x = (int)(b >> 23) - 150 + bits;
+        const uint64_t v = (b & 0x7fffff) | 0x800000;
+        return b < 0x800000 || x <= -24 ? 0 : x >= 0 ? v << x : v >> -x;
     }
-    __device__ __forceinline__ uint64_t mass(float v) const { return fixed(weight(v, top)); }
+    __device__ __forceinline__ uint64_t mass(float v) const { return fixed(weight(v, top), a.mass_bits); }
+    __device__ __forceinline__ bool too_small(float v) const { return min_p > 0 && weight(v, top) < min_p; }
     // the distance to the largest logit, as defined: each step rounded to 32 bits
     __device__ __forceinline__ float part(float v) const { return v == top ? 0.0f : (v - top) / t; }
-    // as `order_of`, of the score
-    __device__ __forceinline__ uint64_t score(float v, uint32_t i) const {
-        return (uint64_t)order_bits(part(v) + gumbel[i]) << 32 | (uint32_t)~i;
+    // the score and the complement of the index: the largest is the answer
+    __device__ __forceinline__ uint64_t score(float v, uint32_t i, float noise) const {
+        return (uint64_t)order_bits(part(v) + noise) << 32 | (uint32_t)~i;
     }
-};
+    __device__ __forceinline__ void answer(int64_t row, uint32_t token) const {
+        a.token[row] = token;
+        a.logprob[row] = part(to_f32(z[token])) - logf(sum);
+    }
 
-struct SampleShared {
-    uint64_t sh[16];
-    float shf[16];
-    uint64_t pick[4];
-    uint32_t n;
-    union {
-        uint64_t list[LIST];
-        uint64_t bins[BINS];
-    };
-};
-
-// list[0..n) in falling order, for the whole workgroup; n <= LIST.
-__device__ __forceinline__ void sort_list(uint64_t *list, int n) {
-    int size = 2;
-    while (size < n) size *= 2;
-    __syncthreads();
-    for (int i = n + threadIdx.x; i < size; i += NT) list[i] = 0;
-    for (int run = 2; run <= size; run *= 2)
-        for (int gap = run / 2; gap; gap /= 2) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < size / 2; i += NT) {
-                const int lo = 2 * i - (i & (gap - 1)), hi = lo + gap;
-                const uint64_t x = list[lo], y = list[hi];
-                if ((x < y) == ((lo & run) == 0)) list[lo] = y, list[hi] = x;
-            }
-        }
-    __syncthreads();
-}
-
-// Puts the tokens for which f(logit, order) holds on the list, at most LIST; returns how many
-// there are (more than LIST: at least that many).
-template <typename S, typename F> __device__ __forceinline__ uint32_t gather(const S &s, SampleShared &m, F f) {
-    __syncthreads();
-    if (threadIdx.x == 0) m.n = 0;
-    __syncthreads();
-    s.pass([&](int first, const float (&x)[S::N]) {
-#pragma unroll
-        for (int k = 0; k < S::N; k++) {
-            const uint64_t o = order_of(x[k], first + k);
-            if (o && f(x[k], o) && *(volatile uint32_t *)&m.n <= LIST) {
-                const uint32_t at = atomicAdd(&m.n, 1u);
-                if (at < LIST) m.list[at] = o;
-            }
-        }
-    });
-    __syncthreads();
-    return m.n;
-}
-
-// The order of the last token that stays, among those from `from` on with logits >= low: by count
-// the want-th, by mass the last before which there is less than `want`; 0 if there are not so many.
-// `above`: the mass of the tokens up to it (by count).
-template <bool MASS, typename S>
-__device__ __forceinline__ uint64_t locate(const S &s, SampleShared &m, uint64_t want, uint64_t from, float low, uint64_t &above) {
-    const float width = (float)BINS / (s.top - fmaxf(low, s.top - 64.0f / s.c));
-    uint64_t a = 0, b = 0, before = 0;  // the range of orders that is divided, and what comes before it
-    for (int level = 0;; level++) {
-        const int shift = level && b - a >= BINS ? 53 - __clzll(b - a) : 0;  // (b - a) >> shift < BINS
-        auto bin_of = [&](float x, uint64_t o) {
-            return level ? (int)((b - o) >> shift) : (int)fminf(fmaxf((s.top - x) * width, 0.0f), BINS - 1.0f);
-        };
-        auto inside = [&](float x, uint64_t o) { return o >= from && x >= low && (!level || (o >= a && o <= b)); };
+    // ---- lists
+    // Puts the tokens with logits >= low for which f(logit, order) holds on the list, at most LIST;
+    // returns how many there are (more than LIST: at least that many).
+    template <typename F> __device__ __forceinline__ uint32_t gather(float low, F f) {
         __syncthreads();
-        for (int i = threadIdx.x; i < BINS; i += NT) m.bins[i] = 0;
-        if (threadIdx.x == 0) m.pick[0] = BINS;
+        if (threadIdx.x == 0) m.n = 0;
         __syncthreads();
-        s.template pass<1>([&](int first, const float (&x)[S::N]) {
+        pass<4>([&](int first, const float (&x)[N]) {
+            if (!(largest(x) >= low)) return;
 #pragma unroll
-            for (int k = 0; k < S::N; k++) {
-                const uint64_t o = order_of(x[k], first + k);
-                if (o && inside(x[k], o))
-                    atomicAdd((unsigned long long *)&m.bins[bin_of(x[k], o)],
-                              (unsigned long long)(MASS ? s.mass(x[k]) : 1));
-            }
+            for (int k = 0; k < N; k++)
+                if (x[k] >= low) list(first + k, x[k], f);
         });
         __syncthreads();
-        const uint64_t v0 = m.bins[2 * threadIdx.x], v1 = m.bins[2 * threadIdx.x + 1];
-        uint64_t total;
-        const uint64_t p = before + block_before(v0 + v1, m.sh, total);
-        if (p < want && want <= p + v0 + v1) {
-            const bool second = want > p + v0;
-            m.pick[0] = 2 * threadIdx.x + second;
-            m.pick[1] = p + (second ? v0 : 0);
-        }
+        return m.n;
+    }
+    template <typename F> __device__ __forceinline__ void list(uint32_t i, float v, F f) {
+        const uint64_t o = order_of(v, i);
+        if (!o || !f(v, o) || *(volatile uint32_t *)&m.n > LIST) return;
+        const uint32_t at = atomicAdd(&m.n, 1u);
+        if (at < LIST) m.list[at] = o;
+    }
+    // the list in registers (0 past its end); the bins take its place
+    __device__ __forceinline__ void hold(uint32_t n, uint64_t (&o)[HELD]) {
+#pragma unroll
+        for (int i = 0; i < HELD; i++) o[i] = threadIdx.x + i * NT < n ? m.list[threadIdx.x + i * NT] : 0;
         __syncthreads();
-        const int bin = (int)m.pick[0];
-        if (bin == BINS) return 0;
-        before = m.pick[1];
-        const uint32_t n =
-            gather(s, m, [&](float x, uint64_t o) { return inside(x, o) && bin_of(x, o) == bin; });
-        if (n <= LIST) {
-            sort_list(m.list, n);
-            // by mass: four neighbours a thread
-            uint64_t o[4], w[4], sum = 0;
+    }
+    // A listed token's count and mass in one number: 13 and 51 bits, sums of LIST of them included.
+    static constexpr int LIST_BITS = 39, COUNT = 51;
+    static constexpr uint64_t MASS = ((uint64_t)1 << COUNT) - 1;
+    __device__ __forceinline__ uint64_t both(uint64_t o) const {
+        return (uint64_t)1 << COUNT | fixed(weight(logit_of(o), top), LIST_BITS);
+    }
+    // Of the held tokens with orders in [from, b]: the last that stays, by count the want-th, by mass
+    // the last before which there is less than `want`; `until` is what there is up to it.  0 if there
+    // are not so many.
+    template <bool BY_MASS>
+    __device__ __forceinline__ uint64_t select(const uint64_t (&o)[HELD], uint64_t want, uint64_t from, uint64_t b,
+                                               uint64_t &until) {
+        uint64_t a = from, before = 0;
+        auto of = [](uint64_t v) { return BY_MASS ? v & MASS : v >> COUNT; };
+        for (;;) {
+            const int shift = b - a >= BINS ? 53 - __clzll(b - a) : 0;  // (b - a) >> shift < BINS
+            for (int i = threadIdx.x; i < BINS; i += NT) m.bins[i] = 0;
+            if (threadIdx.x == 0) m.pick[0] = BINS;
+            __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t at = 4 * threadIdx.x + i;
-                o[i] = at < n ? m.list[at] : 0;
-                w[i] = !o[i] ? 0 : MASS ? s.mass(logit_of(o[i])) : 1;
-                sum += w[i];
-            }
-            uint64_t q = before + block_before(sum, m.sh, total);
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (q < want && want <= q + w[i]) m.pick[2] = o[i];
-                q += w[i];
+            for (int i = 0; i < HELD; i++)
+                if (o[i] >= a && o[i] <= b && o[i])
+                    atomicAdd((unsigned long long *)&m.bins[(b - o[i]) >> shift], (unsigned long long)both(o[i]));
+            __syncthreads();
+            const uint64_t v0 = m.bins[2 * threadIdx.x], v1 = m.bins[2 * threadIdx.x + 1];
+            uint64_t total;
+            const uint64_t p = before + in_front(v0 + v1, total);
+            if (of(p) < want && want <= of(p + v0 + v1)) {
+                const bool second = want > of(p + v0);
+                m.pick[0] = 2 * threadIdx.x + second;
+                m.pick[1] = p + (second ? v0 : 0);
+                m.pick[2] = second ? v1 : v0;
             }
             __syncthreads();
-            const uint64_t last = m.pick[2];
-            if (!MASS) {  // the mass down to it
-                uint64_t sum = 0;
-                s.template pass<1>([&](int first, const float (&x)[S::N]) {
+            const uint64_t bin = m.pick[0], inside = m.pick[2];
+            if (bin == BINS) return 0;
+            before = m.pick[1];
+            b -= bin << shift;
+            a = shift && b - a >= (uint64_t)1 << shift ? b - (((uint64_t)1 << shift) - 1) : shift ? a : b;
+            __syncthreads();
+            if (inside >> COUNT == 1) {  // whose order it is
 #pragma unroll
-                    for (int k = 0; k < S::N; k++)
-                        if (order_of(x[k], first + k) >= last) sum += s.mass(x[k]);
+                for (int i = 0; i < HELD; i++)
+                    if (o[i] >= a && o[i] <= b) m.pick[0] = o[i];
+                __syncthreads();
+                until = before + inside;
+                const uint64_t last = m.pick[0];
+                __syncthreads();
+                return last;
+            }
+        }
+    }
+
+    // Of the row's tokens with orders from `from` on and logits >= low: as `select`, with masses in
+    // multiples of 2^-mass_bits; `until` (by count): their mass up to the last.
+    template <bool BY_MASS>
+    __device__ __forceinline__ uint64_t locate(uint64_t want, uint64_t from, float low, uint64_t &until) {
+        const float width = (float)BINS / (top - fmaxf(low, top - 64.0f / c));
+        uint64_t a = 0, b = 0, before = 0;  // the range of orders that is divided, and what comes before it
+        for (int level = 0;; level++) {
+            const int shift = level && b - a >= BINS ? 53 - __clzll(b - a) : 0;
+            auto bin_of = [&](float x, uint64_t o) {
+                return level ? (int)((b - o) >> shift) : (int)fminf(fmaxf((top - x) * width, 0.0f), BINS - 1.0f);
+            };
+            auto inside = [&](float x, uint64_t o) { return o >= from && x >= low && (!level || (o >= a && o <= b)); };
+            auto each = [&](auto f) {
+                pass<1>([&](int first, const float (&x)[N]) {
+#pragma unroll
+                    for (int k = 0; k < N; k++) {
+                        const uint64_t o = order_of(x[k], first + k);
+                        if (o && inside(x[k], o)) f(x[k], o);
+                    }
                 });
-                above = block_reduce(sum, m.sh, [](uint64_t x, uint64_t y) { return x + y; });
+            };
+            __syncthreads();
+            for (int i = threadIdx.x; i < BINS; i += NT) m.bins[i] = 0;
+            if (threadIdx.x == 0) m.pick[0] = BINS;
+            __syncthreads();
+            each([&](float x, uint64_t o) {
+                atomicAdd((unsigned long long *)&m.bins[bin_of(x, o)], (unsigned long long)(BY_MASS ? mass(x) : 1));
+            });
+            __syncthreads();
+            const uint64_t v0 = m.bins[2 * threadIdx.x], v1 = m.bins[2 * threadIdx.x + 1];
+            uint64_t total;
+            const uint64_t p = before + in_front(v0 + v1, total);
+            if (p < want && want <= p + v0 + v1) {
+                const bool second = want > p + v0;
+                m.pick[0] = 2 * threadIdx.x + second;
+                m.pick[1] = p + (second ? v0 : 0);
             }
-            return last;
-        }
-        // divide the bin by the orders that are in it
-        uint64_t lowest = NONE, highest = 0;
-        s.template pass<1>([&](int first, const float (&x)[S::N]) {
+            __syncthreads();
+            const int bin = (int)m.pick[0];
+            if (bin == BINS) return 0;
+            before = m.pick[1];
+            const uint32_t n = gather(low, [&](float x, uint64_t o) { return inside(x, o) && bin_of(x, o) == bin; });
+            uint64_t lowest = NONE, highest = 0;
+            each([&](float x, uint64_t o) {
+                if (bin_of(x, o) == bin) lowest = o < lowest ? o : lowest, highest = o > highest ? o : highest;
+            });
+            const uint64_t a1 = ~all(~lowest, (uint64_t)0, Larger{}), b1 = all(highest, (uint64_t)0, Larger{});
+            if (n <= LIST) {
+                uint64_t o[HELD], last, unused;
+                hold(n, o);
+                // what is wanted of the list, its masses being multiples of 2^-LIST_BITS
+                uint64_t left = want - before;
+                if (BY_MASS) {
+                    const int s = this->a.mass_bits - LIST_BITS;
+                    left = s >= 0 ? (left >> s) + ((left & (((uint64_t)1 << s) - 1)) != 0) : left << -s;
+                    if (!left) left = 1;
+                }
+                last = select<BY_MASS>(o, left, a1, b1, unused);
+                if (!last) last = a1;  // by rounding: all of them
+                if (!BY_MASS) {
+                    uint64_t sum = 0;
+                    pass<1>([&](int first, const float (&x)[N]) {
 #pragma unroll
-            for (int k = 0; k < S::N; k++) {
-                const uint64_t o = order_of(x[k], first + k);
-                if (!o || !inside(x[k], o) || bin_of(x[k], o) != bin) continue;
-                lowest = smaller(lowest, o), highest = larger(highest, o);
+                        for (int k = 0; k < N; k++)
+                            if (order_of(x[k], first + k) >= last) sum += mass(x[k]);
+                    });
+                    until = all(sum, (uint64_t)0, Sum{});
+                }
+                return last;
             }
-        });
-        const uint64_t a1 = block_reduce(lowest, m.sh, smaller), b1 = block_reduce(highest, m.sh, larger);
-        a = a1, b = b1;
+            a = a1, b = b1;
+        }
     }
-}
+
+    // The best score of the tokens with orders >= last, or (UNTIL) of those in bins < first_bin, whose
+    // mass goes to `above`; those in [first_bin, last_bin] are listed then.
+    template <bool UNTIL>
+    __device__ __forceinline__ uint64_t best(uint64_t last, float width, float first_bin, float last_bin, float &above) {
+        constexpr int U = 2;
+        const float rt = 1.0f / t, low = UNTIL || last <= 1 ? -INFINITY : logit_of(last);
+        uint64_t win = 0;
+        float part_sum = 0;
+        // A score is computed as defined only where a quick one comes near the best so far: the quick
+        // quotient is off by less than 2^-22 of itself, a sum by 2^-23.
+        auto consider = [&](float v, uint32_t i, float noise, float cut) {
+            const float d = fminf((v - top) * rt, 0.0f), quick = d + noise;
+            if (quick < cut - (fabsf(d) + fabsf(quick)) * 0x1p-20f || too_small(v)) return;
+            const uint64_t s = score(v, i, noise);
+            if (s > win) {
+                win = s;
+                if ((uint32_t)(s >> 32) > *(volatile uint32_t *)&m.cut) atomicMax(&m.cut, (uint32_t)(s >> 32));
+            }
+        };
+        auto stays = [&](float v, uint32_t i) {
+            if constexpr (UNTIL) {
+                const float x = fmaxf((top - v) * width, 0.0f);
+                if (x >= first_bin) {
+                    if (x < last_bin + 1.0f) list(i, v, [](float, uint64_t) { return true; });
+                    return false;
+                }
+                part_sum += weight(v, top);
+                return v > -INFINITY;
+            } else {
+                return order_of(v, i) >= last;
+            }
+        };
+        auto handle = [&](int first, const float (&x)[N], const float (&noise)[N]) {
+            // (a reciprocal of a temperature near the largest number has lost its digits)
+            const float cut = t < 0x1p100f ? logit_of((uint64_t)*(volatile uint32_t *)&m.cut << 32) : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < N; k++)
+                if (x[k] >= low && stays(x[k], first + k)) consider(x[k], first + k, noise[k], cut);
+        };
+        const int whole = a.vocab / N;
+        for (int v = threadIdx.x; v < whole; v += U * NT) {
+            float x[U][N], noise[U][N];
+#pragma unroll
+            for (int j = 0; j < U; j++) {
+                const int64_t i = (int64_t)(v + j * NT < whole ? v + j * NT : v) * N;
+                Mask k;
+                if (ok) k = *(const Mask *)(ok + i);
+                logits(*(const Vec *)(z + i), k, x[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < U; j++) {
+                const float most = largest(x[j]);
+                const bool need = v + j * NT < whole && most > -INFINITY &&
+                                  (UNTIL ? fmaxf((top - most) * width, 0.0f) < first_bin : most >= low);
+                if (need) {
+                    const float *g = gumbel + (int64_t)(v + j * NT) * N;
+#pragma unroll
+                    for (int i = 0; i < N; i += 4) {
+                        const Four f = *(const Four *)(g + i);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) noise[j][i + k] = f[k];
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; j++)
+                if (v + j * NT < whole) handle((v + j * NT) * N, x[j], noise[j]);
+        }
+        rest([&](int first, const float (&x)[N]) {
+            float noise[N];
+#pragma unroll
+            for (int k = 0; k < N; k++) noise[k] = first + k < a.vocab ? gumbel[first + k] : 0.0f;
+            handle(first, x, noise);
+        });
+        above = part_sum;
+        return win;
+    }
+};
 
 template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs a) {
     typedef Sampler<T> S;
@@ -290,111 +445,183 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
     const float temp = a.temperature[row];
     const bool greedy = !(temp > 0);
     const int k = a.top_k ? a.top_k[row] : 0;
-    const float p = a.top_p ? a.top_p[row] : 1.0f, min_p = a.min_p ? a.min_p[row] : 0.0f;
-    S s{a, (const T *)a.logits + row * a.logits_stride, a.allowed ? a.allowed + row * a.allowed_stride : nullptr,
-        a.gumbel + row * a.gumbel_stride, greedy ? 1.0f : temp, 0, 0};
+    const float p = a.top_p ? a.top_p[row] : 1.0f;
+    S s{a, m, (const T *)a.logits + row * a.logits_stride, a.allowed ? a.allowed + row * a.allowed_stride : nullptr,
+        a.gumbel + row * a.gumbel_stride, (int)__builtin_amdgcn_readfirstlane(tid >> 6), 0, greedy ? 1.0f : temp};
+    s.min_p = a.min_p ? a.min_p[row] : 0.0f;
     // under 2^-120 the exponents of finite logits stay, and -infinity times it stays -infinity
     s.c = fmaxf(1.44269504f / s.t, 0x1p-120f);
+    m.counts[tid] = 0;
+    if (tid == 0) m.cut = 0, m.pick[0] = NT;
     // the thread's largest logit, where it first occurs, and its mass from there
     float mine = -INFINITY, sum = 0;
-    uint32_t where = 0xffffffffu;
-    s.pass([&](int first, const float (&x)[N]) {
-        float v = x[0];
-#pragma unroll
-        for (int i = 1; i < N; i++) v = fmaxf(v, x[i]);
+    uint32_t where = 0;
+    s.template pass<4>([&](int first, const float (&x)[N]) {
+        const float v = S::largest(x);
         if (v > mine) sum *= s.weight(mine, v), mine = v, where = first;
         if (mine > -INFINITY) {
 #pragma unroll
             for (int i = 0; i < N; i++) sum += s.weight(x[i], mine);
         }
     });
-    const uint64_t best = block_reduce(order_of(mine, where), m.sh, larger);
-    if (!best) {
+    const uint32_t top_bits = s.all(mine > -INFINITY ? order_bits(mine) : 0u, 0u, Larger{});
+    if (!top_bits) {
         if (tid == 0) a.token[row] = -1, a.logprob[row] = -INFINITY;
         return;
     }
-    s.top = logit_of(best);
-    sum = block_reduce(mine > -INFINITY ? sum * s.weight(mine, s.top) : 0.0f, m.shf, [](float x, float y) { return x + y; });
-    auto answer = [&](uint32_t token, float v) {
-        a.token[row] = token;
-        a.logprob[row] = s.part(v) - logf(sum);
-    };
-    if (greedy || k == 1 || p <= 0 || min_p > 1) {  // the first alone: it is in the vector at index_of(best)
+    s.top = logit_of((uint64_t)top_bits << 32);
+    s.sum = s.all(mine > -INFINITY ? sum * s.weight(mine, s.top) : 0.0f, 0.0f, Sum{});
+    if (greedy || k == 1 || p <= 0 || s.min_p > 1) {  // the first alone: it is in the first vector that holds it
+        uint32_t i = ~s.all(mine == s.top ? ~where : 0u, 0u, Larger{});
         if (tid == 0) {
-            uint32_t i = index_of(best);
             while (!(to_f32(s.z[i]) == s.top && (!s.ok || s.ok[i]))) i++;
-            answer(i, s.top);
+            s.answer(row, i);
         }
         return;
     }
     const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1;
-    uint64_t last = 1, win = 0;  // the order of the last that stays; the best score
-    if (by_count || by_mass) {
+    uint64_t win = 0;
+    float unused;
+    // what the mass in front of a token that stays is under, in multiples of 2^-bits
+    auto under = [&](double whole, int bits) {
+        const double w = ceil((double)p * whole * exp2((double)bits));
+        return w > 1 ? (uint64_t)w : (uint64_t)1;
+    };
+    if (!by_count && !by_mass) {
+        win = s.template best<false>(1, 0, 0, 0, unused);
+    } else {
         float low = -INFINITY;
         if (by_count) {
             // the k-th largest of the threads' maxima, or a little less: by bins of equal width
             const uint64_t own = order_of(mine, 0);
-            const float least = logit_of(block_reduce(own ? own : NONE, m.sh, smaller));
-            const float width = 1024.0f / (s.top - least);
-            const int bin = mine > -INFINITY ? (int)fminf(fmaxf((s.top - mine) * width, 0.0f), 1023.0f) : 1024;
-            m.bins[tid] = 0;
-            if (tid == 0) m.pick[0] = 1024;
+            const float least = logit_of(~s.all(own ? ~own : (uint64_t)0, (uint64_t)0, Larger{}));
+            const float range = s.top - least;
+            if (mine > -INFINITY) atomicAdd(&m.counts[(int)fminf(fmaxf((s.top - mine) * (NT / range), 0.0f), NT - 1.0f)], 1u);
             __syncthreads();
-            if (bin < 1024) atomicAdd((unsigned long long *)&m.bins[bin], 1ull);
-            __syncthreads();
-            uint64_t total;
-            const uint64_t v = m.bins[tid], before = block_before(v, m.sh, total);
-            if (before < (uint64_t)k && (uint64_t)k <= before + v) m.pick[0] = tid;
+            uint32_t total;
+            const uint32_t v = m.counts[tid], before = s.in_front(v, total);
+            if (before < (uint32_t)k && (uint32_t)k <= before + v) m.pick[0] = tid;
             __syncthreads();
             const int at = (int)m.pick[0];
-            if (at < 1024) low = logit_of(block_reduce(bin <= at ? own : NONE, m.sh, smaller));
+            // the bin's lower edge, and all that the edge may be off by
+            if (at < NT) low = fmaxf(least, s.top - (float)(at + 1) * (range / NT) * 1.00001f - fabsf(s.top) * 1e-6f);
         } else {
-            low = s.top + (__log2f((1.0f - p) * sum / (float)a.vocab) - 0.0625f) / s.c;
+            low = s.top + (__log2f((1.0f - p) * s.sum / (float)a.vocab) - 0.0625f) / s.c;
         }
         // the list is tried unless nearly every thread has something for it (then it has thousands)
         const int passing = __syncthreads_count(mine > -INFINITY && mine >= low);
         uint32_t n = LIST + 1;
-        if (a.vocab <= LIST || passing <= 1000) n = gather(s, m, [&](float x, uint64_t) { return x >= low; });
-        const double scale = exp2((double)a.mass_bits);
-        auto under = [&](double whole) { return larger(1, (uint64_t)ceil((double)p * whole)); };
-        if (n <= LIST) {
-            sort_list(m.list, n);
-            const uint32_t stay = by_count && (uint32_t)k < n ? k : n;
-            uint64_t o[4], w[4], own = 0, total;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t at = 4 * tid + i;
-                o[i] = at < stay ? m.list[at] : 0;
-                w[i] = o[i] ? s.mass(logit_of(o[i])) : 0;
-                own += w[i];
+        if (a.vocab <= LIST || passing <= NT - 24) n = s.gather(low, [](float, uint64_t) { return true; });
+        if (n <= 64) {  // one wave, a lane a token: its rank and the mass in front of it
+            if (s.wave) return;
+            const uint64_t o = (uint32_t)tid < n ? m.list[tid] : 0;
+            const uint64_t own = o ? s.both(o) : 0;
+            uint64_t q = 0;
+            for (uint32_t j = 0; j < n; j++) {
+                const uint64_t oj = lane(o, j), vj = lane(own, j);
+                q += oj > o ? vj : 0;
             }
-            uint64_t q = block_before(own, m.sh, total);
-            const uint64_t want = by_mass ? under(by_count ? (double)total : (double)sum * scale) : NONE;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const float v = logit_of(o[i]);
-                if (o[i] && q < want && !(min_p > 0 && s.weight(v, s.top) < min_p)) win = larger(win, s.score(v, index_of(o[i])));
-                q += w[i];
+            bool stay = o && (!by_count || (int64_t)(q >> S::COUNT) < k);
+            if (by_mass) {
+                const uint64_t whole = lane(scan64(stay ? own & S::MASS : 0, (uint64_t)0, Sum{}), 63);
+                stay = stay && (q & S::MASS) < (by_count ? under((double)whole * exp2(-S::LIST_BITS), S::LIST_BITS)
+                                                         : under((double)s.sum, S::LIST_BITS));
             }
-            win = block_reduce(win, m.sh, larger);
-            if (tid == 0) answer(index_of(win), to_f32(s.z[index_of(win)]));
+            const float v = logit_of(o);
+            if (stay && !s.too_small(v)) win = s.score(v, index_of(o), s.gumbel[index_of(o)]);
+            win = lane(scan64(win, (uint64_t)0, Larger{}), 63);
+            if (tid == 0) s.answer(row, index_of(win));
             return;
         }
-        uint64_t whole = (uint64_t)((double)sum * scale), unused;
-        if (by_count) last = larger(1, locate<false>(s, m, k, 1, low, whole));
-        if (by_mass) last = larger(last, locate<true>(s, m, under((double)whole), last, low, unused));
-        if (last == 1) last = order_of(low, 0xffffffffu);  // all that pass the bound
-        last = larger(last, 1);
-    }
-    s.pass([&](int first, const float (&x)[N]) {
+        if (n <= LIST) {
+            uint64_t o[HELD], last = 1, until = 0;
+            s.hold(n, o);
+            const uint64_t from = low > -INFINITY ? (uint64_t)order_bits(low) << 32 : 1;
+            const uint64_t to = (uint64_t)top_bits << 32 | 0xffffffffu;
+            if (by_count && (uint32_t)k < n) last = s.template select<false>(o, k, from, to, until);
+            if (by_mass) {
+                double whole = (double)s.sum;
+                if (by_count && (uint32_t)k < n) whole = (double)(until & S::MASS) * exp2(-S::LIST_BITS);
+                const uint64_t l = s.template select<true>(o, under(whole, S::LIST_BITS), larger(from, last), to, until);
+                last = larger(l, last);  // 0: all of them
+            }
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            const uint64_t o = order_of(x[i], first + i);
-            if (o >= last && !(min_p > 0 && s.weight(x[i], s.top) < min_p)) win = larger(win, s.score(x[i], first + i));
+            for (int i = 0; i < HELD; i++) {
+                const float v = logit_of(o[i]);
+                if (o[i] && o[i] >= last && !s.too_small(v))
+                    win = larger(win, s.score(v, index_of(o[i]), s.gumbel[index_of(o[i])]));
+            }
+        } else {
+            uint64_t last = 1;
+            bool found = false;
+            if (!by_count) {
+                // counts in bins down to the bound; a bin's mass by e of its middle, `off` at most off
+                const float range = s.top - low, width = (float)BINS / range;
+                for (int i = tid; i < BINS; i += NT) m.counts[i] = 0;
+                if (tid == 0) m.pick[0] = BINS, m.pick[1] = 0;
+                __syncthreads();
+                s.template pass<4>([&](int first, const float (&x)[N]) {
+#pragma unroll
+                    for (int i = 0; i < N; i++)
+                        if (x[i] >= low && x[i] > -INFINITY)
+                            atomicAdd(&m.counts[(int)fminf(fmaxf((s.top - x[i]) * width, 0.0f), BINS - 1.0f)], 1u);
+                });
+                __syncthreads();
+                const float step = range / BINS * s.c;  // of a bin, in powers of two
+                const float v0 = (float)m.counts[2 * tid] * __builtin_amdgcn_exp2f(-(2 * tid + 0.5f) * step);
+                const float v1 = (float)m.counts[2 * tid + 1] * __builtin_amdgcn_exp2f(-(2 * tid + 1.5f) * step);
+                const float off = __builtin_amdgcn_exp2f(0.5f * step) - 1.0f + 1e-4f, want = p * s.sum;
+                float total;
+                const float b0 = s.in_front(v0 + v1, total), b1 = b0 + v0, b2 = b1 + v1;
+                // the first bin after which there may be `want`, and the last before which there may not
+                if (b0 * (1 + off) < want && b2 * (1 + off) >= want) m.pick[0] = 2 * tid + (b1 * (1 + off) < want);
+                if (b0 * (1 - off) < want)
+                    atomicMax((unsigned long long *)&m.pick[1], (unsigned long long)(2 * tid + (b1 * (1 - off) < want)));
+                __syncthreads();
+                const float first_bin = (float)m.pick[0], last_bin = (float)m.pick[1];
+                __syncthreads();
+                if (first_bin < BINS && step < 0.125f) {
+                    if (tid == 0) m.n = 0;
+                    __syncthreads();
+                    float above;
+                    win = s.template best<true>(0, width, first_bin, last_bin, above);
+                    above = s.all(above, 0.0f, Sum{});
+                    n = m.n;
+                    if (n <= LIST) {
+                        found = true;
+                        uint64_t o[HELD], until;
+                        s.hold(n, o);
+                        const double left = (double)p * s.sum - above;
+                        if (left > 0) {
+                            const double w = ceil(left * exp2(S::LIST_BITS));
+                            last = s.template select<true>(o, w > 1 ? (uint64_t)w : 1, 1, NONE, until);
+#pragma unroll
+                            for (int i = 0; i < HELD; i++) {
+                                const float v = logit_of(o[i]);
+                                if (o[i] && o[i] >= last && !s.too_small(v))
+                                    win = larger(win, s.score(v, index_of(o[i]), s.gumbel[index_of(o[i])]));
+                            }
+                        }
+                    }
+                }
+            }
+            if (!found) {
+                uint64_t whole = (uint64_t)((double)s.sum * exp2((double)a.mass_bits)), none;
+                if (by_count) last = larger(1, s.template locate<false>(k, 1, low, whole));
+                if (by_mass) {
+                    const double w = ceil((double)p * (double)whole);
+                    last = larger(last, s.template locate<true>(w > 1 ? (uint64_t)w : 1, last, low, none));
+                }
+                if (last == 1 && low > -INFINITY) last = order_of(low, 0xffffffffu);  // all that pass the bound
+                __syncthreads();
+                if (tid == 0) m.cut = 0;
+                __syncthreads();
+                win = s.template best<false>(last, 0, 0, 0, unused);
+            }
         }
-    });
-    win = block_reduce(win, m.sh, larger);
-    if (tid == 0) answer(index_of(win), to_f32(s.z[index_of(win)]));
+    }
+    win = s.all(win, (uint64_t)0, Larger{});
+    if (tid == 0) s.answer(row, index_of(win));
 }
 
 }  // namespace ckks_plain
