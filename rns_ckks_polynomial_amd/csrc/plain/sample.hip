@@ -91,9 +91,8 @@ struct SampleShared {
 //    is its count times e of its middle, to half a bin's width; that names a few bins that may hold
 //    the end of the nucleus.  The last read takes the tokens above them, adds up their exact mass
 //    and lists those bins.
-//  - Many tokens by count, or a list that overflows (runs of equal logits): the last token is
-//    located by counts or masses in bins, and the one bin it falls into is listed or, if that does
-//    not fit either, divided again by the tokens' order.
+//  - Many tokens by count, or bins that overflow the list (runs of equal logits): the last token is
+//    located by counts or masses in bins of the tokens' order, eleven bits a read.
 // Masses that are added by atomics are whole multiples of a power of two and float sums go in a
 // fixed order, so the result does not depend on the order of anything.
 template <typename T> struct Sampler {
@@ -210,19 +209,39 @@ template <typename T> struct Sampler {
         if (threadIdx.x == 0) m.n = 0;
         __syncthreads();
         pass<4>([&](int first, const float (&x)[N]) {
-            if (!(largest(x) >= low)) return;
-#pragma unroll
-            for (int k = 0; k < N; k++)
-                if (x[k] >= low) list(first + k, x[k], f);
+            if (largest(x) >= low) append(first, x, [&](float v, uint64_t o) { return v >= low && f(v, o); });
         });
         __syncthreads();
         return m.n;
     }
-    template <typename F> __device__ __forceinline__ void list(uint32_t i, float v, F f) {
-        const uint64_t o = order_of(v, i);
-        if (!o || !f(v, o) || *(volatile uint32_t *)&m.n > LIST) return;
-        const uint32_t at = atomicAdd(&m.n, 1u);
-        if (at < LIST) m.list[at] = o;
+    // a vector's tokens for which f(logit, order) holds: one place in the count for all of them
+    template <typename F> __device__ __forceinline__ void append(int first, const float (&x)[N], F f) {
+        uint64_t o[N];
+        uint32_t n = 0;
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            o[k] = order_of(x[k], first + k);
+            if (o[k] && !f(x[k], o[k])) o[k] = 0;
+            n += o[k] != 0;
+        }
+        if (!n) return;
+        uint32_t at = atomicAdd(&m.n, n);
+#pragma unroll
+        for (int k = 0; k < N; k++)
+            if (o[k] && at < LIST) m.list[at++] = o[k];
+    }
+    // the numbers of tokens with logits >= low in BINS bins of 1 / width from the largest logit down
+    __device__ __forceinline__ void count(float low, float width) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < BINS; i += NT) m.counts[i] = 0;
+        __syncthreads();
+        pass<4>([&](int first, const float (&x)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; i++)
+                if (x[i] >= low && x[i] > -INFINITY)
+                    atomicAdd(&m.counts[(int)fminf(fmaxf((top - x[i]) * width, 0.0f), BINS - 1.0f)], 1u);
+        });
+        __syncthreads();
     }
     // the list in registers (0 past its end); the bins take its place
     __device__ __forceinline__ void hold(uint32_t n, uint64_t (&o)[HELD]) {
@@ -283,33 +302,24 @@ template <typename T> struct Sampler {
         }
     }
 
-    // Of the row's tokens with orders from `from` on and logits >= low: as `select`, with masses in
-    // multiples of 2^-mass_bits; `until` (by count): their mass up to the last.
-    template <bool BY_MASS>
-    __device__ __forceinline__ uint64_t locate(uint64_t want, uint64_t from, float low, uint64_t &until) {
-        const float width = (float)BINS / (top - fmaxf(low, top - 64.0f / c));
-        uint64_t a = 0, b = 0, before = 0;  // the range of orders that is divided, and what comes before it
-        for (int level = 0;; level++) {
-            const int shift = level && b - a >= BINS ? 53 - __clzll(b - a) : 0;
-            auto bin_of = [&](float x, uint64_t o) {
-                return level ? (int)((b - o) >> shift) : (int)fminf(fmaxf((top - x) * width, 0.0f), BINS - 1.0f);
-            };
-            auto inside = [&](float x, uint64_t o) { return o >= from && x >= low && (!level || (o >= a && o <= b)); };
-            auto each = [&](auto f) {
-                pass<1>([&](int first, const float (&x)[N]) {
-#pragma unroll
-                    for (int k = 0; k < N; k++) {
-                        const uint64_t o = order_of(x[k], first + k);
-                        if (o && inside(x[k], o)) f(x[k], o);
-                    }
-                });
-            };
+    // Of the row's tokens with orders in [from, b]: as `select`, with masses in multiples of
+    // 2^-mass_bits, eleven bits of the order at a time.
+    template <bool BY_MASS> __device__ __forceinline__ uint64_t locate(uint64_t want, uint64_t from, uint64_t b) {
+        uint64_t a = from, before = 0;
+        for (;;) {
+            const int shift = b - a >= BINS ? 53 - __clzll(b - a) : 0;  // (b - a) >> shift < BINS
             __syncthreads();
             for (int i = threadIdx.x; i < BINS; i += NT) m.bins[i] = 0;
             if (threadIdx.x == 0) m.pick[0] = BINS;
             __syncthreads();
-            each([&](float x, uint64_t o) {
-                atomicAdd((unsigned long long *)&m.bins[bin_of(x, o)], (unsigned long long)(BY_MASS ? mass(x) : 1));
+            pass<1>([&](int first, const float (&x)[N]) {
+#pragma unroll
+                for (int k = 0; k < N; k++) {
+                    const uint64_t o = order_of(x[k], first + k);
+                    if (o >= a && o <= b)
+                        atomicAdd((unsigned long long *)&m.bins[(b - o) >> shift],
+                                  (unsigned long long)(BY_MASS ? mass(x[k]) : 1));
+                }
             });
             __syncthreads();
             const uint64_t v0 = m.bins[2 * threadIdx.x], v1 = m.bins[2 * threadIdx.x + 1];
@@ -321,40 +331,24 @@ template <typename T> struct Sampler {
                 m.pick[1] = p + (second ? v0 : 0);
             }
             __syncthreads();
-            const int bin = (int)m.pick[0];
+            const uint64_t bin = m.pick[0];
             if (bin == BINS) return 0;
             before = m.pick[1];
-            const uint32_t n = gather(low, [&](float x, uint64_t o) { return inside(x, o) && bin_of(x, o) == bin; });
-            uint64_t lowest = NONE, highest = 0;
-            each([&](float x, uint64_t o) {
-                if (bin_of(x, o) == bin) lowest = o < lowest ? o : lowest, highest = o > highest ? o : highest;
-            });
-            const uint64_t a1 = ~all(~lowest, (uint64_t)0, Larger{}), b1 = all(highest, (uint64_t)0, Larger{});
-            if (n <= LIST) {
-                uint64_t o[HELD], last, unused;
-                hold(n, o);
-                // what is wanted of the list, its masses being multiples of 2^-LIST_BITS
-                uint64_t left = want - before;
-                if (BY_MASS) {
-                    const int s = this->a.mass_bits - LIST_BITS;
-                    left = s >= 0 ? (left >> s) + ((left & (((uint64_t)1 << s) - 1)) != 0) : left << -s;
-                    if (!left) left = 1;
-                }
-                last = select<BY_MASS>(o, left, a1, b1, unused);
-                if (!last) last = a1;  // by rounding: all of them
-                if (!BY_MASS) {
-                    uint64_t sum = 0;
-                    pass<1>([&](int first, const float (&x)[N]) {
-#pragma unroll
-                        for (int k = 0; k < N; k++)
-                            if (order_of(x[k], first + k) >= last) sum += mass(x[k]);
-                    });
-                    until = all(sum, (uint64_t)0, Sum{});
-                }
-                return last;
-            }
-            a = a1, b = b1;
+            b -= bin << shift;
+            if (!shift) return b;
+            const uint64_t width = (uint64_t)1 << shift;
+            a = b - a >= width ? b - (width - 1) : a;
         }
+    }
+    // the mass of the tokens with orders >= last
+    __device__ __forceinline__ uint64_t mass_until(uint64_t last) {
+        uint64_t v = 0;
+        pass<1>([&](int first, const float (&x)[N]) {
+#pragma unroll
+            for (int k = 0; k < N; k++)
+                if (order_of(x[k], first + k) >= last) v += mass(x[k]);
+        });
+        return all(v, (uint64_t)0, Sum{});
     }
 
     // The best score of the tokens with orders >= last, or (UNTIL) of those in bins < first_bin, whose
@@ -376,15 +370,12 @@ template <typename T> struct Sampler {
                 if ((uint32_t)(s >> 32) > *(volatile uint32_t *)&m.cut) atomicMax(&m.cut, (uint32_t)(s >> 32));
             }
         };
+        auto place = [&](float v) { return fmaxf((top - v) * width, 0.0f); };
         auto stays = [&](float v, uint32_t i) {
             if constexpr (UNTIL) {
-                const float x = fmaxf((top - v) * width, 0.0f);
-                if (x >= first_bin) {
-                    if (x < last_bin + 1.0f) list(i, v, [](float, uint64_t) { return true; });
-                    return false;
-                }
+                if (!(v > -INFINITY && place(v) < first_bin)) return false;
                 part_sum += weight(v, top);
-                return v > -INFINITY;
+                return true;
             } else {
                 return order_of(v, i) >= last;
             }
@@ -392,9 +383,14 @@ template <typename T> struct Sampler {
         auto handle = [&](int first, const float (&x)[N], const float (&noise)[N]) {
             // (a reciprocal of a temperature near the largest number has lost its digits)
             const float cut = t < 0x1p100f ? logit_of((uint64_t)*(volatile uint32_t *)&m.cut << 32) : -INFINITY;
+            bool listed = false;
 #pragma unroll
-            for (int k = 0; k < N; k++)
+            for (int k = 0; k < N; k++) {
                 if (x[k] >= low && stays(x[k], first + k)) consider(x[k], first + k, noise[k], cut);
+                if (UNTIL) listed |= place(x[k]) >= first_bin && place(x[k]) < last_bin + 1.0f;
+            }
+            if (listed)
+                append(first, x, [&](float v, uint64_t) { return place(v) >= first_bin && place(v) < last_bin + 1.0f; });
         };
         const int whole = a.vocab / N;
         for (int v = threadIdx.x; v < whole; v += U * NT) {
@@ -508,10 +504,27 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         } else {
             low = s.top + (__log2f((1.0f - p) * s.sum / (float)a.vocab) - 0.0625f) / s.c;
         }
-        // the list is tried unless nearly every thread has something for it (then it has thousands)
+        // Threads with something for the list.  Where most have, a bound from one maximum of each says
+        // little (and none where fewer than k have a token): the tokens are counted in bins down to it,
+        // or down to e = 2^-64, and the k-th one's bin is the bound.  A nucleus for which nearly every
+        // thread has something has thousands: the list is not tried.
         const int passing = __syncthreads_count(mine > -INFINITY && mine >= low);
+        if (by_count && a.vocab > LIST && (passing > NT / 2 || low == -INFINITY)) {
+            const float range = s.top - fmaxf(low, s.top - 64.0f / s.c);
+            if (tid == 0) m.pick[0] = BINS;
+            s.count(low, (float)BINS / range);
+            const uint32_t v0 = m.counts[2 * tid], v1 = m.counts[2 * tid + 1];
+            uint32_t total;
+            const uint32_t before = s.in_front(v0 + v1, total);
+            if (before < (uint32_t)k && (uint32_t)k <= before + v0 + v1)
+                m.pick[0] = 2 * tid + ((uint32_t)k > before + v0);
+            __syncthreads();
+            const int at = (int)m.pick[0];
+            if (at < BINS - 1)  // the last bin has what is below the range too
+                low = fmaxf(low, s.top - (float)(at + 1) * (range / BINS) * 1.00001f - fabsf(s.top) * 1e-6f);
+        }
         uint32_t n = LIST + 1;
-        if (a.vocab <= LIST || passing <= NT - 24) n = s.gather(low, [](float, uint64_t) { return true; });
+        if (by_count || a.vocab <= LIST || passing <= NT - 24) n = s.gather(low, [](float, uint64_t) { return true; });
         if (n <= 64) {  // one wave, a lane a token: its rank and the mass in front of it
             if (s.wave) return;
             const uint64_t o = (uint32_t)tid < n ? m.list[tid] : 0;
@@ -557,16 +570,8 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
             if (!by_count) {
                 // counts in bins down to the bound; a bin's mass by e of its middle, `off` at most off
                 const float range = s.top - low, width = (float)BINS / range;
-                for (int i = tid; i < BINS; i += NT) m.counts[i] = 0;
                 if (tid == 0) m.pick[0] = BINS, m.pick[1] = 0;
-                __syncthreads();
-                s.template pass<4>([&](int first, const float (&x)[N]) {
-#pragma unroll
-                    for (int i = 0; i < N; i++)
-                        if (x[i] >= low && x[i] > -INFINITY)
-                            atomicAdd(&m.counts[(int)fminf(fmaxf((s.top - x[i]) * width, 0.0f), BINS - 1.0f)], 1u);
-                });
-                __syncthreads();
+                s.count(low, width);
                 const float step = range / BINS * s.c;  // of a bin, in powers of two
                 const float v0 = (float)m.counts[2 * tid] * __builtin_amdgcn_exp2f(-(2 * tid + 0.5f) * step);
                 const float v1 = (float)m.counts[2 * tid + 1] * __builtin_amdgcn_exp2f(-(2 * tid + 1.5f) * step);
@@ -594,7 +599,10 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                         const double left = (double)p * s.sum - above;
                         if (left > 0) {
                             const double w = ceil(left * exp2(S::LIST_BITS));
-                            last = s.template select<true>(o, w > 1 ? (uint64_t)w : 1, 1, NONE, until);
+                            // a bin more at both ends, for what the bins' edges are off by
+                            const float lo = s.top - (last_bin + 2.0f) / width, hi = s.top - (first_bin - 1.0f) / width;
+                            last = s.template select<true>(o, w > 1 ? (uint64_t)w : 1, (uint64_t)order_bits(lo) << 32,
+                                                           (uint64_t)order_bits(hi) << 32 | 0xffffffffu, until);
 #pragma unroll
                             for (int i = 0; i < HELD; i++) {
                                 const float v = logit_of(o[i]);
@@ -606,13 +614,13 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                 }
             }
             if (!found) {
-                uint64_t whole = (uint64_t)((double)s.sum * exp2((double)a.mass_bits)), none;
-                if (by_count) last = larger(1, s.template locate<false>(k, 1, low, whole));
-                if (by_mass) {
-                    const double w = ceil((double)p * (double)whole);
-                    last = larger(last, s.template locate<true>(w > 1 ? (uint64_t)w : 1, last, low, none));
-                }
-                if (last == 1 && low > -INFINITY) last = order_of(low, 0xffffffffu);  // all that pass the bound
+                const uint64_t from = low > -INFINITY ? (uint64_t)order_bits(low) << 32 : 1;
+                const uint64_t to = (uint64_t)top_bits << 32 | 0xffffffffu;
+                last = from;
+                double whole = (double)s.sum;
+                if (by_count) last = larger(last, s.template locate<false>(k, from, to));  // 0: there are not so many
+                if (by_count && by_mass) whole = (double)s.mass_until(last) * exp2(-(double)a.mass_bits);
+                if (by_mass) last = larger(last, s.template locate<true>(under(whole, a.mass_bits), last, to));
                 __syncthreads();
                 if (tid == 0) m.cut = 0;
                 __syncthreads();
