@@ -1,22 +1,18 @@
 // sample.hip -- one token for each row of logits (include/ckks_plain.h).
+#include <type_traits>
+
 #include "plain_common.h"
 
 namespace ckks_plain {
 
-// Order of tokens: the logit as an unsigned number of the same order, then the complement of the
-// index, in one 64-bit number; 0 stands for a token that is not possible.
+// A number of the order of a float.
 __device__ __forceinline__ uint32_t order_bits(float z) {
     const uint32_t b = __float_as_uint(z + 0.0f);  // -0 orders as 0
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ uint64_t order_of(float z, uint32_t index) {
-    return z > -INFINITY ? (uint64_t)order_bits(z) << 32 | (uint32_t)~index : 0;
-}
-__device__ __forceinline__ float logit_of(uint64_t order) {
-    const uint32_t k = (uint32_t)(order >> 32);
+__device__ __forceinline__ float of_order_bits(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
-__device__ __forceinline__ uint32_t index_of(uint64_t order) { return ~(uint32_t)order; }
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 struct SampleArgs {
@@ -25,12 +21,13 @@ struct SampleArgs {
     const int32_t *top_k;
     const uint8_t *allowed;
     int64_t logits_stride, gumbel_stride, allowed_stride;
-    int vocab, mass_bits;
+    int vocab, index_bits;  // vocab <= 2^index_bits
     int64_t *token;
     float *logprob;
 };
 
 constexpr int NT = 1024, WAVES = NT / 64, BINS = 2048, LIST = 4096, HELD = LIST / NT;
+constexpr int FINE = 8192, EACH = FINE / NT;  // counted bins, of a thread
 constexpr uint64_t NONE = ~(uint64_t)0;
 
 // The neighbour's value that a cross-lane move brings (`none` where there is no neighbour).
@@ -76,7 +73,7 @@ struct SampleShared {
     union {
         uint64_t list[LIST];
         uint64_t bins[BINS];
-        uint32_t counts[BINS];
+        uint32_t counts[FINE];
     };
 };
 
@@ -109,6 +106,22 @@ template <typename T> struct Sampler {
     int wave, slot;
     float t, c, top;   // temperature, log2(e) / temperature, the largest logit
     float sum, min_p;  // the mass
+
+    // ---- the order of tokens: the logit as an unsigned number of the same order, without the bits
+    // that its type never sets, then the complement of the index; 0: a token that is not possible
+    static constexpr int UNSET = sizeof(T) == 4 ? 0 : std::is_same<T, f16>::value ? 13 : 16;
+    __device__ __forceinline__ uint32_t indexes() const { return (1u << a.index_bits) - 1; }
+    // the lowest and the highest order of a logit
+    __device__ __forceinline__ uint64_t lowest(float v) const { return (uint64_t)(order_bits(v) >> UNSET) << a.index_bits; }
+    __device__ __forceinline__ uint64_t highest(float v) const { return lowest(v) | indexes(); }
+    __device__ __forceinline__ uint64_t order_of(float v, uint32_t i) const {
+        return v > -INFINITY ? lowest(v) | (indexes() - i) : 0;
+    }
+    __device__ __forceinline__ float logit_of(uint64_t o) const {
+        const uint32_t k = (uint32_t)(o >> a.index_bits) << UNSET;
+        return of_order_bits(k & 0x80000000u ? k : k | ((1u << UNSET) - 1));
+    }
+    __device__ __forceinline__ uint32_t index_of(uint64_t o) const { return indexes() - ((uint32_t)o & indexes()); }
 
     // ---- the workgroup's reductions: one barrier each, in eight places in turn
     template <typename V, typename F> __device__ __forceinline__ V across(V v, V none, F f) {  // of each wave's v
@@ -188,7 +201,8 @@ template <typename T> struct Sampler {
         const uint64_t v = (b & 0x7fffff) | 0x800000;
         return b < 0x800000 || x <= -24 ? 0 : x >= 0 ? v << x : v >> -x;
     }
-    __device__ __forceinline__ uint64_t mass(float v) const { return fixed(weight(v, top), a.mass_bits); }
+    __device__ __forceinline__ int mass_bits() const { return 62 - a.index_bits; }  // a row's sum fits
+    __device__ __forceinline__ uint64_t mass(float v) const { return fixed(weight(v, top), mass_bits()); }
     __device__ __forceinline__ bool too_small(float v) const { return min_p > 0 && weight(v, top) < min_p; }
     // the distance to the largest logit, as defined: each step rounded to 32 bits
     __device__ __forceinline__ float part(float v) const { return v == top ? 0.0f : (v - top) / t; }
@@ -214,32 +228,42 @@ template <typename T> struct Sampler {
         __syncthreads();
         return m.n;
     }
-    // a vector's tokens for which f(logit, order) holds: one place in the count for all of them
+    // The tokens of these lanes' vectors for which f(logit, order) holds: one place in the count for
+    // all of them.
     template <typename F> __device__ __forceinline__ void append(int first, const float (&x)[N], F f) {
-        uint64_t o[N];
+        uint64_t o[N], lanes[N];
         uint32_t n = 0;
 #pragma unroll
         for (int k = 0; k < N; k++) {
             o[k] = order_of(x[k], first + k);
-            if (o[k] && !f(x[k], o[k])) o[k] = 0;
-            n += o[k] != 0;
+            if (!o[k] || !f(x[k], o[k])) o[k] = 0;
+            lanes[k] = __ballot(o[k] != 0);
+            n += __popcll(lanes[k]);
         }
         if (!n) return;
-        uint32_t at = atomicAdd(&m.n, n);
+        uint32_t at = 0;
+        if (before_lane(__ballot(1)) == 0) at = atomicAdd(&m.n, n);
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
 #pragma unroll
-        for (int k = 0; k < N; k++)
-            if (o[k] && at < LIST) m.list[at++] = o[k];
+        for (int k = 0; k < N; k++) {
+            const uint32_t place = at + before_lane(lanes[k]);
+            if (o[k] && place < LIST) m.list[place] = o[k];
+            at += __popcll(lanes[k]);
+        }
     }
-    // the numbers of tokens with logits >= low in BINS bins of 1 / width from the largest logit down
+    static __device__ __forceinline__ uint32_t before_lane(uint64_t lanes) {
+        return __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+    }
+    // the numbers of tokens with logits >= low in FINE bins of 1 / width from the largest logit down
     __device__ __forceinline__ void count(float low, float width) {
         __syncthreads();
-        for (int i = threadIdx.x; i < BINS; i += NT) m.counts[i] = 0;
+        for (int i = threadIdx.x; i < FINE; i += NT) m.counts[i] = 0;
         __syncthreads();
         pass<4>([&](int first, const float (&x)[N]) {
 #pragma unroll
             for (int i = 0; i < N; i++)
                 if (x[i] >= low && x[i] > -INFINITY)
-                    atomicAdd(&m.counts[(int)fminf(fmaxf((top - x[i]) * width, 0.0f), BINS - 1.0f)], 1u);
+                    atomicAdd(&m.counts[(int)fminf(fmaxf((top - x[i]) * width, 0.0f), FINE - 1.0f)], 1u);
         });
         __syncthreads();
     }
@@ -382,7 +406,7 @@ template <typename T> struct Sampler {
         };
         auto handle = [&](int first, const float (&x)[N], const float (&noise)[N]) {
             // (a reciprocal of a temperature near the largest number has lost its digits)
-            const float cut = t < 0x1p100f ? logit_of((uint64_t)*(volatile uint32_t *)&m.cut << 32) : -INFINITY;
+            const float cut = t < 0x1p100f ? of_order_bits(*(volatile uint32_t *)&m.cut) : -INFINITY;
             bool listed = false;
 #pragma unroll
             for (int k = 0; k < N; k++) {
@@ -465,7 +489,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         if (tid == 0) a.token[row] = -1, a.logprob[row] = -INFINITY;
         return;
     }
-    s.top = logit_of((uint64_t)top_bits << 32);
+    s.top = of_order_bits(top_bits);
     s.sum = s.all(mine > -INFINITY ? sum * s.weight(mine, s.top) : 0.0f, 0.0f, Sum{});
     if (greedy || k == 1 || p <= 0 || s.min_p > 1) {  // the first alone: it is in the first vector that holds it
         uint32_t i = ~s.all(mine == s.top ? ~where : 0u, 0u, Larger{});
@@ -489,8 +513,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         float low = -INFINITY;
         if (by_count) {
             // the k-th largest of the threads' maxima, or a little less: by bins of equal width
-            const uint64_t own = order_of(mine, 0);
-            const float least = logit_of(~s.all(own ? ~own : (uint64_t)0, (uint64_t)0, Larger{}));
+            const float least = of_order_bits(~s.all(mine > -INFINITY ? ~order_bits(mine) : 0u, 0u, Larger{}));
             const float range = s.top - least;
             if (mine > -INFINITY) atomicAdd(&m.counts[(int)fminf(fmaxf((s.top - mine) * (NT / range), 0.0f), NT - 1.0f)], 1u);
             __syncthreads();
@@ -511,17 +534,22 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         const int passing = __syncthreads_count(mine > -INFINITY && mine >= low);
         if (by_count && a.vocab > LIST && (passing > NT / 2 || low == -INFINITY)) {
             const float range = s.top - fmaxf(low, s.top - 64.0f / s.c);
-            if (tid == 0) m.pick[0] = BINS;
-            s.count(low, (float)BINS / range);
-            const uint32_t v0 = m.counts[2 * tid], v1 = m.counts[2 * tid + 1];
-            uint32_t total;
-            const uint32_t before = s.in_front(v0 + v1, total);
-            if (before < (uint32_t)k && (uint32_t)k <= before + v0 + v1)
-                m.pick[0] = 2 * tid + ((uint32_t)k > before + v0);
+            if (tid == 0) m.pick[0] = FINE;
+            s.count(low, (float)FINE / range);
+            uint32_t own = 0, total;
+#pragma unroll
+            for (int i = 0; i < EACH; i++) own += m.counts[EACH * tid + i];
+            uint32_t before = s.in_front(own, total);
+#pragma unroll
+            for (int i = 0; i < EACH; i++) {
+                const uint32_t v = m.counts[EACH * tid + i];
+                if (before < (uint32_t)k && (uint32_t)k <= before + v) m.pick[0] = EACH * tid + i;
+                before += v;
+            }
             __syncthreads();
             const int at = (int)m.pick[0];
-            if (at < BINS - 1)  // the last bin has what is below the range too
-                low = fmaxf(low, s.top - (float)(at + 1) * (range / BINS) * 1.00001f - fabsf(s.top) * 1e-6f);
+            if (at < FINE - 1)  // the last bin has what is below the range too
+                low = fmaxf(low, s.top - (float)(at + 1) * (range / FINE) * 1.00001f - fabsf(s.top) * 1e-6f);
         }
         uint32_t n = LIST + 1;
         if (by_count || a.vocab <= LIST || passing <= NT - 24) n = s.gather(low, [](float, uint64_t) { return true; });
@@ -540,52 +568,65 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                 stay = stay && (q & S::MASS) < (by_count ? under((double)whole * exp2(-S::LIST_BITS), S::LIST_BITS)
                                                          : under((double)s.sum, S::LIST_BITS));
             }
-            const float v = logit_of(o);
-            if (stay && !s.too_small(v)) win = s.score(v, index_of(o), s.gumbel[index_of(o)]);
+            const float v = s.logit_of(o);
+            if (stay && !s.too_small(v)) win = s.score(v, s.index_of(o), s.gumbel[s.index_of(o)]);
             win = lane(scan64(win, (uint64_t)0, Larger{}), 63);
-            if (tid == 0) s.answer(row, index_of(win));
+            if (tid == 0) s.answer(row, s.index_of(win));
             return;
         }
         if (n <= LIST) {
             uint64_t o[HELD], last = 1, until = 0;
             s.hold(n, o);
-            const uint64_t from = low > -INFINITY ? (uint64_t)order_bits(low) << 32 : 1;
-            const uint64_t to = (uint64_t)top_bits << 32 | 0xffffffffu;
-            if (by_count && (uint32_t)k < n) last = s.template select<false>(o, k, from, to, until);
+            const uint64_t from = low > -INFINITY ? s.lowest(low) : 1, to = s.highest(s.top);
+            if (by_count && (uint32_t)k < n) {
+                last = s.template select<false>(o, k, from, to, until);
+            } else if (by_mass) {
+#pragma unroll
+                for (int i = 0; i < HELD; i++) until += o[i] ? s.both(o[i]) : 0;
+                until = s.all(until, (uint64_t)0, Sum{});
+            }
             if (by_mass) {
-                double whole = (double)s.sum;
-                if (by_count && (uint32_t)k < n) whole = (double)(until & S::MASS) * exp2(-S::LIST_BITS);
+                const double whole = by_count ? (double)(until & S::MASS) * exp2(-S::LIST_BITS) : (double)s.sum;
                 const uint64_t l = s.template select<true>(o, under(whole, S::LIST_BITS), larger(from, last), to, until);
                 last = larger(l, last);  // 0: all of them
             }
 #pragma unroll
             for (int i = 0; i < HELD; i++) {
-                const float v = logit_of(o[i]);
+                const float v = s.logit_of(o[i]);
                 if (o[i] && o[i] >= last && !s.too_small(v))
-                    win = larger(win, s.score(v, index_of(o[i]), s.gumbel[index_of(o[i])]));
+                    win = larger(win, s.score(v, s.index_of(o[i]), s.gumbel[s.index_of(o[i])]));
             }
         } else {
             uint64_t last = 1;
             bool found = false;
             if (!by_count) {
                 // counts in bins down to the bound; a bin's mass by e of its middle, `off` at most off
-                const float range = s.top - low, width = (float)BINS / range;
-                if (tid == 0) m.pick[0] = BINS, m.pick[1] = 0;
+                const float range = s.top - low, width = (float)FINE / range;
+                if (tid == 0) m.pick[0] = FINE, m.pick[1] = 0;
                 s.count(low, width);
-                const float step = range / BINS * s.c;  // of a bin, in powers of two
-                const float v0 = (float)m.counts[2 * tid] * __builtin_amdgcn_exp2f(-(2 * tid + 0.5f) * step);
-                const float v1 = (float)m.counts[2 * tid + 1] * __builtin_amdgcn_exp2f(-(2 * tid + 1.5f) * step);
+                const float step = range / FINE * s.c;  // of a bin, in powers of two
                 const float off = __builtin_amdgcn_exp2f(0.5f * step) - 1.0f + 1e-4f, want = p * s.sum;
-                float total;
-                const float b0 = s.in_front(v0 + v1, total), b1 = b0 + v0, b2 = b1 + v1;
+                float own = 0, total, v[EACH];
+#pragma unroll
+                for (int i = 0; i < EACH; i++) {
+                    const int at = EACH * tid + i;
+                    v[i] = (float)m.counts[at] * __builtin_amdgcn_exp2f(-((float)at + 0.5f) * step);
+                    own += v[i];
+                }
+                float before = s.in_front(own, total);
                 // the first bin after which there may be `want`, and the last before which there may not
-                if (b0 * (1 + off) < want && b2 * (1 + off) >= want) m.pick[0] = 2 * tid + (b1 * (1 + off) < want);
-                if (b0 * (1 - off) < want)
-                    atomicMax((unsigned long long *)&m.pick[1], (unsigned long long)(2 * tid + (b1 * (1 - off) < want)));
+#pragma unroll
+                for (int i = 0; i < EACH; i++) {
+                    const float after = before + v[i];
+                    if (before * (1 + off) < want && after * (1 + off) >= want) m.pick[0] = EACH * tid + i;
+                    if (before * (1 - off) < want && (after * (1 - off) >= want || EACH * tid + i == FINE - 1))
+                        atomicMax((unsigned long long *)&m.pick[1], (unsigned long long)(EACH * tid + i));
+                    before = after;
+                }
                 __syncthreads();
                 const float first_bin = (float)m.pick[0], last_bin = (float)m.pick[1];
                 __syncthreads();
-                if (first_bin < BINS && step < 0.125f) {
+                if (first_bin < FINE && step < 0.125f) {
                     if (tid == 0) m.n = 0;
                     __syncthreads();
                     float above;
@@ -601,26 +642,24 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                             const double w = ceil(left * exp2(S::LIST_BITS));
                             // a bin more at both ends, for what the bins' edges are off by
                             const float lo = s.top - (last_bin + 2.0f) / width, hi = s.top - (first_bin - 1.0f) / width;
-                            last = s.template select<true>(o, w > 1 ? (uint64_t)w : 1, (uint64_t)order_bits(lo) << 32,
-                                                           (uint64_t)order_bits(hi) << 32 | 0xffffffffu, until);
+                            last = s.template select<true>(o, w > 1 ? (uint64_t)w : 1, s.lowest(lo), s.highest(hi), until);
 #pragma unroll
                             for (int i = 0; i < HELD; i++) {
-                                const float v = logit_of(o[i]);
+                                const float v = s.logit_of(o[i]);
                                 if (o[i] && o[i] >= last && !s.too_small(v))
-                                    win = larger(win, s.score(v, index_of(o[i]), s.gumbel[index_of(o[i])]));
+                                    win = larger(win, s.score(v, s.index_of(o[i]), s.gumbel[s.index_of(o[i])]));
                             }
                         }
                     }
                 }
             }
             if (!found) {
-                const uint64_t from = low > -INFINITY ? (uint64_t)order_bits(low) << 32 : 1;
-                const uint64_t to = (uint64_t)top_bits << 32 | 0xffffffffu;
+                const uint64_t from = low > -INFINITY ? s.lowest(low) : 1, to = s.highest(s.top);
                 last = from;
                 double whole = (double)s.sum;
                 if (by_count) last = larger(last, s.template locate<false>(k, from, to));  // 0: there are not so many
-                if (by_count && by_mass) whole = (double)s.mass_until(last) * exp2(-(double)a.mass_bits);
-                if (by_mass) last = larger(last, s.template locate<true>(under(whole, a.mass_bits), last, to));
+                if (by_count && by_mass) whole = (double)s.mass_until(last) * exp2(-(double)s.mass_bits());
+                if (by_mass) last = larger(last, s.template locate<true>(under(whole, s.mass_bits()), last, to));
                 __syncthreads();
                 if (tid == 0) m.cut = 0;
                 __syncthreads();
@@ -629,7 +668,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         }
     }
     win = s.all(win, (uint64_t)0, Larger{});
-    if (tid == 0) s.answer(row, index_of(win));
+    if (tid == 0) s.answer(row, s.index_of(win));
 }
 
 }  // namespace ckks_plain
@@ -669,7 +708,7 @@ extern "C" int ckks_plain_sample(int type, const void *logits, int64_t logits_st
     int bits = 0;
     while (((int64_t)1 << bits) < vocab) bits++;
     const SampleArgs a{logits, gumbel, temperature, top_p, min_p, top_k, allowed, logits_stride, gumbel_stride,
-                       allowed_stride, (int)vocab, 62 - bits, token, logprob};
+                       allowed_stride, (int)vocab, bits, token, logprob};
     auto go = [&](auto ty) {
         k_sample<decltype(ty)><<<dim3((uint32_t)rows), NT, 0, (hipStream_t)stream>>>(a);
         return launched();
