@@ -81,7 +81,8 @@ struct SampleShared {
 // e = exp((z - max) / temperature)); a filter then needs the last token that stays:
 //  - Bounds.  A token under the k-th largest of the threads' own maxima is not among the first k.
 //    One with e < (1 - p) mass / count is not in the nucleus: all such together have less than
-//    (1 - p) of the mass, so what comes before any of them has p of it.
+//    (1 - p) of the mass, so what comes before any of them has p of it.  One with e < min_p does
+//    not stay.
 //  - What passes the bound usually fits the list in LDS: everything else is decided there,
 //    without reading the row again.
 //  - A nucleus that does not fit is counted in bins of equal width over the logits.  A bin's mass
@@ -216,40 +217,44 @@ template <typename T> struct Sampler {
     }
 
     // ---- lists
-    // Puts the tokens with logits >= low for which f(logit, order) holds on the list, at most LIST;
-    // returns how many there are (more than LIST: at least that many).
-    template <typename F> __device__ __forceinline__ uint32_t gather(float low, F f) {
+    // Puts the tokens with logits >= low on the list, at most LIST; returns how many there are.
+    __device__ __forceinline__ uint32_t gather(float low) {
         __syncthreads();
         if (threadIdx.x == 0) m.n = 0;
         __syncthreads();
         pass<4>([&](int first, const float (&x)[N]) {
-            if (largest(x) >= low) append(first, x, [&](float v, uint64_t o) { return v >= low && f(v, o); });
+            if (!(largest(x) >= low)) return;
+            uint32_t hits = 0;
+#pragma unroll
+            for (int k = 0; k < N; k++) hits |= x[k] >= low ? 1u << k : 0;
+            append(first, x, hits);
         });
         __syncthreads();
         return m.n;
     }
-    // The tokens of these lanes' vectors for which f(logit, order) holds: one place in the count for
-    // all of them.
-    template <typename F> __device__ __forceinline__ void append(int first, const float (&x)[N], F f) {
-        uint64_t o[N], lanes[N];
-        uint32_t n = 0;
+    // The tokens of these lanes' vectors that `hits` names go on the list: one place in the count for
+    // all lanes, found by the bits of their numbers.
+    __device__ __forceinline__ void append(int first, const float (&x)[N], uint32_t hits) {
 #pragma unroll
-        for (int k = 0; k < N; k++) {
-            o[k] = order_of(x[k], first + k);
-            if (!o[k] || !f(x[k], o[k])) o[k] = 0;
-            lanes[k] = __ballot(o[k] != 0);
-            n += __popcll(lanes[k]);
-        }
-        if (!n) return;
-        uint32_t at = 0;
-        if (before_lane(__ballot(1)) == 0) at = atomicAdd(&m.n, n);
-        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        for (int k = 0; k < N; k++) hits &= x[k] > -INFINITY ? ~0u : ~(1u << k);
+        const uint32_t n = __popc(hits);
+        uint32_t total = 0, at = 0;
 #pragma unroll
-        for (int k = 0; k < N; k++) {
-            const uint32_t place = at + before_lane(lanes[k]);
-            if (o[k] && place < LIST) m.list[place] = o[k];
-            at += __popcll(lanes[k]);
+        for (int b = 0; 1 << b <= N; b++) {
+            const uint64_t lanes = __ballot(n >> b & 1);
+            total += __popcll(lanes) << b;
+            at += before_lane(lanes) << b;
         }
+        if (!total) return;
+        uint32_t base = 0;
+        if (before_lane(__ballot(1)) == 0) base = atomicAdd(&m.n, total);
+        at += (uint32_t)__builtin_amdgcn_readfirstlane((int)base);
+#pragma unroll
+        for (int k = 0; k < N; k++)
+            if (hits >> k & 1) {
+                if (at < LIST) m.list[at] = order_of(x[k], first + k);
+                at++;
+            }
     }
     static __device__ __forceinline__ uint32_t before_lane(uint64_t lanes) {
         return __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
@@ -407,27 +412,31 @@ template <typename T> struct Sampler {
         auto handle = [&](int first, const float (&x)[N], const float (&noise)[N]) {
             // (a reciprocal of a temperature near the largest number has lost its digits)
             const float cut = t < 0x1p100f ? of_order_bits(*(volatile uint32_t *)&m.cut) : -INFINITY;
-            bool listed = false;
+            uint32_t listed = 0;
 #pragma unroll
             for (int k = 0; k < N; k++) {
                 if (x[k] >= low && stays(x[k], first + k)) consider(x[k], first + k, noise[k], cut);
-                if (UNTIL) listed |= place(x[k]) >= first_bin && place(x[k]) < last_bin + 1.0f;
+                if (UNTIL) listed |= place(x[k]) >= first_bin && place(x[k]) < last_bin + 1.0f ? 1u << k : 0;
             }
-            if (listed)
-                append(first, x, [&](float v, uint64_t) { return place(v) >= first_bin && place(v) < last_bin + 1.0f; });
+            if (listed) append(first, x, listed);
         };
         const int whole = a.vocab / N;
+        Vec r[U];
+        Mask ks[U];
+        auto fetch = [&](int v) {
+#pragma unroll
+            for (int j = 0; j < U; j++) {
+                const int64_t i = (int64_t)(v + j * NT < whole ? v + j * NT : 0) * N;
+                r[j] = *(const Vec *)(z + i);
+                if (ok) ks[j] = *(const Mask *)(ok + i);
+            }
+        };
+        if ((int)threadIdx.x < whole) fetch(threadIdx.x);
         for (int v = threadIdx.x; v < whole; v += U * NT) {
             float x[U][N], noise[U][N];
 #pragma unroll
             for (int j = 0; j < U; j++) {
-                const int64_t i = (int64_t)(v + j * NT < whole ? v + j * NT : v) * N;
-                Mask k;
-                if (ok) k = *(const Mask *)(ok + i);
-                logits(*(const Vec *)(z + i), k, x[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < U; j++) {
+                logits(r[j], ks[j], x[j]);
                 const float most = largest(x[j]);
                 const bool need = v + j * NT < whole && most > -INFINITY &&
                                   (UNTIL ? fmaxf((top - most) * width, 0.0f) < first_bin : most >= low);
@@ -441,6 +450,7 @@ template <typename T> struct Sampler {
                     }
                 }
             }
+            if (v + U * NT < whole) fetch(v + U * NT);  // on their way while these are handled
 #pragma unroll
             for (int j = 0; j < U; j++)
                 if (v + j * NT < whole) handle((v + j * NT) * N, x[j], noise[j]);
@@ -499,7 +509,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         }
         return;
     }
-    const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1;
+    const bool by_count = k > 0 && k < a.vocab, by_mass = p < 1, by_size = s.min_p > 0;
     uint64_t win = 0;
     float unused;
     // what the mass in front of a token that stays is under, in multiples of 2^-bits
@@ -507,7 +517,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         const double w = ceil((double)p * whole * exp2((double)bits));
         return w > 1 ? (uint64_t)w : (uint64_t)1;
     };
-    if (!by_count && !by_mass) {
+    if (!by_count && !by_mass && !by_size) {
         win = s.template best<false>(1, 0, 0, 0, unused);
     } else {
         float low = -INFINITY;
@@ -524,9 +534,12 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
             const int at = (int)m.pick[0];
             // the bin's lower edge, and all that the edge may be off by
             if (at < NT) low = fmaxf(least, s.top - (float)(at + 1) * (range / NT) * 1.00001f - fabsf(s.top) * 1e-6f);
-        } else {
+        } else if (by_mass) {
             low = s.top + (__log2f((1.0f - p) * s.sum / (float)a.vocab) - 0.0625f) / s.c;
         }
+        // nothing under min_p stays; only the mass of the first k by count has it in it
+        const float nucleus = low;
+        if (by_size && !(by_count && by_mass)) low = fmaxf(low, s.top + (__log2f(s.min_p) - 0.0625f) / s.c);
         // Threads with something for the list.  Where most have, a bound from one maximum of each says
         // little (and none where fewer than k have a token): the tokens are counted in bins down to it,
         // or down to e = 2^-64, and the k-th one's bin is the bound.  A nucleus for which nearly every
@@ -552,10 +565,11 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                 low = fmaxf(low, s.top - (float)(at + 1) * (range / FINE) * 1.00001f - fabsf(s.top) * 1e-6f);
         }
         uint32_t n = LIST + 1;
-        if (by_count || a.vocab <= LIST || passing <= NT - 24) n = s.gather(low, [](float, uint64_t) { return true; });
+        if (by_count || a.vocab <= LIST || passing <= NT - 24) n = s.gather(low);
         if (n <= 64) {  // one wave, a lane a token: its rank and the mass in front of it
             if (s.wave) return;
             const uint64_t o = (uint32_t)tid < n ? m.list[tid] : 0;
+            const float noise = o ? s.gumbel[s.index_of(o)] : 0.0f;
             const uint64_t own = o ? s.both(o) : 0;
             uint64_t q = 0;
             for (uint32_t j = 0; j < n; j++) {
@@ -569,7 +583,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                                                          : under((double)s.sum, S::LIST_BITS));
             }
             const float v = s.logit_of(o);
-            if (stay && !s.too_small(v)) win = s.score(v, s.index_of(o), s.gumbel[s.index_of(o)]);
+            if (stay && !s.too_small(v)) win = s.score(v, s.index_of(o), noise);
             win = lane(scan64(win, (uint64_t)0, Larger{}), 63);
             if (tid == 0) s.answer(row, s.index_of(win));
             return;
@@ -599,11 +613,11 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         } else {
             uint64_t last = 1;
             bool found = false;
-            if (!by_count) {
+            if (by_mass && !by_count) {
                 // counts in bins down to the bound; a bin's mass by e of its middle, `off` at most off
-                const float range = s.top - low, width = (float)FINE / range;
+                const float range = s.top - nucleus, width = (float)FINE / range;
                 if (tid == 0) m.pick[0] = FINE, m.pick[1] = 0;
-                s.count(low, width);
+                s.count(nucleus, width);
                 const float step = range / FINE * s.c;  // of a bin, in powers of two
                 const float off = __builtin_amdgcn_exp2f(0.5f * step) - 1.0f + 1e-4f, want = p * s.sum;
                 float own = 0, total, v[EACH];
