@@ -62,7 +62,7 @@ struct TileOrder {
 // (piece p of rows 0..15) or, as the conflict counter says of this GPU, rows 0..3 and 12..15 of one
 // piece with rows 4..11 of the next (p ^ (r / 4 & 3) serves the former only).  The loads write LDS
 // in lane order and permute the pieces on the memory side (within a row's 64 bytes).
-constexpr int STEP = 64, STAGES = 4;
+constexpr int STEP = 64;
 __device__ __forceinline__ int turn(int row) {  // 0, 2, 3, 1 for each four rows in turn
     const int q = row / 4 % 4;
     return q >> 1 | ((q ^ q >> 1) & 1) << 1;
@@ -96,7 +96,7 @@ template <int TN, int TM> __device__ __forceinline__ void mfma_done(v4i (&acc)[T
     for_all<TN * TM>([&](auto at) { not_before(acc[decltype(at)::value / TM][decltype(at)::value % TM]); });
 }
 
-template <typename T, int BM, int BN>
+template <typename T, int BM, int BN, int STAGES>
 __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(MatmulArgs m, T *out, TileOrder order) {
     constexpr int TN = BN / 32, TM = BM / 32, TILES = TN * TM;  // 16 x 16 tiles of a wave
     constexpr int LOADS_W = BN / 64, LOADS = LOADS_W + BM / 64;  // of a wave, per step
@@ -209,6 +209,81 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
     });
 }
 
+// ------------------------------------------------------------------ few tokens
+//
+// With at most 64 tokens the weights are all that has to move.  A wave takes 16 NC channels and all
+// tokens and reads both straight into the operand registers: lane l holds 16 bytes of row l % 16 at
+// 16 (l / 16) of each 64, so two loads use a row's 128 bytes; the tokens come from L2 each time.  The
+// waves of a workgroup share the channels and split the contraction (in turn, 128 bytes each); their
+// sums meet in LDS.
+template <typename T, int MT, int NC, int U>
+__global__ __launch_bounds__(512) void k_matmul_i8_stream(MatmulArgs m, T *out) {
+    extern __shared__ __attribute__((aligned(16))) int sums[];  // [wave][MT * NC][64][4]
+    const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6, pairs = m.padded / 128, c0 = blockIdx.x * 16 * NC;
+    const int8_t *wp[NC], *ap[MT];
+#pragma unroll
+    for (int i = 0; i < NC; i++) {
+        const int c = c0 + 16 * i + l % 16;
+        wp[i] = m.w + (int64_t)(c < m.channels ? c : m.channels - 1) * m.w_stride + l / 16 * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < MT; j++) {
+        const int t = 16 * j + l % 16;
+        ap[j] = m.a + (int64_t)(t < m.rows ? t : m.rows - 1) * m.a_stride + l / 16 * 16;
+    }
+    v4i acc[NC][MT] = {};
+    // n pairs from p on, all loads in front of the products
+    auto take = [&](int p, auto count) {
+        constexpr int n = decltype(count)::value;
+        v4i w[n][2][NC], a[n][2][MT];
+#pragma unroll
+        for (int u = 0; u < n; u++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int64_t at = (int64_t)(p + u * waves) * 128 + h * 64;
+#pragma unroll
+                for (int i = 0; i < NC; i++) w[u][h][i] = __builtin_nontemporal_load((const v4i *)(wp[i] + at));
+#pragma unroll
+                for (int j = 0; j < MT; j++) a[u][h][j] = *(const v4i *)(ap[j] + at);
+            }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < n; u++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+                for (int i = 0; i < NC; i++)
+#pragma unroll
+                    for (int j = 0; j < MT; j++)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][h][i], a[u][h][j], acc[i][j], 0, 0, 0);
+    };
+    int p = wave;
+    for (; p + (U - 1) * waves < pairs; p += U * waves) take(p, Int<U>{});
+    for (; p < pairs; p += waves) take(p, Int<1>{});
+    v4i *mine = (v4i *)sums + wave * MT * NC * 64 + l;
+#pragma unroll
+    for (int i = 0; i < NC; i++)
+#pragma unroll
+        for (int j = 0; j < MT; j++) mine[(i * MT + j) * 64] = acc[i][j];
+    __syncthreads();
+    // each wave adds up its share of the tiles; a lane has channels 4 (l / 16) + 0..3 of token l % 16
+    for (int tile = wave; tile < MT * NC; tile += waves) {
+        v4i v = {0, 0, 0, 0};
+        for (int k = 0; k < waves; k++) v += ((const v4i *)sums)[(k * MT * NC + tile) * 64 + l];
+        const int t = tile % MT * 16 + l % 16, c = c0 + tile / MT * 16 + l / 16 * 4;
+        if (t >= m.rows || c >= m.channels) continue;
+        const int s[4] = {v[0], v[1], v[2], v[3]};
+        float ws[4], bias[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
+            bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
+        }
+        store_sums<T, 4>(m, out, t, c, m.a_scale[t], s, ws, bias);
+    }
+}
+
 }  // namespace ckks_plain
 
 using namespace ckks_plain;
@@ -247,14 +322,31 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
         auto tiles = [&](int bm, int bn) {
             return TileOrder{(int)((rows + bm - 1) / bm), (int)((channels + bn - 1) / bn), 8};
         };
-        const TileOrder big = tiles(256, 256);
-        if (big.tokens * big.channels >= 192) {
-            k_matmul_i8_tile<T, 256, 256><<<dim3(big.tokens * big.channels), 256, 0, (hipStream_t)stream>>>(m, (T *)out, big);
-        } else {
-            const TileOrder small = tiles(128, 128);
-            k_matmul_i8_tile<T, 128, 128>
-                <<<dim3(small.tokens * small.channels), 256, 0, (hipStream_t)stream>>>(m, (T *)out, small);
+        const hipStream_t st = (hipStream_t)stream;
+        if (rows <= 64) {
+            auto few = [&](auto mt, auto nc, auto u) {
+                constexpr int MT = decltype(mt)::value, NC = decltype(nc)::value;
+                const int groups = (int)((channels + 16 * NC - 1) / (16 * NC));
+                int waves = 8;
+                while (waves > 1 && (groups * waves > 8192 || padded / 128 < 4 * waves)) waves /= 2;
+                k_matmul_i8_stream<T, MT, NC, decltype(u)::value>
+                    <<<dim3(groups), 64 * waves, waves * MT * NC * 1024, st>>>(m, (T *)out);
+            };
+            if (rows <= 16) few(Int<1>{}, Int<1>{}, Int<4>{});
+            else if (rows <= 32) few(Int<2>{}, Int<2>{}, Int<4>{});
+            else few(Int<4>{}, Int<2>{}, Int<4>{});
+            return launched();
         }
+        auto tile = [&](auto bm, auto bn, auto stages) {
+            constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
+            const TileOrder o = tiles(BM, BN);
+            k_matmul_i8_tile<T, BM, BN, decltype(stages)::value><<<dim3(o.tokens * o.channels), 256, 0, st>>>(m, (T *)out, o);
+        };
+        auto count = [&](int bm, int bn) { return ((rows + bm - 1) / bm) * ((channels + bn - 1) / bn); };
+        if (count(256, 256) >= 192) tile(Int<256>{}, Int<256>{}, Int<4>{});
+        else if (count(128, 128) >= 256) tile(Int<128>{}, Int<128>{}, Int<4>{});
+        else if (count(128, 64) >= 256) tile(Int<128>{}, Int<64>{}, Int<4>{});
+        else tile(Int<64>{}, Int<64>{}, Int<16>{});
         return launched();
     };
     return out_type == CKKS_PLAIN_BF16 ? go(bf16{}) : out_type == CKKS_PLAIN_F16 ? go(f16{}) : go(0.0f);
