@@ -124,6 +124,14 @@ int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const float *a_scale
                          const float *w_scale, const float *bias, int out_type, void *out, int64_t out_stride,
                          int64_t rows, int64_t channels, int64_t cols, void *ws, size_t ws_bytes, void *stream);
 
+/* ckks_plain_quantize_rows of x and then the product, the 8-bit rows in ws:
+ * ckks_plain_linear_i8_workspace_size bytes, aligned to 16.  cols <=
+ * CKKS_PLAIN_MAX_COLS. */
+int ckks_plain_linear_i8_workspace_size(int64_t rows, int64_t channels, int64_t cols, size_t *bytes);
+int ckks_plain_linear_i8(int type, const void *x, int64_t x_stride, const int8_t *w, int64_t w_stride,
+                         const float *w_scale, const float *bias, int out_type, void *out, int64_t out_stride,
+                         int64_t rows, int64_t channels, int64_t cols, void *ws, size_t ws_bytes, void *stream);
+
 /* One token for each row of logits z [rows][vocab] (type as above).
  * A token is possible if it is allowed (allowed [rows][vocab] bytes, 0 = no;
  * NULL = all) and its logit is neither NaN nor -infinity.  In the order of

@@ -294,14 +294,13 @@ extern "C" int ckks_plain_matmul_i8_workspace_size(int64_t rows, int64_t channel
     return CKKS_OK;
 }
 
-extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w,
-                                    int64_t w_stride, const float *w_scale, const float *bias, int out_type, void *out,
-                                    int64_t out_stride, int64_t rows, int64_t channels, int64_t cols, void *ws,
-                                    size_t ws_bytes, void *stream) {
+// every check of a product with rows and channels
+static int check_matmul(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
+                        const float *w_scale, const float *bias, int out_type, void *out, int64_t out_stride,
+                        int64_t rows, int64_t channels, int64_t cols, void *ws, size_t ws_bytes) {
     size_t need;
     if (int e = ckks_plain_matmul_i8_workspace_size(rows, channels, cols, &need)) return e;
     if (!type_ok(out_type) || rows >= (int64_t)1 << 31 || channels >= (int64_t)1 << 31) return CKKS_EINVAL;
-    if (rows == 0 || channels == 0) return CKKS_OK;
     const size_t z = type_size(out_type);
     const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
     if (!a || !w || !a_scale || !w_scale || a_stride < padded || w_stride < padded || a_stride % CKKS_PLAIN_I8_ROW ||
@@ -312,9 +311,25 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
     const size_t ob = span(rows, out_stride, channels, z);
     if (overlap(out, ob, a, span(rows, a_stride, padded, 1)) || overlap(out, ob, w, span(channels, w_stride, padded, 1)) ||
         overlap(out, ob, a_scale, rows * 4) || overlap(out, ob, w_scale, channels * 4) ||
-        overlap(out, ob, bias, channels * 4))
+        overlap(out, ob, bias, channels * 4) || overlap(out, ob, ws, need))
         return CKKS_EINVAL;
     if (need && (!ws || ws_bytes < need)) return CKKS_EWORKSPACE;
+    return need && !at(ws, 16) ? CKKS_EALIGN : CKKS_OK;
+}
+
+extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w,
+                                    int64_t w_stride, const float *w_scale, const float *bias, int out_type, void *out,
+                                    int64_t out_stride, int64_t rows, int64_t channels, int64_t cols, void *ws,
+                                    size_t ws_bytes, void *stream) {
+    size_t need;
+    if (int e = ckks_plain_matmul_i8_workspace_size(rows, channels, cols, &need)) return e;
+    if (!type_ok(out_type)) return CKKS_EINVAL;
+    if (rows == 0 || channels == 0) return CKKS_OK;
+    if (int e = check_matmul(a, a_stride, a_scale, w, w_stride, w_scale, bias, out_type, out, out_stride, rows, channels,
+                             cols, ws, ws_bytes))
+        return e;
+    const size_t z = type_size(out_type);
+    const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
     const MatmulArgs m{a, w, a_scale, w_scale, bias, a_stride, w_stride, out_stride, (int)rows, (int)channels,
                        (int)padded, out_stride * z % 16 == 0 && at(out, 16)};
     auto go = [&](auto ty) {
@@ -350,4 +365,47 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
         return launched();
     };
     return out_type == CKKS_PLAIN_BF16 ? go(bf16{}) : out_type == CKKS_PLAIN_F16 ? go(f16{}) : go(0.0f);
+}
+
+// the 8-bit rows, their scales, and what the product takes
+static size_t linear_rows_bytes(int64_t rows, int64_t cols) {
+    return (size_t)rows * round_up(cols, CKKS_PLAIN_I8_ROW) + round_up(rows * 4, 16);
+}
+extern "C" int ckks_plain_linear_i8_workspace_size(int64_t rows, int64_t channels, int64_t cols, size_t *bytes) {
+    if (int e = ckks_plain_matmul_i8_workspace_size(rows, channels, cols, bytes)) return e;
+    if (cols > CKKS_PLAIN_MAX_COLS) return CKKS_EUNSUPPORTED;
+    *bytes += linear_rows_bytes(rows, cols);
+    return CKKS_OK;
+}
+extern "C" int ckks_plain_linear_i8(int type, const void *x, int64_t x_stride, const int8_t *w, int64_t w_stride,
+                                    const float *w_scale, const float *bias, int out_type, void *out,
+                                    int64_t out_stride, int64_t rows, int64_t channels, int64_t cols, void *ws,
+                                    size_t ws_bytes, void *stream) {
+    size_t need;
+    if (int e = ckks_plain_linear_i8_workspace_size(rows, channels, cols, &need)) return e;
+    if (rows == 0 || channels == 0) return CKKS_OK;
+    if (!type_ok(type) || rows >= (int64_t)1 << 31) return CKKS_EINVAL;
+    const size_t xb = span(rows, x_stride, cols, type_size(type));
+    if (int e = check_matrix(x, x_stride, cols, type_size(type))) return e;
+    if (!ws || ws_bytes < need) return CKKS_EWORKSPACE;
+    if (!at(ws, 16)) return CKKS_EALIGN;
+    // the product's own checks, before the quantiser runs
+    if (!type_ok(out_type)) return CKKS_EINVAL;
+    if (int e = check_matrix(out, out_stride, channels, type_size(out_type))) return e;
+    const size_t ob = span(rows, out_stride, channels, type_size(out_type));
+    const size_t wb = span(channels, w_stride, round_up(cols, CKKS_PLAIN_I8_ROW), 1);
+    if (overlap(out, ob, x, xb) || overlap(ws, need, x, xb) || overlap(ws, need, out, ob) || overlap(ws, need, w, wb) ||
+        overlap(ws, need, w_scale, channels * 4) || overlap(ws, need, bias, channels * 4))
+        return CKKS_EINVAL;
+    int8_t *q = (int8_t *)ws;
+    const int64_t stride = round_up(cols, CKKS_PLAIN_I8_ROW);
+    float *scale = (float *)(q + rows * stride);
+    char *rest = (char *)ws + linear_rows_bytes(rows, cols);
+    const size_t left = ws_bytes - linear_rows_bytes(rows, cols);
+    if (int e = check_matmul(q, stride, scale, w, w_stride, w_scale, bias, out_type, out, out_stride, rows, channels,
+                             cols, rest, left))
+        return e;
+    if (int e = ckks_plain_quantize_rows(type, x, x_stride, rows, cols, q, stride, scale, stream)) return e;
+    return ckks_plain_matmul_i8(q, stride, scale, w, w_stride, w_scale, bias, out_type, out, out_stride, rows, channels,
+                                cols, rest, left, stream);
 }

@@ -9,6 +9,7 @@ device, outputs and scratch come from torch's allocator.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from collections import namedtuple
 
 import torch
@@ -24,15 +25,44 @@ ResidualNormGrads = namedtuple("ResidualNormGrads",
                                "dx dy next_weight next_bias block_weight block_bias gate")
 
 
+_entry = {}
+
+
 def _call(name, device, *args):
     """One C call on `device` and its current stream."""
-    f = getattr(nat.lib(), name)
-    s = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        nat.check(f(*args, s), name)
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(nat.lib(), name)
+    index = device.index
+    if _current_device() == index:
+        code = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            nat.check(f(*args, s), name)
+            code = f(*args, _raw_stream(index))
+    if code:
+        raise nat.CkksError(code, name)
+
+
+# The addresses of the current device and stream without the objects around them, which take longer than a small
+# kernel does.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace(name, *sizes):
+    """Bytes of scratch that the C call of these sizes takes."""
+    out = C.c_size_t()
+    nat.check(getattr(nat.lib(), name)(*sizes, C.byref(out)), name)
+    return out.value
+
+
+def _scratch(nbytes, device):
+    """(tensor kept alive, address, size)"""
+    if not nbytes:
+        return None, None, 0
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), nbytes
 
 
 def _matrix(t, what, rows=None, cols=None, dtype=None, device=None):
@@ -199,8 +229,8 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
     need = C.c_size_t()
     nat.check(nat.lib().ckks_plain_norm_grad_workspace_size(C.byref(p), C.byref(need)),
               "ckks_plain_norm_grad_workspace_size")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=x.device)
-    _call("ckks_plain_residual_norm_grad", x.device, C.byref(p), C.byref(g), ws.data_ptr(), need.value)
+    _keep, ws, size = _scratch(need.value, x.device)
+    _call("ckks_plain_residual_norm_grad", x.device, C.byref(p), C.byref(g), ws, size)
     return r
 
 
@@ -213,31 +243,44 @@ def quantize_rows(x) -> Int8Rows:
     return r
 
 
+def _product(cols, device, w, bias, dtype):
+    """Checks what both products check; the address of the bias."""
+    if not isinstance(w, Int8Rows):
+        raise ValueError("w: expected Int8Rows")
+    if cols != w.cols or device != w.q.device:
+        raise ValueError(f"{cols} columns on {device}, w has {w.cols} on {w.q.device}")
+    if dtype not in TYPES:
+        raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+    return _vector(bias, "bias", w.rows, torch.float32, device)
+
+
 def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torch.Tensor:
     """out[t, c] = a.scale[t] w.scale[c] sum_k a.q[t, k] w.q[c, k] + bias[c] (ckks_plain_matmul_i8),
     sums exact in 32-bit integers.  bias: float32 [channels]."""
-    if not isinstance(a, Int8Rows) or not isinstance(w, Int8Rows):
-        raise ValueError("expected Int8Rows")
-    if a.cols != w.cols or a.q.device != w.q.device:
-        raise ValueError(f"a has {a.cols} columns on {a.q.device}, w {w.cols} on {w.q.device}")
-    if dtype not in TYPES:
-        raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
-    M, N, dev = a.rows, w.rows, a.q.device
-    bp = _vector(bias, "bias", N, torch.float32, dev)
+    if not isinstance(a, Int8Rows):
+        raise ValueError("a: expected Int8Rows")
+    dev = a.q.device
+    bp = _product(a.cols, dev, w, bias, dtype)
+    M, N = a.rows, w.rows
     out = torch.empty((M, N), dtype=dtype, device=dev)
-    need = C.c_size_t()
-    nat.check(nat.lib().ckks_plain_matmul_i8_workspace_size(M, N, a.cols, C.byref(need)),
-              "ckks_plain_matmul_i8_workspace_size")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), max(_stride(a.q), a.q.shape[1]), a.scale.data_ptr(),
-          w.q.data_ptr(), _stride(w.q), w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols,
-          None if ws is None else ws.data_ptr(), need.value)
+    _keep, ws, size = _scratch(_workspace("ckks_plain_matmul_i8_workspace_size", M, N, a.cols), dev)
+    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), _stride(a.q), a.scale.data_ptr(), w.q.data_ptr(), _stride(w.q),
+          w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols, ws, size)
     return out
 
 
 def linear_i8(x, w: Int8Rows, bias=None, dtype=None) -> torch.Tensor:
-    """matmul_i8 of x quantised row by row; dtype defaults to that of x."""
-    return matmul_i8(quantize_rows(x), w, bias, x.dtype if dtype is None else dtype)
+    """matmul_i8 of x [T, D] quantised row by row (ckks_plain_linear_i8); dtype defaults to that of x."""
+    _matrix(x, "x")
+    dtype = x.dtype if dtype is None else dtype
+    dev, (M, K) = x.device, x.shape
+    bp = _product(K, dev, w, bias, dtype)
+    N = w.rows
+    out = torch.empty((M, N), dtype=dtype, device=dev)
+    _keep, ws, size = _scratch(_workspace("ckks_plain_linear_i8_workspace_size", M, N, K), dev)
+    _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), _stride(x), w.q.data_ptr(), _stride(w.q),
+          w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, K, ws, size)
+    return out
 
 
 def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allowed=None):
@@ -255,13 +298,11 @@ def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allo
         _matrix(allowed, "allowed", B, V, torch.bool, dev)
     token = torch.empty(B, dtype=torch.int64, device=dev)
     logprob = torch.empty(B, dtype=torch.float32, device=dev)
-    need = C.c_size_t()
-    nat.check(nat.lib().ckks_plain_sample_workspace_size(B, V, C.byref(need)), "ckks_plain_sample_workspace_size")
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+    _keep, ws, size = _scratch(_workspace("ckks_plain_sample_workspace_size", B, V), dev)
     _call("ckks_plain_sample", dev, _type(logits, "logits"), logits.data_ptr(), _stride(logits), gumbel.data_ptr(),
           _stride(gumbel), _vector(temperature, "temperature", B, torch.float32, dev),
           _vector(top_k, "top_k", B, torch.int32, dev), _vector(top_p, "top_p", B, torch.float32, dev),
           _vector(min_p, "min_p", B, torch.float32, dev), None if allowed is None else allowed.data_ptr(),
           0 if allowed is None else _stride(allowed), B, V, token.data_ptr(), logprob.data_ptr(),
-          None if ws is None else ws.data_ptr(), need.value)
+          ws, size)
     return token, logprob
