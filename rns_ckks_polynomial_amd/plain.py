@@ -68,11 +68,12 @@ def _scratch(nbytes, device):
 def _matrix(t, what, rows=None, cols=None, dtype=None, device=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: expected a matrix with unit column stride")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+        raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(shape)}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
@@ -83,11 +84,16 @@ def _vector(t, what, n, dtype, device):
     """Address of a contiguous vector of n elements (None: null)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what}: expected {dtype} on {device}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous vector of {n}, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _like(x):
+    """A new contiguous matrix of the shape and type of x."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _stride(t):
@@ -165,7 +171,7 @@ def _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, e
 
 def _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind):
     p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
-    h, u = torch.empty(x.shape, dtype=x.dtype, device=x.device), torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    h, u = _like(x), _like(x)
     D = x.shape[1]
     _call("ckks_plain_residual_norm", x.device, C.byref(p), h.data_ptr(), D, u.data_ptr(), D)
     return h, u
@@ -195,8 +201,9 @@ def residual_norm(x, y, next_weight, next_bias=None, block_weight=None, block_bi
     u = next_weight norm(h) + next_bias.  x, y [T, D]; weights and biases [D]; gate [D] or [G, D]
     (a row for T / G tokens each); one type for all.  Differentiable through torch.autograd (gradients of weights are
     summed in 32 bits, then rounded to their type)."""
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in
-                                       (x, y, next_weight, next_bias, block_weight, block_bias, gate)):
+    wants = lambda t: t is not None and t.requires_grad  # noqa: E731
+    if torch.is_grad_enabled() and (x.requires_grad or y.requires_grad or next_weight.requires_grad or wants(next_bias)
+                                    or wants(block_weight) or wants(block_bias) or wants(gate)):
         return _ResidualNorm.apply(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
     return _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
 
@@ -205,7 +212,7 @@ def residual_norm_i8(x, y, next_weight, next_bias=None, block_weight=None, block
                      scale: float = 1.0, eps: float = 1e-6, kind: str = "rms"):
     """(h, rows): residual_norm with u as 8-bit rows, quantised before any other rounding."""
     p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
-    h, u = torch.empty(x.shape, dtype=x.dtype, device=x.device), Int8Rows.empty(*x.shape, x.device)
+    h, u = _like(x), Int8Rows.empty(*x.shape, x.device)
     _call("ckks_plain_residual_norm_i8", x.device, C.byref(p), h.data_ptr(), x.shape[1], u.q.data_ptr(),
           u.q.shape[1], u.scale.data_ptr())
     return h, u
@@ -220,9 +227,8 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
     _matrix(dh, "dh", T, D, x.dtype, x.device)
     _matrix(du, "du", T, D, x.dtype, x.device)
     new = lambda v: None if v is None else torch.empty(v.shape, dtype=torch.float32, device=x.device)  # noqa: E731
-    r = ResidualNormGrads(torch.empty((T, D), dtype=x.dtype, device=x.device),
-                          torch.empty((T, D), dtype=x.dtype, device=x.device), new(next_weight), new(next_bias),
-                          new(block_weight), new(block_bias), new(gate))
+    r = ResidualNormGrads(_like(x), _like(x), new(next_weight), new(next_bias), new(block_weight), new(block_bias),
+                          new(gate))
     at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
     g = nat.PlainNormGrads(dh.data_ptr(), du.data_ptr(), _stride(dh), _stride(du), r.dx.data_ptr(), r.dy.data_ptr(),
                            D, D, at(r.next_weight), at(r.next_bias), at(r.block_weight), at(r.block_bias), at(r.gate))
