@@ -19,99 +19,116 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 // to nearest, ties to even
 template <typename T> __device__ __forceinline__ T from_f32(float v) { return (T)v; }
 
-template <typename T> constexpr int VEC = 16 / sizeof(T);  // elements of a 16-byte access
-template <typename T> struct VecOf { typedef T type __attribute__((ext_vector_type(16 / sizeof(T)))); };
+// 16 bytes of elements at any element's address (the unaligned access mode of this GPU: a load that
+// straddles a cache line costs one line more, and the neighbouring lanes use it too).
+template <typename T> constexpr int VEC = 16 / sizeof(T);
+template <typename T> struct VecOf {
+    typedef T type __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
+};
 
-// A row of `cols` elements over NT threads, E elements a thread.  VECTOR: 16-byte pieces dealt out
-// in turn (rows have to start at multiples of 16 bytes); else single elements in turn.  Elements
-// past the end read as 0 and are not written.
-template <typename T, int NT, int E, bool VECTOR> struct Row {
-    static constexpr int V = VECTOR ? VEC<T> : 1;
+// A row of `cols` elements over NT threads, E elements a thread in 16-byte pieces dealt out in turn.
+// Elements past the end read as 0 and are not written.
+template <typename T, int NT, int E> struct Row {
+    static constexpr int V = VEC<T>;
+    typedef typename VecOf<T>::type Vec;
     static_assert(E % V == 0, "whole pieces");
     // column of this thread's element i
     static __device__ __forceinline__ int col(int i, int t) { return ((i / V) * NT + t) * V + i % V; }
-    static __device__ __forceinline__ void load(const T *__restrict__ p, int cols, int t, float (&v)[E]) {
-        if constexpr (VECTOR) {
+    struct Raw {
+        Vec v[E / V];
+    };
+    static __device__ __forceinline__ void fetch(const T *__restrict__ p, int cols, int t, Raw &r) {
 #pragma unroll
-            for (int i = 0; i < E; i += V) {
-                const int c = col(i, t);
-                if (c + V <= cols) {
-                    const typename VecOf<T>::type w = *(const typename VecOf<T>::type *)(p + c);
+        for (int i = 0; i < E; i += V) {
+            const int c = col(i, t);
+            if (c + V <= cols) {
+                r.v[i / V] = *(const Vec *)(p + c);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < V; j++) v[i + j] = to_f32(w[j]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < V; j++) v[i + j] = c + j < cols ? to_f32(p[c + j]) : 0.0f;
-                }
+                for (int j = 0; j < V; j++) r.v[i / V][j] = c + j < cols ? p[c + j] : (T)0.0f;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; i++) v[i] = col(i, t) < cols ? to_f32(p[col(i, t)]) : 0.0f;
         }
     }
+    static __device__ __forceinline__ void widen(const Raw &r, float (&v)[E]) {
+#pragma unroll
+        for (int i = 0; i < E; i++) v[i] = to_f32(r.v[i / V][i % V]);
+    }
+    static __device__ __forceinline__ void load(const T *__restrict__ p, int cols, int t, float (&v)[E]) {
+        Raw r;
+        fetch(p, cols, t, r);
+        widen(r, v);
+    }
     static __device__ __forceinline__ void store(T *__restrict__ p, int cols, int t, const float (&v)[E]) {
-        if constexpr (VECTOR) {
 #pragma unroll
-            for (int i = 0; i < E; i += V) {
-                const int c = col(i, t);
-                if (c + V <= cols) {
-                    typename VecOf<T>::type w;
+        for (int i = 0; i < E; i += V) {
+            const int c = col(i, t);
+            if (c + V <= cols) {
+                Vec w;
 #pragma unroll
-                    for (int j = 0; j < V; j++) w[j] = from_f32<T>(v[i + j]);
-                    *(typename VecOf<T>::type *)(p + c) = w;
-                } else {
+                for (int j = 0; j < V; j++) w[j] = from_f32<T>(v[i + j]);
+                *(Vec *)(p + c) = w;
+            } else {
 #pragma unroll
-                    for (int j = 0; j < V; j++)
-                        if (c + j < cols) p[c + j] = from_f32<T>(v[i + j]);
-                }
+                for (int j = 0; j < V; j++)
+                    if (c + j < cols) p[c + j] = from_f32<T>(v[i + j]);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < E; i++)
-                if (col(i, t) < cols) p[col(i, t)] = from_f32<T>(v[i]);
         }
     }
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+// The neighbour's value that a move between lanes brings (`none` where there is no neighbour).
+template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t none, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) {
-        const uint32_t o = __shfl_xor(v, m);
-        v = v > o ? v : o;
-    }
-    return v;
+template <int CTRL, int ROWS> __device__ __forceinline__ float moved(float none, float v) {
+    return __uint_as_float(moved<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
 }
+template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t none, uint64_t v) {
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(none >> 32), (uint32_t)(v >> 32)) << 32 |
+           moved<CTRL, ROWS>((uint32_t)none, (uint32_t)v);
+}
+__device__ __forceinline__ uint32_t lane(uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); }
+__device__ __forceinline__ float lane(float v, int l) { return __uint_as_float(lane(__float_as_uint(v), l)); }
+__device__ __forceinline__ uint64_t lane(uint64_t v, int l) {
+    return (uint64_t)lane((uint32_t)(v >> 32), l) << 32 | lane((uint32_t)v, l);
+}
+// Inclusive scans over rows of 16 lanes and over the wave, in a fixed order (moves within the
+// register file: an exchange through LDS takes ten times as long).
+template <typename V, typename F> __device__ __forceinline__ V scan16(V v, V none, F f) {
+    v = f(moved<0x111, 0xf>(none, v), v);
+    v = f(moved<0x112, 0xf>(none, v), v);
+    v = f(moved<0x114, 0xf>(none, v), v);
+    return f(moved<0x118, 0xf>(none, v), v);
+}
+template <typename V, typename F> __device__ __forceinline__ V scan64(V v, V none, F f) {
+    v = scan16(v, none, f);
+    v = f(moved<0x142, 0xa>(none, v), v);
+    return f(moved<0x143, 0xc>(none, v), v);
+}
+struct Larger {
+    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a > b ? a : b; }
+};
+struct Sum {
+    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+};
 
 // Sum / largest over the NT threads of a row; every thread gets it.  `buf` holds a slot for each
 // wave; with NT > 64 the caller gives reductions in a row different ones (two in turn: a thread
 // that writes the first again has passed the second's barrier, so all have read the first).
-template <int NT> __device__ __forceinline__ float row_sum(float v, float *buf) {
-    v = wave_sum(v);
+template <int NT, typename V, typename F> __device__ __forceinline__ V row_all(V v, V *buf, F f) {
+    v = lane(scan64(v, V(0), f), 63);
     if constexpr (NT > 64) {
         if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0;
+        v = buf[0];
 #pragma unroll
-        for (int w = 0; w < NT / 64; w++) v += buf[w];
+        for (int w = 1; w < NT / 64; w++) v = f(v, buf[w]);
     }
     return v;
 }
+template <int NT> __device__ __forceinline__ float row_sum(float v, float *buf) { return row_all<NT>(v, buf, Sum{}); }
 template <int NT> __device__ __forceinline__ uint32_t row_max(uint32_t v, float *buf) {
-    v = wave_max(v);
-    if constexpr (NT > 64) {
-        uint32_t *b = (uint32_t *)buf;
-        if ((threadIdx.x & 63) == 0) b[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0;
-#pragma unroll
-        for (int w = 0; w < NT / 64; w++) v = v > b[w] ? v : b[w];
-    }
-    return v;
+    return row_all<NT>(v, (uint32_t *)buf, Larger{});
 }
 
 // The row's 8-bit form (ckks_plain_quantize_rows): scale from the largest |v| bit pattern (as
@@ -131,17 +148,15 @@ __device__ __forceinline__ void store_i8(int8_t *__restrict__ q, int padded, int
     for (int i = 0; i < E; i += V) {
         const int c = R::col(i, t);
         if (c >= padded) continue;  // padded is a multiple of V: v is 0 from the last column on
-        if constexpr (V == 1) {
-            q[c] = (int8_t)i8_of(v[i], s);
-        } else {
+        typedef uint32_t Words __attribute__((ext_vector_type(V / 4)));
+        Words w;
 #pragma unroll
-            for (int j = 0; j < V; j += 4) {
-                uint32_t w = 0;
+        for (int j = 0; j < V; j += 4) {
+            w[j / 4] = 0;
 #pragma unroll
-                for (int b = 0; b < 4; b++) w |= (uint32_t)(uint8_t)i8_of(v[i + j + b], s) << (8 * b);
-                *(uint32_t *)(q + c + j) = w;
-            }
+            for (int b = 0; b < 4; b++) w[j / 4] |= (uint32_t)(uint8_t)i8_of(v[i + j + b], s) << (8 * b);
         }
+        *(Words *)(q + c) = w;
     }
 }
 

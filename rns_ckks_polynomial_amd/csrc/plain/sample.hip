@@ -30,42 +30,6 @@ constexpr int NT = 1024, WAVES = NT / 64, BINS = 2048, LIST = 4096, HELD = LIST 
 constexpr int FINE = 8192, EACH = FINE / NT;  // counted bins, of a thread
 constexpr uint64_t NONE = ~(uint64_t)0;
 
-// The neighbour's value that a cross-lane move brings (`none` where there is no neighbour).
-template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t none, uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
-}
-template <int CTRL, int ROWS> __device__ __forceinline__ float moved(float none, float v) {
-    return __uint_as_float(moved<CTRL, ROWS>(__float_as_uint(none), __float_as_uint(v)));
-}
-template <int CTRL, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t none, uint64_t v) {
-    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(none >> 32), (uint32_t)(v >> 32)) << 32 |
-           moved<CTRL, ROWS>((uint32_t)none, (uint32_t)v);
-}
-__device__ __forceinline__ uint32_t lane(uint32_t v, int l) { return (uint32_t)__builtin_amdgcn_readlane((int)v, l); }
-__device__ __forceinline__ float lane(float v, int l) { return __uint_as_float(lane(__float_as_uint(v), l)); }
-__device__ __forceinline__ uint64_t lane(uint64_t v, int l) {
-    return (uint64_t)lane((uint32_t)(v >> 32), l) << 32 | lane((uint32_t)v, l);
-}
-// Inclusive scans over rows of 16 lanes and over the wave, in a fixed order (moves within the
-// register file: an exchange through LDS takes ten times as long).
-template <typename V, typename F> __device__ __forceinline__ V scan16(V v, V none, F f) {
-    v = f(moved<0x111, 0xf>(none, v), v);
-    v = f(moved<0x112, 0xf>(none, v), v);
-    v = f(moved<0x114, 0xf>(none, v), v);
-    return f(moved<0x118, 0xf>(none, v), v);
-}
-template <typename V, typename F> __device__ __forceinline__ V scan64(V v, V none, F f) {
-    v = scan16(v, none, f);
-    v = f(moved<0x142, 0xa>(none, v), v);
-    return f(moved<0x143, 0xc>(none, v), v);
-}
-struct Larger {
-    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a > b ? a : b; }
-};
-struct Sum {
-    template <typename V> __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
-};
-
 struct SampleShared {
     uint64_t slot[8][WAVES];
     uint64_t pick[3];
