@@ -96,11 +96,13 @@ template <int TN, int TM> __device__ __forceinline__ void mfma_done(v4i (&acc)[T
     for_all<TN * TM>([&](auto at) { not_before(acc[decltype(at)::value / TM][decltype(at)::value % TM]); });
 }
 
-template <typename T, int BM, int BN, int STAGES>
-__global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(MatmulArgs m, T *out, TileOrder order) {
-    constexpr int TN = BN / 32, TM = BM / 32, TILES = TN * TM;  // 16 x 16 tiles of a wave
-    constexpr int LOADS_W = BN / 64, LOADS = LOADS_W + BM / 64;  // of a wave, per step
-    constexpr int STAGE = (BN + BM) * STEP;
+template <typename T, int BM, int BN, int SUB, int STAGES>
+__global__ __launch_bounds__(256, STAGES * SUB * (BM + BN) * STEP > 80 * 1024 ? 1 : 2) void k_matmul_i8_tile(
+    MatmulArgs m, T *out, TileOrder order) {
+    constexpr int TN = BN / 32, TM = BM / 32, TILES = TN * TM * SUB;  // 16 x 16 tiles of a wave, and products of a stage
+    constexpr int GROUPS = (BN + BM) / 16, LOADS = GROUPS * SUB / 4;  // loads of 16 rows a step; of a wave a stage
+    constexpr int PLACE = (BN + BM) * STEP, STAGE = PLACE * SUB, READS = (TN + TM) * SUB;
+    static_assert(GROUPS * SUB % 4 == 0 && TM % 2 == 0, "whole shares");
     // the epilogue's: 32 tokens x a wave's channels of sums, rows 16 bytes apart in the banks
     constexpr int SUMS = BN / 2 + 4;
     static_assert(4 * 32 * SUMS * 4 <= STAGES * STAGE, "the epilogue fits");
@@ -110,68 +112,74 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
     const int t0 = tile_t * BM, c0 = tile_c * BN;
     const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int8_t *wp = m.w + (int64_t)c0 * m.w_stride, *ap = m.a + (int64_t)t0 * m.a_stride;
-    // lane's row and piece in a load of 16 rows; rows past the end read the last one (not stored)
+    const int steps = m.padded / STEP, stages = (steps + SUB - 1) / SUB;
+    // A wave's load j of a stage is number 4 j + wave: steps in turn, the weights' rows first.  The
+    // lane's row and piece in it; rows past the end read the last one (not stored).
     uint32_t off[LOADS];
-#pragma unroll
-    for (int j = 0; j < LOADS; j++) {
-        const bool weights = j < LOADS_W;
-        const int r = ((weights ? j : j - LOADS_W) * 4 + wave) * 16 + l / 4;
-        const int left = weights ? m.channels - 1 - c0 : m.rows - 1 - t0;
-        off[j] = (uint32_t)((r < left ? r : left) * (weights ? m.w_stride : m.a_stride)) + ((l % 4) ^ turn(r)) * 16;
-    }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)&lds[0] + wave * 1024;
-    // load j of this wave's share of step s, to place `place`
-    auto fill_one = [&](int s, int place, int j) {
-        const uint32_t at = __builtin_amdgcn_readfirstlane(lds0 + place * STAGE);
-        if (j < LOADS_W)
-            load_to_lds(wp + (int64_t)s * STEP, off[j], at + j * 4096);
-        else
-            load_to_lds(ap + (int64_t)s * STEP, off[j], at + BN * STEP + (j - LOADS_W) * 4096);
+    for_all<LOADS>([&](auto at) {
+        constexpr int j = decltype(at)::value;
+        const int g = (4 * j + wave) % GROUPS, r = g * 16 + l / 4;
+        const bool weights = g < BN / 16;
+        const int row = weights ? r : r - BN, left = weights ? m.channels - 1 - c0 : m.rows - 1 - t0;
+        off[j] = (uint32_t)((row < left ? row : left) * (weights ? m.w_stride : m.a_stride)) + ((l % 4) ^ turn(r)) * 16;
+    });
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)&lds[0];
+    // load j of this wave's share of stage s, to place `place`
+    auto fill_one = [&](int s, int place, auto at) {
+        constexpr int j = decltype(at)::value;
+        // with groups in fours, which step and operand it is does not depend on the wave
+        constexpr bool FOURS = BN / 16 % 4 == 0 && GROUPS % 4 == 0;
+        const int q = 4 * j + wave, sub = FOURS ? 4 * j / GROUPS : q / GROUPS;
+        const int g = FOURS ? 4 * j % GROUPS + wave : q % GROUPS;
+        const bool weights = FOURS ? 4 * j % GROUPS < BN / 16 : g < BN / 16;
+        const int step = s * SUB + sub;  // past the last step: the last one again, which nobody multiplies
+        const int64_t k = (int64_t)(SUB == 1 || step < steps ? step : steps - 1) * STEP;
+        load_to_lds((weights ? wp : ap) + k, off[j],
+                    __builtin_amdgcn_readfirstlane(lds0 + place * STAGE + sub * PLACE + g * 1024));
     };
-    const int steps = m.padded / STEP;
     // wave's quarter; lane's row in a 16-row tile, its 16-byte piece: l / 16
     const int row_w = (wave & 1) * (BN / 2) + l % 16, row_a = BN + (wave >> 1) * (BM / 2) + l % 16;
-    v4i fw[2][TN], fa[2][TM];
+    v4i fw[2][SUB][TN], fa[2][SUB][TM];
     v4i acc[TN][TM] = {};
-    // read n of step s into set h: the weight tiles' pieces, then the tokens'
-    auto read_one = [&](int s, int h, int n) {
-        const int8_t *at = lds + s % STAGES * STAGE + ((l / 16) ^ turn(l)) * 16;
-        if (n < TN)
-            fw[h][n] = *(const v4i *)(at + (row_w + 16 * n) * STEP);
+    // read n of stage s into set h: for each step the weight tiles' pieces, then the tokens'
+    auto read_one = [&](int s, int h, auto at) {
+        constexpr int n = decltype(at)::value, sub = n / (TN + TM), i = n % (TN + TM);
+        const int8_t *from = lds + s % STAGES * STAGE + sub * PLACE + ((l / 16) ^ turn(l)) * 16;
+        if constexpr (i < TN)
+            fw[h][sub][i] = *(const v4i *)(from + (row_w + 16 * i) * STEP);
         else
-            fa[h][n - TN] = *(const v4i *)(at + (row_a + 16 * (n - TN)) * STEP);
+            fa[h][sub][i - TN] = *(const v4i *)(from + (row_a + 16 * (i - TN)) * STEP);
     };
-    // One step, from register set h.  First the next step has to have arrived and the waves to have
-    // read this one, whose place in LDS then takes the step STAGES later.  Reads and loads are
+    // One stage, from register set h.  First the next stage has to have arrived and the waves to have
+    // read this one, whose place in LDS then takes the stage STAGES later.  Reads and loads are
     // spread over the products: a wave that issues them together waits for LDS to take them, and
-    // the matrix cores with it.  The last steps load the last one again and read stale ones, which
-    // nobody uses: so every step is the same code, and the accumulators never move.
-    auto step = [&](int s, auto set) {
+    // the matrix cores with it.  The last stages load the last one again and read stale ones, which
+    // nobody uses: so every stage is the same code, and the accumulators never move.
+    auto stage = [&](int s, auto set) {
         constexpr int h = decltype(set)::value, HALF = TILES / 2;
         tile_wait<(STAGES - 2) * LOADS>();
-        const int next = s + STAGES < steps ? s + STAGES : steps - 1;
+        const int next = s + STAGES < stages ? s + STAGES : stages - 1;
         for_all<TILES>([&](auto at) {
-            constexpr int n = decltype(at)::value, i = n / TM, j = n % TM;
-            mfma_i8(acc[i][j], fw[h][i], fa[h][j]);
-            for_all<TN + TM>([&](auto r) {
-                if constexpr (n == decltype(r)::value * HALF / (TN + TM)) read_one(s + 1, h ^ 1, decltype(r)::value);
+            constexpr int n = decltype(at)::value, sub = n / (TN * TM), i = n % (TN * TM) / TM, j = n % TM;
+            if (SUB == 1 || s * SUB + sub < steps) mfma_i8(acc[i][j], fw[h][sub][i], fa[h][sub][j]);
+            for_all<READS>([&](auto r) {
+                if constexpr (n == decltype(r)::value * HALF / READS) read_one(s + 1, h ^ 1, r);
             });
             for_all<LOADS>([&](auto r) {
-                constexpr int load = decltype(r)::value;
-                if constexpr (n == HALF + load * HALF / LOADS) fill_one(next, s % STAGES, load);
+                if constexpr (n == HALF + decltype(r)::value * HALF / LOADS) fill_one(next, s % STAGES, r);
             });
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-#pragma unroll
-    for (int s = 0; s < STAGES; s++)
-#pragma unroll
-        for (int j = 0; j < LOADS; j++) fill_one(s < steps ? s : steps - 1, s, j);
+    for_all<STAGES>([&](auto s) {
+        constexpr int at = decltype(s)::value;
+        for_all<LOADS>([&](auto j) { fill_one(at < stages ? at : stages - 1, at, j); });
+    });
     tile_wait<(STAGES - 1) * LOADS>();
-    for_all<TN + TM>([&](auto n) { read_one(0, 0, decltype(n)::value); });
-    for (int s = 0; s < steps; s += 2) {  // the number of steps is even
-        step(s, Int<0>{});
-        step(s + 1, Int<1>{});
+    for_all<READS>([&](auto n) { read_one(0, 0, n); });
+    for (int s = 0; s < stages; s += 2) {  // one more than there are, if their number is odd: it multiplies nothing
+        stage(s, Int<0>{});
+        if (SUB == 1 || s + 1 < stages) stage(s + 1, Int<1>{});
     }
     // Epilogue: 32 tokens at a time through LDS (a place for each wave), so that a token's channels
     // leave in whole 16-byte pieces of neighbouring lanes.  A lane holds channels
@@ -211,77 +219,57 @@ __global__ __launch_bounds__(256, BM == 256 ? 1 : 2) void k_matmul_i8_tile(Matmu
 
 // ------------------------------------------------------------------ few tokens
 //
-// With at most 64 tokens the weights are all that has to move.  A wave takes 16 NC channels and all
-// tokens and reads both straight into the operand registers: lane l holds 16 bytes of row l % 16 at
-// 16 (l / 16) of each 64, so two loads use a row's 128 bytes; the tokens come from L2 each time.  The
-// waves of a workgroup share the channels and split the contraction (in turn, 128 bytes each); their
-// sums meet in LDS.
-template <typename T, int MT, int NC, int U>
-__global__ __launch_bounds__(512) void k_matmul_i8_stream(MatmulArgs m, T *out) {
-    extern __shared__ __attribute__((aligned(16))) int sums[];  // [wave][MT * NC][64][4]
+// For a few tokens the weights are all that has to move.  A wave takes 16 channels and all tokens
+// and reads both straight into the operand registers: lane l holds 16 bytes of row l % 16 at
+// 16 (l / 16) of each 64, so two loads use a row's 128 bytes; the tokens come from L2.  The waves of
+// a workgroup share the channels and split the contraction (in turn, 128 bytes each); their sums
+// meet in LDS.  1 x 32768 x 2048: 14.2 us, 4.7 TB/s of weights (a copy of 2 GiB moves 4.8).
+constexpr int FEW = 8;       // tokens: 8 x 8192 x 8192 takes 16.6 us here and 16.3 in tiles, 1 14.2 and 16.5
+constexpr int BATCH = 4;     // pieces of 128 bytes in flight
+template <typename T> __global__ __launch_bounds__(512) void k_matmul_i8_few(MatmulArgs m, T *out) {
+    __shared__ v4i sums[8][64];
     const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6, pairs = m.padded / 128, c0 = blockIdx.x * 16 * NC;
-    const int8_t *wp[NC], *ap[MT];
-#pragma unroll
-    for (int i = 0; i < NC; i++) {
-        const int c = c0 + 16 * i + l % 16;
-        wp[i] = m.w + (int64_t)(c < m.channels ? c : m.channels - 1) * m.w_stride + l / 16 * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < MT; j++) {
-        const int t = 16 * j + l % 16;
-        ap[j] = m.a + (int64_t)(t < m.rows ? t : m.rows - 1) * m.a_stride + l / 16 * 16;
-    }
-    v4i acc[NC][MT] = {};
-    // n pairs from p on, all loads in front of the products
+    const int waves = blockDim.x >> 6, pieces = m.padded / 128, c0 = blockIdx.x * 16;
+    const int cw = c0 + l % 16, tw = l % 16;
+    const int8_t *wp = m.w + (int64_t)(cw < m.channels ? cw : m.channels - 1) * m.w_stride + l / 16 * 16;
+    const int8_t *ap = m.a + (int64_t)(tw < m.rows ? tw : m.rows - 1) * m.a_stride + l / 16 * 16;
+    v4i acc = {0, 0, 0, 0};
+    // n pieces from p on, all loads in front of the products
     auto take = [&](int p, auto count) {
         constexpr int n = decltype(count)::value;
-        v4i w[n][2][NC], a[n][2][MT];
+        v4i w[n][2], a[n][2];
 #pragma unroll
         for (int u = 0; u < n; u++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const int64_t at = (int64_t)(p + u * waves) * 128 + h * 64;
-#pragma unroll
-                for (int i = 0; i < NC; i++) w[u][h][i] = __builtin_nontemporal_load((const v4i *)(wp[i] + at));
-#pragma unroll
-                for (int j = 0; j < MT; j++) a[u][h][j] = *(const v4i *)(ap[j] + at);
+                w[u][h] = __builtin_nontemporal_load((const v4i *)(wp + at));  // read once
+                a[u][h] = *(const v4i *)(ap + at);
             }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < n; u++)
 #pragma unroll
-            for (int h = 0; h < 2; h++)
-#pragma unroll
-                for (int i = 0; i < NC; i++)
-#pragma unroll
-                    for (int j = 0; j < MT; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][h][i], a[u][h][j], acc[i][j], 0, 0, 0);
+            for (int h = 0; h < 2; h++) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][h], a[u][h], acc, 0, 0, 0);
     };
     int p = wave;
-    for (; p + (U - 1) * waves < pairs; p += U * waves) take(p, Int<U>{});
-    for (; p < pairs; p += waves) take(p, Int<1>{});
-    v4i *mine = (v4i *)sums + wave * MT * NC * 64 + l;
-#pragma unroll
-    for (int i = 0; i < NC; i++)
-#pragma unroll
-        for (int j = 0; j < MT; j++) mine[(i * MT + j) * 64] = acc[i][j];
+    for (; p + (BATCH - 1) * waves < pieces; p += BATCH * waves) take(p, Int<BATCH>{});
+    for (; p < pieces; p += waves) take(p, Int<1>{});
+    sums[wave][l] = acc;
     __syncthreads();
-    // each wave adds up its share of the tiles; a lane has channels 4 (l / 16) + 0..3 of token l % 16
-    for (int tile = wave; tile < MT * NC; tile += waves) {
-        v4i v = {0, 0, 0, 0};
-        for (int k = 0; k < waves; k++) v += ((const v4i *)sums)[(k * MT * NC + tile) * 64 + l];
-        const int t = tile % MT * 16 + l % 16, c = c0 + tile / MT * 16 + l / 16 * 4;
-        if (t >= m.rows || c >= m.channels) continue;
-        const int s[4] = {v[0], v[1], v[2], v[3]};
-        float ws[4], bias[4];
+    if (wave) return;
+    for (int k = 1; k < waves; k++) acc += sums[k][l];
+    // a lane has channels 4 (l / 16) + 0..3 of token l % 16
+    const int t = l % 16, c = c0 + l / 16 * 4;
+    if (t >= m.rows || c >= m.channels) return;
+    const int s[4] = {acc[0], acc[1], acc[2], acc[3]};
+    float ws[4], bias[4];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
-            bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
-        }
-        store_sums<T, 4>(m, out, t, c, m.a_scale[t], s, ws, bias);
+    for (int i = 0; i < 4; i++) {
+        ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
+        bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
     }
+    store_sums<T, 4>(m, out, t, c, m.a_scale[t], s, ws, bias);
 }
 
 }  // namespace ckks_plain
@@ -338,30 +326,30 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
             return TileOrder{(int)((rows + bm - 1) / bm), (int)((channels + bn - 1) / bn), 8};
         };
         const hipStream_t st = (hipStream_t)stream;
-        if (rows <= 64) {
-            auto few = [&](auto mt, auto nc, auto u) {
-                constexpr int MT = decltype(mt)::value, NC = decltype(nc)::value;
-                const int groups = (int)((channels + 16 * NC - 1) / (16 * NC));
-                int waves = 8;
-                while (waves > 1 && (groups * waves > 8192 || padded / 128 < 4 * waves)) waves /= 2;
-                k_matmul_i8_stream<T, MT, NC, decltype(u)::value>
-                    <<<dim3(groups), 64 * waves, waves * MT * NC * 1024, st>>>(m, (T *)out);
-            };
-            if (rows <= 16) few(Int<1>{}, Int<1>{}, Int<4>{});
-            else if (rows <= 32) few(Int<2>{}, Int<2>{}, Int<4>{});
-            else few(Int<4>{}, Int<2>{}, Int<4>{});
+        if (rows <= FEW) {
+            // up to eight waves share channels, while that does not make more than 32 a compute unit
+            // and each has a batch of pieces
+            const int groups = (int)((channels + 15) / 16);
+            int waves = 8;
+            while (waves > 1 && (groups * waves > 8192 || padded / 128 < BATCH * waves)) waves /= 2;
+            k_matmul_i8_few<T><<<dim3(groups), 64 * waves, 0, st>>>(m, (T *)out);
             return launched();
         }
-        auto tile = [&](auto bm, auto bn, auto stages) {
+        auto tile = [&](auto bm, auto bn, auto sub, auto stages) {
             constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
             const TileOrder o = tiles(BM, BN);
-            k_matmul_i8_tile<T, BM, BN, decltype(stages)::value><<<dim3(o.tokens * o.channels), 256, 0, st>>>(m, (T *)out, o);
+            k_matmul_i8_tile<T, BM, BN, decltype(sub)::value, decltype(stages)::value>
+                <<<dim3(o.tokens * o.channels), 256, 0, st>>>(m, (T *)out, o);
         };
         auto count = [&](int bm, int bn) { return ((rows + bm - 1) / bm) * ((channels + bn - 1) / bn); };
-        if (count(256, 256) >= 192) tile(Int<256>{}, Int<256>{}, Int<4>{});
-        else if (count(128, 128) >= 256) tile(Int<128>{}, Int<128>{}, Int<4>{});
-        else if (count(128, 64) >= 256) tile(Int<128>{}, Int<64>{}, Int<4>{});
-        else tile(Int<64>{}, Int<64>{}, Int<16>{});
+        // The largest tile that fills three quarters of the 256 compute units; under that, smaller ones
+        // have more of them read the weights (128 x 8192 x 8192: 64 x 64 tiles 29 us, 128 x 128 51 us),
+        // and four 64-byte steps between barriers keep their short steps from waiting for each other.
+        if (count(256, 256) >= 192) tile(Int<256>{}, Int<256>{}, Int<1>{}, Int<4>{});
+        else if (count(128, 128) >= 256) tile(Int<128>{}, Int<128>{}, Int<1>{}, Int<4>{});
+        else if (count(128, 64) >= 256) tile(Int<128>{}, Int<64>{}, Int<2>{}, Int<4>{});
+        else if (count(64, 64) >= 256) tile(Int<64>{}, Int<64>{}, Int<4>{}, Int<4>{});
+        else tile(Int<64>{}, Int<32>{}, Int<4>{}, Int<4>{});
         return launched();
     };
     return out_type == CKKS_PLAIN_BF16 ? go(bf16{}) : out_type == CKKS_PLAIN_F16 ? go(f16{}) : go(0.0f);
