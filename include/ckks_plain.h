@@ -107,9 +107,10 @@ int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckks_plain_nor
  * zeros from cols to the next such multiple.  Producers here write the zeros. */
 #define CKKS_PLAIN_I8_ROW 128
 
-/* q = rint(x / s) clamped to [-127, 127], s = max |x| / 127 of the row (both
- * quotients in 32 bits, ties to even); a row of zeros has s = 0, and a row
- * that holds an infinity or a NaN has s = NaN and q = 0.  cols <=
+/* q = rint(x / s) clamped to [-127, 127], s = max |x| of the row times 1/127
+ * (that constant, the product and the quotient each rounded to 32 bits, ties
+ * to even); a row of zeros has s = 0, and a row that holds an infinity or a
+ * NaN has s = NaN and q = 0.  cols <=
  * CKKS_PLAIN_MAX_COLS. */
 int ckks_plain_quantize_rows(int type, const void *x, int64_t x_stride, int64_t rows, int64_t cols, int8_t *q,
                              int64_t q_stride, float *q_scale, void *stream);

@@ -132,10 +132,11 @@ template <int NT> __device__ __forceinline__ uint32_t row_max(uint32_t v, float 
 }
 
 // The row's 8-bit form (ckks_plain_quantize_rows): scale from the largest |v| bit pattern (as
-// unsigned numbers those order like the magnitudes, infinities and NaN above all), quotients in
-// 32 bits.  The division by the scale is a true one: a reciprocal would move ties.
+// unsigned numbers those order like the magnitudes, infinities and NaN above all) times 1 / 127 in
+// 32 bits, as a division by a constant is usually compiled.  The division by the scale is a true
+// one: a reciprocal would move ties.
 __device__ __forceinline__ float i8_scale(uint32_t max_bits) {
-    return max_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(max_bits) / 127.0f;
+    return max_bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(max_bits) * (1.0f / 127.0f);
 }
 __device__ __forceinline__ int i8_of(float v, float s) {
     if (!(s > 0.0f)) return 0;  // a row of zeros, or not finite

@@ -241,7 +241,7 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
 
 
 def quantize_rows(x) -> Int8Rows:
-    """8-bit rows of x [T, D] (ckks_plain_quantize_rows): scale = max |x| / 127 of the row."""
+    """8-bit rows of x [T, D] (ckks_plain_quantize_rows): scale = max |x| times 1/127 of the row."""
     _matrix(x, "x")
     r = Int8Rows.empty(x.shape[0], x.shape[1], x.device)
     _call("ckks_plain_quantize_rows", x.device, _type(x, "x"), x.data_ptr(), _stride(x), x.shape[0], x.shape[1],

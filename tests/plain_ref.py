@@ -63,11 +63,11 @@ def norm_grad(x, y, dh, du, nw, nb=None, bw=None, bb=None, gate=None, scale=1.0,
 
 
 def quantise(x32):
-    """(q, scale) of float32 rows by the definition: both quotients in 32 bits, ties to even."""
+    """(q, scale) of float32 rows by the definition: 1/127, its product and the quotient in 32 bits, ties to even."""
     x32 = x32.astype(np.float32)
     top = np.abs(x32).max(1).astype(np.float32)
     with np.errstate(all="ignore"):
-        s = (top / np.float32(127)).astype(np.float32)
+        s = (top * (np.float32(1) / np.float32(127))).astype(np.float32)
         s[~np.isfinite(top)] = np.nan
         v = np.rint((x32 / s[:, None]).astype(np.float32))
     q = np.where((s > 0)[:, None], np.clip(v, -127, 127), 0)
