@@ -115,6 +115,8 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_quantize_rows(const T *
 
 // ------------------------------------------------------------------ gradient
 
+constexpr int GRAD_E = 8;  // elements a thread
+
 // The gradient of v -> hat = (v - mu) r from that of hat: r (g - [mean g] - hat mean(g hat)), the
 // bracketed mean for the layer norm alone.
 //
@@ -169,30 +171,37 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         }
     };
     auto center = [](float v, float mu) { return FULL ? v - mu : v; };
+    // with 16 waves a workgroup a thread has 128 registers, and the next row does not fit
+    constexpr bool AHEAD = NT < 1024;
     Raw rx, ry, rdu, rdh;
     auto fetch = [&](int64_t row) {
         R::fetch((const T *)a.y + row * a.y_stride, a.cols, t, ry);
         R::fetch((const T *)a.x + row * a.x_stride, a.cols, t, rx);
         R::fetch((const T *)o.du + row * o.du_stride, a.cols, t, rdu);
-        R::fetch((const T *)o.dh + row * o.dh_stride, a.cols, t, rdh);
+        if constexpr (AHEAD) R::fetch((const T *)o.dh + row * o.dh_stride, a.cols, t, rdh);
     };
-    if (first < last) fetch(first);
+    if (AHEAD && first < last) fetch(first);
     for (int64_t row = first; row < last; row++) {
         float x[E], y[E], h[E], g[E], w[E], du[E], dh[E];
+        if (!AHEAD) fetch(row);
         R::widen(rx, x);
         R::widen(ry, y);
         R::widen(rdu, du);
-        R::widen(rdh, dh);
-        if (row + 1 < last) fetch(row + 1);
+        if constexpr (AHEAD) {
+            R::widen(rdh, dh);
+            if (row + 1 < last) fetch(row + 1);
+        }
         float mu_y = 0, r_y = 1, mu_h, r_h;
         if (a.bw) {
             stats(y, buf, mu_y, r_y);
+#pragma unroll
+            for (int i = 0; i < E; i++) y[i] = center(y[i], mu_y) * r_y;  // y is its norm from here on
+        }
+        // h = n, and g = scale times gate
+        if (a.bw) {
             R::load((const T *)a.bw, a.cols, t, w);
 #pragma unroll
-            for (int i = 0; i < E; i++) {
-                y[i] = center(y[i], mu_y) * r_y;  // y is its norm from here on
-                h[i] = y[i] * w[i];
-            }
+            for (int i = 0; i < E; i++) h[i] = y[i] * w[i];
             if (FULL && a.bb) {
                 R::load((const T *)a.bb, a.cols, t, w);
 #pragma unroll
@@ -202,7 +211,6 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
 #pragma unroll
             for (int i = 0; i < E; i++) h[i] = y[i];
         }
-        // h = n for now; g = scale times gate
         if (a.gate) {
             R::load((const T *)a.gate + row / a.rows_per_gate * a.cols, a.cols, t, g);
 #pragma unroll
@@ -227,9 +235,11 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         }
         s1 = row_sum<NT>(s1, buf[4]) * inv;
         s2 = layer ? row_sum<NT>(s2, buf[5]) * inv : 0.0f;
+        if constexpr (!AHEAD) R::load((const T *)o.dh + row * o.dh_stride, a.cols, t, dh);
+#pragma unroll
+        for (int i = 0; i < E; i++) dh[i] += r_h * (center(du[i], s2) - x[i] * s1);  // the gradient of h
 #pragma unroll
         for (int i = 0; i < E; i++) {
-            dh[i] += r_h * (center(du[i], s2) - x[i] * s1);  // the gradient of h
             acc_g[i] += a.scale * dh[i] * h[i];
             g[i] *= dh[i];  // the gradient of n
         }
@@ -411,11 +421,13 @@ int residual_norm(const ckks_plain_norm *p, void *h, int64_t h_stride, void *u, 
     });
 }
 
-// Rows of a workgroup: enough workgroups to fill the GPU, few enough that the partial sums stay a
-// small part of the traffic.
+// Rows of a workgroup: as many workgroups as run at a time (registers leave a compute unit 16 waves),
+// so that each writes its partial sums once: 8 MB in all for each weight, whatever the columns.  (With
+// 1024 workgroups for any width: 4096 x 8192 bf16 rms 177 us, now 121.)
 GradPlan grad_plan(const ckks_plain_norm *p) {
     GradPlan q;
-    const int64_t target = 1024;
+    int64_t target = 2048;  // also of one wave: more would write as much as they read
+    for (int64_t cols = 128 * GRAD_E; cols < p->cols && target > 256; cols *= 2) target /= 2;
     q.groups = p->groups ? p->groups : 1;
     q.rows_per_gate = p->rows / q.groups;
     const int64_t want = p->rows / target > 1 ? p->rows / target : 1;
@@ -513,7 +525,7 @@ extern "C" int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckk
     sums.part_gate = o.part_gate, sums.gate = g->gate;
     if (p->rows) {
         const NormArgs a = args_of(p);
-        int e = by_type<8>(p->type, p->cols, [&](auto ty, auto nt, auto el) {
+        int e = by_type<GRAD_E>(p->type, p->cols, [&](auto ty, auto nt, auto el) {
             constexpr int NT = decltype(nt)::value, E = decltype(el)::value;
             if (a.layer || a.nb || a.bb)
                 k_norm_grad<decltype(ty), NT, E, true><<<dim3((uint32_t)q.blocks), NT, 0, s>>>(a, o, q);

@@ -57,6 +57,17 @@ def _workspace(name, *sizes):
     return out.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_grad_workspace(rows, cols, groups, next_bias, block_weight, block_bias):
+    """The same for the norm's gradient: it goes by sizes and by which operands there are (16: there is one)."""
+    p = nat.PlainNorm(0, 0, rows, cols, groups, 16, 16, cols, cols, 16, 16 if next_bias else None,
+                      16 if block_weight else None, 16 if block_bias else None, 16 if groups else None, 1.0, 0.0)
+    out = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_norm_grad_workspace_size(C.byref(p), C.byref(out)),
+              "ckks_plain_norm_grad_workspace_size")
+    return out.value
+
+
 def _scratch(nbytes, device):
     """(tensor kept alive, address, size)"""
     if not nbytes:
@@ -232,10 +243,8 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
     at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
     g = nat.PlainNormGrads(dh.data_ptr(), du.data_ptr(), _stride(dh), _stride(du), r.dx.data_ptr(), r.dy.data_ptr(),
                            D, D, at(r.next_weight), at(r.next_bias), at(r.block_weight), at(r.block_bias), at(r.gate))
-    need = C.c_size_t()
-    nat.check(nat.lib().ckks_plain_norm_grad_workspace_size(C.byref(p), C.byref(need)),
-              "ckks_plain_norm_grad_workspace_size")
-    _keep, ws, size = _scratch(need.value, x.device)
+    _keep, ws, size = _scratch(_norm_grad_workspace(T, D, p.groups, next_bias is not None, block_weight is not None,
+                                                    block_bias is not None), x.device)
     _call("ckks_plain_residual_norm_grad", x.device, C.byref(p), C.byref(g), ws, size)
     return r
 
