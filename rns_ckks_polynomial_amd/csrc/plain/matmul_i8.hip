@@ -11,7 +11,6 @@ struct MatmulArgs {
     const float *a_scale, *w_scale, *bias;
     int64_t a_stride, w_stride, out_stride;
     int rows, channels, padded;
-    bool vector_out;  // 16 bytes of channels can be stored at once
 };
 
 // N channels of one token from their sums: the sum, the two scales, their product and the bias
@@ -19,12 +18,12 @@ struct MatmulArgs {
 template <typename T, int N>
 __device__ __forceinline__ void store_sums(const MatmulArgs &m, T *out, int t, int c, float a_scale, const int (&s)[N],
                                            const float (&w_scale)[N], const float (&bias)[N]) {
-    typedef T TN __attribute__((ext_vector_type(N)));
+    typedef T TN __attribute__((ext_vector_type(N), aligned(sizeof(T))));  // at any channel
     T *p = out + (int64_t)t * m.out_stride + c;
     TN v;
 #pragma unroll
     for (int i = 0; i < N; i++) v[i] = from_f32<T>((float)s[i] * (a_scale * w_scale[i]) + bias[i]);
-    if (m.vector_out && c + N <= m.channels) {
+    if (c + N <= m.channels) {
         *(TN *)p = v;
     } else {
 #pragma unroll
@@ -107,6 +106,7 @@ __global__ __launch_bounds__(256, STAGES * SUB * (BM + BN) * STEP > 80 * 1024 ? 
     constexpr int SUMS = BN / 2 + 4;
     static_assert(4 * 32 * SUMS * 4 <= STAGES * STAGE, "the epilogue fits");
     __shared__ __attribute__((aligned(16))) int8_t lds[STAGES * STAGE];
+    __shared__ float scales[BM];
     int tile_t, tile_c;
     order.tile(blockIdx.x, tile_t, tile_c);
     const int t0 = tile_t * BM, c0 = tile_c * BN;
@@ -186,6 +186,7 @@ __global__ __launch_bounds__(256, STAGES * SUB * (BM + BN) * STEP > 80 * 1024 ? 
     // 4 (l / 16) + 0..3 of token l % 16 of each tile.
     tile_wait<0>();
     mfma_done(acc);
+    if (threadIdx.x < BM) scales[threadIdx.x] = m.a_scale[t0 + (int)threadIdx.x < m.rows ? t0 + threadIdx.x : m.rows - 1];
     constexpr int PER = sizeof(T) == 4 ? 4 : 8, LANES = BN / 2 / PER;  // channels a lane stores, lanes a token
     int *sums = (int *)lds + wave * 32 * SUMS;
     const int c = c0 + (wave & 1) * (BN / 2) + l % LANES * PER;
@@ -195,6 +196,7 @@ __global__ __launch_bounds__(256, STAGES * SUB * (BM + BN) * STEP > 80 * 1024 ? 
         ws[i] = c + i < m.channels ? m.w_scale[c + i] : 0.0f;
         bias[i] = m.bias && c + i < m.channels ? m.bias[c + i] : 0.0f;
     }
+    __syncthreads();
     for_all<TM / 2>([&](auto pair) {
         constexpr int j = 2 * decltype(pair)::value;
         for_all<TN>([&](auto i) {
@@ -203,15 +205,15 @@ __global__ __launch_bounds__(256, STAGES * SUB * (BM + BN) * STEP > 80 * 1024 ? 
             *(v4i *)(sums + (16 + l % 16) * SUMS + 16 * at + 4 * (l / 16)) = acc[at][j + 1];
         });
         __builtin_amdgcn_wave_barrier();
-        const int tj = t0 + (wave >> 1) * (BM / 2) + 16 * j;
+        const int tj = (wave >> 1) * (BM / 2) + 16 * j;
 #pragma unroll
         for (int r = 0; r < 32; r += 64 / LANES) {
             const int t = tj + r + l / LANES;
-            if (t >= m.rows) break;
             int v[PER];
 #pragma unroll
-            for (int i = 0; i < PER; i += 4) *(v4i *)(v + i) = *(const v4i *)(sums + (r + l / LANES) * SUMS + l % LANES * PER + i);
-            store_sums<T, PER>(m, out, t, c, m.a_scale[t], v, ws, bias);
+            for (int i = 0; i < PER; i += 4)
+                *(v4i *)(v + i) = *(const v4i *)(sums + (r + l / LANES) * SUMS + l % LANES * PER + i);
+            if (t0 + t < m.rows) store_sums<T, PER>(m, out, t0 + t, c, scales[t], v, ws, bias);
         }
         __builtin_amdgcn_wave_barrier();
     });
@@ -319,12 +321,9 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
     const size_t z = type_size(out_type);
     const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
     const MatmulArgs m{a, w, a_scale, w_scale, bias, a_stride, w_stride, out_stride, (int)rows, (int)channels,
-                       (int)padded, out_stride * z % 16 == 0 && at(out, 16)};
+                       (int)padded};
     auto go = [&](auto ty) {
         typedef decltype(ty) T;
-        auto tiles = [&](int bm, int bn) {
-            return TileOrder{(int)((rows + bm - 1) / bm), (int)((channels + bn - 1) / bn), 8};
-        };
         const hipStream_t st = (hipStream_t)stream;
         if (rows <= FEW) {
             // up to eight waves share channels, while that does not make more than 32 a compute unit
@@ -335,21 +334,36 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
             k_matmul_i8_few<T><<<dim3(groups), 64 * waves, 0, st>>>(m, (T *)out);
             return launched();
         }
+        auto order = [&](int bm, int bn) {
+            return TileOrder{(int)((rows + bm - 1) / bm), (int)((channels + bn - 1) / bn), 8};
+        };
         auto tile = [&](auto bm, auto bn, auto sub, auto stages) {
             constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
-            const TileOrder o = tiles(BM, BN);
+            const TileOrder o = order(BM, BN);
             k_matmul_i8_tile<T, BM, BN, decltype(sub)::value, decltype(stages)::value>
                 <<<dim3(o.tokens * o.channels), 256, 0, st>>>(m, (T *)out, o);
         };
-        auto count = [&](int bm, int bn) { return ((rows + bm - 1) / bm) * ((channels + bn - 1) / bn); };
-        // The largest tile that fills three quarters of the 256 compute units; under that, smaller ones
-        // have more of them read the weights (128 x 8192 x 8192: 64 x 64 tiles 29 us, 128 x 128 51 us),
-        // and four 64-byte steps between barriers keep their short steps from waiting for each other.
-        if (count(256, 256) >= 192) tile(Int<256>{}, Int<256>{}, Int<1>{}, Int<4>{});
-        else if (count(128, 128) >= 256) tile(Int<128>{}, Int<128>{}, Int<1>{}, Int<4>{});
-        else if (count(128, 64) >= 256) tile(Int<128>{}, Int<64>{}, Int<2>{}, Int<4>{});
-        else if (count(64, 64) >= 256) tile(Int<64>{}, Int<64>{}, Int<4>{}, Int<4>{});
-        else tile(Int<64>{}, Int<32>{}, Int<4>{}, Int<4>{});
+        // What a compute unit has to load sets the time of all tiles (35 to 57 GB/s into LDS, measured
+        // from 64 x 32 to 256 x 256): rounds of tiles on 256 units times a tile's rows.  The least of
+        // that; the larger of equals, which reads less in all.  777 x 5003 x 2051: 128 x 256 tiles (140)
+        // 18 us, 128 x 128 (280: two rounds) 28 us; 128 x 8192 x 8192: 64 x 64 (256) 29 us, 128 x 128
+        // (64) 51 us.  Four steps between barriers keep the short steps of small tiles from waiting.
+        constexpr int SHAPES[6][2] = {{256, 256}, {128, 256}, {128, 128}, {128, 64}, {64, 64}, {64, 32}};
+        int best = 0;
+        int64_t least = INT64_MAX;
+        for (int i = 0; i < 6; i++) {
+            const TileOrder o = order(SHAPES[i][0], SHAPES[i][1]);
+            const int64_t cost = ((int64_t)o.tokens * o.channels + 255) / 256 * (SHAPES[i][0] + SHAPES[i][1]);
+            if (cost < least) best = i, least = cost;
+        }
+        switch (best) {
+            case 0: tile(Int<256>{}, Int<256>{}, Int<1>{}, Int<4>{}); break;
+            case 1: tile(Int<128>{}, Int<256>{}, Int<1>{}, Int<4>{}); break;
+            case 2: tile(Int<128>{}, Int<128>{}, Int<1>{}, Int<4>{}); break;
+            case 3: tile(Int<128>{}, Int<64>{}, Int<2>{}, Int<4>{}); break;
+            case 4: tile(Int<64>{}, Int<64>{}, Int<4>{}, Int<4>{}); break;
+            default: tile(Int<64>{}, Int<32>{}, Int<4>{}, Int<4>{});
+        }
         return launched();
     };
     return out_type == CKKS_PLAIN_BF16 ? go(bf16{}) : out_type == CKKS_PLAIN_F16 ? go(f16{}) : go(0.0f);
