@@ -346,8 +346,8 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
         // What a compute unit has to load sets the time of all tiles (35 to 57 GB/s into LDS, measured
         // from 64 x 32 to 256 x 256): rounds of tiles on 256 units times a tile's rows.  The least of
         // that; the larger of equals, which reads less in all.  777 x 5003 x 2051: 128 x 256 tiles (140)
-        // 18 us, 128 x 128 (280: two rounds) 28 us; 128 x 8192 x 8192: 64 x 64 (256) 29 us, 128 x 128
-        // (64) 51 us.  Four steps between barriers keep the short steps of small tiles from waiting.
+        // 24 us, 256 x 256 (80) 36 us; 128 x 8192 x 8192: 64 x 64 (256) 29 us, 128 x 128 (64) 51 us.
+        // Four steps between barriers keep the short steps of small tiles from waiting.
         constexpr int SHAPES[6][2] = {{256, 256}, {128, 256}, {128, 128}, {128, 64}, {64, 64}, {64, 32}};
         int best = 0;
         int64_t least = INT64_MAX;
