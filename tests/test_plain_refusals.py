@@ -114,6 +114,33 @@ def test_matmul_arguments(kw, code):
     assert nat.lib().ckks_plain_matmul_i8(*{**MM, **kw}.values(), None) == code
 
 
+LIN = dict(type=0, x=X, x_stride=D, w=W, w_stride=128, w_scale=G, bias=None, out_type=0, out=H, out_stride=32,
+           rows=T, channels=32, cols=D, ws=WSP, ws_bytes=1 << 20)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(type=3), INV), (dict(out_type=-1), INV), (dict(x=None), INV), (dict(w=None), INV), (dict(w_scale=None), INV),
+    (dict(out=None), INV), (dict(x_stride=D - 1), INV), (dict(w_stride=64), INV), (dict(out_stride=31), INV),
+    (dict(rows=-1), INV), (dict(channels=-1), INV), (dict(cols=0), INV), (dict(rows=1 << 31), INV),
+    (dict(cols=16385, x_stride=16385, w_stride=1 << 15), UNSUP), (dict(x=X + 1), ALIGN), (dict(w=W + 8), ALIGN),
+    (dict(out=H + 1), ALIGN), (dict(bias=S + 2), ALIGN), (dict(ws=WSP + 8), ALIGN), (dict(ws=None), WS),
+    (dict(ws_bytes=T * 128), WS), (dict(out=X), INV), (dict(out=W + 128), INV), (dict(out=G), INV),
+    (dict(bias=S, out=S), INV), (dict(ws=X), INV), (dict(ws=H), INV), (dict(ws=W), INV), (dict(ws=G), INV),
+    (dict(bias=S, ws=S), INV),
+])
+def test_linear_arguments(kw, code):
+    assert nat.lib().ckks_plain_linear_i8(*{**LIN, **kw}.values(), None) == code
+
+
+def test_linear_workspace():
+    lib, n = nat.lib(), C.c_size_t()
+    assert lib.ckks_plain_linear_i8_workspace_size(T, 32, D, C.byref(n)) == 0 and n.value >= T * 128 + T * 4
+    assert lib.ckks_plain_linear_i8(*{**LIN, "ws_bytes": n.value - 1}.values(), None) == WS
+    assert lib.ckks_plain_linear_i8_workspace_size(T, 32, 16385, C.byref(n)) == UNSUP
+    assert lib.ckks_plain_linear_i8_workspace_size(T, 32, D, None) == INV
+    assert lib.ckks_plain_linear_i8(*{**LIN, "rows": 0}.values(), None) == 0
+
+
 SMP = dict(type=0, logits=X, logits_stride=D, gumbel=Y, gumbel_stride=D, temperature=W, top_k=None, top_p=None,
            min_p=None, allowed=None, allowed_stride=0, rows=T, vocab=D, token=H, logprob=U, ws=WSP, ws_bytes=1 << 30)
 
@@ -153,3 +180,5 @@ def test_binding_wants_device_matrices():
         plain.sample(x, x, torch.ones(2))
     with pytest.raises(ValueError, match="Int8Rows"):
         plain.matmul_i8(x, x)
+    with pytest.raises(ValueError, match="device tensor|Int8Rows"):
+        plain.linear_i8(x, x)
