@@ -58,7 +58,7 @@ struct SampleShared {
 // Masses that are added by atomics are whole multiples of a power of two and float sums go in a
 // fixed order, so the result does not depend on the order of anything.
 //
-// 256 x 131072 bf16, top-p 0.95 of normal logits (deviation 2.5, a nucleus of 26000): 88 to 93 us for
+// 256 x 131072 bf16, top-p 0.95 of normal logits (deviation 2.5, a nucleus of 26000): 80 to 85 us for
 // 290 MB from memory, three reads of the logits and the noise lines that hold a token of the nucleus;
 // each read has a compute unit's vector instructions beside its loads.  1 x 32768 f32, top-k 50 and
 // top-p: 14 us, one read, then latency; 33 x 50021 f16, masked, min-p and top-k 1000: 22 us.
@@ -87,10 +87,11 @@ template <typename T> struct Sampler {
     __device__ __forceinline__ uint64_t order_of(float v, uint32_t i) const {
         return v > -INFINITY ? lowest(v) | (indexes() - i) : 0;
     }
-    __device__ __forceinline__ float logit_of(uint64_t o) const {
-        const uint32_t k = (uint32_t)(o >> a.index_bits) << UNSET;
+    static __device__ __forceinline__ float of_key(uint32_t key) {
+        const uint32_t k = key << UNSET;
         return of_order_bits(k & 0x80000000u ? k : k | ((1u << UNSET) - 1));
     }
+    __device__ __forceinline__ float logit_of(uint64_t o) const { return of_key((uint32_t)(o >> a.index_bits)); }
     __device__ __forceinline__ uint32_t index_of(uint64_t o) const { return indexes() - ((uint32_t)o & indexes()); }
 
     // ---- the workgroup's reductions: one barrier each, in eight places in turn
@@ -228,6 +229,20 @@ template <typename T> struct Sampler {
     static __device__ __forceinline__ uint32_t before_lane(uint64_t lanes) {
         return __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
     }
+    // where a logit lies in bins of 1 / width from the largest down (infinity - infinity: 0)
+    __device__ __forceinline__ float place(float v, float width) const { return fmaxf((top - v) * width, 0.0f); }
+    // The smallest logit with place < b (b >= 1, the largest logit finite: it is one), 64 candidates at
+    // a time.  -infinity is none.
+    __device__ __forceinline__ float edge(float b, float width) const {
+        uint32_t under = order_bits(-INFINITY) >> UNSET, from = order_bits(top) >> UNSET;  // not one; one
+        while (from - under > 1) {
+            const uint32_t step = (from - under + 63) / 64, k = under + (threadIdx.x % 64 + 1) * step;
+            const uint64_t lanes = __ballot(k >= from || place(of_key(k), width) < b);
+            from = under + (uint32_t)__ffsll((unsigned long long)lanes) * step;
+            under = from - step;
+        }
+        return of_key(from);
+    }
     // the numbers of tokens with logits >= low in FINE bins of 1 / width from the largest logit down
     __device__ __forceinline__ void count(float low, float width) {
         __syncthreads();
@@ -236,8 +251,7 @@ template <typename T> struct Sampler {
         pass<4>([&](int first, const float (&x)[N]) {
 #pragma unroll
             for (int i = 0; i < N; i++)
-                if (x[i] >= low && x[i] > -INFINITY)
-                    atomicAdd(&m.counts[(int)fminf(fmaxf((top - x[i]) * width, 0.0f), FINE - 1.0f)], 1u);
+                if (x[i] >= low && x[i] > -INFINITY) atomicAdd(&m.counts[(int)fminf(place(x[i], width), FINE - 1.0f)], 1u);
         });
         __syncthreads();
     }
@@ -354,40 +368,43 @@ template <typename T> struct Sampler {
     template <bool UNTIL>
     __device__ __forceinline__ uint64_t best(uint64_t last, float width, float first_bin, float last_bin, float &above) {
         constexpr int U = 2;
-        const float rt = 1.0f / t, low = UNTIL || last <= 1 ? -INFINITY : logit_of(last);
+        // UNTIL: tokens from `low` on stay, those from `listing` on to it are listed
+        const float low = UNTIL ? first_bin >= 1 ? edge(first_bin, width) : INFINITY : last <= 1 ? -INFINITY : logit_of(last);
+        const float listing = UNTIL ? edge(last_bin + 1.0f, width) : 0.0f;
+        const float rt = 1.0f / t;
+        // no quick score where the reciprocal of the temperature has lost digits, or off infinity
+        const bool slow = !(t > 0x1p-100f && t < 0x1p100f) || top == INFINITY;
         uint64_t win = 0;
         float part_sum = 0;
         // A score is computed as defined only where a quick one comes near the best so far: the quick
-        // quotient is off by less than 2^-22 of itself, a sum by 2^-23.
-        auto consider = [&](float v, uint32_t i, float noise, float cut) {
-            const float d = fminf((v - top) * rt, 0.0f), quick = d + noise;
-            if (quick < cut - (fabsf(d) + fabsf(quick)) * 0x1p-20f || too_small(v)) return;
+        // quotient is off by less than 2^-22 of itself, a sum by 2^-23.  `quick` is that with 2^-20 of
+        // both on top.
+        auto consider = [&](float v, uint32_t i, float noise) {
+            if (!(v >= low) || (!UNTIL && order_of(v, i) < last) || too_small(v)) return;
             const uint64_t s = score(v, i, noise);
             if (s > win) {
                 win = s;
                 if ((uint32_t)(s >> 32) > *(volatile uint32_t *)&m.cut) atomicMax(&m.cut, (uint32_t)(s >> 32));
             }
         };
-        auto place = [&](float v) { return fmaxf((top - v) * width, 0.0f); };
-        auto stays = [&](float v, uint32_t i) {
-            if constexpr (UNTIL) {
-                if (!(v > -INFINITY && place(v) < first_bin)) return false;
-                part_sum += weight(v, top);
-                return true;
-            } else {
-                return order_of(v, i) >= last;
-            }
-        };
         auto handle = [&](int first, const float (&x)[N], const float (&noise)[N]) {
-            // (a reciprocal of a temperature near the largest number has lost its digits)
-            const float cut = t < 0x1p100f ? of_order_bits(*(volatile uint32_t *)&m.cut) : -INFINITY;
+            const float cut = of_order_bits(*(volatile uint32_t *)&m.cut);  // NaN before the first
+            float quick = -INFINITY;
             uint32_t listed = 0;
 #pragma unroll
             for (int k = 0; k < N; k++) {
-                if (x[k] >= low && stays(x[k], first + k)) consider(x[k], first + k, noise[k], cut);
-                if (UNTIL) listed |= place(x[k]) >= first_bin && place(x[k]) < last_bin + 1.0f ? 1u << k : 0;
+                const float off = (x[k] >= low ? x[k] : -INFINITY) - top, d = off * rt, score = d + noise[k];
+                if constexpr (UNTIL) {
+                    part_sum += __builtin_amdgcn_exp2f(off * c);
+                    listed |= x[k] >= listing && x[k] < low ? 1u << k : 0;
+                }
+                quick = fmaxf(quick, score + (fabsf(d) + fabsf(score)) * 0x1p-20f);
             }
-            if (listed) append(first, x, listed);
+            if (slow || !(quick < cut)) {
+#pragma unroll
+                for (int k = 0; k < N; k++) consider(x[k], first + k, noise[k]);
+            }
+            if (UNTIL && listed) append(first, x, listed);
         };
         const int whole = a.vocab / N;
         Vec r[U];
@@ -407,8 +424,7 @@ template <typename T> struct Sampler {
             for (int j = 0; j < U; j++) {
                 logits(r[j], ks[j], x[j]);
                 const float most = largest(x[j]);
-                const bool need = v + j * NT < whole && most > -INFINITY &&
-                                  (UNTIL ? fmaxf((top - most) * width, 0.0f) < first_bin : most >= low);
+                const bool need = v + j * NT < whole && most > -INFINITY && most >= low;
                 if (need) {
                     const float *g = gumbel + (int64_t)(v + j * NT) * N;
 #pragma unroll
@@ -448,8 +464,9 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
     S s{a, m, (const T *)a.logits + row * a.logits_stride, a.allowed ? a.allowed + row * a.allowed_stride : nullptr,
         a.gumbel + row * a.gumbel_stride, (int)__builtin_amdgcn_readfirstlane(tid >> 6), 0, greedy ? 1.0f : temp};
     s.min_p = a.min_p ? a.min_p[row] : 0.0f;
-    // under 2^-120 the exponents of finite logits stay, and -infinity times it stays -infinity
-    s.c = fmaxf(1.44269504f / s.t, 0x1p-120f);
+    // from 2^-120 on a product with -infinity stays that, up to 2^126 one with 0 stays 0 (but for
+    // subnormal differences of logits neither bound is felt)
+    s.c = fminf(fmaxf(1.44269504f / s.t, 0x1p-120f), 0x1p126f);
     m.counts[tid] = 0;
     if (tid == 0) m.cut = 0, m.pick[0] = NT;
     // the thread's largest logit, where it first occurs, and its mass from there
@@ -460,7 +477,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         if (v > mine) sum *= s.weight(mine, v), mine = v, where = first;
         if (mine > -INFINITY) {
 #pragma unroll
-            for (int i = 0; i < N; i++) sum += s.weight(x[i], mine);
+            for (int i = 0; i < N; i++) sum += __builtin_amdgcn_exp2f((x[i] - mine) * s.c);
         }
     });
     const uint32_t top_bits = s.all(mine > -INFINITY ? order_bits(mine) : 0u, 0u, Larger{});
@@ -469,6 +486,13 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         return;
     }
     s.top = of_order_bits(top_bits);
+    if (s.top == INFINITY) {  // infinity - infinity: each is worth 1, and nothing else anything
+        sum = 0;
+        s.template pass<1>([&](int first, const float (&x)[N]) {
+#pragma unroll
+            for (int i = 0; i < N; i++) sum += x[i] == INFINITY ? 1.0f : 0.0f;
+        });
+    }
     s.sum = s.all(mine > -INFINITY ? sum * s.weight(mine, s.top) : 0.0f, 0.0f, Sum{});
     if (greedy || k == 1 || p <= 0 || s.min_p > 1) {  // the first alone: it is in the first vector that holds it
         uint32_t i = ~s.all(mine == s.top ? ~where : 0u, 0u, Larger{});

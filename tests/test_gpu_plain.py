@@ -473,6 +473,21 @@ def test_sample_shapes_of_distributions(V, k, p):
     check_sample(z, noise(V, B, V), full(B, 0.8), full(B, k, torch.int32), full(B, p))
 
 
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("p,m,t", [(0.95, 0.0, 0.8), (0.95, 0.001, 1.3), (0.999, 0.0, 30.0), (0.5, 0.0, 1.0),
+                                   (0.9, 0.0, 1e-30), (0.9, 0.0, 1e32)])
+def test_sample_large_nuclei(ty, p, m, t):
+    """Nuclei of many thousands of tokens, at the ends of the temperature's range too; half of what
+    min_p is tested with is masked."""
+    V = 40003
+    say(f"sample nucleus {ty} top_p={p} min_p={m} T={t}")
+    spread = t if ty != "f16" and t in (1e-30, 1e32) else 2.5
+    z = rnd(V, 3, V) * spread
+    z[1] -= 20 * spread
+    allowed = torch.from_numpy(np.random.default_rng(V).random((3, V)) < 0.5).cuda() if m else None
+    check_sample(z.to(TYPE[ty]).cuda(), noise(V + 3, 3, V), full(3, t), None, full(3, p), full(3, m) if m else None, allowed)
+
+
 @pytest.mark.parametrize("ty", ["bf16", "f32"])
 def test_sample_masks(ty):
     B, V = 16, 3001
