@@ -154,18 +154,43 @@ struct GradArgs {
 // worked on.  16384 x 2048 bf16 rms, with the block's norm and a gate: 103 us for 403 MB and 25 MB of
 // partial sums (4.2 TB/s), and 6.5 us to add those up.
 template <typename T, int NT, int E, bool FULL>
-__global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPlan p) {
+__global__ __launch_bounds__(NT, FULL && E == 8 ? 4 : 1) void k_norm_grad(NormArgs a, GradArgs o, GradPlan p) {
     typedef Row<T, NT, E> R;
     typedef typename R::Raw Raw;
+    typedef float Four __attribute__((ext_vector_type(4)));
+    // The columns' sums: of next_weight, block_weight, next_bias, block_bias in this order; the first
+    // IN_LDS of them there, each thread its own, the others (and the gate's) in registers.  LDS has room
+    // for 16 waves' (128 KB of four) and time: 1 part in 25 of the row's from memory.  In registers they
+    // leave 8 or 12 waves, or spill with 16: 8192 x 4096 bf16 layer norm with biases 167 us, so 136;
+    // f32 234, so 194; 3118 x 5313 f32 360, so 245.  Without biases they fit, up to 4096 columns.
+    constexpr int IN_LDS = E > 8 ? 2 : FULL ? 4 : NT < 1024 ? 0 : 2;
+    __shared__ Four sums[IN_LDS ? IN_LDS * E / 4 * NT : 1];
     __shared__ float buf[8][16];
     const int t = threadIdx.x;
+    float acc[4][E] = {}, acc_g[E] = {};
+#pragma unroll
+    for (int i = 0; i < IN_LDS * E / 4; i++) sums[i * NT + t] = Four{0, 0, 0, 0};
+    auto add = [&](auto which, auto value) {
+        constexpr int K = decltype(which)::value;
+        if constexpr (K < IN_LDS) {
+#pragma unroll
+            for (int i = 0; i < E / 4; i++) {
+                Four f = sums[(K * E / 4 + i) * NT + t];
+#pragma unroll
+                for (int j = 0; j < 4; j++) f[j] += value(4 * i + j);
+                sums[(K * E / 4 + i) * NT + t] = f;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i++) acc[K][i] += value(i);
+        }
+    };
     const int64_t group = p.chunks > 1 ? blockIdx.x / p.chunks : 0;
     const int64_t first = p.chunks > 1 ? group * p.rows_per_gate + blockIdx.x % p.chunks * p.span
                                        : (int64_t)blockIdx.x * p.span;
     const int64_t end = p.chunks > 1 ? (group + 1) * p.rows_per_gate : a.rows;
     const int64_t last = first + p.span < end ? first + p.span : end;
     const float inv = 1.0f / (float)a.cols;
-    float acc_nw[E] = {}, acc_bw[E] = {}, acc_g[E] = {}, acc_nb[FULL ? E : 1] = {}, acc_bb[FULL ? E : 1] = {};
     const bool layer = FULL && a.layer;
     // sum of squares around the mean, as row_stats; what is past the end is 0 and counts where there is no mean
     auto stats = [&](const float (&v)[E], float (*b)[16], float &mu, float &r) {
@@ -180,8 +205,9 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         }
     };
     auto center = [](float v, float mu) { return FULL ? v - mu : v; };
-    // with 16 waves a workgroup a thread has 128 registers, and the next row does not fit
-    constexpr bool AHEAD = NT < 1024;
+    // The next row, where it fits in 128 registers (16 waves a compute unit); rows of at most 4096
+    // columns without biases run with fewer waves for it.
+    constexpr bool AHEAD = E == 8 && (sizeof(T) == 2 || (!FULL && NT < 1024));
     Raw rx, ry, rdu, rdh;
     auto fetch = [&](int64_t row) {
         R::fetch((const T *)a.y + row * a.y_stride, a.cols, t, ry);
@@ -234,10 +260,11 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         R::load((const T *)a.nw, a.cols, t, w);
         float s1 = 0, s2 = 0;
 #pragma unroll
+        for (int i = 0; i < E; i++) x[i] = center(x[i], mu_h) * r_h;  // x is the norm of h from here on
+        add(Int<0>{}, [&](int i) { return du[i] * x[i]; });
+        if constexpr (FULL) add(Int<2>{}, [&](int i) { return du[i]; });
+#pragma unroll
         for (int i = 0; i < E; i++) {
-            x[i] = center(x[i], mu_h) * r_h;  // x is the norm of h from here on
-            acc_nw[i] += du[i] * x[i];
-            if constexpr (FULL) acc_nb[i] += du[i];
             du[i] *= w[i];
             s1 += du[i] * x[i];
             if constexpr (FULL) s2 += du[i];
@@ -256,10 +283,10 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         if (a.bw) {
             R::load((const T *)a.bw, a.cols, t, w);
             s1 = 0, s2 = 0;
+            add(Int<1>{}, [&](int i) { return g[i] * y[i]; });
+            if constexpr (FULL) add(Int<3>{}, [&](int i) { return g[i]; });
 #pragma unroll
             for (int i = 0; i < E; i++) {
-                acc_bw[i] += g[i] * y[i];
-                if constexpr (FULL) acc_bb[i] += g[i];
                 g[i] *= w[i];
                 s1 += g[i] * y[i];
                 if constexpr (FULL) s2 += g[i];
@@ -286,12 +313,20 @@ __global__ __launch_bounds__(NT) void k_norm_grad(NormArgs a, GradArgs o, GradPl
         for (int i = 0; i < E; i++)
             if (R::col(i, t) < a.cols) base[R::col(i, t)] = v[i];
     };
-    put(o.part[0], acc_nw);
-    put(o.part[2], acc_bw);
+    auto put_sum = [&](float *base, auto which) {
+        constexpr int K = decltype(which)::value;
+        if constexpr (K < IN_LDS) {
+#pragma unroll
+            for (int i = 0; i < E; i++) acc[K][i] = sums[(K * E / 4 + i / 4) * NT + t][i % 4];
+        }
+        put(base, acc[K]);
+    };
     put(o.part_gate, acc_g);
+    put_sum(o.part[0], Int<0>{});
+    put_sum(o.part[2], Int<1>{});
     if constexpr (FULL) {
-        put(o.part[1], acc_nb);
-        put(o.part[3], acc_bb);
+        put_sum(o.part[1], Int<2>{});
+        put_sum(o.part[3], Int<3>{});
     }
 }
 
@@ -439,13 +474,14 @@ GradPlan grad_plan(const ckks_plain_norm *p) {
     for (int64_t cols = 128 * GRAD_E; cols < p->cols && target > 256; cols *= 2) target /= 2;
     q.groups = p->groups ? p->groups : 1;
     q.rows_per_gate = p->rows / q.groups;
-    const int64_t want = p->rows / target > 1 ? p->rows / target : 1;
+    // never a few more than run at a time: 3118 x 5313 f32 layer norm took 245 us with 260 of them
+    const int64_t want = p->rows > target ? (p->rows + target - 1) / target : 1;
     if (q.rows_per_gate <= want) {
         q.chunks = 1;
-        q.span = q.rows_per_gate ? want / q.rows_per_gate * q.rows_per_gate : 1;
+        q.span = q.rows_per_gate ? (want + q.rows_per_gate - 1) / q.rows_per_gate * q.rows_per_gate : 1;
         q.blocks = (p->rows + q.span - 1) / q.span;
     } else {
-        q.chunks = (q.rows_per_gate + want - 1) / want;
+        q.chunks = target / q.groups;  // groups < target, as rows_per_gate > rows / target
         q.span = (q.rows_per_gate + q.chunks - 1) / q.chunks;
         q.chunks = (q.rows_per_gate + q.span - 1) / q.span;
         q.blocks = q.groups * q.chunks;
