@@ -204,6 +204,16 @@ __global__ __launch_bounds__(NT, FULL && E == 8 ? 4 : 1) void k_norm_grad(NormAr
             r = 1.0f / sqrtf(row_sum<NT>(s, b[1]) * inv + a.eps);
         }
     };
+    // s2's for the layer norm alone
+    auto means = [&](float &s1, float &s2, float (*b)[16]) {
+        if (layer) {
+            row_sums<NT>(s1, s2, b[0], b[1]);
+            s2 *= inv;
+        } else {
+            s1 = row_sum<NT>(s1, b[0]), s2 = 0;
+        }
+        s1 *= inv;
+    };
     auto center = [](float v, float mu) { return FULL ? v - mu : v; };
     // The next row, where it fits in 128 registers (16 waves a compute unit); rows of at most 4096
     // columns without biases run with fewer waves for it.
@@ -269,8 +279,7 @@ __global__ __launch_bounds__(NT, FULL && E == 8 ? 4 : 1) void k_norm_grad(NormAr
             s1 += du[i] * x[i];
             if constexpr (FULL) s2 += du[i];
         }
-        s1 = row_sum<NT>(s1, buf[4]) * inv;
-        s2 = layer ? row_sum<NT>(s2, buf[5]) * inv : 0.0f;
+        means(s1, s2, buf + 4);
         if constexpr (!AHEAD) R::load((const T *)o.dh + row * o.dh_stride, a.cols, t, dh);
 #pragma unroll
         for (int i = 0; i < E; i++) dh[i] += r_h * (center(du[i], s2) - x[i] * s1);  // the gradient of h
@@ -291,8 +300,7 @@ __global__ __launch_bounds__(NT, FULL && E == 8 ? 4 : 1) void k_norm_grad(NormAr
                 s1 += g[i] * y[i];
                 if constexpr (FULL) s2 += g[i];
             }
-            s1 = row_sum<NT>(s1, buf[6]) * inv;
-            s2 = layer ? row_sum<NT>(s2, buf[7]) * inv : 0.0f;
+            means(s1, s2, buf + 6);
 #pragma unroll
             for (int i = 0; i < E; i++) g[i] = r_y * (center(g[i], s2) - y[i] * s1);
         }

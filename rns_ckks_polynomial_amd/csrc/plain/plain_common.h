@@ -127,6 +127,18 @@ template <int NT, typename V, typename F> __device__ __forceinline__ V row_all(V
     return v;
 }
 template <int NT> __device__ __forceinline__ float row_sum(float v, float *buf) { return row_all<NT>(v, buf, Sum{}); }
+// two sums behind one barrier
+template <int NT> __device__ __forceinline__ void row_sums(float &v, float &w, float *buf_v, float *buf_w) {
+    v = lane(scan64(v, 0.0f, Sum{}), 63);
+    w = lane(scan64(w, 0.0f, Sum{}), 63);
+    if constexpr (NT > 64) {
+        if ((threadIdx.x & 63) == 0) buf_v[threadIdx.x >> 6] = v, buf_w[threadIdx.x >> 6] = w;
+        __syncthreads();
+        v = buf_v[0], w = buf_w[0];
+#pragma unroll
+        for (int i = 1; i < NT / 64; i++) v += buf_v[i], w += buf_w[i];
+    }
+}
 template <int NT> __device__ __forceinline__ uint32_t row_max(uint32_t v, float *buf) {
     return row_all<NT>(v, (uint32_t *)buf, Larger{});
 }
