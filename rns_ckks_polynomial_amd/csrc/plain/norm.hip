@@ -154,15 +154,16 @@ struct GradArgs {
 // worked on.  16384 x 2048 bf16 rms, with the block's norm and a gate: 103 us for 403 MB and 25 MB of
 // partial sums (4.2 TB/s), and 6.5 us to add those up.
 template <typename T, int NT, int E, bool FULL>
-__global__ __launch_bounds__(NT, FULL && E == 8 ? 4 : 1) void k_norm_grad(NormArgs a, GradArgs o, GradPlan p) {
+__global__ __launch_bounds__(NT, FULL && E == 8 && NT != 768 ? 4 : 1)  // 12 waves go one workgroup a unit
+void k_norm_grad(NormArgs a, GradArgs o, GradPlan p) {
     typedef Row<T, NT, E> R;
     typedef typename R::Raw Raw;
     typedef float Four __attribute__((ext_vector_type(4)));
     // The columns' sums: of next_weight, block_weight, next_bias, block_bias in this order; the first
     // IN_LDS of them there, each thread its own, the others (and the gate's) in registers.  LDS has room
     // for 16 waves' (128 KB of four) and time: 1 part in 25 of the row's from memory.  In registers they
-    // leave 8 or 12 waves, or spill with 16: 8192 x 4096 bf16 layer norm with biases 167 us, so 136;
-    // f32 234, so 194; 3118 x 5313 f32 360, so 245.  Without biases they fit, up to 4096 columns.
+    // leave 8 or 12 waves, or spill with 16: 8192 x 4096 bf16 layer norm with biases 167 us, so 133;
+    // f32 234, so 191; 4096 x 8192 bf16 156, so 147.  Without biases they fit, up to 4096 columns.
     constexpr int IN_LDS = E > 8 ? 2 : FULL ? 4 : NT < 1024 ? 0 : 2;
     __shared__ Four sums[IN_LDS ? IN_LDS * E / 4 * NT : 1];
     __shared__ float buf[8][16];
@@ -388,12 +389,15 @@ __global__ void k_zero(float *p, size_t n) {
 
 // ------------------------------------------------------------------ launches
 
-// f(type tag, threads, elements) for the smallest row shape that holds the columns
+// f(type tag, threads, elements) for the smallest row shape that holds the columns.  12 waves between 8
+// and 16 are worth their code: 8192 x 10000 bf16 143 us with 16, 131 with 12; 1021 x 5003 f32 layer norm
+// 19.8 and 18.3; gradient of 3118 x 5313 bf16 layer norm 147 and 136.
 template <int E, typename T, typename F> int by_shape(int64_t cols, F f) {
     if (cols <= 64 * E) return f(T{}, Int<64>{}, Int<E>{});
     if (cols <= 128 * E) return f(T{}, Int<128>{}, Int<E>{});
     if (cols <= 256 * E) return f(T{}, Int<256>{}, Int<E>{});
     if (cols <= 512 * E) return f(T{}, Int<512>{}, Int<E>{});
+    if (cols <= 768 * E) return f(T{}, Int<768>{}, Int<E>{});
     if (cols <= 1024 * E) return f(T{}, Int<1024>{}, Int<E>{});
     return f(T{}, Int<1024>{}, Int<16>{});
 }
