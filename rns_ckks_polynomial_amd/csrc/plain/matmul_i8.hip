@@ -62,7 +62,7 @@ struct TileOrder {
 // piece with rows 4..11 of the next (p ^ (r / 4 & 3) serves the former only).  The loads write LDS
 // in lane order and permute the pieces on the memory side (within a row's 64 bytes).
 //
-// 8192 x 8192 x 8192 on normal values, bf16 out: 452 to 480 us (2.3 to 2.4 POP/s), the matrix cores
+// 8192 x 8192 x 8192 on normal values, bf16 out: 440 to 480 us (2.3 to 2.5 POP/s), the matrix cores
 // busy 61 % of the cycles, no LDS conflicts.  A tile's fill and its epilogue (16 us of 256 x 256
 // together) are not hidden behind another tile's products: a second accumulator does not fit.  777 x
 // 2051 x 5003 f16 24 to 26 us, two thirds of that the load of 33 steps; 64 x 8192 x 8192 16.6 us, 4.1

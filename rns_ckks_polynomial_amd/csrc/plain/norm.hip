@@ -38,7 +38,7 @@ __device__ __forceinline__ void row_stats(const float (&v)[E], const NormArgs &a
 // read to its one write: x, y in, h, u out, nothing else moves but the weights, which stay in L2.
 // Bound by memory: 8192 x 4096 bf16, norm of the block and a gate, 46.5 us for 268 MB (5.8 TB/s: part
 // comes from the last-level cache; a copy of 2 GiB moves 4.8); 1021 x 5003 f32, rows at odd strides,
-// layer norm with biases, 21 us for 82 MB (3.8 TB/s: one round of workgroups, each with two means to
+// layer norm with biases, 20 us for 82 MB (4.0 TB/s: one round of workgroups, each with two means to
 // wait for); 4 x 2048 bf16 2.8 us, all latency.
 template <typename T, int NT, int E, bool I8>
 __global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_residual_norm(NormArgs a, T *h_out, int64_t h_stride,
@@ -151,7 +151,7 @@ struct GradArgs {
 //
 // FULL has means and biases; without them (the rms norm of most decoders) a third of the arithmetic
 // goes, which is what bounds this kernel.  The next row's operands are fetched while a row is
-// worked on.  16384 x 2048 bf16 rms, with the block's norm and a gate: 103 us for 403 MB and 25 MB of
+// worked on.  16384 x 2048 bf16 rms, with the block's norm and a gate: 101 us for 403 MB and 25 MB of
 // partial sums (4.2 TB/s), and 6.5 us to add those up.
 template <typename T, int NT, int E, bool FULL>
 __global__ __launch_bounds__(NT, FULL && E == 8 && NT != 768 ? 4 : 1)  // 12 waves go one workgroup a unit
