@@ -261,8 +261,10 @@ template <typename T> struct Sampler {
         for (int i = 0; i < HELD; i++) o[i] = threadIdx.x + i * NT < n ? m.list[threadIdx.x + i * NT] : 0;
         __syncthreads();
     }
-    // A listed token's count and mass in one number: 13 and 51 bits, sums of LIST of them included.
-    static constexpr int LIST_BITS = 39, COUNT = 51;
+    // A listed token's count and mass in one number, 13 and 51 bits.  A mass is at most 2^LIST_BITS, so LIST
+    // of them add up to 2^50 at most, and their count to 2^12: neither sum leaves its place.
+    static constexpr int LIST_BITS = 38, COUNT = 51;
+    static_assert(((uint64_t)LIST << LIST_BITS) < (uint64_t)1 << COUNT && LIST < 1 << (64 - COUNT), "sums fit");
     static constexpr uint64_t MASS = ((uint64_t)1 << COUNT) - 1;
     __device__ __forceinline__ uint64_t both(uint64_t o) const {
         return (uint64_t)1 << COUNT | fixed(weight(logit_of(o), top), LIST_BITS);

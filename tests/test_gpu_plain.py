@@ -450,6 +450,32 @@ def test_sample_ties(levels, V):
     check_sample(z, noise(V + 1, 12, V), full(12, 0.0), k, p)
 
 
+@pytest.mark.parametrize("n", [4095, 4096, 4097])
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V,k,t", [(0, 0, 1.0), (0, 0, 1e9), (5000, 4500, 1.0), (5000, 4999, 1.0), (60000, 0, 1.0)])
+def test_sample_as_many_equals_as_a_list_holds(n, ty, V, k, t):
+    """n tokens that all weigh one: the whole row (V = 0), the allowed ones of V, or the top of V with a tail.  Row
+    by row all the noise is on one token around the end of the nucleus, then it is spread."""
+    say(f"sample {n} equals of {V} {ty} top_k={k} T={t}")
+    B, width, r = 8, max(V, n), np.random.default_rng(n + V)
+    z = np.full((B, width), -9.0) if V == 60000 else np.zeros((B, width))
+    ids = np.sort(r.permutation(width)[:n])
+    z[:, ids] = 0
+    if t > 1:
+        z = z + r.standard_normal((B, width))  # nearly flat at that temperature: each weighs one in 32 bits
+    allowed = torch.zeros(B, width, dtype=torch.bool, device="cuda")
+    allowed[:, torch.from_numpy(ids).cuda()] = True
+    z = torch.from_numpy(z).to(TYPE[ty]).cuda()
+    g = noise(n, B, width)
+    p = np.float32([0.5, 0.5, 0.3, 0.3, 0.9, 0.9, 0.7, 0.999])
+    mass = n + (width - n) * np.exp(-9.0) * (V == 60000)
+    ranked = np.argsort(-z.float().cpu().numpy(), axis=1, kind="stable")
+    for row, d in ((0, 0), (1, -1), (2, 1), (3, -2), (4, 1), (5, -1)):
+        g[row, ranked[row, int(np.ceil(p[row].astype(np.float64) * mass)) + d]] = 50.0
+    check_sample(z, g, full(B, t), full(B, k, torch.int32) if k else None, torch.from_numpy(p).cuda(), None,
+                 allowed if V == 5000 else None)
+
+
 @pytest.mark.parametrize("V", [5000, 20011, 70000])
 @pytest.mark.parametrize("k,p", [(50, 1.0), (4500, 1.0), (4999, 0.9), (0, 0.5), (0, 0.9999), (3000, 0.8)])
 def test_sample_shapes_of_distributions(V, k, p):
