@@ -469,7 +469,8 @@ def test_sample_as_many_equals_as_a_list_holds(n, ty, V, k, t):
     g = noise(n, B, width)
     p = np.float32([0.5, 0.5, 0.3, 0.3, 0.9, 0.9, 0.7, 0.999])
     mass = n + (width - n) * np.exp(-9.0) * (V == 60000)
-    ranked = np.argsort(-z.float().cpu().numpy(), axis=1, kind="stable")
+    possible = z.masked_fill(~allowed, -np.inf) if V == 5000 else z
+    ranked = np.argsort(-possible.float().cpu().numpy(), axis=1, kind="stable")
     for row, d in ((0, 0), (1, -1), (2, 1), (3, -2), (4, 1), (5, -1)):
         g[row, ranked[row, int(np.ceil(p[row].astype(np.float64) * mass)) + d]] = 50.0
     check_sample(z, g, full(B, t), full(B, k, torch.int32) if k else None, torch.from_numpy(p).cuda(), None,
