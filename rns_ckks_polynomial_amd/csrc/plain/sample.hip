@@ -611,7 +611,6 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
             if (by_mass && !by_count) {
                 // counts in bins down to the bound; a bin's mass by e of its middle, `off` at most off
                 const float range = s.top - nucleus, width = (float)FINE / range;
-                if (tid == 0) m.pick[0] = FINE, m.pick[1] = 0;
                 s.count(nucleus, width);
                 const float step = range / FINE * s.c;  // of a bin, in powers of two
                 const float off = __builtin_amdgcn_exp2f(0.5f * step) - 1.0f + 1e-4f, want = p * s.sum;
@@ -622,19 +621,19 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                     v[i] = (float)m.counts[at] * __builtin_amdgcn_exp2f(-((float)at + 0.5f) * step);
                     own += v[i];
                 }
-                float before = s.in_front(own, total);
-                // the first bin after which there may be `want`, and the last before which there may not
+                float after = s.in_front(own, total);
+                // The first bin after which there may be `want`, and the first after which there must be (the last
+                // one if none: nothing under it is in the nucleus).  Each is the least over all bins, so it does
+                // not matter that a thread's last sum and the next thread's first differ in their rounding.
+                uint32_t may = FINE, must = FINE;
 #pragma unroll
                 for (int i = 0; i < EACH; i++) {
-                    const float after = before + v[i];
-                    if (before * (1 + off) < want && after * (1 + off) >= want) m.pick[0] = EACH * tid + i;
-                    if (before * (1 - off) < want && (after * (1 - off) >= want || EACH * tid + i == FINE - 1))
-                        atomicMax((unsigned long long *)&m.pick[1], (unsigned long long)(EACH * tid + i));
-                    before = after;
+                    after += v[i];
+                    if (may == FINE && after * (1 + off) >= want) may = EACH * tid + i;
+                    if (must == FINE && after * (1 - off) >= want) must = EACH * tid + i;
                 }
-                __syncthreads();
-                const float first_bin = (float)m.pick[0], last_bin = (float)m.pick[1];
-                __syncthreads();
+                const float first_bin = (float)~s.all(~may, 0u, Larger{});
+                const float last_bin = fminf((float)~s.all(~must, 0u, Larger{}), FINE - 1.0f);
                 if (first_bin < FINE && step < 0.125f) {
                     if (tid == 0) m.n = 0;
                     __syncthreads();

@@ -515,6 +515,29 @@ def test_sample_large_nuclei(ty, p, m, t):
     check_sample(z.to(TYPE[ty]).cuda(), noise(V + 3, 3, V), full(3, t), None, full(3, p), full(3, m) if m else None, allowed)
 
 
+def test_sample_nucleus_that_ends_where_two_threads_bins_meet():
+    """A large nucleus is counted in bins, some for each thread, and the running sums on both sides of a thread's
+    border round apart.  Rows (seed, index of its top_p) whose nucleus ends within such a difference; all the noise
+    is on the fourth token before the end."""
+    V = 40003
+    pairs = [(19, 1957), (20, 1737), (40, 677), (56, 239), (56, 1810), (94, 1260), (109, 779), (141, 1417), (151, 640),
+             (170, 287), (176, 1592), (207, 1745), (229, 1636), (247, 1307), (260, 314), (274, 1734), (291, 246),
+             (299, 2011), (315, 868), (327, 1743), (329, 750), (337, 1166), (339, 269), (375, 1774), (383, 531),
+             (387, 1259), (391, 533)]
+    z, p = np.empty((len(pairs), V), np.float32), np.empty(len(pairs), np.float32)
+    g = torch.zeros(len(pairs), V)
+    for row, (seed, at) in enumerate(pairs):
+        r = np.random.default_rng(seed)
+        z[row] = (r.standard_normal(V) * 2.5).astype(np.float32)
+        p[row] = r.uniform(0.6, 0.99, 2048).astype(np.float32)[at]
+        order = np.argsort(-z[row], kind="stable")
+        e = np.exp(z[row][order].astype(np.float64) - np.float64(z[row].max()))
+        before = np.cumsum(e) - e
+        g[row, order[np.searchsorted(before, np.float64(p[row]) * e.sum()) - 4]] = 50.0
+    B = len(pairs)
+    check_sample(torch.from_numpy(z).cuda(), g.cuda(), full(B, 1.0), None, torch.from_numpy(p).cuda())
+
+
 @pytest.mark.parametrize("ty", ["bf16", "f32"])
 def test_sample_masks(ty):
     B, V = 16, 3001
