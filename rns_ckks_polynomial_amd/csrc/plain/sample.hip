@@ -301,8 +301,12 @@ template <typename T> struct Sampler {
             if (bin == BINS) return 0;
             before = m.pick[1];
             b -= bin << shift;
-            a = shift && b - a >= (uint64_t)1 << shift ? b - (((uint64_t)1 << shift) - 1) : shift ? a : b;
+            a = b - a >= (uint64_t)1 << shift ? b - (((uint64_t)1 << shift) - 1) : a;
             __syncthreads();
+            if (!shift) {  // a bin is an order: at most six turns, whatever is on the list
+                until = before + inside;
+                return b;
+            }
             if (inside >> COUNT == 1) {  // whose order it is
 #pragma unroll
                 for (int i = 0; i < HELD; i++)
