@@ -112,6 +112,27 @@ def _stride(t):
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
+class _NoGradient(torch.autograd.Function):
+    """Hands results on as they are; a gradient through them, which nothing here computes, is an error."""
+    @staticmethod
+    def forward(ctx, name, results, *operands):
+        ctx.name = name
+        return results
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} has no gradient")
+
+
+def _tracked(*operands):
+    """Whether autograd follows one of the operands (None: no such operand)."""
+    if torch.is_grad_enabled():
+        for t in operands:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
 def _type(t, what):
     if t.dtype not in TYPES:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
@@ -210,11 +231,9 @@ def residual_norm(x, y, next_weight, next_bias=None, block_weight=None, block_bi
     """(h, u): the residual stream x takes the block output y, and its norm for the next block
     (ckks_plain_residual_norm).  n = y, or block_weight norm(y) + block_bias; h = x + scale gate n;
     u = next_weight norm(h) + next_bias.  x, y [T, D]; weights and biases [D]; gate [D] or [G, D]
-    (a row for T / G tokens each); one type for all.  Differentiable through torch.autograd (gradients of weights are
-    summed in 32 bits, then rounded to their type)."""
-    wants = lambda t: t is not None and t.requires_grad  # noqa: E731
-    if torch.is_grad_enabled() and (x.requires_grad or y.requires_grad or next_weight.requires_grad or wants(next_bias)
-                                    or wants(block_weight) or wants(block_bias) or wants(gate)):
+    (a row for T / G tokens each); one type for all.  Differentiable once through torch.autograd (gradients of weights
+    are summed in 32 bits, then rounded to their type; a second derivative raises)."""
+    if _tracked(x, y, next_weight, next_bias, block_weight, block_bias, gate):
         return _ResidualNorm.apply(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
     return _norm_forward(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
 
@@ -232,7 +251,8 @@ def residual_norm_i8(x, y, next_weight, next_bias=None, block_weight=None, block
 def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=None, block_bias=None, gate=None,
                        scale: float = 1.0, eps: float = 1e-6, kind: str = "rms") -> ResidualNormGrads:
     """Gradients of residual_norm's operands from those of h and u: dx and dy in the type of x, those
-    of weights, biases and gate (of the gate's shape) in float32, None where there is no such operand."""
+    of weights, biases and gate (of the gate's shape) in float32, None where there is no such operand.
+    They have no gradient of their own: a second derivative raises."""
     p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
     T, D = x.shape
     _matrix(dh, "dh", T, D, x.dtype, x.device)
@@ -246,6 +266,10 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
     _keep, ws, size = _scratch(_norm_grad_workspace(T, D, p.groups, next_bias is not None, block_weight is not None,
                                                     block_bias is not None), x.device)
     _call("ckks_plain_residual_norm_grad", x.device, C.byref(p), C.byref(g), ws, size)
+    operands = (x, y, dh, du, next_weight, next_bias, block_weight, block_bias, gate)
+    if _tracked(*operands):
+        some = iter(_NoGradient.apply("residual_norm_grad", tuple(v for v in r if v is not None), *operands))
+        r = ResidualNormGrads(*(v if v is None else next(some) for v in r))
     return r
 
 

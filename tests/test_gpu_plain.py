@@ -275,6 +275,26 @@ def test_residual_norm_autograd():
         assert torch.equal(leaf.grad, want.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("outer", ["linear", "square"])
+def test_residual_norm_has_first_derivatives_only(outer):
+    """A second derivative through the norm raises, also next to a path that has one: its terms would be missing."""
+    x, y, p = inputs(72, 4, 128, "f32", True, True, 0)
+    leaf = x.detach().clone().requires_grad_()
+    h, u = plain.residual_norm(leaf, y, kind="layer", **p)
+    loss = u.sum() + h.sum() if outer == "linear" else (u * u).sum()
+    g, = torch.autograd.grad(loss, leaf, create_graph=True)
+    first = plain.residual_norm_grad(x, y, *((torch.ones_like(x),) * 2 if outer == "linear" else
+                                             (torch.zeros_like(x), 2 * u.detach())), kind="layer", **p)
+    assert torch.equal(g.detach(), first.dx)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        ((g * g).sum() + (leaf ** 3).sum()).backward()
+    g = plain.residual_norm_grad(leaf, y, x, x, kind="layer", **p)
+    with pytest.raises(RuntimeError, match="no gradient"):
+        g.next_bias.sum().backward()
+    with torch.no_grad():
+        assert not plain.residual_norm_grad(leaf, y, x, x, kind="layer", **p).dx.requires_grad
+
+
 # ------------------------------------------------------------------ products
 
 def i8(seed, rows, cols, full=False):
