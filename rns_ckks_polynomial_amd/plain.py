@@ -5,6 +5,9 @@ Argument checks and marshalling only: every step of the computation runs in
 the HIP library.  Matrices are 2-D device tensors with unit column stride (any
 row stride); calls are enqueued on the current torch stream of the tensors'
 device, outputs and scratch come from torch's allocator.
+
+residual_norm has a gradient.  Results of the other calls have none: where autograd
+follows an operand, asking for a derivative through them raises.
 """
 from __future__ import annotations
 
@@ -245,6 +248,9 @@ def residual_norm_i8(x, y, next_weight, next_bias=None, block_weight=None, block
     h, u = _like(x), Int8Rows.empty(*x.shape, x.device)
     _call("ckks_plain_residual_norm_i8", x.device, C.byref(p), h.data_ptr(), x.shape[1], u.q.data_ptr(),
           u.q.shape[1], u.scale.data_ptr())
+    operands = (x, y, next_weight, next_bias, block_weight, block_bias, gate)
+    if _tracked(*operands):
+        h, u.q, u.scale = _NoGradient.apply("residual_norm_i8", (h, u.q, u.scale), *operands)
     return h, u
 
 
@@ -279,6 +285,8 @@ def quantize_rows(x) -> Int8Rows:
     r = Int8Rows.empty(x.shape[0], x.shape[1], x.device)
     _call("ckks_plain_quantize_rows", x.device, _type(x, "x"), x.data_ptr(), _stride(x), x.shape[0], x.shape[1],
           r.q.data_ptr(), r.q.shape[1], r.scale.data_ptr())
+    if _tracked(x):
+        r.q, r.scale = _NoGradient.apply("quantize_rows", (r.q, r.scale), x)
     return r
 
 
@@ -305,6 +313,8 @@ def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torc
     _keep, ws, size = _scratch(_workspace("ckks_plain_matmul_i8_workspace_size", M, N, a.cols), dev)
     _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), _stride(a.q), a.scale.data_ptr(), w.q.data_ptr(), _stride(w.q),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols, ws, size)
+    if _tracked(a.scale, w.scale, bias):
+        out, = _NoGradient.apply("matmul_i8", (out,), a.scale, w.scale, bias)
     return out
 
 
@@ -319,6 +329,8 @@ def linear_i8(x, w: Int8Rows, bias=None, dtype=None) -> torch.Tensor:
     _keep, ws, size = _scratch(_workspace("ckks_plain_linear_i8_workspace_size", M, N, K), dev)
     _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), _stride(x), w.q.data_ptr(), _stride(w.q),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, K, ws, size)
+    if _tracked(x, w.scale, bias):
+        out, = _NoGradient.apply("linear_i8", (out,), x, w.scale, bias)
     return out
 
 
@@ -344,4 +356,6 @@ def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allo
           _vector(min_p, "min_p", B, torch.float32, dev), None if allowed is None else allowed.data_ptr(),
           0 if allowed is None else _stride(allowed), B, V, token.data_ptr(), logprob.data_ptr(),
           ws, size)
+    if _tracked(logits, gumbel, temperature, top_p, min_p):
+        token, logprob = _NoGradient.apply("sample", (token, logprob), logits, gumbel, temperature, top_p, min_p)
     return token, logprob

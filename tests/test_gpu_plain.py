@@ -634,6 +634,43 @@ def test_sample_follows_the_distribution():
 
 # ------------------------------------------------------------------ use
 
+def test_results_without_a_gradient_say_so():
+    """Where autograd follows an operand the values are the same, and a derivative through them raises; elsewhere
+    nothing is attached."""
+    x, y, p = inputs(95, 4, 256, "f32", True, False, 0)
+    q, s = i8(96, 300, 256)
+    w = plain.Int8Rows(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda())
+    g = noise(97, 4, 300)
+
+    def results(x, nw, bias, temperature):
+        h, rows = plain.residual_norm_i8(x, y, **{**p, "next_weight": nw})
+        direct = plain.quantize_rows(x)
+        logits = plain.matmul_i8(rows, w, bias, torch.float32)
+        line = plain.linear_i8(x, w)
+        token, logprob = plain.sample(logits, g, temperature)
+        floats = {"residual_norm_i8": h, "residual_norm_i8 ": rows.scale, "quantize_rows": direct.dequantize(),
+                  "matmul_i8": logits, "linear_i8": line, "sample": logprob}
+        return floats, [rows.q, direct.q, token]
+
+    operands = (x, p["next_weight"], torch.ones(300, device="cuda"), full(4, 0.9))
+    want, whole = results(*operands)
+    assert not any(v.requires_grad for v in want.values())
+    for followed in range(4):
+        leaves = [v.clone().requires_grad_(i == followed) for i, v in enumerate(operands)]
+        with torch.no_grad():
+            got, _ = results(*leaves)
+            assert not any(v.requires_grad for v in got.values())
+        got, ints = results(*leaves)
+        assert all(torch.equal(a, b) and not a.requires_grad for a, b in zip(ints, whole))
+        reached = {0: want, 1: ["residual_norm_i8", "residual_norm_i8 ", "matmul_i8", "sample"], 2: ["matmul_i8", "sample"],
+                   3: ["sample"]}[followed]
+        for name, v in got.items():
+            assert torch.equal(v.detach(), want[name]) and v.requires_grad == (name in reached), (name, followed)
+            if v.requires_grad:
+                with pytest.raises(RuntimeError, match=f"{name.strip()} has no gradient"):
+                    v.sum().backward()
+
+
 def test_on_another_stream_and_in_a_graph():
     x, y, p = inputs(90, 4, 2048, "bf16", True, False, 0)
     qw, sw = i8(91, 4096, 2048)
