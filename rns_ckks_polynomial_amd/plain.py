@@ -7,7 +7,8 @@ row stride); calls are enqueued on the current torch stream of the tensors'
 device, outputs and scratch come from torch's allocator.
 
 residual_norm has a gradient.  Results of the other calls have none: where autograd
-follows an operand, asking for a derivative through them raises.
+follows an operand, asking for a derivative through them raises.  Operands with a
+tangent of forward-mode differentiation are refused by all of them.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ import functools
 from collections import namedtuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _native as nat
 
@@ -128,7 +130,10 @@ class _NoGradient(torch.autograd.Function):
 
 
 def _tracked(*operands):
-    """Whether autograd follows one of the operands (None: no such operand)."""
+    """Whether autograd may follow one of the operands (None: no such operand).  Tangents of forward mode do not
+    show in requires_grad; a Function refuses them, as none here has a rule for them."""
+    if forward_ad._current_level >= 0:
+        return True
     if torch.is_grad_enabled():
         for t in operands:
             if t is not None and t.requires_grad:

@@ -671,6 +671,29 @@ def test_results_without_a_gradient_say_so():
                     v.sum().backward()
 
 
+def test_forward_mode_is_refused():
+    """A tangent would be lost; next to none in the same level the values are as ever, under no_grad too."""
+    from torch.autograd import forward_ad
+    x, y, p = inputs(98, 4, 256, "f32", True, False, 0)
+    q, s = i8(99, 300, 256)
+    w = plain.Int8Rows(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda())
+    g, t = noise(97, 4, 256), full(4, 0.9)
+    calls = [lambda v: plain.residual_norm(v, y, **p)[1], lambda v: plain.residual_norm_i8(v, y, **p)[0],
+             lambda v: plain.residual_norm_grad(v, y, x, x, **p).dx, lambda v: plain.residual_norm(x, y, **{**p, "next_weight": v[0]})[1],
+             lambda v: plain.quantize_rows(v).scale, lambda v: plain.linear_i8(v, w), lambda v: plain.sample(v, g, t)[1],
+             lambda v: plain.matmul_i8(plain.Int8Rows(w.q[:4], v[:, 0].contiguous(), 256), w)]
+    want = [f(x) for f in calls]
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for f, v in zip(calls, want):
+            assert torch.equal(f(x), v)
+            with pytest.raises((RuntimeError, NotImplementedError), match="forward"):
+                f(dual)
+            with torch.no_grad(), pytest.raises((RuntimeError, NotImplementedError), match="forward"):
+                f(dual)
+    assert all(torch.equal(f(x), v) for f, v in zip(calls, want))
+
+
 def test_on_another_stream_and_in_a_graph():
     x, y, p = inputs(90, 4, 2048, "bf16", True, False, 0)
     qw, sw = i8(91, 4096, 2048)
