@@ -26,7 +26,7 @@
  *  - An output whose byte range overlaps an input's is rejected (CKKS_EINVAL)
  *    unless the call says otherwise.
  *  - Zero rows are valid; nothing is launched, except that gradients of
- *    weights are written (as zeros).
+ *    weights are written (as zeros).  There are fewer than 2^31.
  *  - Errors are the codes of ckks_gpu.h; arguments are validated before any
  *    launch.  CKKS_EALIGN: a pointer not aligned to its element type (8-bit
  *    rows: to 16 bytes).
@@ -118,8 +118,9 @@ int ckks_plain_quantize_rows(int type, const void *x, int64_t x_stride, int64_t 
 /* out[t][c] = a_scale[t] w_scale[c] sum_k a[t][k] w[c][k] + bias[c]: a is
  * [rows][cols], w [channels][cols] (both 8-bit rows as above), bias [channels]
  * in 32 bits or NULL, out [rows][channels] of out_type.  The sum is exact in
- * 32-bit integers: cols < 131072; a_stride and w_stride < 2^23.  ws: ckks_plain_matmul_i8_workspace_size
- * bytes, aligned to 16 (may be NULL where that is 0). */
+ * 32-bit integers: cols < 131072; a_stride and w_stride < 2^23; rows and
+ * channels <= 2^31 - 256.  ws: ckks_plain_matmul_i8_workspace_size bytes,
+ * aligned to 16 (may be NULL where that is 0). */
 int ckks_plain_matmul_i8_workspace_size(int64_t rows, int64_t channels, int64_t cols, size_t *bytes);
 int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
                          const float *w_scale, const float *bias, int out_type, void *out, int64_t out_stride,

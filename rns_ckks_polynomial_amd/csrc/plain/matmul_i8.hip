@@ -290,13 +290,16 @@ extern "C" int ckks_plain_matmul_i8_workspace_size(int64_t rows, int64_t channel
     return CKKS_OK;
 }
 
+constexpr int64_t MOST = ((int64_t)1 << 31) - 256;  // rows, channels
+
 // every check of a product with rows and channels
 static int check_matmul(const int8_t *a, int64_t a_stride, const float *a_scale, const int8_t *w, int64_t w_stride,
                         const float *w_scale, const float *bias, int out_type, void *out, int64_t out_stride,
                         int64_t rows, int64_t channels, int64_t cols, void *ws, size_t ws_bytes) {
     size_t need;
     if (int e = ckks_plain_matmul_i8_workspace_size(rows, channels, cols, &need)) return e;
-    if (!type_ok(out_type) || rows >= (int64_t)1 << 31 || channels >= (int64_t)1 << 31) return CKKS_EINVAL;
+    // 32-bit indexes of whole tiles, and of one store past them
+    if (!type_ok(out_type) || rows > MOST || channels > MOST) return CKKS_EINVAL;
     const size_t z = type_size(out_type);
     const int64_t padded = round_up(cols, CKKS_PLAIN_I8_ROW);
     if (!a || !w || !a_scale || !w_scale || a_stride < padded || w_stride < padded || a_stride % CKKS_PLAIN_I8_ROW ||
@@ -331,7 +334,7 @@ extern "C" int ckks_plain_matmul_i8(const int8_t *a, int64_t a_stride, const flo
     auto go = [&](auto ty) {
         typedef decltype(ty) T;
         const hipStream_t st = (hipStream_t)stream;
-        if (rows <= FEW) {
+        if (rows <= FEW && channels < (int64_t)1 << 30) {  // four threads a channel: fewer than 2^32 in all
             // up to eight waves share channels, while that does not make more than 32 a compute unit
             // and each has a batch of pieces
             const int groups = (int)((channels + 15) / 16);
@@ -392,7 +395,7 @@ extern "C" int ckks_plain_linear_i8(int type, const void *x, int64_t x_stride, c
     size_t need;
     if (int e = ckks_plain_linear_i8_workspace_size(rows, channels, cols, &need)) return e;
     if (rows == 0 || channels == 0) return CKKS_OK;
-    if (!type_ok(type) || rows >= (int64_t)1 << 31) return CKKS_EINVAL;
+    if (!type_ok(type) || rows > MOST) return CKKS_EINVAL;
     const size_t xb = span(rows, x_stride, cols, type_size(type));
     if (int e = check_matrix(x, x_stride, cols, type_size(type))) return e;
     if (!ws || ws_bytes < need) return CKKS_EWORKSPACE;

@@ -11,6 +11,7 @@ struct NormArgs {
     int cols;
     bool layer;
     float scale, eps;
+    int64_t first;  // row of the first workgroup
 };
 
 // Mean (0 for rms) and 1 / sqrt(mean square around it + eps) of a row in registers; the mean
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_residual_norm(NormArgs 
     typedef Row<T, NT, E> R;
     __shared__ float buf[5][16];
     const int t = NT == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t row = NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+    const int64_t row = a.first + (NT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x);
     if (row >= a.rows) return;
     float x[E], n[E], w[E];
     R::load((const T *)a.x + row * a.x_stride, a.cols, t, x);
@@ -441,7 +442,7 @@ bool norm_overlap(const ckks_plain_norm *p, const void *out, size_t bytes, bool 
 NormArgs args_of(const ckks_plain_norm *p) {
     return NormArgs{p->x, p->y, p->next_weight, p->next_bias, p->block_weight, p->block_bias, p->gate, p->rows,
                     p->x_stride, p->y_stride, p->groups ? p->rows / p->groups : p->rows, (int)p->cols,
-                    p->kind == CKKS_PLAIN_LAYER, p->scale, p->eps};
+                    p->kind == CKKS_PLAIN_LAYER, p->scale, p->eps, 0};
 }
 template <bool I8>
 int residual_norm(const ckks_plain_norm *p, void *h, int64_t h_stride, void *u, int64_t u_stride, float *q_scale,
@@ -466,14 +467,17 @@ int residual_norm(const ckks_plain_norm *p, void *h, int64_t h_stride, void *u, 
         if (norm_overlap(p, q_scale, sb, true) || overlap(q_scale, sb, u, ub) || overlap(q_scale, sb, h, hb))
             return CKKS_EINVAL;
     }
-    const NormArgs a = args_of(p);
+    NormArgs a = args_of(p);
     return by_rows(p->type, p->rows, p->cols, [&](auto ty, auto nt, auto e) {
         typedef decltype(ty) T;
         constexpr int NT = decltype(nt)::value;
-        const int64_t blocks = NT == 64 ? (p->rows + 3) / 4 : p->rows;
-        k_residual_norm<T, NT, decltype(e)::value, I8>
-            <<<dim3((uint32_t)blocks), NT == 64 ? 256 : NT, 0, s>>>(a, (T *)h, h_stride, u, u_stride, q_scale);
-        return launched();
+        return in_parts(p->rows, NT, [&](int64_t first, int64_t rows) {
+            a.first = first;
+            k_residual_norm<T, NT, decltype(e)::value, I8>
+                <<<dim3((uint32_t)(NT == 64 ? (rows + 3) / 4 : rows)), NT == 64 ? 256 : NT, 0, s>>>(
+                    a, (T *)h, h_stride, u, u_stride, q_scale);
+            return launched();
+        });
     });
 }
 
@@ -617,9 +621,12 @@ extern "C" int ckks_plain_quantize_rows(int type, const void *x, int64_t x_strid
     return by_rows(type, rows, cols, [&](auto ty, auto nt, auto e) {
         typedef decltype(ty) T;
         constexpr int NT = decltype(nt)::value;
-        k_quantize_rows<T, NT, decltype(e)::value>
-            <<<dim3((uint32_t)(NT == 64 ? (rows + 3) / 4 : rows)), NT == 64 ? 256 : NT, 0, (hipStream_t)stream>>>(
-                (const T *)x, x_stride, rows, (int)cols, q, q_stride, q_scale);
-        return launched();
+        return in_parts(rows, NT, [&](int64_t first, int64_t n) {
+            k_quantize_rows<T, NT, decltype(e)::value>
+                <<<dim3((uint32_t)(NT == 64 ? (n + 3) / 4 : n)), NT == 64 ? 256 : NT, 0, (hipStream_t)stream>>>(
+                    (const T *)x + first * x_stride, x_stride, n, (int)cols, q + first * q_stride, q_stride,
+                    q_scale + first);
+            return launched();
+        });
     });
 }

@@ -202,6 +202,13 @@ inline int check_matrix(const void *p, int64_t stride, int64_t cols, size_t size
     if (!p || stride < cols) return CKKS_EINVAL;
     return at(p, size) ? CKKS_OK : CKKS_EALIGN;
 }
+// A grid holds fewer than 2^32 threads: f(first row, rows) for each part of the rows, `threads` a row.
+template <typename F> int in_parts(int64_t rows, int threads, F f) {
+    const int64_t most = ((int64_t)1 << 31) / threads / 4 * 4;  // whole workgroups, also of four rows
+    for (int64_t first = 0; first < rows; first += most)
+        if (int e = f(first, rows - first < most ? rows - first : most)) return e;
+    return CKKS_OK;
+}
 inline int launched() { return hipGetLastError() == hipSuccess ? CKKS_OK : CKKS_EHIP; }
 
 }  // namespace ckks_plain

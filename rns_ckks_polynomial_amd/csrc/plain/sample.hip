@@ -719,11 +719,17 @@ extern "C" int ckks_plain_sample(int type, const void *logits, int64_t logits_st
     if (need && (!ws || ws_bytes < need)) return CKKS_EWORKSPACE;
     int bits = 0;
     while (((int64_t)1 << bits) < vocab) bits++;
-    const SampleArgs a{logits, gumbel, temperature, top_p, min_p, top_k, allowed, logits_stride, gumbel_stride,
-                       allowed_stride, (int)vocab, bits, token, logprob};
     auto go = [&](auto ty) {
-        k_sample<decltype(ty)><<<dim3((uint32_t)rows), NT, 0, (hipStream_t)stream>>>(a);
-        return launched();
+        typedef decltype(ty) T;
+        return in_parts(rows, NT, [&](int64_t first, int64_t n) {
+            auto from = [&](auto *p, int64_t at) { return p ? p + at : nullptr; };
+            const SampleArgs a{(const T *)logits + first * logits_stride, gumbel + first * gumbel_stride,
+                               temperature + first, from(top_p, first), from(min_p, first), from(top_k, first),
+                               from(allowed, first * allowed_stride), logits_stride, gumbel_stride, allowed_stride,
+                               (int)vocab, bits, token + first, logprob + first};
+            k_sample<T><<<dim3((uint32_t)n), NT, 0, (hipStream_t)stream>>>(a);
+            return launched();
+        });
     };
     return type == CKKS_PLAIN_BF16 ? go(bf16{}) : type == CKKS_PLAIN_F16 ? go(f16{}) : go(0.0f);
 }

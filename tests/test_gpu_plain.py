@@ -632,6 +632,56 @@ def test_sample_follows_the_distribution():
     assert (np.abs(got - n * p) <= 5 * np.sqrt(n * p * (1 - p)) + 1e-9).all(), (got, n * p)
 
 
+# ------------------------------------------------------------------ more rows than a grid has threads for
+
+@pytest.fixture
+def memory_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def same_in_parts(call, rows, border):
+    """call(slice) of all rows against calls of the rows around `border` and at both ends, bit for bit."""
+    whole = call(slice(0, rows))
+    for at in (slice(0, 1000), slice(border - 500, border + 500), slice(rows - 1000, rows)):
+        for a, b in zip(whole, call(at)):
+            assert torch.equal(a[at], b)
+
+
+def test_sample_of_millions_of_rows(memory_back):
+    B, V = (1 << 22) + 37, 3
+    z, g = torch.randn(B, V, device="cuda"), torch.rand(B, V, device="cuda")
+    t, k, p, m = torch.rand(B, device="cuda"), full(B, 2, torch.int32), torch.rand(B, device="cuda"), full(B, 0.1)
+    allowed = torch.rand(B, V, device="cuda") < 0.7
+    same_in_parts(lambda r: plain.sample(z[r], g[r], t[r], k[r], p[r], m[r], allowed[r]), B, 1 << 21)
+    same_in_parts(lambda r: plain.sample(z[r], g[r], t[r]), B, 1 << 22)
+
+
+def test_norms_of_millions_of_rows(memory_back):
+    T, D, border = (1 << 26) + 37, 2, 1 << 25
+    x, y, gate = (torch.randn(T, D, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    w = torch.ones(D, device="cuda", dtype=torch.bfloat16)
+    rows = lambda r: (r.q, r.scale)  # noqa: E731
+    same_in_parts(lambda r: plain.residual_norm(x[r], y[r], w, gate=gate[r]), T, border)
+    same_in_parts(lambda r: rows(plain.quantize_rows(x[r])), T, border)
+    same_in_parts(lambda r: rows(plain.residual_norm_i8(x[r], y[r], w, gate=gate[r])[1]), T, border)
+
+
+def test_product_of_a_billion_channels(memory_back):
+    """One token; 137 GB of weights, all zero but the last."""
+    N = 1 << 30
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GiB free")
+    w, s = torch.zeros((N, 128), dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda")
+    q, _ = i8(100, 1000, 128)
+    w[-1000:] = torch.from_numpy(q).cuda()
+    a, sa = i8(101, 1, 128)
+    out = plain.matmul_i8(plain.Int8Rows(torch.from_numpy(a).cuda(), torch.from_numpy(sa).cuda()), plain.Int8Rows(w, s))
+    ref = product_ref(a, sa, q, np.ones(1000, np.float32), None)
+    close(out[:, -1000:], ref, np.abs(ref), 4, "bf16", "out")
+    assert not out[:, :-1000].any()
+
+
 # ------------------------------------------------------------------ use
 
 def test_results_without_a_gradient_say_so():

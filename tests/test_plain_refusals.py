@@ -182,3 +182,11 @@ def test_binding_wants_device_matrices():
         plain.matmul_i8(x, x)
     with pytest.raises(ValueError, match="device tensor|Int8Rows"):
         plain.linear_i8(x, x)
+
+
+@pytest.mark.parametrize("kw", [dict(rows=(1 << 31) - 255), dict(channels=(1 << 31) - 255, out_stride=1 << 31)])
+def test_products_whose_indexes_pass_32_bits(kw):
+    far = {"out": 1 << 60, "a": 1 << 50, "w": 1 << 52}  # nothing overlaps at any size
+    assert nat.lib().ckks_plain_matmul_i8(*{**MM, **far, **kw}.values(), None) == INV
+    far = {"out": 1 << 60, "x": 1 << 50, "w": 1 << 52, "ws": 1 << 55, "ws_bytes": 1 << 54}
+    assert nat.lib().ckks_plain_linear_i8(*{**LIN, **far, **kw}.values(), None) == INV
