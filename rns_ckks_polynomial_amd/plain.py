@@ -3,7 +3,7 @@ stream and norms around a block, products of 8-bit rows, and token sampling.
 
 Argument checks and marshalling only: every step of the computation runs in
 the HIP library.  Matrices are 2-D device tensors with unit column stride (any
-row stride); calls are enqueued on the current torch stream of the tensors'
+row stride of at least their columns); calls are enqueued on the current torch stream of the tensors'
 device, outputs and scratch come from torch's allocator.
 
 residual_norm has a gradient.  Results of the other calls have none: where autograd
@@ -164,7 +164,7 @@ class Int8Rows:
             raise ValueError(f"cols: {cols} of {q.shape[1]}")
         _vector(scale, "scale", q.shape[0], torch.float32, q.device)
         padded = -(-cols // I8_ROW) * I8_ROW
-        if q.shape[1] < padded or q.stride(1) != 1 or q.stride(0) % I8_ROW or q.data_ptr() % 16:
+        if q.shape[1] < padded or q.stride(1) != 1 or q.stride(0) % I8_ROW or q.stride(0) < padded or q.data_ptr() % 16:
             rows = torch.zeros((q.shape[0], padded), dtype=torch.int8, device=q.device)
             rows[:, :cols] = q[:, :cols]
             q = rows
@@ -316,7 +316,7 @@ def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torc
     M, N = a.rows, w.rows
     out = torch.empty((M, N), dtype=dtype, device=dev)
     _keep, ws, size = _scratch(_workspace("ckks_plain_matmul_i8_workspace_size", M, N, a.cols), dev)
-    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), _stride(a.q), a.scale.data_ptr(), w.q.data_ptr(), _stride(w.q),
+    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), a.q.stride(0), a.scale.data_ptr(), w.q.data_ptr(), w.q.stride(0),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols, ws, size)
     if _tracked(a.scale, w.scale, bias):
         out, = _NoGradient.apply("matmul_i8", (out,), a.scale, w.scale, bias)
@@ -332,7 +332,7 @@ def linear_i8(x, w: Int8Rows, bias=None, dtype=None) -> torch.Tensor:
     N = w.rows
     out = torch.empty((M, N), dtype=dtype, device=dev)
     _keep, ws, size = _scratch(_workspace("ckks_plain_linear_i8_workspace_size", M, N, K), dev)
-    _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), _stride(x), w.q.data_ptr(), _stride(w.q),
+    _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), _stride(x), w.q.data_ptr(), w.q.stride(0),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, K, ws, size)
     if _tracked(x, w.scale, bias):
         out, = _NoGradient.apply("linear_i8", (out,), x, w.scale, bias)

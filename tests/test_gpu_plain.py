@@ -366,6 +366,21 @@ def test_matmul_i8_layouts():
     assert plain.matmul_i8(plain.Int8Rows(t.q[:0], s[:0], 300), w).shape == (0, 50)
 
 
+def test_int8_rows_of_any_stride():
+    """Rows that lie over each other (a row repeated), and a single row whose stride says nothing."""
+    qa, sa = i8(31, 1, 300)
+    qw, sw = i8(32, 40, 300)
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    w = plain.Int8Rows(dev(qw), dev(sw))
+    ref = product_ref(qa, sa, qw, sw, None)
+    buf = torch.zeros(1024, dtype=torch.int8, device="cuda")
+    buf[:300] = dev(qa)[0]
+    for rows, width, stride in ((5, 384, 0), (5, 400, 0), (1, 400, 0), (1, 384, 128), (1, 400, 128), (1, 400, 384), (1, 400, 7)):
+        a = plain.Int8Rows(buf.as_strided((rows, width), (stride, 1)), dev(np.repeat(sa, rows)), 300)
+        for out in (plain.matmul_i8(a, w, dtype=torch.float32), plain.matmul_i8(w, a, dtype=torch.float32).t()):
+            close(out, np.repeat(ref, rows, 0), np.repeat(np.abs(ref), rows, 0), 4, "f32", f"{rows} x {width} by {stride}")
+
+
 def test_matmul_i8_offsets_past_32_bits():
     """Weights of 2.3 GB and an output of 4.4 GB: the last rows, and the last token's channels."""
     N, K = 1 << 16, 35000
