@@ -151,10 +151,13 @@ class Int8Rows:
     """8-bit rows: row t stands for scale[t] * q[t, :cols].
 
     q: int8 [rows, >= cols rounded up to I8_ROW] with rows that start at multiples of I8_ROW bytes
-    and zeros behind the columns (at least in one operand of a product) is kept as it is; any other
-    layout is copied into such rows once, here.  scale: float32 [rows]."""
+    is kept as it is; any other layout is copied into such rows once, here.  scale: float32 [rows].
 
-    __slots__ = ("q", "scale", "cols")
+    Kernels multiply whole pieces of I8_ROW bytes, so one operand of a product has to hold zeros behind
+    the columns.  Rows made here do.  What lies there in rows kept as they are is not looked at (that
+    would wait for the GPU): a product of two such operands takes a copy of the smaller."""
+
+    __slots__ = ("q", "scale", "cols", "_ends_in_zeros")
 
     def __init__(self, q: torch.Tensor, scale: torch.Tensor, cols: int | None = None):
         if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != torch.int8 or q.dim() != 2:
@@ -164,18 +167,23 @@ class Int8Rows:
             raise ValueError(f"cols: {cols} of {q.shape[1]}")
         _vector(scale, "scale", q.shape[0], torch.float32, q.device)
         padded = -(-cols // I8_ROW) * I8_ROW
+        self.q, self.scale, self.cols, self._ends_in_zeros = q, scale, cols, cols == padded
         if q.shape[1] < padded or q.stride(1) != 1 or q.stride(0) % I8_ROW or q.stride(0) < padded or q.data_ptr() % 16:
-            rows = torch.zeros((q.shape[0], padded), dtype=torch.int8, device=q.device)
-            rows[:, :cols] = q[:, :cols]
-            q = rows
-        self.q, self.scale, self.cols = q, scale, cols
+            self.q, self._ends_in_zeros = self._copy(), True
+
+    def _copy(self) -> torch.Tensor:
+        """The columns in rows of whole pieces, zeros behind them."""
+        rows = torch.zeros((self.q.shape[0], -(-self.cols // I8_ROW) * I8_ROW), dtype=torch.int8, device=self.q.device)
+        rows[:, :self.cols] = self.q[:, :self.cols]
+        return rows
 
     @staticmethod
     def empty(rows: int, cols: int, device) -> "Int8Rows":
+        """For a call that writes whole rows, zeros behind the columns included."""
         self = object.__new__(Int8Rows)
         self.q = torch.empty((rows, -(-cols // I8_ROW) * I8_ROW), dtype=torch.int8, device=device)
         self.scale = torch.empty(rows, dtype=torch.float32, device=device)
-        self.cols = cols
+        self.cols, self._ends_in_zeros = cols, True
         return self
 
     @property
@@ -316,7 +324,10 @@ def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torc
     M, N = a.rows, w.rows
     out = torch.empty((M, N), dtype=dtype, device=dev)
     _keep, ws, size = _scratch(_workspace("ckks_plain_matmul_i8_workspace_size", M, N, a.cols), dev)
-    _call("ckks_plain_matmul_i8", dev, a.q.data_ptr(), a.q.stride(0), a.scale.data_ptr(), w.q.data_ptr(), w.q.stride(0),
+    aq, wq = a.q, w.q
+    if not (a._ends_in_zeros or w._ends_in_zeros):
+        aq, wq = (a._copy(), wq) if M <= N else (aq, w._copy())
+    _call("ckks_plain_matmul_i8", dev, aq.data_ptr(), aq.stride(0), a.scale.data_ptr(), wq.data_ptr(), wq.stride(0),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, a.cols, ws, size)
     if _tracked(a.scale, w.scale, bias):
         out, = _NoGradient.apply("matmul_i8", (out,), a.scale, w.scale, bias)

@@ -381,6 +381,24 @@ def test_int8_rows_of_any_stride():
             close(out, np.repeat(ref, rows, 0), np.repeat(np.abs(ref), rows, 0), 4, "f32", f"{rows} x {width} by {stride}")
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 70, 300), (40, 70, 129), (300, 200, 1)])
+def test_product_of_rows_with_something_behind_the_columns(M, N, K):
+    qa, sa = i8(41, M, K)
+    qw, sw = i8(42, N, K)
+    dev = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    ref = product_ref(qa, sa, qw, sw, None)
+    wide = [torch.full((n, 512), 77, dtype=torch.int8, device="cuda") for n in (M, N)]
+    for buf, q in zip(wide, (qa, qw)):
+        buf[:, :K] = dev(q)
+    a, w = plain.Int8Rows(wide[0], dev(sa), K), plain.Int8Rows(wide[1], dev(sw), K)
+    assert a.q.data_ptr() == wide[0].data_ptr() and w.q.data_ptr() == wide[1].data_ptr()
+    clean = plain.Int8Rows(dev(qa), dev(sa)), plain.Int8Rows(dev(qw), dev(sw))
+    for one, other in ((a, w), (a, clean[1]), (clean[0], w)):
+        close(plain.matmul_i8(one, other, dtype=torch.float32), ref, np.abs(ref), 4, "f32", "out")
+    x = rnd(43, M, K).cuda().float()
+    assert torch.equal(plain.linear_i8(x, w), plain.linear_i8(x, clean[1]))
+
+
 def test_matmul_i8_offsets_past_32_bits():
     """Weights of 2.3 GB and an output of 4.4 GB: the last rows, and the last token's channels."""
     N, K = 1 << 16, 35000
