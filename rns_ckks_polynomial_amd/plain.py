@@ -136,7 +136,7 @@ def _tracked(*operands):
         return True
     if torch.is_grad_enabled():
         for t in operands:
-            if t is not None and t.requires_grad:
+            if getattr(t, "requires_grad", False):
                 return True
     return False
 
@@ -204,6 +204,8 @@ def _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, e
         raise ValueError(f"kind: expected 'rms' or 'layer', got {kind!r}")
     groups, gp = 0, None
     if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise ValueError("gate: expected a device tensor")
         if gate.dim() == 1:
             groups, gp = 1, _vector(gate, "gate", D, dt, dev)
         else:

@@ -824,3 +824,19 @@ def test_binding_refusals():
                       (lambda: plain.sample(x, x, w[:4], top_k=w[:4]), "top_k")]:
         with pytest.raises(ValueError, match=what):
             bad()
+
+
+def test_binding_refuses_what_is_no_tensor():
+    x, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    rows = plain.quantize_rows(x)
+    for bad, what in [(lambda: plain.residual_norm([1.0], x, w), "x"), (lambda: plain.residual_norm(x, 1.0, w), "y"),
+                      (lambda: plain.residual_norm(x, x, [1.0] * 64), "next_weight"),
+                      (lambda: plain.residual_norm(x, x, w, gate=[1.0] * 64), "gate"),
+                      (lambda: plain.residual_norm_i8(x, x, w, gate=0.5), "gate"),
+                      (lambda: plain.residual_norm_grad(x, x, None, x, w), "dh"),
+                      (lambda: plain.quantize_rows([1.0]), "x"), (lambda: plain.linear_i8(None, rows), "x"),
+                      (lambda: plain.matmul_i8(rows, x), "w"), (lambda: plain.matmul_i8(rows, rows, bias=[0.0] * 4), "bias"),
+                      (lambda: plain.sample(None, x, w), "logits"), (lambda: plain.sample(x, None, w), "gumbel"),
+                      (lambda: plain.sample(x, x, [1.0] * 4), "temperature")]:
+        with pytest.raises(ValueError, match=what):
+            bad()
