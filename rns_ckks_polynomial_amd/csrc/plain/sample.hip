@@ -114,12 +114,26 @@ template <typename T> struct Sampler {
     // ---- the row
     // f(first index, logits) for this thread's vectors; a token that is not possible has -infinity.
     // Rows need no alignment beyond their elements'.
+    // NaN: -infinity.  The compiler takes a widened bfloat16 for a quiet number, so the larger of a signalling
+    // NaN and -infinity would be a NaN; of bits in a float's place it assumes nothing.
+    static __device__ __forceinline__ float value(T z) {
+        if constexpr (std::is_same<T, bf16>::value) return upper((uint32_t)__builtin_bit_cast(uint16_t, z) << 16);
+        return fmaxf(to_f32(z), -INFINITY);
+    }
+    static __device__ __forceinline__ float upper(uint32_t bits) { return fmaxf(__uint_as_float(bits), -INFINITY); }
     __device__ __forceinline__ void logits(const Vec &r, const Mask &k, float (&x)[N]) const {
+        if constexpr (std::is_same<T, bf16>::value) {  // two of a word: a shift, and a mask
+            typedef uint32_t Words __attribute__((ext_vector_type(4)));
+            const Words w = __builtin_bit_cast(Words, r);
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            x[i] = fmaxf(to_f32(r[i]), -INFINITY);  // NaN: -infinity
-            if (ok) x[i] = k[i] ? x[i] : -INFINITY;
+            for (int i = 0; i < N; i++) x[i] = upper(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i++) x[i] = value(r[i]);
         }
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (ok) x[i] = k[i] ? x[i] : -INFINITY;
     }
     template <typename F> __device__ __forceinline__ void rest(F f) const {  // the last, broken vector
         const int whole = a.vocab / N, rest = a.vocab % N;
@@ -128,7 +142,7 @@ template <typename T> struct Sampler {
 #pragma unroll
         for (int k = 0; k < N; k++) {
             const bool there = k < rest && (!ok || ok[whole * N + k]);
-            x[k] = there ? fmaxf(to_f32(z[whole * N + k]), -INFINITY) : -INFINITY;
+            x[k] = there ? value(z[whole * N + k]) : -INFINITY;
         }
         f(whole * N, x);
     }

@@ -15,7 +15,7 @@ import plain_ref
 from gpu_util import require_gpu, say, torch
 from rns_ckks_polynomial_amd import _native as nat
 from rns_ckks_polynomial_amd import plain
-from test_gpu_plain import EPS, TYPE, close, f64, forward_sizes, i8, inputs, product_ref, ref_args, rnd, top, wide
+from test_gpu_plain import EPS, TYPE, check_sample, close, f64, forward_sizes, full, i8, inputs, noise, product_ref, ref_args, rnd, top, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -233,3 +233,21 @@ def test_products_write_their_channels_only(M, ty, N, pad):
                                           None, 0, torch.cuda.current_stream().cuda_stream) == 0
     assert untouched(out, M, N, 7)
     assert torch.equal(out[1:M + 1, :N], plain.matmul_i8(a, w, dtype=TYPE[ty]))
+
+
+# ------------------------------------------------------------------ sampling
+
+@pytest.mark.parametrize("ty,bits", [("bf16", 0x7f81), ("f16", 0x7c01), ("f32", 0x7f800001)])
+def test_sample_signalling_nan(ty, bits):
+    """A NaN of either kind and sign is not possible, masked or not."""
+    B, V = 4, 5003
+    whole = torch.int32 if ty == "f32" else torch.int16
+    z = (rnd(7, B, V) * 2).to(TYPE[ty]).cuda()
+    sign = -(1 << 31) if ty == "f32" else -(1 << 15)
+    z.view(whole)[:, ::3] = bits
+    z.view(whole)[:, 1::7] = bits + sign
+    z.view(whole)[3] = bits
+    t = torch.tensor([0.0, 0.8, 0.8, 0.8], device="cuda")
+    for k, p, m in ((0, 1.0, 0.0), (40, 0.9, 0.0), (0, 0.95, 0.01)):
+        token = check_sample(z, noise(8, B, V), t, full(B, k, torch.int32), full(B, p), full(B, m))
+        assert token[3] == -1
