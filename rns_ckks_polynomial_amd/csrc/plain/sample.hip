@@ -76,6 +76,7 @@ template <typename T> struct Sampler {
     int wave, slot;
     float t, c, top;   // temperature, log2(e) / temperature, the largest logit
     float sum, min_p;  // the mass
+    float least;       // log2 of min_p, -infinity without
 
     // ---- the order of tokens: the logit as an unsigned number of the same order, without the bits
     // that its type never sets, then the complement of the index; 0: a token that is not possible
@@ -188,7 +189,8 @@ template <typename T> struct Sampler {
     }
     __device__ __forceinline__ int mass_bits() const { return 62 - a.index_bits; }  // a row's sum fits
     __device__ __forceinline__ uint64_t mass(float v) const { return fixed(weight(v, top), mass_bits()); }
-    __device__ __forceinline__ bool too_small(float v) const { return min_p > 0 && weight(v, top) < min_p; }
+    // e < min_p, by the exponents: e of a high temperature rounds to 1 where it is less, and is not min_p = 1
+    __device__ __forceinline__ bool too_small(float v) const { return (v - top) * c < least; }
     // the distance to the largest logit, as defined: each step rounded to 32 bits
     __device__ __forceinline__ float part(float v) const { return v == top ? 0.0f : (v - top) / t; }
     // the score and the complement of the index: the largest is the answer
@@ -484,6 +486,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
     S s{a, m, (const T *)a.logits + row * a.logits_stride, a.allowed ? a.allowed + row * a.allowed_stride : nullptr,
         a.gumbel + row * a.gumbel_stride, (int)__builtin_amdgcn_readfirstlane(tid >> 6), 0, greedy ? 1.0f : temp};
     s.min_p = a.min_p ? a.min_p[row] : 0.0f;
+    s.least = s.min_p > 0 ? log2f(s.min_p) : -INFINITY;
     // from 2^-120 on a product with -infinity stays that, up to 2^126 one with 0 stays 0 (but for
     // subnormal differences of logits neither bound is felt)
     s.c = fminf(fmaxf(1.44269504f / s.t, 0x1p-120f), 0x1p126f);

@@ -251,3 +251,22 @@ def test_sample_signalling_nan(ty, bits):
     for k, p, m in ((0, 1.0, 0.0), (40, 0.9, 0.0), (0, 0.95, 0.01)):
         token = check_sample(z, noise(8, B, V), t, full(B, k, torch.int32), full(B, p), full(B, m))
         assert token[3] == -1
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [50, 3000, 60001])
+@pytest.mark.parametrize("k,p", [(0, 1.0), (0, 0.9), (40, 1.0), (2500, 0.9)])
+def test_sample_min_p_of_one(ty, V, k, p):
+    """Only equals of the largest logit stay, also where a temperature of thousands leaves e less than 2^-24 below 1;
+    the noise is on the second largest value, then on the last of the equals, then spread."""
+    B, r = 9, np.random.default_rng(V)
+    z = np.round(-r.exponential(1, (B, V)) * 512) / 4096 - 1 / 4096   # many near the top, in every type's steps
+    z[:, r.permutation(V)[:6]] = 0
+    z = torch.from_numpy(z).to(TYPE[ty]).cuda()
+    ranked = np.argsort(-z.float().cpu().numpy(), axis=1, kind="stable")
+    g = noise(V, B, V)
+    for row in range(6):
+        g[row, ranked[row, 6 if row < 3 else 5]] = 50.0
+    t = torch.tensor([1.0, 1e3, 1e6] * 3, device="cuda")
+    token = check_sample(z, g, t, full(B, k, torch.int32), full(B, p), full(B, 1.0))
+    assert (z.gather(1, token[:, None]) == 0).all()
