@@ -270,3 +270,22 @@ def test_sample_min_p_of_one(ty, V, k, p):
     t = torch.tensor([1.0, 1e3, 1e6] * 3, device="cuda")
     token = check_sample(z, g, t, full(B, k, torch.int32), full(B, p), full(B, 1.0))
     assert (z.gather(1, token[:, None]) == 0).all()
+
+
+@pytest.mark.parametrize("ty,k,p", [("f32", 0, 0.5), ("bf16", 3000, 0.9)])
+def test_sample_largest_vocabulary(ty, k, p):
+    """2^24 tokens, the most there may be: a greedy row, a peaked one, one whose noise is on the last token."""
+    B, V = 3, 1 << 24
+    say(f"sample {B}x{V} {ty} top_k={k} top_p={p}")
+    z = (rnd(5, 1, V) * 2.5).to(TYPE[ty]).cuda().repeat(B, 1)
+    z[2, V - 1] = z[2].max()
+    g = noise(6, 1, V).repeat(B, 1)
+    g[2, V - 1] = 60.0
+    t = torch.tensor([0.0, 0.3, 0.5], device="cuda")
+    k, p = full(B, k, torch.int32) if k else None, full(B, p)
+    token, logprob = plain.sample(z, g, t, k, p)
+    host = lambda v: None if v is None else v.cpu().float().numpy()  # noqa: E731
+    want, ref = plain_ref.sample(host(z), host(g), host(t), host(k), host(p))
+    assert np.array_equal(token.cpu().numpy(), want) and want[2] == V - 1
+    # as everywhere, and a thread's sum of V / 1024 terms in order: each addition rounds
+    assert (np.abs(f64(logprob) - ref) <= 2.0 ** -22 * (2 + 2 * np.abs(ref)) + V / 1024 * EPS).all()
