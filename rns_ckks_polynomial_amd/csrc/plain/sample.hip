@@ -548,8 +548,9 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
             if (before < (uint32_t)k && (uint32_t)k <= before + v) m.pick[0] = tid;
             __syncthreads();
             const int at = (int)m.pick[0];
-            // the bin's lower edge, and all that the edge may be off by
-            if (at < NT) low = fmaxf(least, s.top - (float)(at + 1) * (range / NT) * 1.00001f - fabsf(s.top) * 1e-6f);
+            // the bin's lower edge, and all that the edge may be off by (a part of the range, as a bin's width may be
+            // less than the smallest number)
+            if (at < NT) low = fmaxf(least, s.top - range * ((float)(at + 1) / NT) * 1.00001f - fabsf(s.top) * 1e-6f);
         } else if (by_mass) {
             low = s.top + (__log2f((1.0f - p) * s.sum / (float)a.vocab) - 0.0625f) / s.c;
         }
@@ -578,7 +579,7 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
             __syncthreads();
             const int at = (int)m.pick[0];
             if (at < FINE - 1)  // the last bin has what is below the range too
-                low = fmaxf(low, s.top - (float)(at + 1) * (range / FINE) * 1.00001f - fabsf(s.top) * 1e-6f);
+                low = fmaxf(low, s.top - range * ((float)(at + 1) / FINE) * 1.00001f - fabsf(s.top) * 1e-6f);
         }
         uint32_t n = LIST + 1;
         if (by_count || a.vocab <= LIST || passing <= NT - 24) n = s.gather(low);

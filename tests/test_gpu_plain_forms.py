@@ -289,3 +289,18 @@ def test_sample_largest_vocabulary(ty, k, p):
     assert np.array_equal(token.cpu().numpy(), want) and want[2] == V - 1
     # as everywhere, and a thread's sum of V / 1024 terms in order: each addition rounds
     assert (np.abs(f64(logprob) - ref) <= 2.0 ** -22 * (2 + 2 * np.abs(ref)) + V / 1024 * EPS).all()
+
+
+@pytest.mark.parametrize("unit", [2.0 ** -149, 2.0 ** -140, 2.0 ** -126, 2.0 ** -118, 2.0 ** -100, 2.0 ** 100])
+@pytest.mark.parametrize("V", [3000, 20011])
+def test_sample_top_k_of_tiny_and_huge_steps(unit, V):
+    """The first k are found by the order alone, whatever the logits' scale (the bounds' arithmetic loses digits in
+    subnormal numbers).  The noise is on the k-th token, then on the next, then spread."""
+    B, r = 9, np.random.default_rng(V)
+    z = (r.integers(-200, 201, (B, V)) * unit).astype(np.float32)
+    k = np.array([5, 50, 500] * 3, np.int32)
+    g = noise(V, B, V)
+    ranked = np.argsort(-z, axis=1, kind="stable")
+    for row in range(6):
+        g[row, ranked[row, k[row] - (row < 3)]] = 50.0
+    check_sample(torch.from_numpy(z).cuda(), g, full(B, unit if unit > 1e-35 else 1.0), torch.from_numpy(k).cuda())
