@@ -656,7 +656,8 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
                 }
                 const float first_bin = (float)~s.all(~may, 0u, Larger{});
                 const float last_bin = fminf((float)~s.all(~must, 0u, Larger{}), FINE - 1.0f);
-                if (first_bin < FINE && step < 0.125f) {
+                // (a range under 2.4e-35 has no such width in 32 bits: its bins are the largest logit's and the rest)
+                if (first_bin < FINE && step < 0.125f && width < INFINITY) {
                     if (tid == 0) m.n = 0;
                     __syncthreads();
                     float above;

@@ -304,3 +304,19 @@ def test_sample_top_k_of_tiny_and_huge_steps(unit, V):
     for row in range(6):
         g[row, ranked[row, k[row] - (row < 3)]] = 50.0
     check_sample(torch.from_numpy(z).cuda(), g, full(B, unit if unit > 1e-35 else 1.0), torch.from_numpy(k).cuda())
+
+
+def test_sample_nucleus_over_a_range_too_narrow_for_bins():
+    """3000 equals and the first token behind them, at a temperature of 10^-37: that token's noise decides."""
+    V, n, r = 40003, 3000, np.random.default_rng(3)
+    t = np.float32(1e-37)
+    z = np.float32(-1) * (r.exponential(6, V).astype(np.float32) + np.float32(0.5)) * t
+    z[r.permutation(V)[:n]] = 0
+    e = np.exp(z.astype(np.float64) / np.float64(t))
+    behind = np.argsort(-z, kind="stable")[n]
+    p = np.float32([n * (1 + 5e-5) / e.sum(), (n + 0.5 + e[behind]) / e.sum(), 0.9 * n / e.sum()])
+    g = torch.zeros(3, V)
+    g[:, behind] = 50.0
+    z = torch.from_numpy(np.repeat(z[None], 3, 0)).cuda()
+    token = check_sample(z, g.cuda(), full(3, float(t)), None, torch.from_numpy(p).cuda())
+    assert token[0] == behind and token[1] == behind and token[2] != behind
