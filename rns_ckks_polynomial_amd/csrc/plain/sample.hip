@@ -487,9 +487,9 @@ template <typename T> __global__ __launch_bounds__(NT) void k_sample(SampleArgs 
         a.gumbel + row * a.gumbel_stride, (int)__builtin_amdgcn_readfirstlane(tid >> 6), 0, greedy ? 1.0f : temp};
     s.min_p = a.min_p ? a.min_p[row] : 0.0f;
     s.least = s.min_p > 0 ? log2f(s.min_p) : -INFINITY;
-    // from 2^-120 on a product with -infinity stays that, up to 2^126 one with 0 stays 0 (but for
-    // subnormal differences of logits neither bound is felt)
-    s.c = fminf(fmaxf(1.44269504f / s.t, 0x1p-120f), 0x1p126f);
+    // above 0 a product with -infinity stays that, up to 2^126 one with 0 stays 0 (felt by subnormal differences
+    // of logits alone)
+    s.c = fminf(fmaxf(1.44269504f / s.t, 0x1p-149f), 0x1p126f);
     m.counts[tid] = 0;
     if (tid == 0) m.cut = 0, m.pick[0] = NT;
     // the thread's largest logit, where it first occurs, and its mass from there

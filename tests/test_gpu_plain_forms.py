@@ -320,3 +320,13 @@ def test_sample_nucleus_over_a_range_too_narrow_for_bins():
     z = torch.from_numpy(np.repeat(z[None], 3, 0)).cuda()
     token = check_sample(z, g.cuda(), full(3, float(t)), None, torch.from_numpy(p).cuda())
     assert token[0] == behind and token[1] == behind and token[2] != behind
+
+
+@pytest.mark.parametrize("ty", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1e36, 1e37, 1e38, 3e38])
+@pytest.mark.parametrize("k,p,m", [(0, 0.7, 0.0), (0, 1.0, 0.5), (500, 0.8, 0.1), (200, 1.0, 0.0)])
+def test_sample_temperatures_up_to_the_largest_number(ty, t, k, p, m):
+    """Logits of the temperature's size (differences within 32 bits)."""
+    B, V = 3, 9001
+    z = (torch.rand(B, V, generator=torch.Generator().manual_seed(V), dtype=torch.float64) - 0.5) * min(6 * t, 3e38)
+    check_sample(z.to(TYPE[ty]).cuda(), noise(V, B, V), full(B, t), full(B, k, torch.int32), full(B, p), full(B, m))
