@@ -22,7 +22,8 @@
  *    enqueue work: no synchronisation, no allocation, no state kept between
  *    calls.  Results are the same bits on every run.
  *  - Sums, means, deviations and softmax masses are held in 32 bits or more;
- *    a result is rounded once, where it is stored in a 16-bit type.
+ *    a result is rounded once, where it is stored in a 16-bit type.  The squares
+ *    of a normalised row have to add up to less than 2^128.
  *  - An output whose byte range overlaps an input's is rejected (CKKS_EINVAL)
  *    unless the call says otherwise.
  *  - Zero rows are valid; nothing is launched, except that gradients of
@@ -151,7 +152,9 @@ int ckks_plain_linear_i8(int type, const void *x, int64_t x_stride, const int8_t
  * temperature 1 where temperature[r] <= 0.  A row without a possible token:
  * token -1, logprob -infinity.  gumbel [rows][vocab] in 32 bits, no NaN;
  * top_k, top_p and min_p may be NULL (off); an infinite logit outweighs every
- * finite one.  vocab <= 2^24.  ws: ckks_plain_sample_workspace_size bytes,
+ * finite one.  Masses are held in 32 bits (or whole multiples of 2^-38 and
+ * less): tokens whose difference is lost there, or is a subnormal number, weigh
+ * the same.  vocab <= 2^24.  ws: ckks_plain_sample_workspace_size bytes,
  * aligned to 16. */
 int ckks_plain_sample_workspace_size(int64_t rows, int64_t vocab, size_t *bytes);
 int ckks_plain_sample(int type, const void *logits, int64_t logits_stride, const float *gumbel, int64_t gumbel_stride,
