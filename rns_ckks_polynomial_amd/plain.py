@@ -82,18 +82,23 @@ def _scratch(nbytes, device):
 
 
 def _matrix(t, what, rows=None, cols=None, dtype=None, device=None):
+    """Row stride of a matrix argument (torch leaves that of a matrix with at most one row open)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what}: expected a device tensor")
     shape = t.shape
-    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
+    if len(shape) != 2:
         raise ValueError(f"{what}: expected a matrix with unit column stride")
-    if (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
+    T, D = shape
+    down, across = t.stride()
+    if D > 1 and across != 1:
+        raise ValueError(f"{what}: expected a matrix with unit column stride")
+    if (rows is not None and T != rows) or (cols is not None and D != cols):
         raise ValueError(f"{what}: expected {rows} x {cols}, got {tuple(shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
-    return t
+    return down if T > 1 else max(down, D)
 
 
 def _vector(t, what, n, dtype, device):
@@ -110,11 +115,6 @@ def _vector(t, what, n, dtype, device):
 def _like(x):
     """A new contiguous matrix of the shape and type of x."""
     return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-
-
-def _stride(t):
-    """Row stride; torch leaves that of a matrix with at most one row open."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 class _NoGradient(torch.autograd.Function):
@@ -135,16 +135,20 @@ def _tracked(*operands):
     if forward_ad._current_level >= 0:
         return True
     if torch.is_grad_enabled():
-        for t in operands:
-            if getattr(t, "requires_grad", False):
-                return True
+        try:
+            for t in operands:
+                if t is not None and t.requires_grad:
+                    return True
+        except AttributeError:  # no tensor: the checks name it
+            pass
     return False
 
 
 def _type(t, what):
-    if t.dtype not in TYPES:
+    code = TYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
-    return TYPES[t.dtype]
+    return code
 
 
 class Int8Rows:
@@ -168,7 +172,8 @@ class Int8Rows:
         _vector(scale, "scale", q.shape[0], torch.float32, q.device)
         padded = -(-cols // I8_ROW) * I8_ROW
         self.q, self.scale, self.cols, self._ends_in_zeros = q, scale, cols, cols == padded
-        if q.shape[1] < padded or q.stride(1) != 1 or q.stride(0) % I8_ROW or q.stride(0) < padded or q.data_ptr() % 16:
+        down, across = q.stride()
+        if q.shape[1] < padded or across != 1 or down % I8_ROW or down < padded or q.data_ptr() % 16:
             self.q, self._ends_in_zeros = self._copy(), True
 
     def _copy(self) -> torch.Tensor:
@@ -196,10 +201,10 @@ class Int8Rows:
 
 def _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind):
     """ckks_plain_norm of the arguments."""
-    _matrix(x, "x")
+    x_stride = _matrix(x, "x")
     T, D = x.shape
     dev, dt = x.device, x.dtype
-    _matrix(y, "y", T, D, dt, dev)
+    y_stride = _matrix(y, "y", T, D, dt, dev)
     if kind not in KINDS:
         raise ValueError(f"kind: expected 'rms' or 'layer', got {kind!r}")
     groups, gp = 0, None
@@ -213,7 +218,7 @@ def _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, e
             if not gate.is_contiguous() or gate.shape[0] < 1 or T % gate.shape[0]:
                 raise ValueError(f"gate: expected contiguous rows, a divisor of {T}, got {tuple(gate.shape)}")
             groups, gp = gate.shape[0], gate.data_ptr()
-    return nat.PlainNorm(_type(x, "x"), KINDS[kind], T, D, groups, x.data_ptr(), y.data_ptr(), _stride(x), _stride(y),
+    return nat.PlainNorm(_type(x, "x"), KINDS[kind], T, D, groups, x.data_ptr(), y.data_ptr(), x_stride, y_stride,
                          _vector(next_weight, "next_weight", D, dt, dev), _vector(next_bias, "next_bias", D, dt, dev),
                          _vector(block_weight, "block_weight", D, dt, dev),
                          _vector(block_bias, "block_bias", D, dt, dev), gp, scale, eps)
@@ -276,13 +281,13 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
     They have no gradient of their own: a second derivative raises."""
     p = _norm(x, y, next_weight, next_bias, block_weight, block_bias, gate, scale, eps, kind)
     T, D = x.shape
-    _matrix(dh, "dh", T, D, x.dtype, x.device)
-    _matrix(du, "du", T, D, x.dtype, x.device)
+    dh_stride = _matrix(dh, "dh", T, D, x.dtype, x.device)
+    du_stride = _matrix(du, "du", T, D, x.dtype, x.device)
     new = lambda v: None if v is None else torch.empty(v.shape, dtype=torch.float32, device=x.device)  # noqa: E731
     r = ResidualNormGrads(_like(x), _like(x), new(next_weight), new(next_bias), new(block_weight), new(block_bias),
                           new(gate))
     at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
-    g = nat.PlainNormGrads(dh.data_ptr(), du.data_ptr(), _stride(dh), _stride(du), r.dx.data_ptr(), r.dy.data_ptr(),
+    g = nat.PlainNormGrads(dh.data_ptr(), du.data_ptr(), dh_stride, du_stride, r.dx.data_ptr(), r.dy.data_ptr(),
                            D, D, at(r.next_weight), at(r.next_bias), at(r.block_weight), at(r.block_bias), at(r.gate))
     _keep, ws, size = _scratch(_norm_grad_workspace(T, D, p.groups, next_bias is not None, block_weight is not None,
                                                     block_bias is not None), x.device)
@@ -296,9 +301,9 @@ def residual_norm_grad(x, y, dh, du, next_weight, next_bias=None, block_weight=N
 
 def quantize_rows(x) -> Int8Rows:
     """8-bit rows of x [T, D] (ckks_plain_quantize_rows): scale = max |x| times 1/127 of the row."""
-    _matrix(x, "x")
+    stride = _matrix(x, "x")
     r = Int8Rows.empty(x.shape[0], x.shape[1], x.device)
-    _call("ckks_plain_quantize_rows", x.device, _type(x, "x"), x.data_ptr(), _stride(x), x.shape[0], x.shape[1],
+    _call("ckks_plain_quantize_rows", x.device, _type(x, "x"), x.data_ptr(), stride, x.shape[0], x.shape[1],
           r.q.data_ptr(), r.q.shape[1], r.scale.data_ptr())
     if _tracked(x):
         r.q, r.scale = _NoGradient.apply("quantize_rows", (r.q, r.scale), x)
@@ -338,14 +343,14 @@ def matmul_i8(a: Int8Rows, w: Int8Rows, bias=None, dtype=torch.bfloat16) -> torc
 
 def linear_i8(x, w: Int8Rows, bias=None, dtype=None) -> torch.Tensor:
     """matmul_i8 of x [T, D] quantised row by row (ckks_plain_linear_i8); dtype defaults to that of x."""
-    _matrix(x, "x")
+    stride = _matrix(x, "x")
     dtype = x.dtype if dtype is None else dtype
     dev, (M, K) = x.device, x.shape
     bp = _product(K, dev, w, bias, dtype)
     N = w.rows
     out = torch.empty((M, N), dtype=dtype, device=dev)
     _keep, ws, size = _scratch(_workspace("ckks_plain_linear_i8_workspace_size", M, N, K), dev)
-    _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), _stride(x), w.q.data_ptr(), w.q.stride(0),
+    _call("ckks_plain_linear_i8", dev, _type(x, "x"), x.data_ptr(), stride, w.q.data_ptr(), w.q.stride(0),
           w.scale.data_ptr(), bp, TYPES[dtype], out.data_ptr(), N, M, N, K, ws, size)
     if _tracked(x, w.scale, bias):
         out, = _NoGradient.apply("linear_i8", (out,), x, w.scale, bias)
@@ -357,22 +362,23 @@ def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allo
     [B, V], -log(-log u) of uniform numbers; temperature, top_p, min_p: float32 [B]; top_k: int32 [B];
     allowed: bool [B, V].  temperature <= 0: the largest logit.  A row without a possible token:
     token -1, logprob -infinity."""
-    _matrix(logits, "logits")
+    z_stride = _matrix(logits, "logits")
     B, V = logits.shape
     dev = logits.device
-    _matrix(gumbel, "gumbel", B, V, torch.float32, dev)
+    g_stride = _matrix(gumbel, "gumbel", B, V, torch.float32, dev)
     if temperature is None:
         raise ValueError("temperature: expected float32 of every row")
+    a_stride = 0
     if allowed is not None:
-        _matrix(allowed, "allowed", B, V, torch.bool, dev)
+        a_stride = _matrix(allowed, "allowed", B, V, torch.bool, dev)
     token = torch.empty(B, dtype=torch.int64, device=dev)
     logprob = torch.empty(B, dtype=torch.float32, device=dev)
     _keep, ws, size = _scratch(_workspace("ckks_plain_sample_workspace_size", B, V), dev)
-    _call("ckks_plain_sample", dev, _type(logits, "logits"), logits.data_ptr(), _stride(logits), gumbel.data_ptr(),
-          _stride(gumbel), _vector(temperature, "temperature", B, torch.float32, dev),
+    _call("ckks_plain_sample", dev, _type(logits, "logits"), logits.data_ptr(), z_stride, gumbel.data_ptr(),
+          g_stride, _vector(temperature, "temperature", B, torch.float32, dev),
           _vector(top_k, "top_k", B, torch.int32, dev), _vector(top_p, "top_p", B, torch.float32, dev),
           _vector(min_p, "min_p", B, torch.float32, dev), None if allowed is None else allowed.data_ptr(),
-          0 if allowed is None else _stride(allowed), B, V, token.data_ptr(), logprob.data_ptr(),
+          a_stride, B, V, token.data_ptr(), logprob.data_ptr(),
           ws, size)
     if _tracked(logits, gumbel, temperature, top_p, min_p):
         token, logprob = _NoGradient.apply("sample", (token, logprob), logits, gumbel, temperature, top_p, min_p)
