@@ -62,11 +62,13 @@ struct TileOrder {
 // piece with rows 4..11 of the next (p ^ (r / 4 & 3) serves the former only).  The loads write LDS
 // in lane order and permute the pieces on the memory side (within a row's 64 bytes).
 //
-// 8192 x 8192 x 8192 on normal values, bf16 out: 440 to 480 us (2.3 to 2.5 POP/s), the matrix cores
-// busy 61 % of the cycles, no LDS conflicts.  A tile's fill and its epilogue (16 us of 256 x 256
-// together) are not hidden behind another tile's products: a second accumulator does not fit.  777 x
-// 2051 x 5003 f16 24 to 26 us, two thirds of that the load of 33 steps; 64 x 8192 x 8192 16.6 us, 4.1
-// TB/s of weights.
+// 8192 x 8192 x 8192 on normal values, bf16 out: 440 to 490 us (2.2 to 2.5 POP/s), no LDS conflicts.  A
+// compute unit is busy for 838000 cycles, so the clock is 1.8 GHz under this load; its matrix cores are
+// busy in 62 % of them (the 275 us of the products alone).  A wave, one to a matrix core, issues in 36 %
+// of its cycles, waits for a unit to take its instruction in 52 and for loads, LDS or the other waves in
+// 12.  A tile's fill and its epilogue (16 us of 256 x 256 together, four times) are not hidden behind
+// another tile's products: a second accumulator does not fit.  777 x 5003 x 2051 f16 24 to 25 us, two
+// thirds of that the load of 34 steps; 64 x 8192 x 8192 16.4 us, 4.1 TB/s of weights.
 constexpr int STEP = 64;
 __device__ __forceinline__ int turn(int row) {  // 0, 2, 3, 1 for each four rows in turn
     const int q = row / 4 % 4;

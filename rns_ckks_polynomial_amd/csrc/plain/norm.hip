@@ -40,7 +40,7 @@ __device__ __forceinline__ void row_stats(const float (&v)[E], const NormArgs &a
 // Bound by memory: 8192 x 4096 bf16, norm of the block and a gate, 46.5 us for 268 MB (5.8 TB/s: part
 // comes from the last-level cache; a copy of 2 GiB moves 4.8); 1021 x 5003 f32, rows at odd strides,
 // layer norm with biases, 20 us for 82 MB (4.0 TB/s: one round of workgroups, each with two means to
-// wait for); 4 x 2048 bf16 2.8 us, all latency.
+// wait for); 4 x 2048 bf16 2.4 to 2.8 us, all latency.
 template <typename T, int NT, int E, bool I8>
 __global__ __launch_bounds__(NT == 64 ? 256 : NT) void k_residual_norm(NormArgs a, T *h_out, int64_t h_stride,
                                                                       void *u_out, int64_t u_stride, float *q_scale) {

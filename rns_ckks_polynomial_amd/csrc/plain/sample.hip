@@ -60,10 +60,12 @@ struct SampleShared {
 // Masses that are added by atomics are whole multiples of a power of two and float sums go in a
 // fixed order, so the result does not depend on the order of anything.
 //
-// 256 x 131072 bf16, top-p 0.95 of normal logits (deviation 2.5, a nucleus of 26000): 80 to 85 us for
+// 256 x 131072 bf16, top-p 0.95 of normal logits (deviation 2.5, a nucleus of 26000): 72 to 80 us for
 // 290 MB from memory, three reads of the logits and the noise lines that hold a token of the nucleus;
-// each read has a compute unit's vector instructions beside its loads.  1 x 32768 f32, top-k 50 and
-// top-p: 14 us, one read, then latency; 33 x 50021 f16, masked, min-p and top-k 1000: 22 us.
+// each read has a compute unit's vector instructions beside its loads (the waves wait in 55 % of their
+// cycles).  The same rows without filters 47 us, the largest alone 16.  1 x 32768 f32, top-k 50 and
+// top-p: 13 us, one read, then latency; 33 x 50021 f16, masked, min-p and top-k 1000: 21 us.  Few long
+// rows leave most compute units idle: 16 x 262144 bf16 top-p 116 us.
 template <typename T> struct Sampler {
     static constexpr int N = 16 / sizeof(T);  // logits of a vector
     typedef T Vec __attribute__((ext_vector_type(16 / sizeof(T)), aligned(sizeof(T))));
