@@ -4,14 +4,20 @@
  * What the key holder computes in clear around the encrypted layers: a
  * decrypted hop is a few tokens' hidden states (the slots of a token's
  * ciphertexts), and next to it stand the values an encrypted layer is checked
- * against.  Three operators, which follow each other:
+ * against.  The operators, in the order of a token's way:
+ *   embed:         rows of a table by token, scaled, before their encryption
+ *                  (with the table's gradient);
  *   residual_norm: the residual stream takes a gated, optionally normalised
  *                  block output and is normalised for the next block (with its
  *                  gradient, and with an 8-bit output);
+ *   head_norm_rotate: queries and keys normalised for each head and rotated by
+ *                  position (with its gradient);
  *   matmul_i8:     rows quantised to 8 bits times 8-bit weights, with a scale
  *                  for each row (token) and each weight row (channel);
  *   sample:        the next token from logits by temperature, top-k, top-p and
- *                  min-p, from given random numbers.
+ *                  min-p, from given random numbers;
+ *   token_logprobs: log probabilities of given tokens, the entropy and the
+ *                  largest alternatives (with the logits' gradient).
  *
  * Conventions shared by every call
  *  - Data pointers are DEVICE pointers on the calling thread's current HIP
@@ -27,7 +33,7 @@
  *  - An output whose byte range overlaps an input's is rejected (CKKS_EINVAL)
  *    unless the call says otherwise.
  *  - Zero rows are valid; nothing is launched, except that gradients of
- *    weights are written (as zeros).  There are fewer than 2^31.
+ *    weights and tables are written (as zeros).  There are fewer than 2^31.
  *  - Errors are the codes of ckks_gpu.h; arguments are validated before any
  *    launch.  CKKS_EALIGN: a pointer not aligned to its element type (8-bit
  *    rows: to 16 bytes).
@@ -102,6 +108,57 @@ int ckks_plain_norm_grad_workspace_size(const ckks_plain_norm *p, size_t *bytes)
 int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckks_plain_norm_grads *g, void *ws, size_t ws_bytes,
                                   void *stream);
 
+/* Queries and keys [tokens][heads][head_dim], normalised for each head and
+ * rotated by position; y of a head x:
+ *   n = x / sqrt(mean x^2 + eps) weight         (weight NULL: n = x)
+ *   dimensions a and b of pair i < rotary / 2, at the angle
+ *   f = positions[t] inv_freq[i]:
+ *   y_a = n_a cos f - n_b sin f,  y_b = n_b cos f + n_a sin f,
+ *   (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved; from
+ *   rotary on, y = n.
+ * Element (t, h, i) of a tensor is at t token + h head + i: unit stride in a
+ * head, the other two strides at least head_dim where there is more than one
+ * token or head.  head_dim and rotary are even, rotary <= head_dim <=
+ * CKKS_PLAIN_MAX_HEAD.  positions [tokens] and inv_freq [rotary / 2] may be
+ * NULL where rotary is 0; the angle's product and its turns are held in 64
+ * bits, its sine and cosine in 32.  k_heads = 0: queries alone (k and k_weight
+ * NULL).  Weights have the type of q and k. */
+#define CKKS_PLAIN_MAX_HEAD 512
+typedef struct {
+    int64_t token, head;
+} ckks_plain_head_strides;
+typedef struct {
+    int type; /* CKKS_PLAIN_BF16, _F16 or _F32 */
+    int interleaved;
+    int64_t tokens, q_heads, k_heads, head_dim, rotary;
+    const void *q, *k;
+    ckks_plain_head_strides q_strides, k_strides;
+    const void *q_weight, *k_weight; /* [head_dim] */
+    const int64_t *positions;
+    const float *inv_freq;
+    float eps;
+} ckks_plain_heads;
+
+/* q_out and k_out may be q and k themselves (the same pointer and strides);
+ * elements of an output do not share memory. */
+int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, ckks_plain_head_strides q_out_strides,
+                                void *k_out, ckks_plain_head_strides k_out_strides, void *stream);
+
+/* Gradients, given those of the outputs (dq, dk): dq_in, dk_in of the type of
+ * q; of the weights in 32 bits, each where the forward call has that operand
+ * (NULL otherwise).  ws: scratch of ckks_plain_head_grad_workspace_size bytes,
+ * aligned to 16 (may be NULL where that is 0). */
+typedef struct {
+    const void *dq, *dk;
+    ckks_plain_head_strides dq_strides, dk_strides;
+    void *dq_in, *dk_in;
+    ckks_plain_head_strides dq_in_strides, dk_in_strides;
+    float *q_weight, *k_weight; /* [head_dim] */
+} ckks_plain_head_grads;
+int ckks_plain_head_grad_workspace_size(const ckks_plain_heads *p, size_t *bytes);
+int ckks_plain_head_norm_rotate_grad(const ckks_plain_heads *p, const ckks_plain_head_grads *g, void *ws,
+                                     size_t ws_bytes, void *stream);
+
 /* 8-bit rows: row t stands for scale[t] q[t][0..cols).  They start at
  * multiples of CKKS_PLAIN_I8_ROW bytes (q aligned to 16 bytes, q_stride a
  * multiple of CKKS_PLAIN_I8_ROW and at least cols rounded up to one) and hold
@@ -161,6 +218,66 @@ int ckks_plain_sample(int type, const void *logits, int64_t logits_stride, const
                       const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                       const uint8_t *allowed, int64_t allowed_stride, int64_t rows, int64_t vocab, int64_t *token,
                       float *logprob, void *ws, size_t ws_bytes, void *stream);
+
+/* For each row of logits z [rows][vocab], with the possible tokens of
+ * ckks_plain_sample, its temperature (temperature NULL, or temperature[r] <= 0:
+ * 1) and x = (z - max z) / temperature of them (an infinite logit outweighs
+ * every finite one, and x of the largest is 0):
+ *   largest = max z, log_mass = log sum exp x;
+ *   logprob = x[tokens[r]] - log_mass, -infinity if that token is not
+ *             possible; 0 if tokens[r] is outside [0, vocab) (a padded row);
+ *   entropy = -sum p log p, p = exp(x - log_mass);
+ *   top_token, top_logprob [rows][top]: the `top` largest in the order of
+ *             falling logits (lower index first among equals), behind the
+ *             last possible one token -1, log probability -infinity.
+ * A row without a possible token: largest and log_mass -infinity, entropy 0.
+ * top <= CKKS_PLAIN_MAX_TOP (0: top_token and top_logprob NULL), vocab <= 2^24.
+ * Temperatures below 2^-127 count as that.  ws:
+ * ckks_plain_token_logprobs_workspace_size bytes, aligned to 16 (may be NULL
+ * where that is 0). */
+#define CKKS_PLAIN_MAX_TOP 64
+int ckks_plain_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int64_t top, size_t *bytes);
+int ckks_plain_token_logprobs(int type, const void *logits, int64_t logits_stride, const int64_t *tokens,
+                              const float *temperature, const uint8_t *allowed, int64_t allowed_stride, int64_t rows,
+                              int64_t vocab, int64_t top, float *logprob, float *entropy, float *largest,
+                              float *log_mass, int64_t *top_token, float *top_logprob, void *ws, size_t ws_bytes,
+                              void *stream);
+
+/* Gradient of the logits from those of logprob and entropy (either may be
+ * NULL: zero), given the entropy, largest and log_mass of the call above:
+ *   dz = (dlogprob (1 at the token - p) - dentropy p (log p + entropy)) / temperature
+ * for possible tokens, 0 for others; a token that is not possible or outside
+ * [0, vocab) takes no part.  dlogits [rows][vocab] has the type of the logits
+ * and may be the logits themselves (the same pointer and stride). */
+int ckks_plain_token_logprobs_grad(int type, const void *logits, int64_t logits_stride, const int64_t *tokens,
+                                   const float *temperature, const uint8_t *allowed, int64_t allowed_stride,
+                                   int64_t rows, int64_t vocab, const float *entropy, const float *largest,
+                                   const float *log_mass, const float *dlogprob, const float *dentropy, void *dlogits,
+                                   int64_t dlogits_stride, void *stream);
+
+/* out[t] = scale table[tokens[t]]: table [vocab][cols], out [rows][cols] of
+ * out_type; the product is rounded to 32 bits, then to out_type.  A row whose
+ * token is outside [0, vocab) (padding, or what ckks_plain_sample says where
+ * nothing is possible) is zeros.  vocab <= 2^24, cols < 2^31. */
+int ckks_plain_embed(int type, const void *table, int64_t table_stride, int64_t vocab, int64_t cols,
+                     const int64_t *tokens, int64_t rows, float scale, int out_type, void *out, int64_t out_stride,
+                     void *stream);
+/* The same from 8-bit rows (their columns alone are read): out[t] = (scale
+ * q_scale[v]) q[v], v = tokens[t]. */
+int ckks_plain_embed_i8(const int8_t *q, int64_t q_stride, const float *q_scale, int64_t vocab, int64_t cols,
+                        const int64_t *tokens, int64_t rows, float scale, int out_type, void *out, int64_t out_stride,
+                        void *stream);
+
+/* Gradient of the table from that of the rows, drows [rows][cols] of `type`:
+ *   out[v] = scale sum of drows[t] over the rows of token v   [+ out[v] if add]
+ * out: [vocab][cols] of out_type.  Sums are held in 32 bits, go in a fixed
+ * order and are rounded once.  Without `add` every row of out is written;
+ * with it, those of the tokens alone.  ws: scratch of
+ * ckks_plain_embed_grad_workspace_size bytes, aligned to 16. */
+int ckks_plain_embed_grad_workspace_size(int64_t rows, int64_t vocab, int64_t cols, size_t *bytes);
+int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_stride, const int64_t *tokens, int64_t rows,
+                          int64_t vocab, int64_t cols, float scale, int out_type, void *out, int64_t out_stride,
+                          int add, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -53,6 +53,28 @@ class PlainNormGrads(C.Structure):
                 ("block_bias", C.c_void_p), ("gate", C.c_void_p)]
 
 
+class PlainHeadStrides(C.Structure):
+    """ckks_plain_head_strides (include/ckks_plain.h)."""
+    _fields_ = [("token", C.c_int64), ("head", C.c_int64)]
+
+
+class PlainHeads(C.Structure):
+    """ckks_plain_heads (include/ckks_plain.h)."""
+    _fields_ = [("type", C.c_int), ("interleaved", C.c_int), ("tokens", C.c_int64), ("q_heads", C.c_int64),
+                ("k_heads", C.c_int64), ("head_dim", C.c_int64), ("rotary", C.c_int64), ("q", C.c_void_p),
+                ("k", C.c_void_p), ("q_strides", PlainHeadStrides), ("k_strides", PlainHeadStrides),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("positions", C.c_void_p),
+                ("inv_freq", C.c_void_p), ("eps", C.c_float)]
+
+
+class PlainHeadGrads(C.Structure):
+    """ckks_plain_head_grads (include/ckks_plain.h)."""
+    _fields_ = [("dq", C.c_void_p), ("dk", C.c_void_p), ("dq_strides", PlainHeadStrides),
+                ("dk_strides", PlainHeadStrides), ("dq_in", C.c_void_p), ("dk_in", C.c_void_p),
+                ("dq_in_strides", PlainHeadStrides), ("dk_in_strides", PlainHeadStrides), ("q_weight", C.c_void_p),
+                ("k_weight", C.c_void_p)]
+
+
 class KernelStat(C.Structure):
     _fields_ = [("name", C.c_char * 48), ("launches", C.c_int), ("total_ms", C.c_double),
                 ("min_ms", C.c_double), ("max_ms", C.c_double)]
@@ -111,6 +133,27 @@ SIGNATURES = {
     "ckks_plain_norm_grad_workspace_size": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(C.c_size_t)]),
     "ckks_plain_residual_norm_grad": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(PlainNormGrads), C.c_void_p,
                                                 C.c_size_t, C.c_void_p]),
+    "ckks_plain_head_norm_rotate": (C.c_int, [C.POINTER(PlainHeads), C.c_void_p, PlainHeadStrides, C.c_void_p,
+                                              PlainHeadStrides, C.c_void_p]),
+    "ckks_plain_head_grad_workspace_size": (C.c_int, [C.POINTER(PlainHeads), C.POINTER(C.c_size_t)]),
+    "ckks_plain_head_norm_rotate_grad": (C.c_int, [C.POINTER(PlainHeads), C.POINTER(PlainHeadGrads), C.c_void_p,
+                                                   C.c_size_t, C.c_void_p]),
+    "ckks_plain_embed": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                   C.c_float, C.c_int, C.c_void_p, C.c_int64, C.c_void_p]),
+    "ckks_plain_embed_i8": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_int64,
+                                      C.c_float, C.c_int, C.c_void_p, C.c_int64, C.c_void_p]),
+    "ckks_plain_embed_grad_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "ckks_plain_embed_grad": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int64, C.c_int64,
+                                        C.c_float, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_size_t,
+                                        C.c_void_p]),
+    "ckks_plain_token_logprobs_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),
+    "ckks_plain_token_logprobs": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                            C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p,
+                                            C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                            C.c_void_p]),
+    "ckks_plain_token_logprobs_grad": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                 C.c_int64, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                                 C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
     "ckks_plain_quantize_rows": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.c_void_p,
                                            C.c_int64, C.c_void_p, C.c_void_p]),
     "ckks_plain_matmul_i8_workspace_size": (C.c_int, [C.c_int64, C.c_int64, C.c_int64, C.POINTER(C.c_size_t)]),

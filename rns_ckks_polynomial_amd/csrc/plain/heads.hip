@@ -1,0 +1,461 @@
+// heads.hip -- queries and keys: a norm for each head and the rotation by position in one pass, and its gradient.
+#include "plain_common.h"
+
+namespace ckks_plain {
+
+// One tensor of heads and what becomes of it.
+struct HeadSide {
+    const void *x, *weight, *dy;  // dy: the gradient of the output (gradient alone)
+    void *out;                    // the output, or the gradient of x
+    float *part;                  // [blocks][head_dim]: the weight's gradient from each workgroup
+    ckks_plain_head_strides x_strides, dy_strides, out_strides;
+    int heads, blocks;
+};
+struct HeadArgs {
+    HeadSide side[2];
+    const int64_t *positions;
+    const float *inv_freq;
+    int64_t tokens, span;  // span: tokens of a workgroup
+    int half, r;           // head_dim / 2, rotary / 2
+    int step;              // tokens whose angles are in LDS at a time
+    int log_l;             // threads of a head
+    float eps, inv_dim;
+    bool interleaved;
+};
+
+// Sum over groups of 2^log_l neighbouring lanes, the same bits in each of a group's lanes.
+__device__ __forceinline__ float group_sum(float v, int log_l) {
+    if (log_l > 0) v += moved<0xb1, 0xf>(0.0f, v);   // quad: neighbours
+    if (log_l > 1) v += moved<0x4e, 0xf>(0.0f, v);   // quad: pairs
+    if (log_l > 2) v += moved<0x141, 0xf>(0.0f, v);  // half row mirrored
+    if (log_l > 3) v += moved<0x140, 0xf>(0.0f, v);  // row mirrored
+    if (log_l > 4) v += __shfl_xor(v, 16);
+    if (log_l > 5) v += __shfl_xor(v, 32);
+    return v;
+}
+
+// A thread's share of a head: K times V pairs of dimensions, a vector of V elements `lo` and one `hi`
+// each.  Pair u < r turns by angle u; the pairs behind take what is left over, half and half.
+template <typename T, int V, int K> struct Head {
+    typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    Vec lo[K], hi[K];
+    // first dimension of the vectors of pair u, and the distance between them
+    static __device__ __forceinline__ int place(const HeadArgs &a, int u, int &apart) {
+        if (a.interleaved) {
+            apart = V;
+            return 2 * u;
+        }
+        apart = u < a.r ? a.r : a.half - a.r;
+        return u < a.r ? u : a.r + u;
+    }
+    __device__ __forceinline__ void fetch(const HeadArgs &a, const T *p, int l) {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int u = ((k << a.log_l) + l) * V;
+            if (u < a.half) {
+                int apart;
+                const T *q = p + place(a, u, apart);
+                lo[k] = *(const Vec *)q;
+                hi[k] = *(const Vec *)(q + apart);
+            } else {
+                lo[k] = (Vec)(T)0.0f;
+                hi[k] = (Vec)(T)0.0f;
+            }
+        }
+    }
+    // the pairs' elements in 32 bits
+    __device__ __forceinline__ void widen(const HeadArgs &a, float (&x)[K][V], float (&y)[K][V]) const {
+#pragma unroll
+        for (int k = 0; k < K; k++)
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                if (a.interleaved) {
+                    x[k][j] = to_f32(2 * j < V ? lo[k][2 * j % V] : hi[k][2 * j % V]);
+                    y[k][j] = to_f32(2 * j + 1 < V ? lo[k][(2 * j + 1) % V] : hi[k][(2 * j + 1) % V]);
+                } else {
+                    x[k][j] = to_f32(lo[k][j]);
+                    y[k][j] = to_f32(hi[k][j]);
+                }
+            }
+    }
+    static __device__ __forceinline__ void store(const HeadArgs &a, T *p, int l, const float (&x)[K][V],
+                                                 const float (&y)[K][V]) {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int u = ((k << a.log_l) + l) * V;
+            if (u >= a.half) continue;
+            Vec lo, hi;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const int i = V + j;
+                lo[j] = from_f32<T>(!a.interleaved ? x[k][j] : j % 2 ? y[k][j / 2] : x[k][j / 2]);
+                hi[j] = from_f32<T>(!a.interleaved ? y[k][j] : i % 2 ? y[k][i / 2] : x[k][i / 2]);
+            }
+            int apart;
+            T *q = p + place(a, u, apart);
+            *(Vec *)q = lo;
+            *(Vec *)(q + apart) = hi;
+        }
+    }
+    // the pairs turned by their angles (`sign` -1: back)
+    static __device__ __forceinline__ void turn(const HeadArgs &a, const float2 *angles, int l, float sign,
+                                                float (&x)[K][V], float (&y)[K][V]) {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            const int u = ((k << a.log_l) + l) * V;
+            if (u >= a.r) continue;
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const float2 cs = angles[u + j];
+                const float s = sign * cs.y, p = x[k][j], q = y[k][j];
+                x[k][j] = p * cs.x - q * s;
+                y[k][j] = q * cs.x + p * s;
+            }
+        }
+    }
+};
+
+// cos and sin of positions[t] inv_freq[i] for the tokens [first, last).  The angle in whole turns, in 64
+// bits: its fraction is what a far position leaves, and 32 bits hold it.
+__device__ __forceinline__ void head_angles(const HeadArgs &a, int64_t first, int64_t last, float2 *angles) {
+    for (int i = threadIdx.x; i < (int)(last - first) * a.r; i += 256) {
+        const int64_t t = first + i / a.r;
+        const double turns = (double)a.positions[t] * ((double)a.inv_freq[i % a.r] * 0.15915494309189533577);
+        float2 cs;
+        sincospif((float)(2.0 * (turns - rint(turns))), &cs.y, &cs.x);
+        angles[i] = cs;
+    }
+}
+
+// A workgroup's tokens on one side: f(token, head, angles of the token) for each head by 2^log_l threads,
+// `step` tokens at a time.
+template <typename F>
+__device__ __forceinline__ void each_head(const HeadArgs &a, int heads, int64_t block, float2 *angles, F f) {
+    const int64_t first = block * a.span;
+    const int64_t last = first + a.span < a.tokens ? first + a.span : a.tokens;
+    const int groups = 256 >> a.log_l, g = threadIdx.x >> a.log_l;
+    for (int64_t t = first; t < last; t += a.step) {
+        const int64_t end = t + a.step < last ? t + a.step : last;
+        __syncthreads();  // the angles before are not read any more
+        head_angles(a, t, end, angles);
+        __syncthreads();
+        for (int i = g; i < (int)(end - t) * heads; i += groups) f(t + i / heads, i % heads, angles + i / heads * a.r);
+    }
+}
+
+template <typename T, int V, int K>
+__global__ __launch_bounds__(256) void k_head_norm_rotate(HeadArgs a) {
+    typedef Head<T, V, K> H;
+    extern __shared__ float2 angles[];
+    const int which = blockIdx.x >= a.side[0].blocks;
+    const HeadSide &s = a.side[which];
+    const int l = threadIdx.x & ((1 << a.log_l) - 1);
+    H hw;
+    if (s.weight) hw.fetch(a, (const T *)s.weight, l);
+    each_head(a, s.heads, blockIdx.x - (which ? a.side[0].blocks : 0), angles, [&](int64_t t, int h, const float2 *cs) {
+        H hx;
+        float x[K][V], y[K][V];
+        hx.fetch(a, (const T *)s.x + t * s.x_strides.token + h * s.x_strides.head, l);
+        hx.widen(a, x, y);
+        if (s.weight) {
+            float w[K][V], v[K][V], sum = 0;
+#pragma unroll
+            for (int k = 0; k < K; k++)
+#pragma unroll
+                for (int j = 0; j < V; j++) sum += x[k][j] * x[k][j] + y[k][j] * y[k][j];
+            const float r = 1.0f / sqrtf(group_sum(sum, a.log_l) * a.inv_dim + a.eps);
+            hw.widen(a, w, v);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+#pragma unroll
+                for (int j = 0; j < V; j++) x[k][j] *= r * w[k][j], y[k][j] *= r * v[k][j];
+        }
+        H::turn(a, cs, l, 1.0f, x, y);
+        H::store(a, (T *)s.out + t * s.out_strides.token + h * s.out_strides.head, l, x, y);
+    });
+}
+
+// dn: dy turned back.  With a weight: dx = r (a - hat mean(a hat)), a = dn weight, hat = x r; the weight's
+// sum of dn hat over a workgroup's heads leaves as one row of partial sums.
+template <typename T, int V, int K>
+__global__ __launch_bounds__(256) void k_head_grad(HeadArgs a) {
+    typedef Head<T, V, K> H;
+    extern __shared__ float2 angles[];
+    const int which = blockIdx.x >= a.side[0].blocks;
+    const HeadSide &s = a.side[which];
+    const int block = blockIdx.x - (which ? a.side[0].blocks : 0);
+    const int l = threadIdx.x & ((1 << a.log_l) - 1);
+    float ax[K][V] = {}, ay[K][V] = {};
+    H hw;
+    if (s.weight) hw.fetch(a, (const T *)s.weight, l);
+    each_head(a, s.heads, block, angles, [&](int64_t t, int h, const float2 *cs) {
+        H hd;
+        float p[K][V], q[K][V];
+        hd.fetch(a, (const T *)s.dy + t * s.dy_strides.token + h * s.dy_strides.head, l);
+        hd.widen(a, p, q);
+        H::turn(a, cs, l, -1.0f, p, q);
+        if (s.weight) {
+            H hx;
+            float x[K][V], y[K][V], w[K][V], v[K][V], sum = 0, dot = 0;
+            hx.fetch(a, (const T *)s.x + t * s.x_strides.token + h * s.x_strides.head, l);
+            hx.widen(a, x, y);
+            hw.widen(a, w, v);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+#pragma unroll
+                for (int j = 0; j < V; j++) sum += x[k][j] * x[k][j] + y[k][j] * y[k][j];
+            const float r = 1.0f / sqrtf(group_sum(sum, a.log_l) * a.inv_dim + a.eps);
+#pragma unroll
+            for (int k = 0; k < K; k++)
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    x[k][j] *= r, y[k][j] *= r;
+                    ax[k][j] += p[k][j] * x[k][j], ay[k][j] += q[k][j] * y[k][j];
+                    p[k][j] *= w[k][j], q[k][j] *= v[k][j];
+                    dot += p[k][j] * x[k][j] + q[k][j] * y[k][j];
+                }
+            dot = group_sum(dot, a.log_l) * a.inv_dim;
+#pragma unroll
+            for (int k = 0; k < K; k++)
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    p[k][j] = r * (p[k][j] - x[k][j] * dot);
+                    q[k][j] = r * (q[k][j] - y[k][j] * dot);
+                }
+        }
+        H::store(a, (T *)s.out + t * s.out_strides.token + h * s.out_strides.head, l, p, q);
+    });
+    if (!s.part) return;
+    // the groups' sums in their order: a group's in LDS at a time
+    __shared__ float sums[2 * 256];
+    const int groups = 256 >> a.log_l, g = threadIdx.x >> a.log_l;
+    for (int k = 0; k < K; k++) {
+        const int u = ((k << a.log_l) + l) * V;
+#pragma unroll
+        for (int j = 0; j < V; j++) {
+            __syncthreads();
+            sums[threadIdx.x] = ax[k][j], sums[256 + threadIdx.x] = ay[k][j];
+            __syncthreads();
+            if (g == 0 && u < a.half) {
+                float x = 0, y = 0;
+                for (int i = 0; i < groups; i++) x += sums[(i << a.log_l) + l], y += sums[256 + (i << a.log_l) + l];
+                int apart;
+                const int at = H::place(a, u, apart);
+                float *o = s.part + (int64_t)block * 2 * a.half;
+                o[at + (a.interleaved ? 2 * j : j)] = x;
+                o[at + (a.interleaved ? 2 * j + 1 : apart + j)] = y;
+            }
+        }
+    }
+}
+
+// out[c] = the sum of part[b][c] over b, 64 columns and a side a workgroup, 16 waves on the rows in turn.
+__global__ __launch_bounds__(1024) void k_head_weight_sum(const float *part0, const float *part1, int blocks0,
+                                                          int blocks1, float *out0, float *out1, int dim) {
+    __shared__ float sh[16][64];
+    const float *part = blockIdx.y ? part1 : part0;
+    float *out = blockIdx.y ? out1 : out0;
+    const int n = blockIdx.y ? blocks1 : blocks0, wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int c = blockIdx.x * 64 + l;
+    if (!out) return;
+    float v = 0;
+    if (c < dim)
+        for (int b = wave; b < n; b += 16) v += part[(int64_t)b * dim + c];
+    sh[wave][l] = v;
+    __syncthreads();
+    if (wave || c >= dim) return;
+    for (int w = 1; w < 16; w++) v += sh[w][l];
+    out[c] = v;
+}
+
+// ------------------------------------------------------------------ launches
+
+// first and last element of a tensor of heads, as a number of bytes from its pointer
+size_t head_span(int64_t tokens, int64_t heads, int64_t dim, const ckks_plain_head_strides &s, size_t size) {
+    return tokens && heads ? ((size_t)(tokens - 1) * s.token + (size_t)(heads - 1) * s.head + dim) * size : 0;
+}
+bool same(const ckks_plain_head_strides &a, const ckks_plain_head_strides &b) {
+    return a.token == b.token && a.head == b.head;
+}
+int check_side(const ckks_plain_heads *p, const void *x, int64_t heads, const ckks_plain_head_strides &s, bool output) {
+    if (!p->tokens || !heads) return CKKS_OK;
+    if (!x || (p->tokens > 1 && s.token < p->head_dim) || (heads > 1 && s.head < p->head_dim)) return CKKS_EINVAL;
+    // heads within a token, or tokens within a head
+    if (output && p->tokens > 1 && heads > 1 && s.token < (heads - 1) * s.head + p->head_dim &&
+        s.head < (p->tokens - 1) * s.token + p->head_dim)
+        return CKKS_EINVAL;
+    return at(x, type_size(p->type)) ? CKKS_OK : CKKS_EALIGN;
+}
+int check_heads(const ckks_plain_heads *p) {
+    if (!p || !type_ok(p->type) || (p->interleaved != 0 && p->interleaved != 1)) return CKKS_EINVAL;
+    if (p->tokens < 0 || p->tokens >= (int64_t)1 << 31 || p->q_heads < 1 || p->k_heads < 0) return CKKS_EINVAL;
+    if (p->head_dim < 2 || p->rotary < 0 || p->rotary > p->head_dim || !(p->eps >= 0)) return CKKS_EINVAL;
+    if (p->head_dim % 2 || p->rotary % 2 || p->head_dim > CKKS_PLAIN_MAX_HEAD || p->q_heads > 65535 ||
+        p->k_heads > 65535)
+        return CKKS_EUNSUPPORTED;
+    if (!p->k_heads && (p->k || p->k_weight)) return CKKS_EINVAL;
+    const size_t z = type_size(p->type);
+    if (!at(p->q_weight, z) || !at(p->k_weight, z) || !at(p->positions, 8) || !at(p->inv_freq, 4)) return CKKS_EALIGN;
+    if (p->tokens && p->rotary && (!p->positions || !p->inv_freq)) return CKKS_EINVAL;
+    if (int e = check_side(p, p->q, p->q_heads, p->q_strides, false)) return e;
+    return check_side(p, p->k, p->k_heads, p->k_strides, false);
+}
+// an output's range against every input of the call (which: 0 and 1 leave out q or k)
+bool heads_overlap(const ckks_plain_heads *p, const void *out, size_t bytes, int without) {
+    const size_t z = type_size(p->type);
+    return (without != 0 && overlap(out, bytes, p->q, head_span(p->tokens, p->q_heads, p->head_dim, p->q_strides, z))) ||
+           (without != 1 && overlap(out, bytes, p->k, head_span(p->tokens, p->k_heads, p->head_dim, p->k_strides, z))) ||
+           overlap(out, bytes, p->q_weight, p->head_dim * z) || overlap(out, bytes, p->k_weight, p->head_dim * z) ||
+           overlap(out, bytes, p->positions, p->tokens * 8) || overlap(out, bytes, p->inv_freq, p->rotary / 2 * 4);
+}
+
+// Pairs of a vector: as many as 16 bytes hold, where pairs that turn, and all pairs, are whole vectors.
+int head_vector(const ckks_plain_heads *p) {
+    const int whole = 16 / (int)type_size(p->type);
+    const int64_t r = p->rotary / 2, half = p->head_dim / 2;
+    if (r % whole == 0 && half % whole == 0) return whole;
+    return r % 2 == 0 && half % 2 == 0 ? 2 : 1;
+}
+// f(type tag, pairs of a vector, vectors of a thread)
+template <typename T, typename F> int by_head(const ckks_plain_heads *p, F f) {
+    const int v = head_vector(p);
+    const int64_t units = p->head_dim / 2;
+    if (v == VEC<T>) return f(T{}, Int<VEC<T>>{}, Int<1>{});  // at most 64 threads of 4 or more
+    if (v == 2) return units <= 128 ? f(T{}, Int<2>{}, Int<1>{}) : f(T{}, Int<2>{}, Int<2>{});
+    return units <= 64 ? f(T{}, Int<1>{}, Int<1>{}) : units <= 128 ? f(T{}, Int<1>{}, Int<2>{}) : f(T{}, Int<1>{}, Int<4>{});
+}
+template <typename F> int by_head(const ckks_plain_heads *p, F f) {
+    switch (p->type) {
+        case CKKS_PLAIN_BF16: return by_head<bf16>(p, f);
+        case CKKS_PLAIN_F16: return by_head<f16>(p, f);
+        default: return by_head<float>(p, f);
+    }
+}
+
+// Threads of a head, tokens of a step and of a workgroup.
+struct HeadPlan {
+    int log_l, step, span;
+    int64_t blocks;
+};
+HeadPlan head_plan(const ckks_plain_heads *p, bool grad) {
+    HeadPlan h;
+    by_head(p, [&](auto, auto v, auto k) {
+        const int64_t share = decltype(v)::value * decltype(k)::value;
+        h.log_l = 0;
+        while ((share << h.log_l) < p->head_dim / 2) h.log_l++;
+        return 0;
+    });
+    const int64_t groups = 256 >> h.log_l;
+    h.step = (int)(p->q_heads < groups ? groups / p->q_heads : 1);
+    const int64_t most = grad ? 1024 : 1 << 22;  // workgroups of a side
+    h.span = (int)((p->tokens + most * h.step - 1) / (most * h.step) * h.step);
+    if (h.span < h.step) h.span = h.step;
+    h.blocks = (p->tokens + h.span - 1) / h.span;
+    return h;
+}
+HeadArgs head_args(const ckks_plain_heads *p, const HeadPlan &h) {
+    HeadArgs a{};
+    a.side[0].x = p->q, a.side[0].weight = p->q_weight, a.side[0].x_strides = p->q_strides;
+    a.side[1].x = p->k, a.side[1].weight = p->k_weight, a.side[1].x_strides = p->k_strides;
+    a.side[0].heads = (int)p->q_heads, a.side[1].heads = (int)p->k_heads;
+    a.side[0].blocks = (int)h.blocks, a.side[1].blocks = p->k_heads ? (int)h.blocks : 0;
+    a.positions = p->positions, a.inv_freq = p->inv_freq, a.tokens = p->tokens;
+    a.half = (int)p->head_dim / 2, a.r = (int)p->rotary / 2;
+    a.step = h.step, a.span = h.span, a.log_l = h.log_l;
+    a.eps = p->eps, a.inv_dim = 1.0f / (float)p->head_dim, a.interleaved = p->interleaved != 0;
+    return a;
+}
+
+}  // namespace ckks_plain
+
+using namespace ckks_plain;
+
+extern "C" int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, ckks_plain_head_strides q_out_strides,
+                                           void *k_out, ckks_plain_head_strides k_out_strides, void *stream) {
+    if (int e = check_heads(p)) return e;
+    if (!p->k_heads && k_out) return CKKS_EINVAL;
+    if (int e = check_side(p, q_out, p->q_heads, q_out_strides, true)) return e;
+    if (int e = check_side(p, k_out, p->k_heads, k_out_strides, true)) return e;
+    if (p->tokens == 0) return CKKS_OK;
+    const size_t z = type_size(p->type);
+    const size_t qb = head_span(p->tokens, p->q_heads, p->head_dim, q_out_strides, z);
+    const size_t kb = head_span(p->tokens, p->k_heads, p->head_dim, k_out_strides, z);
+    const bool q_in_place = q_out == p->q && same(q_out_strides, p->q_strides);
+    const bool k_in_place = k_out == p->k && same(k_out_strides, p->k_strides);
+    if (heads_overlap(p, q_out, qb, q_in_place ? 0 : -1) || heads_overlap(p, k_out, kb, k_in_place ? 1 : -1) ||
+        overlap(q_out, qb, k_out, kb))
+        return CKKS_EINVAL;
+    const HeadPlan h = head_plan(p, false);
+    HeadArgs a = head_args(p, h);
+    a.side[0].out = q_out, a.side[0].out_strides = q_out_strides;
+    a.side[1].out = k_out, a.side[1].out_strides = k_out_strides;
+    return by_head(p, [&](auto ty, auto v, auto k) {
+        k_head_norm_rotate<decltype(ty), decltype(v)::value, decltype(k)::value>
+            <<<dim3((uint32_t)(a.side[0].blocks + a.side[1].blocks)), 256, (size_t)a.step * a.r * 8,
+               (hipStream_t)stream>>>(a);
+        return launched();
+    });
+}
+
+extern "C" int ckks_plain_head_grad_workspace_size(const ckks_plain_heads *p, size_t *bytes) {
+    if (!bytes) return CKKS_EINVAL;
+    if (int e = check_heads(p)) return e;
+    const HeadPlan h = head_plan(p, true);
+    *bytes = ((p->q_weight != nullptr) + (p->k_weight != nullptr)) *
+             (size_t)round_up(h.blocks * p->head_dim * 4, 16);
+    return CKKS_OK;
+}
+
+extern "C" int ckks_plain_head_norm_rotate_grad(const ckks_plain_heads *p, const ckks_plain_head_grads *g, void *ws,
+                                                size_t ws_bytes, void *stream) {
+    if (!g) return CKKS_EINVAL;
+    size_t need;
+    if (int e = ckks_plain_head_grad_workspace_size(p, &need)) return e;
+    if (!p->q_weight != !g->q_weight || !p->k_weight != !g->k_weight) return CKKS_EINVAL;
+    if (!p->k_heads && (g->dk || g->dk_in)) return CKKS_EINVAL;
+    if (!at(g->q_weight, 4) || !at(g->k_weight, 4)) return CKKS_EALIGN;
+    if (int e = check_side(p, g->dq, p->q_heads, g->dq_strides, false)) return e;
+    if (int e = check_side(p, g->dk, p->k_heads, g->dk_strides, false)) return e;
+    if (int e = check_side(p, g->dq_in, p->q_heads, g->dq_in_strides, true)) return e;
+    if (int e = check_side(p, g->dk_in, p->k_heads, g->dk_in_strides, true)) return e;
+    const size_t z = type_size(p->type);
+    const size_t dqb = head_span(p->tokens, p->q_heads, p->head_dim, g->dq_strides, z);
+    const size_t dkb = head_span(p->tokens, p->k_heads, p->head_dim, g->dk_strides, z);
+    struct { const void *p; size_t n; } w[5] = {
+        {g->dq_in, head_span(p->tokens, p->q_heads, p->head_dim, g->dq_in_strides, z)},
+        {g->dk_in, head_span(p->tokens, p->k_heads, p->head_dim, g->dk_in_strides, z)},
+        {g->q_weight, (size_t)p->head_dim * 4}, {g->k_weight, (size_t)p->head_dim * 4}, {ws, need}};
+    for (int i = 0; i < 5; i++) {
+        if (heads_overlap(p, w[i].p, w[i].n, -1) || overlap(w[i].p, w[i].n, g->dq, dqb) ||
+            overlap(w[i].p, w[i].n, g->dk, dkb))
+            return CKKS_EINVAL;
+        for (int j = 0; j < i; j++)
+            if (overlap(w[i].p, w[i].n, w[j].p, w[j].n)) return CKKS_EINVAL;
+    }
+    if (need && (!ws || ws_bytes < need)) return CKKS_EWORKSPACE;
+    if (!at(ws, 16)) return CKKS_EALIGN;
+    const HeadPlan h = head_plan(p, true);
+    HeadArgs a = head_args(p, h);
+    a.side[0].dy = g->dq, a.side[0].dy_strides = g->dq_strides;
+    a.side[1].dy = g->dk, a.side[1].dy_strides = g->dk_strides;
+    a.side[0].out = g->dq_in, a.side[0].out_strides = g->dq_in_strides;
+    a.side[1].out = g->dk_in, a.side[1].out_strides = g->dk_in_strides;
+    const size_t one = (size_t)round_up(h.blocks * p->head_dim * 4, 16);
+    if (p->q_weight) a.side[0].part = (float *)ws;
+    if (p->k_weight) a.side[1].part = (float *)((char *)ws + (p->q_weight ? one : 0));
+    const hipStream_t s = (hipStream_t)stream;
+    if (p->tokens) {
+        int e = by_head(p, [&](auto ty, auto v, auto k) {
+            k_head_grad<decltype(ty), decltype(v)::value, decltype(k)::value>
+                <<<dim3((uint32_t)(a.side[0].blocks + a.side[1].blocks)), 256, (size_t)a.step * a.r * 8, s>>>(a);
+            return launched();
+        });
+        if (e) return e;
+    }
+    if (!p->q_weight && !p->k_weight) return CKKS_OK;
+    // without tokens the sums of nothing are written
+    k_head_weight_sum<<<dim3((uint32_t)((p->head_dim + 63) / 64), 2), 1024, 0, s>>>(
+        a.side[0].part, a.side[1].part, a.side[0].blocks, a.side[1].blocks, g->q_weight, g->k_weight,
+        (int)p->head_dim);
+    return launched();
+}

@@ -76,6 +76,42 @@ template <typename T, int NT, int E> struct Row {
     }
 };
 
+// Eight elements at p, `left` of them there (others read as 0 and are not written): pieces of rows that more
+// than one thread, workgroup or type share.
+template <typename T> struct Eight {
+    static constexpr int V = sizeof(T) == 1 ? 8 : VEC<T>;
+    typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+    Vec v[8 / V];
+    __device__ __forceinline__ void fetch(const T *p, int64_t left) {
+        if (left >= 8) {
+#pragma unroll
+            for (int i = 0; i < 8 / V; i++) v[i] = *(const Vec *)(p + i * V);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i / V][i % V] = i < left ? p[i] : (T)0;
+        }
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if constexpr (sizeof(T) == 1) return (float)(int)v[i / V][i % V];
+        else return to_f32(v[i / V][i % V]);
+    }
+    static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[8]) {
+        if (left >= 8) {
+#pragma unroll
+            for (int i = 0; i < 8; i += V) {
+                Vec w;
+#pragma unroll
+                for (int j = 0; j < V; j++) w[j] = from_f32<T>(f[i + j]);
+                *(Vec *)(p + i) = w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (i < left) p[i] = from_f32<T>(f[i]);
+        }
+    }
+};
+
 // The neighbour's value that a move between lanes brings (`none` where there is no neighbour).
 template <int CTRL, int ROWS> __device__ __forceinline__ uint32_t moved(uint32_t none, uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
@@ -171,6 +207,15 @@ __device__ __forceinline__ void store_i8(int8_t *__restrict__ q, int padded, int
         }
         *(Words *)(q + c) = w;
     }
+}
+
+// A number of the order of a float.
+__device__ __forceinline__ uint32_t order_bits(float z) {
+    const uint32_t b = __float_as_uint(z + 0.0f);  // -0 orders as 0
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float of_order_bits(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
 // Compile-time numbers and flags as arguments.

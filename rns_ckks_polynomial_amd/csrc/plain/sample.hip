@@ -5,14 +5,6 @@
 
 namespace ckks_plain {
 
-// A number of the order of a float.
-__device__ __forceinline__ uint32_t order_bits(float z) {
-    const uint32_t b = __float_as_uint(z + 0.0f);  // -0 orders as 0
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float of_order_bits(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 struct SampleArgs {

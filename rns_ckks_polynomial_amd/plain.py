@@ -1,13 +1,14 @@
-"""The plaintext side of an encrypted decoder (include/ckks_plain.h): residual
-stream and norms around a block, products of 8-bit rows, and token sampling.
+"""The plaintext side of an encrypted decoder (include/ckks_plain.h): embedding,
+residual stream and norms around a block, norms and rotation of heads, products
+of 8-bit rows, token sampling and the log probabilities of given tokens.
 
 Argument checks and marshalling only: every step of the computation runs in
 the HIP library.  Matrices are 2-D device tensors with unit column stride (any
 row stride of at least their columns); calls are enqueued on the current torch stream of the tensors'
 device, outputs and scratch come from torch's allocator.
 
-residual_norm has a gradient.  Results of the other calls have none: where autograd
-follows an operand, asking for a derivative through them raises.  Operands with a
+embed, residual_norm, head_norm_rotate and token_logprobs have a gradient.  Results of the other calls have none:
+where autograd follows an operand, asking for a derivative through them raises.  Operands with a
 tangent of forward-mode differentiation are refused by all of them.
 """
 from __future__ import annotations
@@ -25,9 +26,13 @@ TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 KINDS = {"rms": 0, "layer": 1}
 I8_ROW = 128        # CKKS_PLAIN_I8_ROW
 MAX_COLS = 16384    # CKKS_PLAIN_MAX_COLS
+MAX_HEAD = 512      # CKKS_PLAIN_MAX_HEAD
+MAX_TOP = 64        # CKKS_PLAIN_MAX_TOP
 
 ResidualNormGrads = namedtuple("ResidualNormGrads",
                                "dx dy next_weight next_bias block_weight block_bias gate")
+HeadNormRotateGrads = namedtuple("HeadNormRotateGrads", "dq dk q_weight k_weight")
+TokenLogprobs = namedtuple("TokenLogprobs", "logprob entropy top_token top_logprob largest log_mass")
 
 
 _entry = {}
@@ -383,3 +388,319 @@ def sample(logits, gumbel, temperature, top_k=None, top_p=None, min_p=None, allo
     if _tracked(logits, gumbel, temperature, top_p, min_p):
         token, logprob = _NoGradient.apply("sample", (token, logprob), logits, gumbel, temperature, top_p, min_p)
     return token, logprob
+
+
+# ------------------------------------------------------------------ embedding
+
+def _embed(tokens, table, scale, dtype):
+    is_i8 = isinstance(table, Int8Rows)
+    t = table.q if is_i8 else table
+    if is_i8:
+        (V, D), stride, code = (table.rows, table.cols), t.stride(0), None
+    else:
+        stride = _matrix(t, "table")
+        (V, D), code = t.shape, _type(t, "table")
+    dtype = (torch.bfloat16 if is_i8 else t.dtype) if dtype is None else dtype
+    if dtype not in TYPES:
+        raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+    dev, T = t.device, _count(tokens, "tokens")
+    tp = _vector(tokens, "tokens", T, torch.int64, dev)
+    out = torch.empty((T, D), dtype=dtype, device=dev)
+    if is_i8:
+        _call("ckks_plain_embed_i8", dev, t.data_ptr(), stride, table.scale.data_ptr(), V, D, tp, T, scale,
+              TYPES[dtype], out.data_ptr(), D)
+    else:
+        _call("ckks_plain_embed", dev, code, t.data_ptr(), stride, V, D, tp, T, scale, TYPES[dtype], out.data_ptr(), D)
+    return out
+
+
+def _count(t, what):
+    """Elements of a vector argument."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{what}: expected a device vector")
+    return t.shape[0]
+
+
+class _Embed(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, table, scale, dtype):
+        ctx.save_for_backward(tokens)
+        ctx.rest = (table.shape[0], scale, table.dtype)
+        return _embed(tokens, table, scale, dtype)
+
+    @staticmethod
+    def backward(ctx, drows):
+        tokens, = ctx.saved_tensors
+        vocab, scale, dtype = ctx.rest
+        return None, embed_grad(drows.contiguous(), tokens, vocab, scale, dtype), None, None
+
+
+def embed(tokens, table, scale: float = 1.0, dtype=None) -> torch.Tensor:
+    """[T, D]: scale times the table's row of each token (ckks_plain_embed).  tokens: int64 [T]; a token outside
+    [0, V) (padding, or the -1 of sample) gives zeros.  table: [V, D], or Int8Rows (the weights of the vocabulary
+    product, whose scales then multiply too).  dtype defaults to that of the table, bfloat16 for Int8Rows.
+    Differentiable once through torch.autograd for a table of numbers: its gradient is summed in 32 bits, in a fixed
+    order, and rounded to its type."""
+    if isinstance(table, Int8Rows):
+        out = _embed(tokens, table, scale, dtype)
+        if _tracked(table.scale):
+            out, = _NoGradient.apply("embed of Int8Rows", (out,), table.scale)
+        return out
+    if _tracked(table):
+        return _Embed.apply(tokens, table, scale, dtype)
+    return _embed(tokens, table, scale, dtype)
+
+
+def embed_grad(drows, tokens, vocab: int, scale: float = 1.0, dtype=torch.float32, into=None) -> torch.Tensor:
+    """[vocab, D]: gradient of embed's table from that of its rows (ckks_plain_embed_grad): row v is scale times the
+    sum of drows over the tokens v.  into: a matrix [vocab, D] (of any of the three types) that the sums are added to
+    and that is returned; only rows of the tokens are touched, where a new matrix is written whole.  The gradient has
+    none of its own: a second derivative raises."""
+    stride = _matrix(drows, "drows")
+    T, D = drows.shape
+    dev = drows.device
+    if _count(tokens, "tokens") != T:
+        raise ValueError(f"tokens: expected {T}, got {tokens.shape[0]}")
+    tp = _vector(tokens, "tokens", T, torch.int64, dev)
+    if into is None:
+        if dtype not in TYPES:
+            raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
+        out, out_stride = torch.empty((vocab, D), dtype=dtype, device=dev), D
+    else:
+        out, out_stride = into, _matrix(into, "into", vocab, D, None, dev)
+        if into.requires_grad or _tracked(drows):
+            raise ValueError("into: sums that autograd follows cannot be added to a matrix")
+    _keep, ws, size = _scratch(_workspace("ckks_plain_embed_grad_workspace_size", T, vocab, D), dev)
+    _call("ckks_plain_embed_grad", dev, _type(drows, "drows"), drows.data_ptr(), stride, tp, T, vocab, D, scale,
+          _type(out, "into"), out.data_ptr(), out_stride, into is not None, ws, size)
+    if into is not None:
+        if not into.is_inference():
+            torch.autograd.graph.increment_version(into)
+    elif _tracked(drows):
+        out, = _NoGradient.apply("embed_grad", (out,), drows)
+    return out
+
+
+# ------------------------------------------------------------------ heads
+
+def _heads(t, what, tokens=None, dim=None, dtype=None, device=None):
+    """(address, strides) of a tensor of heads."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{what}: expected a device tensor [tokens, heads, head_dim]")
+    T, H, d = t.shape
+    if (tokens is not None and T != tokens) or (dim is not None and d != dim):
+        raise ValueError(f"{what}: expected [{tokens}, heads, {dim}], got {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    token, head, across = t.stride()
+    if d > 1 and across != 1:
+        raise ValueError(f"{what}: expected unit stride within a head")
+    return t.data_ptr(), nat.PlainHeadStrides(token, head)
+
+
+_NO_STRIDES = nat.PlainHeadStrides(0, 0)
+
+
+def _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
+    """ckks_plain_heads of the arguments."""
+    qp, qs = _heads(q, "q")
+    T, H, d = q.shape
+    dev, dt = q.device, q.dtype
+    kp, ks, k_heads = None, _NO_STRIDES, 0
+    if k is not None:
+        kp, ks = _heads(k, "k", T, d, dt, dev)
+        k_heads = k.shape[1]
+        if k_heads < 1:
+            raise ValueError("k: expected at least one head")
+    elif k_weight is not None:
+        raise ValueError("k_weight: there is no k")
+    rotary, pp, fp = 0, None, None
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq: expected both or none")
+    if positions is not None:
+        pp = _vector(positions, "positions", T, torch.int64, dev)
+        n = _count(inv_freq, "inv_freq")
+        fp, rotary = _vector(inv_freq, "inv_freq", n, torch.float32, dev), 2 * n
+    return nat.PlainHeads(_type(q, "q"), 1 if interleaved else 0, T, H, k_heads, d, rotary, qp, kp, qs, ks,
+                          _vector(q_weight, "q_weight", d, dt, dev), _vector(k_weight, "k_weight", d, dt, dev), pp, fp,
+                          eps)
+
+
+def _new_heads(t):
+    """(tensor of t's shape and type, its strides)"""
+    if t is None:
+        return None, None, _NO_STRIDES
+    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return out, out.data_ptr(), nat.PlainHeadStrides(t.shape[1] * t.shape[2], t.shape[2])
+
+
+def _head_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
+    p = _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+    q_out, qp, qs = _new_heads(q)
+    k_out, kp, ks = _new_heads(k)
+    _call("ckks_plain_head_norm_rotate", q.device, C.byref(p), qp, qs, kp, ks)
+    return q_out, k_out
+
+
+class _HeadNormRotate(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
+        ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
+        ctx.rest = (eps, interleaved)
+        return _head_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        q, k, positions, inv_freq, qw, kw = ctx.saved_tensors
+        if ctx.needs_input_grad[3]:
+            raise RuntimeError("head_norm_rotate has no gradient of inv_freq")
+        eps, interleaved = ctx.rest
+        unit = lambda v: v if v is None or v.stride(-1) == 1 else v.contiguous()  # noqa: E731
+        dq, dk = (v if v is None or min(v.stride()) else v.contiguous() for v in (unit(dq), unit(dk)))
+        g = head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, qw, kw, eps, interleaved)
+        like = lambda v, p: None if p is None else v.to(p.dtype)  # noqa: E731
+        return g.dq, g.dk, None, None, like(g.q_weight, qw), like(g.k_weight, kw), None, None
+
+
+def head_norm_rotate(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False):
+    """(q, k) [T, heads, d], each head normalised (x / sqrt(mean x^2 + eps) weight) and then rotated by position
+    (ckks_plain_head_norm_rotate): pair i of its dimensions, (i, i + r) or (2 i, 2 i + 1) if interleaved, turns by
+    positions[t] inv_freq[i]; dimensions from 2 r on stay.  q, k: heads of any strides with unit stride within a head
+    (views of a joint projection, say), k may be None.  positions: int64 [T]; inv_freq: float32 [r], 2 r <= d; both
+    None: no rotation.  q_weight, k_weight: [d], of the type of q; None: no norm.  d is even, at most MAX_HEAD.
+    Differentiable once through torch.autograd (gradients of weights are summed in 32 bits, then rounded to their
+    type; a second derivative raises, as does one by inv_freq)."""
+    if _tracked(q, k, inv_freq, q_weight, k_weight):
+        return _HeadNormRotate.apply(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+    return _head_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+
+
+def head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,
+                          interleaved: bool = False) -> HeadNormRotateGrads:
+    """Gradients of head_norm_rotate's q, k and weights from those of its results dq, dk: of q and k in their type,
+    of the weights in float32, None where there is no such operand.  They have no gradient of their own: a second
+    derivative raises."""
+    p = _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
+    T, d = q.shape[0], q.shape[2]
+    side = []
+    for x, g, what in ((q, dq, "dq"), (k, dk, "dk")):
+        if (x is None) != (g is None):
+            raise ValueError(f"{what}: expected the gradient of each result")
+        if x is None:
+            side.append((None, _NO_STRIDES))
+            continue
+        side.append(_heads(g, what, T, d, x.dtype, x.device))
+        if g.shape[1] != x.shape[1]:
+            raise ValueError(f"{what}: expected {x.shape[1]} heads, got {g.shape[1]}")
+    dq_in, qp, qs = _new_heads(q)
+    dk_in, kp, ks = _new_heads(k)
+    new = lambda v: None if v is None else torch.empty(v.shape, dtype=torch.float32, device=q.device)  # noqa: E731
+    r = HeadNormRotateGrads(dq_in, dk_in, new(q_weight), new(k_weight))
+    at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
+    g = nat.PlainHeadGrads(side[0][0], side[1][0], side[0][1], side[1][1], qp, kp, qs, ks, at(r.q_weight),
+                           at(r.k_weight))
+    size = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_head_grad_workspace_size(C.byref(p), C.byref(size)),
+              "ckks_plain_head_grad_workspace_size")
+    _keep, ws, size = _scratch(size.value, q.device)
+    _call("ckks_plain_head_norm_rotate_grad", q.device, C.byref(p), C.byref(g), ws, size)
+    operands = (q, k, dq, dk, inv_freq, q_weight, k_weight)
+    if _tracked(*operands):
+        some = iter(_NoGradient.apply("head_norm_rotate_grad", tuple(v for v in r if v is not None), *operands))
+        r = HeadNormRotateGrads(*(v if v is None else next(some) for v in r))
+    return r
+
+
+# ------------------------------------------------------------------ log probabilities
+
+def _score_args(logits, tokens, temperature, allowed):
+    """What both calls begin with, up to the number of columns."""
+    stride = _matrix(logits, "logits")
+    B, V = logits.shape
+    dev = logits.device
+    if tokens is None:
+        raise ValueError("tokens: expected int64 of every row")
+    a_stride = 0
+    if allowed is not None:
+        a_stride = _matrix(allowed, "allowed", B, V, torch.bool, dev)
+    return (_type(logits, "logits"), logits.data_ptr(), stride, _vector(tokens, "tokens", B, torch.int64, dev),
+            _vector(temperature, "temperature", B, torch.float32, dev),
+            None if allowed is None else allowed.data_ptr(), a_stride, B, V)
+
+
+def _score(logits, tokens, top, temperature, allowed):
+    args = _score_args(logits, tokens, temperature, allowed)
+    B, V = logits.shape
+    dev = logits.device
+    new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+    if not 0 <= top <= MAX_TOP:
+        raise ValueError(f"top: expected 0 to {MAX_TOP}, got {top}")
+    f32 = torch.float32
+    r = TokenLogprobs(new(f32, B), new(f32, B), new(torch.int64, B, top), new(f32, B, top), new(f32, B), new(f32, B))
+    _keep, ws, size = _scratch(_workspace("ckks_plain_token_logprobs_workspace_size", B, V, top), dev)
+    _call("ckks_plain_token_logprobs", dev, *args, top, r.logprob.data_ptr(), r.entropy.data_ptr(),
+          r.largest.data_ptr(), r.log_mass.data_ptr(), r.top_token.data_ptr() if top else None,
+          r.top_logprob.data_ptr() if top else None, ws, size)
+    return r
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top, temperature, allowed):
+        ctx.set_materialize_grads(False)
+        r = _score(logits, tokens, top, temperature, allowed)
+        ctx.save_for_backward(logits, tokens, temperature, allowed, *r)
+        ctx.mark_non_differentiable(r.top_token)
+        return tuple(r)
+
+    @staticmethod
+    def backward(ctx, dlogprob, dentropy, _token, *others):
+        if ctx.needs_input_grad[3]:
+            raise RuntimeError("token_logprobs has no gradient of the temperature")
+        if any(g is not None for g in others):
+            raise RuntimeError("token_logprobs has a gradient of logprob and entropy alone")
+        logits, tokens, temperature, allowed, *r = ctx.saved_tensors
+        whole = lambda g: None if g is None else g.contiguous()  # noqa: E731
+        return token_logprobs_grad(logits, tokens, TokenLogprobs(*r), whole(dlogprob), whole(dentropy), temperature,
+                                   allowed), None, None, None, None
+
+
+def token_logprobs(logits, tokens, top: int = 0, temperature=None, allowed=None) -> TokenLogprobs:
+    """Log probabilities of given tokens under logits [B, V] (ckks_plain_token_logprobs), as sample has them: a token is
+    possible if allowed (bool [B, V]) and its logit neither NaN nor -infinity; x = (logit - largest) / temperature
+    (float32 [B]; None or <= 0: 1) of those, and
+      logprob [B]                of tokens (int64 [B]): x - log_mass; -infinity if it is not possible, 0 if it is
+                                 outside [0, V) (a padded row);
+      entropy [B]                in natural units;
+      top_token, top_logprob     [B, top]: the largest, lower index first among equals; -1 and -infinity behind the
+                                 last possible one;
+      largest, log_mass [B]      the largest logit and log sum exp x.
+    A row without a possible token: entropy 0, largest and log_mass -infinity.  Differentiable once through
+    torch.autograd, by the logits, for logprob and entropy; any other derivative raises."""
+    if _tracked(logits, temperature):
+        return TokenLogprobs(*_TokenLogprobs.apply(logits, tokens, top, temperature, allowed))
+    return _score(logits, tokens, top, temperature, allowed)
+
+
+def token_logprobs_grad(logits, tokens, scores: TokenLogprobs, dlogprob=None, dentropy=None, temperature=None,
+                        allowed=None) -> torch.Tensor:
+    """Gradient of the logits, in their type, from those of logprob and entropy (float32 [B], None: zero;
+    ckks_plain_token_logprobs_grad).  scores: what token_logprobs returned for the same operands.  Tokens that are not
+    possible get 0.  The gradient has none of its own: a second derivative raises."""
+    args = _score_args(logits, tokens, temperature, allowed)
+    B, V = logits.shape
+    dev = logits.device
+    f32 = lambda v, what: _vector(v, what, B, torch.float32, dev)  # noqa: E731
+    stats = [getattr(scores, n, None) for n in ("entropy", "largest", "log_mass")]
+    if any(v is None for v in stats):
+        raise ValueError("scores: expected what token_logprobs returned")
+    out = _like(logits)
+    _call("ckks_plain_token_logprobs_grad", dev, *args, *(f32(v, "scores") for v in stats), f32(dlogprob, "dlogprob"),
+          f32(dentropy, "dentropy"), out.data_ptr(), V)
+    operands = (logits, *stats, dlogprob, dentropy, temperature)
+    if _tracked(*operands):
+        out, = _NoGradient.apply("token_logprobs_grad", (out,), *operands)
+    return out
