@@ -25,82 +25,262 @@ __device__ __forceinline__ float inverse_temperature(const float *temperature, i
 // The distance of a logit to the largest, 0 also where both are infinite.
 __device__ __forceinline__ float distance(float z, float largest) { return z == largest ? 0.0f : z - largest; }
 
-// Logits c ... c + 7 of a row, -infinity where there is no possible token.
+constexpr int MAX_SLICES = 32, JOIN_KEYS = MAX_SLICES * CKKS_PLAIN_MAX_TOP;
+
 template <typename T, bool MASK>
-__device__ __forceinline__ void fetch_logits(const T *z, const uint8_t *allowed, int64_t c, int64_t vocab,
-                                             float (&f)[8]) {
-    Eight<T> e;
-    Eight<int8_t> ok;
-    e.fetch(z + c, vocab - c);
-    if constexpr (MASK) ok.fetch((const int8_t *)allowed + c, vocab - c);
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        f[i] = e.at(i);
-        if (!(c + i < vocab) || !(f[i] > -INFINITY) || (MASK && !ok.v[0][i])) f[i] = -INFINITY;
+__device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const T *z, const uint8_t *allowed,
+                                          float largest, float log_mass, float mean, float inv_t) {
+    const int64_t token = a.tokens[row];
+    float lp = 0;
+    if (token >= 0 && token < a.vocab) {
+        const float v = to_f32(z[token]);
+        lp = v > -INFINITY && (!MASK || allowed[token]) ? distance(v, largest) * inv_t - log_mass : -INFINITY;
     }
+    a.logprob[row] = lp;
+    a.entropy[row] = log_mass > -INFINITY ? log_mass - LN2 * mean : 0.0f;  // mean: of the distances, in powers of two
+    a.largest[row] = largest;
+    a.log_mass[row] = log_mass;
 }
 
-// A workgroup a row: its largest logit, then its sums, then one read for each alternative.
-constexpr int SCORE_NT = 1024;
-template <typename T, bool MASK>
-__global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a) {
-    __shared__ uint64_t buf[2][SCORE_NT / 64];
-    __shared__ float sums[2][SCORE_NT / 64];
+// Logits c ... c + 7 of a row; -infinity or NaN where there is no possible token.
+template <typename T, bool MASK> struct Logits {
+    Eight<T> e;
+    Eight<int8_t> ok;
+    __device__ __forceinline__ void fetch(const T *z, const uint8_t *allowed, int c, int end) {
+        e.fetch(z + c, end - c);
+        if constexpr (MASK) ok.fetch((const int8_t *)allowed + c, end - c);
+    }
+    __device__ __forceinline__ void widen(int c, int end, float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            f[i] = e.at(i);
+            if (MASK && !ok.v[0][i]) f[i] = -INFINITY;
+        }
+        if (c + 8 > end) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (c + i >= end) f[i] = -INFINITY;
+        }
+    }
+};
+
+constexpr int SCORE_NT = 512, GROUPS = 64, GROUP_LANES = SCORE_NT / GROUPS, CANDIDATES = 1024;
+constexpr float LEAST = -200.0f;  // exp2 of it is 0
+
+// A sum of 2^x and of x 2^x over logits, x = (z - m) scale, in terms of the largest so far.
+struct Mass {
+    float m, mass, moment;  // m: the lowest number where there is none yet
+    // in terms of a larger one
+    __device__ __forceinline__ void move(float to, float scale) {
+        const float d = fmaxf((m - to) * scale, LEAST), k = __builtin_amdgcn_exp2f(d);
+        moment = k * (moment + d * mass);
+        mass *= k;
+        m = to;
+    }
+    // v: their largest; to: the larger of it and m
+    __device__ __forceinline__ void add(const float (&f)[8], float scale) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float x = fmaxf((f[i] - m) * scale, LEAST);  // LEAST for -infinity and NaN
+            const float e = __builtin_amdgcn_exp2f(x);
+            mass += e;
+            moment += e * x;
+        }
+    }
+};
+// (NaN is no larger than anything)
+__device__ __forceinline__ float largest_of(const float (&f)[8]) {
+    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+}
+// The order of tokens as a number: by logit, then the lower index.  0 is below all.
+__device__ __forceinline__ uint64_t token_key(float z, int index) { return (uint64_t)order_bits(z) << 32 | (uint32_t)~index; }
+__device__ __forceinline__ float key_logit(uint64_t k) { return of_order_bits((uint32_t)(k >> 32)); }
+
+// Alternative `rank` of a row (key 0: there is none), or of its slice.
+__device__ __forceinline__ void put_top(const ScoreArgs &a, int64_t row, int rank, uint64_t key, float largest,
+                                        float log_mass, float inv_t, uint64_t *keys) {
+    if (keys) {
+        keys[(row * gridDim.y + blockIdx.y) * a.top + rank] = key;
+        return;
+    }
+    a.top_token[row * a.top + rank] = key ? (int64_t)(uint32_t)~(uint32_t)key : -1;
+    a.top_logprob[row * a.top + rank] = key ? distance(key_logit(key), largest) * inv_t - log_mass : -INFINITY;
+}
+
+struct ScoreShared {
+    uint64_t groups[GROUPS], list[CANDIDATES], bound;
+    uint32_t slots[SCORE_NT / 64], winners[SCORE_NT], n_winners, n;
+    float sums[2][SCORE_NT / 64];
+};
+// What a slice of a row leaves for the whole: these and its `top` largest keys, in order.
+struct Part {
+    float m, mass, moment, unused;
+};
+
+// The rank of a key of sh.list: how many of its first n are larger.
+__device__ __forceinline__ int rank_in_list(const uint64_t *list, int n, uint64_t key) {
+    int r = 0;
+    for (int i = 0; i < n; i++) r += list[i] > key;
+    return r;
+}
+
+// A workgroup reads a slice of a row once.  Each thread keeps the sums and the largest of what it reads in
+// terms of its own largest.  The alternatives:  a thread's key is its largest logit and the end of the vector
+// where that first came, so at least one token is not below it.  The top-th largest of the keys of 64 groups
+// of threads is a bound which at least `top` tokens pass; they are all among the tokens of threads whose largest
+// logit passes it from its vector's start (`winners`, little more than `top`), which are read again.  What passes goes on a list, and a
+// token's rank there is its place.  Where the list is too short (runs of equal logits, rows in bad order), the
+// top-th largest on it is a better bound: all that were on it below that one do not come back, so it ends.
+template <typename T, bool MASK, bool TOP>
+__global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {
+    __shared__ ScoreShared sh;
+    const int t = threadIdx.x;
     const int64_t row = a.first + blockIdx.x;
     const T *z = (const T *)a.logits + row * a.stride;
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
-    auto best_under = [&](uint64_t bound, uint64_t *at) {  // the largest key below it (0: none)
-        uint64_t best = 0;
-        for (int c = threadIdx.x * 8; c < a.vocab; c += SCORE_NT * 8) {
-            float f[8];
-            fetch_logits<T, MASK>(z, allowed, c, a.vocab, f);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint64_t key = (uint64_t)order_bits(f[i]) << 32 | (uint32_t)~(c + i);
-                if (f[i] > -INFINITY && key < bound && key > best) best = key;
-            }
-        }
-        return row_all<SCORE_NT>(best, at, Larger{});
-    };
-    const uint64_t first = best_under(~(uint64_t)0, buf[0]);
-    const float m = first ? of_order_bits((uint32_t)(first >> 32)) : -INFINITY;
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
-    float mass = 0, moment = 0;
-    if (first)
-        for (int c = threadIdx.x * 8; c < a.vocab; c += SCORE_NT * 8) {
+    const int begin = blockIdx.y * slice, end = begin + slice < a.vocab ? begin + slice : a.vocab;
+    Mass s{-3.402823466e38f, 0, 0};
+    float best = -INFINITY;
+    int best_at = 0;
+    if (t == 0) sh.bound = 1, sh.n_winners = sh.n = 0;
+    for (int c = begin + t * 8; c < end; c += SCORE_NT * 16) {
+        const int d = c + SCORE_NT * 8;
+        Logits<T, MASK> p, q;
+        float f[8], g[8];
+        p.fetch(z, allowed, c, end);
+        if (d < end) q.fetch(z, allowed, d, end);
+        p.widen(c, end, f);
+        if (d < end) {
+            q.widen(d, end, g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) g[i] = -INFINITY;
+        }
+        const float v = largest_of(f), w = largest_of(g);
+        if (TOP) {
+            if (v > best) best = v, best_at = c;
+            if (w > best) best = w, best_at = d;
+        }
+        s.move(fmaxf(fmaxf(s.m, v), w), scale);
+        s.add(f, scale);
+        s.add(g, scale);
+    }
+    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(s.m), sh.slots, Larger{}));
+    s.move(m, scale);
+    if (m == INFINITY) {  // their number counts, whatever the rest
+        s.mass = s.moment = 0;
+        for (int c = begin + t * 8; c < end; c += SCORE_NT * 8) {
+            Logits<T, MASK> p;
             float f[8];
-            fetch_logits<T, MASK>(z, allowed, c, a.vocab, f);
+            p.fetch(z, allowed, c, end);
+            p.widen(c, end, f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) s.mass += f[i] == INFINITY;
+        }
+    }
+    row_sums<SCORE_NT>(s.mass, s.moment, sh.sums[0], sh.sums[1]);
+    const bool some = s.mass > 0;
+    const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
+    if (t == 0) {
+        if (parts) {
+            parts[row * gridDim.y + blockIdx.y] = Part{m, s.mass, s.moment, 0};
+        } else {
+            put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
+        }
+    }
+    if (!TOP) return;
+    const uint64_t mine = best > -INFINITY ? token_key(best, best_at + 7) : 0;
+    uint64_t group = mine;
+    group = Larger{}(group, moved<0xb1, 0xf>((uint64_t)0, group));
+    group = Larger{}(group, moved<0x4e, 0xf>((uint64_t)0, group));
+    group = Larger{}(group, moved<0x141, 0xf>((uint64_t)0, group));
+    if (t % GROUP_LANES == 0) sh.groups[t / GROUP_LANES] = group;
+    __syncthreads();
+    if (t < 64) {
+        const uint64_t key = sh.groups[t];
+        int rank = 0;
+        for (int i = 0; i < GROUPS; i++) rank += lane(key, i) > key;
+        if (rank == a.top - 1 && key) sh.bound = key;
+    }
+    const int steps = (end - begin + SCORE_NT * 8 - 1) / (SCORE_NT * 8);  // vectors of a thread
+    int n;
+    for (;;) {
+        __syncthreads();
+        const uint64_t bound = sh.bound;
+        if (mine && mine + 7 >= bound) sh.winners[atomicAdd(&sh.n_winners, 1u)] = t;
+        __syncthreads();
+        const int jobs = (int)sh.n_winners * steps;
+        for (int j = t; j < jobs; j += SCORE_NT) {
+            const int c = begin + (j % steps * SCORE_NT + (int)sh.winners[j / steps]) * 8;
+            if (c >= end) continue;
+            Logits<T, MASK> p;
+            float f[8];
+            p.fetch(z, allowed, c, end);
+            p.widen(c, end, f);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float x = fmaxf(distance(f[i], m) * scale, -200.0f);  // 2^-200 is 0
-                const float e = f[i] > -INFINITY ? __builtin_amdgcn_exp2f(x) : 0.0f;
-                mass += e;
-                moment += e * x;
+                const uint64_t key = token_key(f[i], c + i);
+                if (f[i] > -INFINITY && key >= bound) {
+                    const uint32_t at = atomicAdd(&sh.n, 1u);
+                    if (at < CANDIDATES) sh.list[at] = key;
+                }
             }
         }
-    row_sums<SCORE_NT>(mass, moment, sums[0], sums[1]);
-    const float log_mass = first ? logf(mass) : -INFINITY;
-    if (threadIdx.x == 0) {
-        const int64_t token = a.tokens[row];
-        float lp = 0;
-        if (token >= 0 && token < a.vocab) {
-            const float v = to_f32(z[token]);
-            const bool possible = v > -INFINITY && (!MASK || allowed[token]);
-            lp = possible ? distance(v, m) * inv_t - log_mass : -INFINITY;
-        }
-        a.logprob[row] = lp;
-        a.entropy[row] = first ? log_mass - LN2 * (moment / mass) : 0.0f;
-        a.largest[row] = m;
-        a.log_mass[row] = log_mass;
+        __syncthreads();
+        n = (int)sh.n;
+        if (n <= CANDIDATES) break;
+        for (int i = t; i < CANDIDATES; i += SCORE_NT)
+            if (rank_in_list(sh.list, CANDIDATES, sh.list[i]) == a.top - 1) sh.bound = sh.list[i];
+        __syncthreads();
+        if (t == 0) sh.n_winners = sh.n = 0;
     }
-    uint64_t key = first;
-    for (int k = 0; k < a.top; k++) {
-        if (threadIdx.x == 0) {
-            a.top_token[row * a.top + k] = key ? (int64_t)(uint32_t)~(uint32_t)key : -1;
-            a.top_logprob[row * a.top + k] =
-                key ? distance(of_order_bits((uint32_t)(key >> 32)), m) * inv_t - log_mass : -INFINITY;
+    for (int i = t; i < n; i += SCORE_NT) {
+        const int rank = rank_in_list(sh.list, n, sh.list[i]);
+        if (rank < a.top) put_top(a, row, rank, sh.list[i], largest, log_mass, inv_t, keys);
+    }
+    for (int i = n + t; i < a.top; i += SCORE_NT) put_top(a, row, i, 0, largest, log_mass, inv_t, keys);
+}
+
+// A row's slices together: one workgroup a row.
+template <typename T, bool MASK>
+__global__ __launch_bounds__(SCORE_NT) void k_join_logprobs(ScoreArgs a, int slices, const Part *parts,
+                                                            const uint64_t *keys) {
+    __shared__ uint64_t list[JOIN_KEYS];
+    __shared__ uint32_t slots[SCORE_NT / 64];
+    __shared__ float sums[2][SCORE_NT / 64];
+    const int t = threadIdx.x;
+    const int64_t row = a.first + blockIdx.x;
+    const T *z = (const T *)a.logits + row * a.stride;
+    const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
+    const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
+    Mass s{-3.402823466e38f, 0, 0};
+    if (t < slices) {
+        const Part p = parts[row * slices + t];
+        s = Mass{p.m, p.mass, p.moment};
+    }
+    for (int i = t; i < slices * a.top; i += SCORE_NT) list[i] = keys[row * slices * a.top + i];
+    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(s.m), slots, Larger{}));
+    if (s.m != m) s.move(m, scale);  // two infinities have no distance
+    row_sums<SCORE_NT>(s.mass, s.moment, sums[0], sums[1]);
+    const bool some = s.mass > 0;
+    const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
+    if (t == 0) put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
+    // Each slice's keys fall: a key's place among all is where it would stand in each of them.
+    for (int i = t; i < slices * a.top; i += SCORE_NT) {
+        const uint64_t key = list[i];
+        int rank = i % a.top;
+        for (int k = 0; k < slices && rank < a.top; k++) {
+            if (k == i / a.top) continue;
+            int low = 0, high = a.top;  // the first `low` are larger
+            while (low < high) {
+                const int mid = (low + high) / 2;
+                if (list[k * a.top + mid] > key || (list[k * a.top + mid] == key && k < i / a.top)) low = mid + 1;
+                else high = mid;
+            }
+            rank += low;
         }
-        if (k + 1 < a.top && key) key = best_under(key, buf[(k + 1) % 2]);
+        if (rank < a.top) put_top(a, row, rank, key, largest, log_mass, inv_t, nullptr);
     }
 }
 
@@ -127,15 +307,17 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
     float dl = 0;
     if (a.dlogprob && token >= 0 && token < a.vocab && to_f32(z[token]) > -INFINITY && (!MASK || allowed[token]))
         dl = a.dlogprob[row];
-    const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 8;
+    const int c = ((int)blockIdx.y * 256 + threadIdx.x) * 8;
     if (c >= a.vocab) return;
     float f[8];
-    fetch_logits<T, MASK>(z, allowed, c, a.vocab, f);
+    Logits<T, MASK> p;
+    p.fetch(z, allowed, c, a.vocab);
+    p.widen(c, a.vocab, f);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const float lp = fmaxf(distance(f[i], m) * inv_t - log_mass, -200.0f);
-        const float p = __builtin_amdgcn_exp2f(lp * LOG2E);  // 0 at the bound
-        const float g = (c + i == token ? dl : 0.0f) - p * (dl + dh * (lp + h));
+        const float e = __builtin_amdgcn_exp2f(lp * LOG2E);  // 0 at the bound
+        const float g = (c + i == token ? dl : 0.0f) - e * (dl + dh * (lp + h));
         f[i] = f[i] > -INFINITY ? g * inv_t : 0.0f;
     }
     Eight<T>::store((T *)a.dlogits + row * a.out_stride + c, a.vocab - c, f);
@@ -153,6 +335,13 @@ template <typename F> int by_mask(int type, bool mask, F f) {
 int check_score(int64_t rows, int64_t vocab) {
     if (rows < 0 || rows >= (int64_t)1 << 31 || vocab < 1) return CKKS_EINVAL;
     return vocab > (int64_t)1 << 24 ? CKKS_EUNSUPPORTED : CKKS_OK;
+}
+// Slices of a row: enough workgroups for the GPU where there are few rows, none of less than a read of all
+// its threads.
+int64_t score_slices(int64_t rows, int64_t vocab) {
+    const int64_t most = vocab / (SCORE_NT * 16), want = rows ? 512 / rows : 1;
+    const int64_t n = want < most ? want : most;
+    return n < 1 ? 1 : n < MAX_SLICES ? n : MAX_SLICES;
 }
 struct Range {
     const void *p;
@@ -175,7 +364,8 @@ extern "C" int ckks_plain_token_logprobs_workspace_size(int64_t rows, int64_t vo
     if (!bytes || top < 0) return CKKS_EINVAL;
     if (int e = check_score(rows, vocab)) return e;
     if (top > CKKS_PLAIN_MAX_TOP) return CKKS_EUNSUPPORTED;
-    *bytes = 0;
+    const int64_t slices = score_slices(rows, vocab);
+    *bytes = slices > 1 ? (size_t)(rows * slices) * (sizeof(Part) + top * 8) : 0;
     return CKKS_OK;
 }
 
@@ -212,10 +402,20 @@ extern "C" int ckks_plain_token_logprobs(int type, const void *logits, int64_t l
     ScoreArgs a{logits, tokens, temperature, allowed, logits_stride, allowed_stride, 0, (int)vocab, (int)top,
                 logprob, entropy, largest, log_mass, top_token, top_logprob};
     return by_mask(type, allowed != nullptr, [&](auto ty, auto mask) {
-        return in_parts(rows, SCORE_NT, [&](int64_t first, int64_t n) {
+        typedef decltype(ty) T;
+        constexpr bool MASK = decltype(mask)::value;
+        const int slices = (int)score_slices(rows, vocab);
+        const int slice = (int)round_up((vocab + slices - 1) / slices, 8);
+        Part *parts = slices > 1 ? (Part *)ws : nullptr;
+        uint64_t *keys = slices > 1 && top ? (uint64_t *)(parts + rows * slices) : nullptr;
+        return in_parts(rows, SCORE_NT * slices, [&](int64_t first, int64_t n) {
             a.first = first;
-            k_token_logprobs<decltype(ty), decltype(mask)::value>
-                <<<dim3((uint32_t)n), SCORE_NT, 0, (hipStream_t)stream>>>(a);
+            const dim3 grid((uint32_t)n, slices);
+            if (top) k_token_logprobs<T, MASK, true><<<grid, SCORE_NT, 0, (hipStream_t)stream>>>(a, slice, parts, keys);
+            else k_token_logprobs<T, MASK, false><<<grid, SCORE_NT, 0, (hipStream_t)stream>>>(a, slice, parts, keys);
+            if (int e = launched()) return e;
+            if (slices == 1) return CKKS_OK;
+            k_join_logprobs<T, MASK><<<dim3((uint32_t)n), SCORE_NT, 0, (hipStream_t)stream>>>(a, slices, parts, keys);
             return launched();
         });
     });
