@@ -247,8 +247,7 @@ int ckks_plain_token_logprobs(int type, const void *logits, int64_t logits_strid
  * NULL: zero), given the entropy, largest and log_mass of the call above:
  *   dz = (dlogprob (1 at the token - p) - dentropy p (log p + entropy)) / temperature
  * for possible tokens, 0 for others; a token that is not possible or outside
- * [0, vocab) takes no part.  dlogits [rows][vocab] has the type of the logits
- * and may be the logits themselves (the same pointer and stride). */
+ * [0, vocab) takes no part.  dlogits [rows][vocab] has the type of the logits. */
 int ckks_plain_token_logprobs_grad(int type, const void *logits, int64_t logits_stride, const int64_t *tokens,
                                    const float *temperature, const uint8_t *allowed, int64_t allowed_stride,
                                    int64_t rows, int64_t vocab, const float *entropy, const float *largest,

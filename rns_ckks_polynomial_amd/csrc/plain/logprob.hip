@@ -46,16 +46,23 @@ __device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const
 template <typename T, bool MASK> struct Logits {
     Eight<T> e;
     Eight<int8_t> ok;
+    __device__ __forceinline__ void fetch(const T *z, const uint8_t *allowed, int c) {  // whole
+        e.fetch_once(z + c);
+        if constexpr (MASK) ok.fetch_once((const int8_t *)allowed + c);
+    }
     __device__ __forceinline__ void fetch(const T *z, const uint8_t *allowed, int c, int end) {
         e.fetch(z + c, end - c);
         if constexpr (MASK) ok.fetch((const int8_t *)allowed + c, end - c);
     }
-    __device__ __forceinline__ void widen(int c, int end, float (&f)[8]) const {
+    __device__ __forceinline__ void widen(float (&f)[8]) const {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             f[i] = e.at(i);
             if (MASK && !ok.v[0][i]) f[i] = -INFINITY;
         }
+    }
+    __device__ __forceinline__ void widen(int c, int end, float (&f)[8]) const {
+        widen(f);
         if (c + 8 > end) {
 #pragma unroll
             for (int i = 0; i < 8; i++)
@@ -67,30 +74,33 @@ template <typename T, bool MASK> struct Logits {
 constexpr int SCORE_NT = 512, GROUPS = 64, GROUP_LANES = SCORE_NT / GROUPS, CANDIDATES = 1024;
 constexpr float LEAST = -200.0f;  // exp2 of it is 0
 
-// A sum of 2^x and of x 2^x over logits, x = (z - m) scale, in terms of the largest so far.
+// Sums of 2^x and of x 2^x over logits z, x = z scale - at, where `at` is near the largest z scale so far.
 struct Mass {
-    float m, mass, moment;  // m: the lowest number where there is none yet
-    // in terms of a larger one
-    __device__ __forceinline__ void move(float to, float scale) {
-        const float d = fmaxf((m - to) * scale, LEAST), k = __builtin_amdgcn_exp2f(d);
+    float at, mass, moment;
+    __device__ __forceinline__ void shift(float d) {  // every x by d
+        const float k = __builtin_amdgcn_exp2f(d);
         moment = k * (moment + d * mass);
         mass *= k;
-        m = to;
     }
-    // v: their largest; to: the larger of it and m
+    __device__ __forceinline__ void move(float to) {
+        shift(fmaxf(at - to, LEAST));
+        at = to;
+    }
     __device__ __forceinline__ void add(const float (&f)[8], float scale) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const float x = fmaxf((f[i] - m) * scale, LEAST);  // LEAST for -infinity and NaN
+            const float x = fmaxf(__builtin_fmaf(f[i], scale, -at), LEAST);  // LEAST for -infinity and NaN
             const float e = __builtin_amdgcn_exp2f(x);
             mass += e;
-            moment += e * x;
+            moment = __builtin_fmaf(e, x, moment);
         }
     }
 };
-// (NaN is no larger than anything)
+// NaN where there is one (the instruction that lets them through takes numbers as they are loaded)
+__device__ __forceinline__ float max_or_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float largest_of(const float (&f)[8]) {
-    return fmaxf(fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));
+    return max_or_nan(max_or_nan(max_or_nan(f[0], f[1]), max_or_nan(f[2], f[3])),
+                      max_or_nan(max_or_nan(f[4], f[5]), max_or_nan(f[6], f[7])));
 }
 // The order of tokens as a number: by logit, then the lower index.  0 is below all.
 __device__ __forceinline__ uint64_t token_key(float z, int index) { return (uint64_t)order_bits(z) << 32 | (uint32_t)~index; }
@@ -109,7 +119,7 @@ __device__ __forceinline__ void put_top(const ScoreArgs &a, int64_t row, int ran
 
 struct ScoreShared {
     uint64_t groups[GROUPS], list[CANDIDATES], bound;
-    uint32_t slots[SCORE_NT / 64], winners[SCORE_NT], n_winners, n;
+    uint32_t slots[SCORE_NT / 64], more[SCORE_NT / 64], winners[SCORE_NT], n_winners, n_readers, n;
     float sums[2][SCORE_NT / 64];
 };
 // What a slice of a row leaves for the whole: these and its `top` largest keys, in order.
@@ -124,13 +134,20 @@ __device__ __forceinline__ int rank_in_list(const uint64_t *list, int n, uint64_
     return r;
 }
 
-// A workgroup reads a slice of a row once.  Each thread keeps the sums and the largest of what it reads in
-// terms of its own largest.  The alternatives:  a thread's key is its largest logit and the end of the vector
-// where that first came, so at least one token is not below it.  The top-th largest of the keys of 64 groups
-// of threads is a bound which at least `top` tokens pass; they are all among the tokens of threads whose largest
-// logit passes it from its vector's start (`winners`, little more than `top`), which are read again.  What passes goes on a list, and a
-// token's rank there is its place.  Where the list is too short (runs of equal logits, rows in bad order), the
+// A workgroup reads a slice of a row once; each thread keeps the sums of what it reads.  Their `at` is the
+// rounded product of its largest logit and the scale: one multiply-add gives an x, whose shift by that
+// rounding is taken out at the end.  Where the products have no room (beyond 2^20, that rounding is no small
+// number: infinite logits, tiny temperatures, rows of the type's lowest value) or a logit is NaN, the slice is
+// read twice more, with distances to its largest logit.
+//
+// The alternatives:  a thread's key is its largest logit and the end of the vector where that first came, so
+// at least one token is not below it.  The top-th largest of the keys of 64 groups of threads is a bound which
+// at least `top` tokens pass; they are all among the tokens of threads whose largest logit passes it from its
+// vector's start (`winners`, little more than `top`).  Such a thread's vector is read again, and its others where
+// the largest of them may pass too (all of them would be lines of memory: 2048 x 131072 bf16 top 20 117 us).  What
+// passes goes on a list, and a token's rank there is its place.  Where the list is too short (runs of equal logits, rows in bad order), the
 // top-th largest on it is a better bound: all that were on it below that one do not come back, so it ends.
+constexpr float ROOM = 0x1p20f;
 template <typename T, bool MASK, bool TOP>
 __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {
     __shared__ ScoreShared sh;
@@ -140,43 +157,78 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
     const int begin = blockIdx.y * slice, end = begin + slice < a.vocab ? begin + slice : a.vocab;
-    Mass s{-3.402823466e38f, 0, 0};
-    float best = -INFINITY;
+    Mass s{-ROOM, 0, 0};
+    float best = -INFINITY;  // the largest; best_at: the first vector that has it
     int best_at = 0;
-    if (t == 0) sh.bound = 1, sh.n_winners = sh.n = 0;
-    for (int c = begin + t * 8; c < end; c += SCORE_NT * 16) {
-        const int d = c + SCORE_NT * 8;
-        Logits<T, MASK> p, q;
-        float f[8], g[8];
-        p.fetch(z, allowed, c, end);
-        if (d < end) q.fetch(z, allowed, d, end);
-        p.widen(c, end, f);
-        if (d < end) {
-            q.widen(d, end, g);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) g[i] = -INFINITY;
-        }
+    float next = -INFINITY;  // the largest of the other vectors
+    if (t == 0) sh.bound = 1, sh.n_winners = sh.n_readers = sh.n = 0;
+    // two vectors at a time, the next two on their way
+    auto take = [&](const float (&f)[8], int c, const float (&g)[8], int d) {
         const float v = largest_of(f), w = largest_of(g);
         if (TOP) {
-            if (v > best) best = v, best_at = c;
-            if (w > best) best = w, best_at = d;
+            if (v > best) best_at = c;
+            next = __builtin_amdgcn_fmed3f(v, best, next);
+            best = max_or_nan(best, v);
+            if (w > best) best_at = d;
+            next = __builtin_amdgcn_fmed3f(w, best, next);
+            best = max_or_nan(best, w);
+        } else {
+            best = max_or_nan(best, max_or_nan(v, w));
         }
-        s.move(fmaxf(fmaxf(s.m, v), w), scale);
+        s.move(fmaxf(best * scale, -ROOM));
         s.add(f, scale);
         s.add(g, scale);
+    };
+    constexpr int STEP = SCORE_NT * 8;
+    const int whole = (end - begin) / (2 * STEP);
+    int c = begin + t * 8;
+    Logits<T, MASK> p, q;
+    if (whole) p.fetch(z, allowed, c), q.fetch(z, allowed, c + STEP);
+    for (int i = 0; i < whole; i++, c += 2 * STEP) {
+        float f[8], g[8];
+        p.widen(f);
+        q.widen(g);
+        if (i + 1 < whole) p.fetch(z, allowed, c + 2 * STEP), q.fetch(z, allowed, c + 3 * STEP);
+        take(f, c, g, c + STEP);
     }
-    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(s.m), sh.slots, Larger{}));
-    s.move(m, scale);
-    if (m == INFINITY) {  // their number counts, whatever the rest
+    if (c < end) {
+        float f[8], g[8];
+        p.fetch(z, allowed, c, end);
+        p.widen(c, end, f);
+        if (c + STEP < end) q.fetch(z, allowed, c + STEP, end);
+        q.widen(c + STEP, end, g);
+        take(f, c, g, c + STEP);
+    }
+    const uint32_t top_bits = row_all<SCORE_NT>(best != best ? ~0u : order_bits(best), sh.slots, Larger{});
+    float m = of_order_bits(top_bits);  // -infinity where nothing is possible
+    if (top_bits != ~0u && fabsf(m * scale) < ROOM) {
+        const float at = m * scale;
+        s.move(at);
+        s.shift(-__builtin_fmaf(m, scale, -at));
+    } else if (m != -INFINITY) {
+        best = next = -INFINITY;
+        for (int c = begin + t * 8; c < end; c += STEP) {
+            float f[8], v = -INFINITY;
+            p.fetch(z, allowed, c, end);
+            p.widen(c, end, f);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v = fmaxf(v, f[i]);  // not NaN
+            next = fmaxf(next, fminf(v, best));
+            if (v > best) best = v, best_at = c;
+        }
+        m = of_order_bits(row_all<SCORE_NT>(order_bits(best), sh.more, Larger{}));
         s.mass = s.moment = 0;
-        for (int c = begin + t * 8; c < end; c += SCORE_NT * 8) {
-            Logits<T, MASK> p;
+        for (int c = begin + t * 8; c < end; c += STEP) {
             float f[8];
             p.fetch(z, allowed, c, end);
             p.widen(c, end, f);
 #pragma unroll
-            for (int i = 0; i < 8; i++) s.mass += f[i] == INFINITY;
+            for (int i = 0; i < 8; i++) {
+                const float x = fmaxf(distance(f[i], m) * scale, LEAST);
+                const float e = f[i] > -INFINITY ? __builtin_amdgcn_exp2f(x) : 0.0f;
+                s.mass += e;
+                s.moment += e * x;
+            }
         }
     }
     row_sums<SCORE_NT>(s.mass, s.moment, sh.sums[0], sh.sums[1]);
@@ -184,7 +236,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
     if (t == 0) {
         if (parts) {
-            parts[row * gridDim.y + blockIdx.y] = Part{m, s.mass, s.moment, 0};
+            parts[row * gridDim.y + blockIdx.y] = Part{largest, s.mass, s.moment, 0};
         } else {
             put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
         }
@@ -194,7 +246,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
     uint64_t group = mine;
     group = Larger{}(group, moved<0xb1, 0xf>((uint64_t)0, group));
     group = Larger{}(group, moved<0x4e, 0xf>((uint64_t)0, group));
-    group = Larger{}(group, moved<0x141, 0xf>((uint64_t)0, group));
+    if (GROUP_LANES > 4) group = Larger{}(group, moved<0x141, 0xf>((uint64_t)0, group));
     if (t % GROUP_LANES == 0) sh.groups[t / GROUP_LANES] = group;
     __syncthreads();
     if (t < 64) {
@@ -208,12 +260,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
     for (;;) {
         __syncthreads();
         const uint64_t bound = sh.bound;
-        if (mine && mine + 7 >= bound) sh.winners[atomicAdd(&sh.n_winners, 1u)] = t;
-        __syncthreads();
-        const int jobs = (int)sh.n_winners * steps;
-        for (int j = t; j < jobs; j += SCORE_NT) {
-            const int c = begin + (j % steps * SCORE_NT + (int)sh.winners[j / steps]) * 8;
-            if (c >= end) continue;
+        auto list_vector = [&](int c) {
             Logits<T, MASK> p;
             float f[8];
             p.fetch(z, allowed, c, end);
@@ -226,6 +273,19 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
                     if (at < CANDIDATES) sh.list[at] = key;
                 }
             }
+        };
+        if (mine && mine + 7 >= bound) {
+            // its other vectors, if one may hold a token that passes; the front of `winners` is those to read in
+            // full, the back those of one vector
+            if (token_key(next, 0) >= bound) sh.winners[atomicAdd(&sh.n_readers, 1u)] = t;
+            else sh.winners[SCORE_NT - 1 - atomicAdd(&sh.n_winners, 1u)] = best_at;
+        }
+        __syncthreads();
+        const int jobs = (int)sh.n_readers * steps, ones = (int)sh.n_winners;
+        for (int j = t; j < jobs + ones; j += SCORE_NT) {
+            const int c = j < jobs ? begin + (j % steps * SCORE_NT + (int)sh.winners[j / steps]) * 8
+                                   : (int)sh.winners[SCORE_NT - 1 - (j - jobs)];
+            if (c < end) list_vector(c);
         }
         __syncthreads();
         n = (int)sh.n;
@@ -233,7 +293,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
         for (int i = t; i < CANDIDATES; i += SCORE_NT)
             if (rank_in_list(sh.list, CANDIDATES, sh.list[i]) == a.top - 1) sh.bound = sh.list[i];
         __syncthreads();
-        if (t == 0) sh.n_winners = sh.n = 0;
+        if (t == 0) sh.n_winners = sh.n_readers = sh.n = 0;
     }
     for (int i = t; i < n; i += SCORE_NT) {
         const int rank = rank_in_list(sh.list, n, sh.list[i]);
@@ -254,14 +314,12 @@ __global__ __launch_bounds__(SCORE_NT) void k_join_logprobs(ScoreArgs a, int sli
     const T *z = (const T *)a.logits + row * a.stride;
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
-    Mass s{-3.402823466e38f, 0, 0};
-    if (t < slices) {
-        const Part p = parts[row * slices + t];
-        s = Mass{p.m, p.mass, p.moment};
-    }
+    Part p{-INFINITY, 0, 0, 0};
+    if (t < slices) p = parts[row * slices + t];
     for (int i = t; i < slices * a.top; i += SCORE_NT) list[i] = keys[row * slices * a.top + i];
-    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(s.m), slots, Larger{}));
-    if (s.m != m) s.move(m, scale);  // two infinities have no distance
+    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(p.m), slots, Larger{}));
+    Mass s{0, p.mass, p.moment};
+    if (p.m != m) s.shift(fmaxf((p.m - m) * scale, LEAST));  // two infinities have no distance
     row_sums<SCORE_NT>(s.mass, s.moment, sums[0], sums[1]);
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
@@ -295,11 +353,17 @@ struct ScoreGradArgs {
     int64_t stride, allowed_stride, out_stride;
     int vocab;
 };
-// 2048 logits of a row for a workgroup.
+// A piece of a row for a workgroup, GRAD_EACH vectors a thread.  With lp = ln 2 x, x = z A - B,
+//   dz = p (c0 + c1 x) + [token] dlogprob / temperature,  p = 2^x,
+// of which a row's constants are worked out first (B in 64 bits; what its rounding to 32 leaves is in c0 and c1).
+// Where they have no room, x comes from distances as above.
+constexpr int GRAD_EACH = 4, GRAD_PIECE = 256 * 8 * GRAD_EACH;
 template <typename T, bool MASK>
-__global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, int64_t first) {
-    const int64_t row = first + blockIdx.x;
+__global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, int64_t last, uint32_t pieces) {
+    // from the last row on: the loss has just read those, and the last-level cache may hold them
+    const int64_t row = last - blockIdx.x / pieces;
     const T *z = (const T *)a.logits + row * a.stride;
+    T *out = (T *)a.dlogits + row * a.out_stride;
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
     const float inv_t = inverse_temperature(a.temperature, row), m = a.largest[row], log_mass = a.log_mass[row];
     const float h = a.entropy[row], dh = a.dentropy ? a.dentropy[row] : 0.0f;
@@ -307,20 +371,46 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
     float dl = 0;
     if (a.dlogprob && token >= 0 && token < a.vocab && to_f32(z[token]) > -INFINITY && (!MASK || allowed[token]))
         dl = a.dlogprob[row];
-    const int c = ((int)blockIdx.y * 256 + threadIdx.x) * 8;
-    if (c >= a.vocab) return;
-    float f[8];
-    Logits<T, MASK> p;
-    p.fetch(z, allowed, c, a.vocab);
-    p.widen(c, a.vocab, f);
+    const int begin = (int)(blockIdx.x % pieces) * GRAD_PIECE + threadIdx.x * 8;
+    const float scale = inv_t * LOG2E;
+    const double exact = (double)m * scale + (double)log_mass * 1.4426950408889634074;
+    const float b = (float)exact;
+    const float off = (float)(exact - b), k = -__builtin_amdgcn_exp2f(-off) * inv_t;
+    Logits<T, MASK> v[GRAD_EACH];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float lp = fmaxf(distance(f[i], m) * inv_t - log_mass, -200.0f);
-        const float e = __builtin_amdgcn_exp2f(lp * LOG2E);  // 0 at the bound
-        const float g = (c + i == token ? dl : 0.0f) - e * (dl + dh * (lp + h));
-        f[i] = f[i] > -INFINITY ? g * inv_t : 0.0f;
+    for (int j = 0; j < GRAD_EACH; j++) {
+        const int c = begin + j * 2048;
+        if (c < a.vocab) v[j].fetch(z, allowed, c, a.vocab);
     }
-    Eight<T>::store((T *)a.dlogits + row * a.out_stride + c, a.vocab - c, f);
+    const float c0 = k * (dl + dh * (h - LN2 * off)), c1 = k * dh * LN2;
+    const bool room = fabsf(b) < ROOM && fabsf(c0) < INFINITY && fabsf(c1) < INFINITY;
+#pragma unroll
+    for (int j = 0; j < GRAD_EACH; j++) {
+        const int c = begin + j * 2048;
+        if (c >= a.vocab) break;
+        float f[8];
+        v[j].widen(c, a.vocab, f);
+        if (room) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float x = fmaxf(__builtin_fmaf(f[i], scale, -b), LEAST);
+                f[i] = __builtin_amdgcn_exp2f(x) * __builtin_fmaf(c1, x, c0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const float lp = fmaxf(distance(f[i], m) * inv_t - log_mass, LEAST);
+                const float e = __builtin_amdgcn_exp2f(lp * LOG2E);  // 0 at the bound
+                f[i] = f[i] > -INFINITY ? -e * (dl + dh * (lp + h)) * inv_t : 0.0f;
+            }
+        }
+        if ((uint64_t)(token - c) < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (c + i == token) f[i] += dl * inv_t;
+        }
+        Eight<T>::store(out + c, a.vocab - c, f);
+    }
 }
 
 // ------------------------------------------------------------------ launches
@@ -440,18 +530,17 @@ extern "C" int ckks_plain_token_logprobs_grad(int type, const void *logits, int6
     const Range in[9] = {{logits, (int64_t)span(rows, logits_stride, vocab, z)}, {tokens, rows * 8}, {temperature, r4},
                          {allowed, (int64_t)span(rows, allowed_stride, vocab, 1)}, {entropy, r4}, {largest, r4},
                          {log_mass, r4}, {dlogprob, r4}, {dentropy, r4}};
-    const bool in_place = dlogits == logits && dlogits_stride == logits_stride;
-    for (int i = in_place; i < 9; i++)
-        if (overlap(dlogits, ob, in[i].p, in[i].n)) return CKKS_EINVAL;
+    for (const Range &r : in)
+        if (overlap(dlogits, ob, r.p, r.n)) return CKKS_EINVAL;
     for (const float *p : {entropy, largest, log_mass, dlogprob, dentropy})
         if (!at(p, 4)) return CKKS_EALIGN;
     const ScoreGradArgs a{logits, tokens, temperature, entropy, largest, log_mass, dlogprob, dentropy, allowed,
                           dlogits, logits_stride, allowed_stride, dlogits_stride, (int)vocab};
     return by_mask(type, allowed != nullptr, [&](auto ty, auto mask) {
-        const uint32_t pieces = (uint32_t)((vocab + 2047) / 2048);
+        const uint32_t pieces = (uint32_t)((vocab + GRAD_PIECE - 1) / GRAD_PIECE);
         return in_parts(rows, 256 * (int)pieces, [&](int64_t first, int64_t n) {
             k_token_logprobs_grad<decltype(ty), decltype(mask)::value>
-                <<<dim3((uint32_t)n, pieces), 256, 0, (hipStream_t)stream>>>(a, first);
+                <<<dim3((uint32_t)(n * pieces)), 256, 0, (hipStream_t)stream>>>(a, rows - 1 - first, pieces);
             return launched();
         });
     });

@@ -91,6 +91,11 @@ template <typename T> struct Eight {
             for (int i = 0; i < 8; i++) v[i / V][i % V] = i < left ? p[i] : (T)0;
         }
     }
+    // all eight, of what is read this once: the caches keep other things for it
+    __device__ __forceinline__ void fetch_once(const T *p) {
+#pragma unroll
+        for (int i = 0; i < 8 / V; i++) v[i] = __builtin_nontemporal_load((const Vec *)(p + i * V));
+    }
     __device__ __forceinline__ float at(int i) const {
         if constexpr (sizeof(T) == 1) return (float)(int)v[i / V][i % V];
         else return to_f32(v[i / V][i % V]);

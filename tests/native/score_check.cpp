@@ -16,6 +16,7 @@ static uint32_t update_dpp(uint32_t none, uint32_t v, int ctrl, int rows) {
 #undef __builtin_amdgcn_update_dpp
 #define __builtin_amdgcn_update_dpp(none, v, ctrl, rows, banks, bound) \
     ((int)update_dpp((uint32_t)(none), (uint32_t)(v), ctrl, rows))
+#define __builtin_amdgcn_fmed3f(a, b, c) std::max(std::min(a, b), std::min(std::max(a, b), c))
 #include "device.inc"
 
 using namespace ckks_plain;

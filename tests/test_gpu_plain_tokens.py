@@ -518,7 +518,7 @@ def test_token_logprobs_of_the_largest_vocabulary():
     near(r.log_mass, [np.log(mass)], (V / 256 + 64) * EPS, "log_mass")
 
 
-def test_token_logprobs_grad_in_place_and_rows_of_a_wider_buffer():
+def test_token_logprobs_grad_into_rows_of_a_wider_buffer():
     z = wide(rnd(17, 5, 3000) * 2, torch.bfloat16, 11, 5)
     tok = on_gpu(ints(13, 5, 0, 3000), torch.int64)
     r = plain.token_logprobs(z, tok)
@@ -532,8 +532,7 @@ def test_token_logprobs_grad_in_place_and_rows_of_a_wider_buffer():
     assert call(buf[:, 3:].data_ptr(), 3021) == 0
     torch.cuda.synchronize()
     assert torch.equal(buf[:, 3:3003], want) and buf[:, :3].eq(9).all() and buf[:, 3003:].eq(9).all()
-    assert call(z.data_ptr(), z.stride(0)) == 0
-    assert torch.equal(z, want)
+    assert call(z.data_ptr(), z.stride(0)) == nat.EINVAL  # the logits are read while gradients are written
 
 
 def test_token_logprobs_agree_with_sample():

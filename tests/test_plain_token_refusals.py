@@ -182,7 +182,7 @@ SG = dict(type=0, logits=X, logits_stride=V, tokens=Y, temperature=None, allowed
     (dict(largest=None), INV), (dict(log_mass=None), INV), (dict(dlogits=None), INV), (dict(dlogits_stride=V - 1), INV),
     (dict(vocab=0), INV), (dict(vocab=(1 << 24) + 1), UNSUP), (dict(rows=-1), INV), (dict(dlogits=U + 1), ALIGN),
     (dict(entropy=H + 2), ALIGN), (dict(dlogprob=G + 1), ALIGN), (dict(dentropy=G + 2), ALIGN), (dict(dlogits=Y), INV),
-    (dict(dlogits=X + 2), INV), (dict(dlogits=X, dlogits_stride=V + 1), INV), (dict(dlogits=H), INV), (dict(dlogits=G), INV),
+    (dict(dlogits=X + 2), INV), (dict(dlogits=X), INV), (dict(dlogits=X, dlogits_stride=V + 1), INV), (dict(dlogits=H), INV), (dict(dlogits=G), INV),
     (dict(allowed=Q, allowed_stride=V, dlogits=Q), INV), (dict(allowed=Q), INV), (dict(temperature=S, dlogits=S), INV),
 ])
 def test_score_grad_arguments(kw, code):
