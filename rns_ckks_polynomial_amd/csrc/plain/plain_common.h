@@ -100,14 +100,16 @@ template <typename T> struct Eight {
         if constexpr (sizeof(T) == 1) return (float)(int)v[i / V][i % V];
         else return to_f32(v[i / V][i % V]);
     }
-    static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[8]) {
+    // ONCE: nothing reads it soon
+    template <bool ONCE = false> static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[8]) {
         if (left >= 8) {
 #pragma unroll
             for (int i = 0; i < 8; i += V) {
                 Vec w;
 #pragma unroll
                 for (int j = 0; j < V; j++) w[j] = from_f32<T>(f[i + j]);
-                *(Vec *)(p + i) = w;
+                if (ONCE) __builtin_nontemporal_store(w, (Vec *)(p + i));
+                else *(Vec *)(p + i) = w;
             }
         } else {
 #pragma unroll

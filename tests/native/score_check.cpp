@@ -52,7 +52,8 @@ static void check(const char *what, int vocab, int top, int slices, bool masked,
         Part *p = slices > 1 ? parts.get() : nullptr;
         uint64_t *k = slices > 1 ? keys.get() : nullptr;
         done = host::run(SCORE_NT, 20000000, [&] {
-            masked ? k_token_logprobs<float, true, true>(a, slice, p, k) : k_token_logprobs<float, false, true>(a, slice, p, k);
+            masked ? k_token_logprobs<float, true, true, false>(a, slice, p, k)
+                   : k_token_logprobs<float, false, true, false>(a, slice, p, k);
         });
     }
     blockIdx = {0, 0, 0};
