@@ -331,9 +331,19 @@ __global__ __launch_bounds__(SCORE_NT) void k_join_logprobs(ScoreArgs a, int sli
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
     if (t == 0) put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
+    if (!a.top) return;
+    // Bounds that `top` keys pass: a slice's last, and the least of the slices' keys at a place that makes `top`
+    // of them together.
+    __shared__ uint64_t ends[2][SCORE_NT / 64];
+    uint64_t last = 0, least = 0;
+    if (t < slices) last = list[t * a.top + a.top - 1], least = ~list[t * a.top + (a.top - 1) / slices];
+    last = row_all<SCORE_NT>(last, ends[0], Larger{});
+    least = ~row_all<SCORE_NT>(least, ends[1], Larger{});
+    const uint64_t bound = last > least ? last : least;
     // Each slice's keys fall: a key's place among all is where it would stand in each of them.
     for (int i = t; i < slices * a.top; i += SCORE_NT) {
         const uint64_t key = list[i];
+        if (key < bound) continue;
         int rank = i % a.top;
         for (int k = 0; k < slices && rank < a.top; k++) {
             if (k == i / a.top) continue;
@@ -437,10 +447,11 @@ int check_score(int64_t rows, int64_t vocab) {
 // Logits that the last-level cache (256 MB) does not hold beside their gradient go past the caches: 4096 x 32768
 // bf16 with its gradient 130 us, so, else 141 to 149; 512 x 32768 f32 43 us, else 41.
 bool past_caches(int64_t rows, int64_t vocab, size_t size) { return rows * vocab * (int64_t)size > (int64_t)128 << 20; }
-// Slices of a row: enough workgroups for the GPU where there are few rows, none of less than a read of all
-// its threads.
+// Slices of a row: a workgroup for each compute unit where there are few rows, none of less than 32768 logits
+// (16 x 131072 bf16 top 20: 13.7 us with four slices, 15.0 with one, 19.3 with 16; 4 x 32768 f32 top 5: 8.1 us, with
+// four 10.9; 200 x 131072: 15.5 us, with two 19.9).
 int64_t score_slices(int64_t rows, int64_t vocab) {
-    const int64_t most = vocab / (SCORE_NT * 16), want = rows ? 512 / rows : 1;
+    const int64_t most = vocab / 32768, want = rows ? 256 / rows : 1;
     const int64_t n = want < most ? want : most;
     return n < 1 ? 1 : n < MAX_SLICES ? n : MAX_SLICES;
 }

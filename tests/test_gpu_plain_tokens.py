@@ -535,6 +535,29 @@ def test_token_logprobs_grad_into_rows_of_a_wider_buffer():
     assert call(z.data_ptr(), z.stride(0)) == nat.EINVAL  # the logits are read while gradients are written
 
 
+@pytest.mark.parametrize("B,V", [(1, 262144), (3, 70001), (5, 1 << 20), (100, 65536)])
+@pytest.mark.parametrize("top", [0, 5, 64])
+def test_token_logprobs_of_few_long_rows(B, V, top):
+    """Rows in slices: equal logits across them, slices without a possible token, infinities in two of them."""
+    z = (rnd(27, B, V) * 2).to(torch.bfloat16).cuda()
+    z[0, V // 3:] = float("-inf")
+    allowed = None
+    if B > 1:
+        z[1] = torch.arange(V, device="cuda").remainder(7).to(torch.bfloat16)
+        z[2, :100] = -3.0
+        z[2, 100:] = float("nan")
+        allowed = torch.ones(B, V, dtype=torch.bool, device="cuda")
+        allowed[0] = False
+    check_score(z, ints(28, B, 0, V), top, None, allowed, grad=B < 100)
+    z[0, 5] = z[0, V - 1] = float("inf")
+    check_score(z, ints(28, B, 0, V), top, grad=False)
+
+
+def test_token_logprobs_past_the_caches():
+    """More than 128 MiB of logits."""
+    check_score((rnd(29, 264, 131072) * 2).float().cuda(), ints(29, 264, 0, 131072), 3)
+
+
 def test_token_logprobs_agree_with_sample():
     """The drawn tokens' log probabilities are those that sample reports, for every temperature and mask."""
     B, V = 40, 5000
