@@ -3,12 +3,17 @@
 
 namespace ckks_plain {
 
-// out[t] = scale table[tokens[t]], 2^log_l threads of 8 elements a row, the rest of 256 threads on other
-// rows.
+// Elements of a vector of types T and O: 16 bytes of the wider, so that neighbouring lanes' accesses join to
+// whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction: the table's
+// gradient in f32 97 us, so ...).
+template <typename T, typename O> constexpr int JOINT = 16 / (int)(sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
+
+// out[t] = scale table[tokens[t]], 2^log_l threads a row, the rest of 256 threads on other rows.
 template <typename T, typename O>
 __global__ __launch_bounds__(256) void k_embed(const T *table, int64_t table_stride, const float *table_scale,
                                                int64_t vocab, int64_t cols, const int64_t *tokens, int64_t first,
                                                int64_t rows, float scale, O *out, int64_t out_stride, int log_l) {
+    constexpr int V = JOINT<T, O>;
     const int64_t row = first + ((int64_t)blockIdx.x << (8 - log_l)) + (threadIdx.x >> log_l);
     if (row >= rows) return;
     const int64_t v = tokens[row];
@@ -16,13 +21,20 @@ __global__ __launch_bounds__(256) void k_embed(const T *table, int64_t table_str
     if (table_scale && there) scale *= table_scale[v];
     const T *p = table + (there ? v : 0) * table_stride;
     O *o = out + row * out_stride;
-    for (int64_t c = (threadIdx.x & ((1 << log_l) - 1)) * 8; c < cols; c += (int64_t)8 << log_l) {
-        float f[8];
-        Eight<T> e;
-        e.fetch(p + c, there ? cols - c : 0);
+    const int64_t step = (int64_t)V << log_l;
+    for (int64_t c = (threadIdx.x & ((1 << log_l) - 1)) * V; c < cols; c += 2 * step) {
+        Piece<T, V> e[2];
+        if (there) {
+            e[0].fetch(p + c, cols - c);
+            if (c + step < cols) e[1].fetch(p + c + step, cols - c - step);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; i++) f[i] = there ? e.at(i) * scale : 0.0f;
-        Eight<O>::store(o + c, cols - c, f);
+        for (int k = 0; k < 2; k++) {
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; i++) f[i] = there ? e[k].at(i) * scale : 0.0f;
+            if (c + k * step < cols) Piece<O, V>::store(o + c + k * step, cols - c - k * step, f);
+        }
     }
 }
 
@@ -31,28 +43,51 @@ __global__ __launch_bounds__(256) void k_embed(const T *table, int64_t table_str
 constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 
 // order[0 ...): the rows with a token in [0, vocab), by token and, among equals, by row; starts[v]: how
-// many of them have a token below v (v <= vocab).  A workgroup has 2^log_bins tokens of the vocabulary
-// and reads all rows' tokens itself, so nothing is joined between workgroups: wave w counts those of its
-// part of the rows, and after a sum over waves and bins puts its rows where they belong, in order.
+// many of them have a token below v (v <= vocab).  Of each `chunk` places, firsts and lasts: the tokens at both
+// ends.
+//
+// A workgroup has 2^log_bins tokens of the vocabulary and reads all rows' tokens itself, so nothing is joined
+// between workgroups and one launch does: wave w counts those of its part of the rows, and after a sum over
+// waves and bins puts its rows where they belong, in order.  The tokens of up to HELD * 64 rows a wave stay in
+// registers in between.
+constexpr int HELD = 16;
+constexpr uint32_t NONE = ~0u;
+struct TokenOrder {
+    int32_t *order, *starts, *firsts, *lasts;
+    int64_t chunk;
+};
+__device__ __forceinline__ uint32_t token_at(const int64_t *tokens, int64_t i, int64_t last, int64_t vocab) {
+    const int64_t v = i < last ? tokens[i] : -1;
+    return v >= 0 && v < vocab ? (uint32_t)v : NONE;
+}
 __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens, int64_t rows, int64_t vocab,
-                                                          int log_bins, int32_t *order, int32_t *starts) {
+                                                          int log_bins, TokenOrder o) {
     extern __shared__ uint32_t places[];  // [wave][bin]: counts, then the next place
-    __shared__ uint32_t buf[ORDER_WAVES], sums[ORDER_WAVES];
-    const int bins = 1 << log_bins, wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int64_t low = (int64_t)blockIdx.x << log_bins;
-    const int64_t high = low + bins < vocab ? low + bins : vocab;
+    __shared__ uint32_t buf[ORDER_WAVES], sums[ORDER_WAVES], ends[ORDER_WAVES];
+    const uint32_t bins = 1u << log_bins, wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const uint32_t low = blockIdx.x << log_bins;
     const int64_t part = (rows + ORDER_NT - 1) / ORDER_NT * 64;
     const int64_t first = wave * part, last = first + part < rows ? first + part : rows;
+    const int64_t step = HELD * 64;
     uint32_t *mine = places + (wave << log_bins);
-    for (int i = threadIdx.x; i < ORDER_WAVES << log_bins; i += ORDER_NT) places[i] = 0;
+    for (uint32_t i = threadIdx.x; i < ORDER_WAVES << log_bins; i += ORDER_NT) places[i] = 0;
     __syncthreads();
-    uint32_t below = 0;
-    for (int64_t i = first + l; i < last; i += 64) {
-        const int64_t v = tokens[i];
-        below += v >= 0 && v < low;
-        if (v >= low && v < high) atomicAdd(&mine[v - low], 1u);
+    uint32_t below = 0, all = 0, v[HELD];
+    auto fetch = [&](int64_t from) {
+#pragma unroll
+        for (int k = 0; k < HELD; k++) v[k] = token_at(tokens, from + k * 64 + l, last, vocab);
+    };
+    for (int64_t i = first; i < last; i += step) {
+        fetch(i);
+#pragma unroll
+        for (int k = 0; k < HELD; k++) {
+            below += v[k] < low;
+            all += v[k] != NONE;
+            if (v[k] - low < bins) atomicAdd(&mine[v[k] - low], 1u);
+        }
     }
     below = row_all<ORDER_NT>(below, buf, Sum{});  // its barrier ends the counting
+    all = row_all<ORDER_NT>(all, ends, Sum{});
     uint32_t n = 0;
     if (threadIdx.x < bins)
         for (int w = 0; w < ORDER_WAVES; w++) n += places[(w << log_bins) + threadIdx.x];
@@ -60,10 +95,19 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
     if (l == 63) sums[wave] = upto;
     __syncthreads();
     uint32_t at = below + upto - n;
-    for (int w = 0; w < wave; w++) at += sums[w];
+    for (uint32_t w = 0; w < wave; w++) at += sums[w];
     if (threadIdx.x < bins) {
-        if (low + threadIdx.x < vocab) starts[low + threadIdx.x] = (int32_t)at;
-        if (low + threadIdx.x == vocab - 1) starts[vocab] = (int32_t)(at + n);
+        const int64_t token = (int64_t)low + threadIdx.x;
+        if (token < vocab) o.starts[token] = (int32_t)at;
+        if (token == vocab - 1) o.starts[vocab] = (int32_t)all;
+        if (n && o.firsts) {
+            // the ends of chunks that fall into its run
+            for (int64_t j = (at + o.chunk - 1) / o.chunk; j * o.chunk < at + n; j++) o.firsts[j] = (int32_t)token;
+            for (int64_t j = at / o.chunk; j <= (at + n - 1) / o.chunk; j++) {
+                const int64_t end = (j + 1) * o.chunk < all ? (j + 1) * o.chunk : all;
+                if (end <= at + n) o.lasts[j] = (int32_t)token;
+            }
+        }
         for (int w = 0; w < ORDER_WAVES; w++) {
             const uint32_t c = places[(w << log_bins) + threadIdx.x];
             places[(w << log_bins) + threadIdx.x] = at;
@@ -71,19 +115,24 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
         }
     }
     __syncthreads();
-    for (int64_t i = first + l; i - l < last; i += 64) {
-        const int64_t v = i < last ? tokens[i] : -1;
-        const bool in = v >= low && v < high;
-        const uint32_t bin = in ? (uint32_t)(v - low) : 0;
-        for (uint64_t left = __ballot(in); left;) {  // one token of the wave's at a time
-            const uint32_t b = lane(bin, __ffsll((unsigned long long)left) - 1);
-            const uint64_t same = __ballot(in && bin == b);
-            const uint32_t place = mine[b];
-            if (in && bin == b)
-                order[place + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
-                                                        __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] = (int32_t)i;
-            mine[b] = place + (uint32_t)__popcll(same);  // every lane the same
-            left &= ~same;
+    for (int64_t i = first; i < last; i += step) {
+        if (part > step) fetch(i);
+#pragma unroll
+        for (int k = 0; k < HELD; k++) {
+            const uint32_t bin = v[k] - low;
+            const bool in = bin < bins;  // NONE: low + bins is at most 2^24 + 2^9
+            for (uint64_t left = __ballot(in); left;) {  // one token of the wave's at a time
+                const int leader = __ffsll((unsigned long long)left) - 1;
+                const uint32_t b = lane(bin, leader), place = mine[b];
+                const uint64_t same = __ballot(in && bin == b);
+                if (in && bin == b)
+                    o.order[place + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
+                                                              __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] =
+                        (int32_t)(i + k * 64 + l);
+                if (l == (uint32_t)leader) mine[b] = place + (uint32_t)__popcll(same);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's other lanes read it next
+                left &= ~same;
+            }
         }
     }
 }
@@ -94,87 +143,131 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
 // it holds the first or the last), and k_embed_join adds up the parts.
 struct EmbedSums {
     const int64_t *tokens;
-    const int32_t *order, *starts;
+    const int32_t *order, *starts, *firsts, *lasts;
     int64_t rows, vocab, cols, chunk, chunks;
     float scale;
     float *parts;
 };
 
-// The sum of rows order[from, to) at columns c ... c + 7.
-template <typename T>
-__device__ __forceinline__ void run_sum(const EmbedSums &s, const T *drows, int64_t stride, int64_t from, int64_t to,
-                                        int64_t c, float (&f)[8]) {
+// A thread's share of a row, eight elements: vectors of V, `apart` elements from one to the next.
+template <typename T, int V> struct Share {
+    static constexpr int N = 8 / V;
+    Piece<T, V> e[N];
+    __device__ __forceinline__ void fetch(const T *row, int64_t c, int64_t apart, int64_t cols) {
 #pragma unroll
-    for (int j = 0; j < 8; j++) f[j] = 0;
+        for (int n = 0; n < N; n++)
+            if (c + n * apart < cols) e[n].fetch(row + c + n * apart, cols - c - n * apart);
+    }
+    __device__ __forceinline__ void add_to(float (&f)[N][V]) const {
+#pragma unroll
+        for (int n = 0; n < N; n++)
+#pragma unroll
+            for (int j = 0; j < V; j++) f[n][j] += e[n].at(j);
+    }
+    // scale f [+ what is there]
+    template <bool ADD> static __device__ __forceinline__ void put(T *row, int64_t c, int64_t apart, int64_t cols,
+                                                                    float scale, float (&f)[N][V]) {
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            if (c + n * apart >= cols) continue;
+            T *p = row + c + n * apart;
+            Piece<T, V> old;
+            if (ADD) old.fetch(p, cols - c - n * apart);
+#pragma unroll
+            for (int j = 0; j < V; j++) f[n][j] = (ADD ? old.at(j) : 0.0f) + f[n][j] * scale;
+            Piece<T, V>::store(p, cols - c - n * apart, f[n]);
+        }
+    }
+};
+
+// Adds a share of the rows order[from, to).
+template <typename T, int V>
+__device__ __forceinline__ void add_run(const EmbedSums &s, const T *drows, int64_t stride, int64_t from, int64_t to,
+                                        int64_t c, int64_t apart, float (&f)[8 / V][V]) {
     int64_t i = from;
     for (; i + 4 <= to; i += 4) {  // four rows in flight
-        Eight<T> e[4];
+        Share<T, V> e[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++) e[k].fetch(drows + s.order[i + k] * stride + c, s.cols - c);
+        for (int k = 0; k < 4; k++) e[k].fetch(drows + s.order[i + k] * stride, c, apart, s.cols);
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-#pragma unroll
-            for (int j = 0; j < 8; j++) f[j] += e[k].at(j);
+        for (int k = 0; k < 4; k++) e[k].add_to(f);
     }
     for (; i < to; i++) {
-        Eight<T> e;
-        e.fetch(drows + s.order[i] * stride + c, s.cols - c);
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[j] += e.at(j);
+        Share<T, V> e;
+        e.fetch(drows + s.order[i] * stride, c, apart, s.cols);
+        e.add_to(f);
     }
 }
 
-template <typename O, bool ADD>
-__device__ __forceinline__ void put_sum(O *p, int64_t left, float scale, float (&f)[8]) {
-    if constexpr (ADD) {
-        Eight<O> old;
-        old.fetch(p, left);
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[j] = old.at(j) + f[j] * scale;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++) f[j] *= scale;
-    }
-    Eight<O>::store(p, left, f);
-}
-
-// Workgroups from `chunks` on: a row of the table for 2^log_l threads (with ADD: a place of the order,
-// the first of its token).  Those before: the parts of long runs in a chunk.
-template <typename T, typename O, bool ADD>
-__global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, int64_t stride, O *out,
-                                                   int64_t out_stride, int64_t first, int64_t chunks, int log_l) {
-    const int lanes = 1 << log_l;
-    if (blockIdx.x < chunks) {
-        const int64_t from = blockIdx.x * s.chunk, n = s.starts[s.vocab];
-        const int64_t to = from + s.chunk < n ? from + s.chunk : n;
-        if (from >= to) return;
-        const int64_t va = s.tokens[s.order[from]], vb = s.tokens[s.order[to - 1]];
-        for (int k = 0; k < (va == vb ? 1 : 2); k++) {
-            const int64_t v = k ? vb : va, a = s.starts[v], b = s.starts[v + 1];
-            if (b - a <= s.chunk) continue;
-            for (int64_t c = (int64_t)threadIdx.x * 8; c < s.cols; c += 256 * 8) {
-                float f[8];
-                run_sum(s, drows, stride, a > from ? a : from, b < to ? b : to, c, f);
-                Eight<float>::store(s.parts + (2 * (int64_t)blockIdx.x + k) * s.cols + c, s.cols - c, f);
-            }
+// The parts of long runs in chunk j, by a workgroup.
+template <typename T>
+__device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, int64_t stride, int64_t j) {
+    constexpr int V = JOINT<T, float>;
+    const int64_t from = j * s.chunk, n = s.starts[s.vocab], to = from + s.chunk < n ? from + s.chunk : n;
+    if (from >= to) return;
+    const int64_t va = s.firsts[j], vb = s.lasts[j];
+    for (int k = 0; k < (va == vb ? 1 : 2); k++) {
+        const int64_t v = k ? vb : va, a = s.starts[v], b = s.starts[v + 1];
+        if (b - a <= s.chunk) continue;
+        for (int64_t c = (int64_t)threadIdx.x * V; c < s.cols; c += 256 * 8) {
+            float f[8 / V][V] = {};
+            add_run<T, V>(s, drows, stride, a > from ? a : from, b < to ? b : to, c, 256 * V, f);
+            Share<float, V>::template put<false>(s.parts + (2 * j + k) * s.cols, c, 256 * V, s.cols, 1.0f, f);
         }
-        return;
     }
+}
+
+// The first `chunks` workgroups: parts of long runs.  The others: 2^log_l threads on TABLE_ROWS rows of the table,
+// with the first row of each run, and where those start, on their way together.
+constexpr int TABLE_ROWS = 4;
+template <typename T, typename O>
+__global__ __launch_bounds__(256) void k_embed_table(EmbedSums s, const T *drows, int64_t stride, O *out,
+                                                     int64_t out_stride, int64_t first, int64_t chunks, int log_l) {
+    if (blockIdx.x < chunks) return sum_parts(s, drows, stride, blockIdx.x);
+    constexpr int V = JOINT<T, O>;
+    const int64_t group = ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
+    const int64_t v = first + group * TABLE_ROWS, apart = (int64_t)V << log_l;
+    if (v >= s.vocab) return;
+    int32_t at[TABLE_ROWS + 1], row[TABLE_ROWS];
+#pragma unroll
+    for (int k = 0; k <= TABLE_ROWS; k++) at[k] = s.starts[v + k < s.vocab ? v + k : s.vocab];
+#pragma unroll
+    for (int k = 0; k < TABLE_ROWS; k++) {
+        const int32_t n = at[k + 1] - at[k];
+        row[k] = n && n <= s.chunk ? s.order[at[k]] : -1;
+    }
+    for (int64_t c = (int64_t)(threadIdx.x & ((1 << log_l) - 1)) * V; c < s.cols; c += (int64_t)8 << log_l) {
+        Share<T, V> e[TABLE_ROWS];
+#pragma unroll
+        for (int k = 0; k < TABLE_ROWS; k++)
+            if (row[k] >= 0) e[k].fetch(drows + row[k] * stride, c, apart, s.cols);
+#pragma unroll
+        for (int k = 0; k < TABLE_ROWS; k++) {
+            if (v + k >= s.vocab || at[k + 1] - at[k] > s.chunk) continue;
+            float f[8 / V][V] = {};
+            if (row[k] >= 0) {
+                e[k].add_to(f);
+                add_run<T, V>(s, drows, stride, at[k] + 1, at[k + 1], c, apart, f);
+            }
+            Share<O, V>::template put<false>(out + (v + k) * out_stride, c, apart, s.cols, s.scale, f);
+        }
+    }
+}
+
+// The same with the sums added to `out`: a place of the order for 2^log_l threads, the first of its token.
+template <typename T, typename O>
+__global__ __launch_bounds__(256) void k_embed_add(EmbedSums s, const T *drows, int64_t stride, O *out,
+                                                   int64_t out_stride, int64_t first, int64_t chunks, int log_l) {
+    if (blockIdx.x < chunks) return sum_parts(s, drows, stride, blockIdx.x);
+    constexpr int V = JOINT<T, O>;
     const int64_t i = first + ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
-    int64_t v = i;
-    if (ADD) {
-        if (i >= s.starts[s.vocab]) return;
-        v = s.tokens[s.order[i]];
-        if (i != s.starts[v]) return;
-    } else if (i >= s.vocab) {
-        return;
-    }
-    const int64_t a = s.starts[v], b = s.starts[v + 1];
-    if (b - a > s.chunk) return;
-    for (int64_t c = (int64_t)(threadIdx.x & (lanes - 1)) * 8; c < s.cols; c += (int64_t)8 << log_l) {
-        float f[8];
-        run_sum(s, drows, stride, a, b, c, f);
-        put_sum<O, ADD>(out + v * out_stride + c, s.cols - c, s.scale, f);
+    if (i >= s.starts[s.vocab]) return;
+    const int64_t v = s.tokens[s.order[i]], apart = (int64_t)V << log_l;
+    if (i != s.starts[v] || s.starts[v + 1] - i > s.chunk) return;
+    for (int64_t c = (int64_t)(threadIdx.x & ((1 << log_l) - 1)) * V; c < s.cols; c += (int64_t)8 << log_l) {
+        float f[8 / V][V] = {};
+        add_run<T, V>(s, drows, stride, i, s.starts[v + 1], c, apart, f);
+        Share<O, V>::template put<true>(out + v * out_stride, c, apart, s.cols, s.scale, f);
     }
 }
 
@@ -187,26 +280,25 @@ __global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_
     const int64_t j = blockIdx.x, n = s.starts[s.vocab], from = j * s.chunk;
     const int64_t to = from + s.chunk < n ? from + s.chunk : n;
     if (from >= to) return;
-    const int64_t v = s.tokens[s.order[to - 1]], a = s.starts[v], b = s.starts[v + 1];
+    const int64_t v = s.lasts[j], a = s.starts[v], b = s.starts[v + 1];
     if (b - a <= s.chunk || a < from) return;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.y * JOIN_COLS + l * 8, last = (b - 1) / s.chunk;
-    float f[8] = {};
-    if (c < s.cols)
-        for (int64_t k = j + wave; k <= last; k += 16) {
-            Eight<float> e;
-            e.fetch(s.parts + (2 * k + (k == j && a > from)) * s.cols + c, s.cols - c);
+    const int64_t c = (int64_t)blockIdx.y * JOIN_COLS + l * 4, last = (b - 1) / s.chunk;
+    float f[2][4] = {};
+    for (int64_t k = j + wave; k <= last; k += 16) {
+        Share<float, 4> e{};
+        e.fetch(s.parts + (2 * k + (k == j && a > from)) * s.cols, c, 256, s.cols);
+        e.add_to(f);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; i++) f[i] += e.at(i);
-        }
-#pragma unroll
-    for (int i = 0; i < 8; i++) sh[wave][l * 8 + i] = f[i];
+    for (int i = 0; i < 8; i++) sh[wave][i / 4 * 256 + l * 4 + i % 4] = f[i / 4][i % 4];
     __syncthreads();
-    if (wave || c >= s.cols) return;
-    for (int w = 1; w < 16; w++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) f[i] += sh[w][l * 8 + i];
-    put_sum<O, ADD>(out + v * out_stride + c, s.cols - c, s.scale, f);
+    const int64_t mine = (int64_t)blockIdx.y * JOIN_COLS + threadIdx.x;
+    if (threadIdx.x >= JOIN_COLS || mine >= s.cols) return;
+    float sum = 0;
+    for (int w = 0; w < 16; w++) sum += sh[w][threadIdx.x];
+    O *p = out + v * out_stride + mine;
+    *p = from_f32<O>((ADD ? to_f32(*p) : 0.0f) + sum * s.scale);
 }
 
 // ------------------------------------------------------------------ launches
@@ -271,7 +363,7 @@ int64_t chunk_rows(int64_t rows) {
 }
 struct EmbedPlan {
     int64_t chunk, chunks;
-    size_t order, starts, parts;  // bytes
+    size_t order, starts, ends, parts;  // bytes
 };
 EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     EmbedPlan p;
@@ -279,6 +371,7 @@ EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     p.chunks = rows > p.chunk ? (rows + p.chunk - 1) / p.chunk : 0;  // without a long run none are needed
     p.order = (size_t)round_up(rows * 4, 16);
     p.starts = (size_t)round_up((vocab + 1) * 4, 16);
+    p.ends = (size_t)round_up(p.chunks * 4, 16);
     p.parts = (size_t)p.chunks * 2 * cols * 4;
     return p;
 }
@@ -313,7 +406,7 @@ extern "C" int ckks_plain_embed_grad_workspace_size(int64_t rows, int64_t vocab,
     if (!bytes) return CKKS_EINVAL;
     if (int e = check_embed(vocab, cols, rows, CKKS_PLAIN_F32)) return e;
     const EmbedPlan p = embed_plan(rows, vocab, cols);
-    *bytes = p.order + p.starts + p.parts;
+    *bytes = p.order + p.starts + 2 * p.ends + p.parts;
     return CKKS_OK;
 }
 
@@ -342,10 +435,13 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
     const EmbedPlan p = embed_plan(rows, vocab, cols);
     const int b = log_bins(vocab), l = log_lanes(cols);
     char *w = (char *)ws;
-    EmbedSums a{tokens, (int32_t *)w, (int32_t *)(w + p.order), rows, vocab, cols, p.chunk, p.chunks, scale,
-                (float *)(w + p.order + p.starts)};
+    TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), nullptr, nullptr, p.chunk};
+    w += p.order + p.starts;
+    if (p.chunks) o.firsts = (int32_t *)w, o.lasts = (int32_t *)(w + p.ends);
+    const EmbedSums a{tokens, o.order, o.starts, o.firsts, o.lasts, rows, vocab, cols, p.chunk, p.chunks, scale,
+                      (float *)(w + 2 * p.ends)};
     k_token_order<<<dim3((uint32_t)((vocab + (1 << b) - 1) >> b)), ORDER_NT, (size_t)ORDER_WAVES * 4 << b, s>>>(
-        tokens, rows, vocab, b, (int32_t *)a.order, (int32_t *)a.starts);
+        tokens, rows, vocab, b, o);
     if (int e = launched()) return e;
     return typed(type, [&](auto ty) {
         return typed(out_type, [&](auto oy) {
@@ -354,10 +450,15 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
             auto go = [&](auto addition) {
                 constexpr bool ADD = decltype(addition)::value;
                 int64_t chunks = p.chunks;  // with the first part of the rows
-                int e = in_parts(ADD ? rows : vocab, 1 << l, [&](int64_t first, int64_t n) {
-                    const int64_t blocks = (n + (256 >> l) - 1) >> (8 - l);
-                    k_embed_sum<T, O, ADD><<<dim3((uint32_t)(blocks + chunks)), 256, 0, s>>>(
-                        a, (const T *)drows, drows_stride, (O *)out, out_stride, first, chunks, l);
+                const int64_t each = ADD ? 1 : TABLE_ROWS, n = ADD ? rows : (vocab + each - 1) / each;
+                int e = in_parts(n, 1 << l, [&](int64_t first, int64_t n) {
+                    const dim3 grid((uint32_t)(((n + (256 >> l) - 1) >> (8 - l)) + chunks));
+                    if constexpr (ADD)
+                        k_embed_add<T, O><<<grid, 256, 0, s>>>(a, (const T *)drows, drows_stride, (O *)out, out_stride,
+                                                               first, chunks, l);
+                    else
+                        k_embed_table<T, O><<<grid, 256, 0, s>>>(a, (const T *)drows, drows_stride, (O *)out,
+                                                                 out_stride, first * each, chunks, l);
                     chunks = 0;
                     return launched();
                 });

@@ -44,14 +44,14 @@ __device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const
 
 // Logits c ... c + 7 of a row; -infinity or NaN where there is no possible token.
 template <typename T, bool MASK> struct Logits {
-    Eight<T> e;
-    Eight<int8_t> ok;
+    Piece<T, 8> e;
+    Piece<int8_t, 8> ok;
     // STREAM: past the caches
     template <bool STREAM> __device__ __forceinline__ void fetch(const T *z, const uint8_t *allowed, int c) {  // whole
         if (STREAM) e.fetch_once(z + c);
-        else e.fetch(z + c, 8);
+        else e.fetch(z + c);
         if (MASK && STREAM) ok.fetch_once((const int8_t *)allowed + c);
-        else if (MASK) ok.fetch((const int8_t *)allowed + c, 8);
+        else if (MASK) ok.fetch((const int8_t *)allowed + c);
     }
     __device__ __forceinline__ void fetch(const T *z, const uint8_t *allowed, int c, int end) {
         e.fetch(z + c, end - c);
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
             for (int i = 0; i < 8; i++)
                 if (c + i == token) f[i] += dl * inv_t;
         }
-        Eight<T>::template store<STREAM>(out + c, a.vocab - c, f);
+        Piece<T, 8>::template store<STREAM>(out + c, a.vocab - c, f);
     }
 }
 

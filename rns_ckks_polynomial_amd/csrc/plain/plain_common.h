@@ -76,44 +76,47 @@ template <typename T, int NT, int E> struct Row {
     }
 };
 
-// Eight elements at p, `left` of them there (others read as 0 and are not written): pieces of rows that more
-// than one thread, workgroup or type share.
-template <typename T> struct Eight {
-    static constexpr int V = sizeof(T) == 1 ? 8 : VEC<T>;
-    typedef T Vec __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-    Vec v[8 / V];
-    __device__ __forceinline__ void fetch(const T *p, int64_t left) {
-        if (left >= 8) {
+// V elements at p, `left` of them there (others read as 0 and are not written): pieces of rows that more than one
+// thread, workgroup or type share.
+template <typename T, int V_> struct Piece {
+    static constexpr int V = V_, LOAD = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;  // elements of a load
+    typedef T Vec __attribute__((ext_vector_type(LOAD), aligned(sizeof(T))));
+    Vec v[V / LOAD];
+    __device__ __forceinline__ void fetch(const T *p) {  // whole
 #pragma unroll
-            for (int i = 0; i < 8 / V; i++) v[i] = *(const Vec *)(p + i * V);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; i++) v[i / V][i % V] = i < left ? p[i] : (T)0;
-        }
+        for (int i = 0; i < V / LOAD; i++) v[i] = *(const Vec *)(p + i * LOAD);
     }
-    // all eight, of what is read this once: the caches keep other things for it
+    // of what is read this once: the caches keep other things for it
     __device__ __forceinline__ void fetch_once(const T *p) {
 #pragma unroll
-        for (int i = 0; i < 8 / V; i++) v[i] = __builtin_nontemporal_load((const Vec *)(p + i * V));
+        for (int i = 0; i < V / LOAD; i++) v[i] = __builtin_nontemporal_load((const Vec *)(p + i * LOAD));
+    }
+    __device__ __forceinline__ void fetch(const T *p, int64_t left) {
+        if (left >= V) {
+            fetch(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) v[i / LOAD][i % LOAD] = i < left ? p[i] : (T)0;
+        }
     }
     __device__ __forceinline__ float at(int i) const {
-        if constexpr (sizeof(T) == 1) return (float)(int)v[i / V][i % V];
-        else return to_f32(v[i / V][i % V]);
+        if constexpr (sizeof(T) == 1) return (float)(int)v[i / LOAD][i % LOAD];
+        else return to_f32(v[i / LOAD][i % LOAD]);
     }
     // ONCE: nothing reads it soon
-    template <bool ONCE = false> static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[8]) {
-        if (left >= 8) {
+    template <bool ONCE = false> static __device__ __forceinline__ void store(T *p, int64_t left, const float (&f)[V]) {
+        if (left >= V) {
 #pragma unroll
-            for (int i = 0; i < 8; i += V) {
+            for (int i = 0; i < V; i += LOAD) {
                 Vec w;
 #pragma unroll
-                for (int j = 0; j < V; j++) w[j] = from_f32<T>(f[i + j]);
+                for (int j = 0; j < LOAD; j++) w[j] = from_f32<T>(f[i + j]);
                 if (ONCE) __builtin_nontemporal_store(w, (Vec *)(p + i));
                 else *(Vec *)(p + i) = w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++)
+            for (int i = 0; i < V; i++)
                 if (i < left) p[i] = from_f32<T>(f[i]);
         }
     }

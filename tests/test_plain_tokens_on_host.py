@@ -32,3 +32,8 @@ def _run(tmp_path, source, check, replaced=()):
 
 def test_alternatives_of_rows_in_any_order(tmp_path):
     assert "score: ok" in _run(tmp_path, "logprob.hip", "score_check.cpp")
+
+
+def test_order_of_tokens(tmp_path):
+    shared = ("extern __shared__ uint32_t places[];", "static uint32_t places[ORDER_WAVES << 9];")
+    assert "order: ok" in _run(tmp_path, "embed.hip", "order_check.cpp", [shared])
