@@ -54,7 +54,7 @@ constexpr int HELD = 16;
 constexpr uint32_t NONE = ~0u;
 struct TokenOrder {
     int32_t *order, *starts, *firsts, *lasts;
-    int64_t chunk;
+    int log_chunk;
 };
 __device__ __forceinline__ uint32_t token_at(const int64_t *tokens, int64_t i, int64_t last, int64_t vocab) {
     const int64_t v = i < last ? tokens[i] : -1;
@@ -102,11 +102,10 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
         if (token == vocab - 1) o.starts[vocab] = (int32_t)all;
         if (n && o.firsts) {
             // the ends of chunks that fall into its run
-            for (int64_t j = (at + o.chunk - 1) / o.chunk; j * o.chunk < at + n; j++) o.firsts[j] = (int32_t)token;
-            for (int64_t j = at / o.chunk; j <= (at + n - 1) / o.chunk; j++) {
-                const int64_t end = (j + 1) * o.chunk < all ? (j + 1) * o.chunk : all;
-                if (end <= at + n) o.lasts[j] = (int32_t)token;
-            }
+            const uint32_t chunk = 1u << o.log_chunk, end = at + n;
+            for (uint32_t j = (at + chunk - 1) >> o.log_chunk; j << o.log_chunk < end; j++) o.firsts[j] = (int32_t)token;
+            for (uint32_t j = at >> o.log_chunk; j << o.log_chunk < end; j++)
+                if (end == all || (j + 1) << o.log_chunk <= end) o.lasts[j] = (int32_t)token;
         }
         for (int w = 0; w < ORDER_WAVES; w++) {
             const uint32_t c = places[(w << log_bins) + threadIdx.x];
@@ -165,6 +164,7 @@ template <typename T, int V> struct Share {
             for (int j = 0; j < V; j++) f[n][j] += e[n].at(j);
     }
     // scale f [+ what is there]
+    // (a table's gradient is larger than the caches, and stores past them are faster: 268 MB in 52 us, else 70)
     template <bool ADD> static __device__ __forceinline__ void put(T *row, int64_t c, int64_t apart, int64_t cols,
                                                                     float scale, float (&f)[N][V]) {
 #pragma unroll
@@ -175,7 +175,7 @@ template <typename T, int V> struct Share {
             if (ADD) old.fetch(p, cols - c - n * apart);
 #pragma unroll
             for (int j = 0; j < V; j++) f[n][j] = (ADD ? old.at(j) : 0.0f) + f[n][j] * scale;
-            Piece<T, V>::store(p, cols - c - n * apart, f[n]);
+            Piece<T, V>::template store<!ADD>(p, cols - c - n * apart, f[n]);
         }
     }
 };
@@ -355,19 +355,21 @@ int log_bins(int64_t vocab) {
     while (b < 9 && ((int64_t)256 << b) < vocab) b++;
     return b;
 }
-// Rows of a chunk: at most 2048 chunks.
-int64_t chunk_rows(int64_t rows) {
-    int64_t c = 32;
-    while (c * 2048 < rows) c *= 2;
-    return c;
+// Rows of a chunk, as a power of two: at most 2048 chunks.
+int log_chunk_rows(int64_t rows) {
+    int l = 5;
+    while ((int64_t)2048 << l < rows) l++;
+    return l;
 }
 struct EmbedPlan {
+    int log_chunk;
     int64_t chunk, chunks;
     size_t order, starts, ends, parts;  // bytes
 };
 EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     EmbedPlan p;
-    p.chunk = chunk_rows(rows);
+    p.log_chunk = log_chunk_rows(rows);
+    p.chunk = (int64_t)1 << p.log_chunk;
     p.chunks = rows > p.chunk ? (rows + p.chunk - 1) / p.chunk : 0;  // without a long run none are needed
     p.order = (size_t)round_up(rows * 4, 16);
     p.starts = (size_t)round_up((vocab + 1) * 4, 16);
@@ -435,7 +437,7 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
     const EmbedPlan p = embed_plan(rows, vocab, cols);
     const int b = log_bins(vocab), l = log_lanes(cols);
     char *w = (char *)ws;
-    TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), nullptr, nullptr, p.chunk};
+    TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), nullptr, nullptr, p.log_chunk};
     w += p.order + p.starts;
     if (p.chunks) o.firsts = (int32_t *)w, o.lasts = (int32_t *)(w + p.ends);
     const EmbedSums a{tokens, o.order, o.starts, o.firsts, o.lasts, rows, vocab, cols, p.chunk, p.chunks, scale,

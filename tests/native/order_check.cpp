@@ -11,7 +11,8 @@ using namespace ckks_plain;
 static uint32_t state = 777;
 static uint32_t rnd() { return (state = state * 1664525u + 1013904223u) >> 8; }
 
-static int check(int rows, int vocab, int log_bins, int64_t chunk, int kind) {
+static int check(int rows, int vocab, int log_bins, int log_chunk, int kind) {
+    const int64_t chunk = 1 << log_chunk;
     std::vector<int64_t> tokens(rows);
     for (int i = 0; i < rows; i++)
         tokens[i] = kind == 0 ? (int64_t)(rnd() % (vocab + 2)) - 1 : kind == 1 ? vocab - 1 : kind == 2 ? -5
@@ -22,7 +23,7 @@ static int check(int rows, int vocab, int log_bins, int64_t chunk, int kind) {
     std::stable_sort(want.begin(), want.end(), [&](int a, int b) { return tokens[a] < tokens[b]; });
     const int64_t n = want.size(), chunks = (rows + chunk - 1) / chunk;
     std::vector<int32_t> order(rows, -9), starts(vocab + 1, -9), firsts(chunks, -9), lasts(chunks, -9);
-    const TokenOrder o{order.data(), starts.data(), firsts.data(), lasts.data(), chunk};
+    const TokenOrder o{order.data(), starts.data(), firsts.data(), lasts.data(), log_chunk};
     for (int b = 0; b < (vocab + (1 << log_bins) - 1) >> log_bins; b++) {
         blockIdx = {(unsigned)b, 0, 0};
         if (!host::run(ORDER_NT, 20000000, [&] { k_token_order(tokens.data(), rows, vocab, log_bins, o); })) return 1;
@@ -42,11 +43,11 @@ static int check(int rows, int vocab, int log_bins, int64_t chunk, int kind) {
 int main() {
     int bad = 0;
     for (int kind = 0; kind < 5; kind++) {
-        bad += check(1, 1, 2, 32, kind);
-        bad += check(300, 7, 2, 32, kind);
-        bad += check(1500, 1000, 9, 32, kind);
-        bad += check(1025, 20, 3, 4, kind);
-        bad += check(17000, 50, 5, 64, kind);
+        bad += check(1, 1, 2, 5, kind);
+        bad += check(300, 7, 2, 5, kind);
+        bad += check(1500, 1000, 9, 5, kind);
+        bad += check(1025, 20, 3, 2, kind);
+        bad += check(17000, 50, 5, 6, kind);
     }
     printf(bad ? "order: wrong\n" : "order: ok\n");
     return bad;
