@@ -42,9 +42,8 @@ __global__ __launch_bounds__(256) void k_embed(const T *table, int64_t table_str
 
 constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 
-// order[0 ...): the rows with a token in [0, vocab), by token and, among equals, by row; starts[v]: how
-// many of them have a token below v (v <= vocab).  Of each `chunk` places, firsts and lasts: the tokens at both
-// ends.
+// order[0 ...): the rows with a token in [0, vocab), by token and, among equals, by row, and token_of these
+// places; starts[v]: how many of them have a token below v (v <= vocab).
 //
 // A workgroup has 2^log_bins tokens of the vocabulary and reads all rows' tokens itself, so nothing is joined
 // between workgroups and one launch does: wave w counts those of its part of the rows, and after a sum over
@@ -53,8 +52,7 @@ constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 constexpr int HELD = 16;
 constexpr uint32_t NONE = ~0u;
 struct TokenOrder {
-    int32_t *order, *starts, *firsts, *lasts;
-    int log_chunk;
+    int32_t *order, *token_of, *starts;
 };
 __device__ __forceinline__ uint32_t token_at(const int64_t *tokens, int64_t i, int64_t last, int64_t vocab) {
     const int64_t v = i < last ? tokens[i] : -1;
@@ -100,13 +98,6 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
         const int64_t token = (int64_t)low + threadIdx.x;
         if (token < vocab) o.starts[token] = (int32_t)at;
         if (token == vocab - 1) o.starts[vocab] = (int32_t)all;
-        if (n && o.firsts) {
-            // the ends of chunks that fall into its run
-            const uint32_t chunk = 1u << o.log_chunk, end = at + n;
-            for (uint32_t j = (at + chunk - 1) >> o.log_chunk; j << o.log_chunk < end; j++) o.firsts[j] = (int32_t)token;
-            for (uint32_t j = at >> o.log_chunk; j << o.log_chunk < end; j++)
-                if (end == all || (j + 1) << o.log_chunk <= end) o.lasts[j] = (int32_t)token;
-        }
         for (int w = 0; w < ORDER_WAVES; w++) {
             const uint32_t c = places[(w << log_bins) + threadIdx.x];
             places[(w << log_bins) + threadIdx.x] = at;
@@ -124,10 +115,12 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
                 const int leader = __ffsll((unsigned long long)left) - 1;
                 const uint32_t b = lane(bin, leader), place = mine[b];
                 const uint64_t same = __ballot(in && bin == b);
-                if (in && bin == b)
-                    o.order[place + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
-                                                              __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0))] =
-                        (int32_t)(i + k * 64 + l);
+                if (in && bin == b) {
+                    const uint32_t to = place + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
+                                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+                    o.order[to] = (int32_t)(i + k * 64 + l);
+                    o.token_of[to] = (int32_t)v[k];
+                }
                 if (l == (uint32_t)leader) mine[b] = place + (uint32_t)__popcll(same);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's other lanes read it next
                 left &= ~same;
@@ -141,21 +134,30 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
 // parts[2 chunk] if the run holds the chunk's first place, else into parts[2 chunk + 1] (it is long, so
 // it holds the first or the last), and k_embed_join adds up the parts.
 struct EmbedSums {
-    const int64_t *tokens;
-    const int32_t *order, *starts, *firsts, *lasts;
-    int64_t rows, vocab, cols, chunk, chunks;
+    const int32_t *order, *token_of, *starts;
+    int64_t rows, vocab, cols, chunk;
     float scale;
     float *parts;
 };
 
-// A thread's share of a row, eight elements: vectors of V, `apart` elements from one to the next.
-template <typename T, int V> struct Share {
-    static constexpr int N = 8 / V;
+// A thread's share of a row, E elements: the columns of its vectors of V.
+template <int V, int E> struct Columns {
+    static constexpr int N = E / V;
+    int64_t at[N], cols;
+    // from column c on, `apart` columns from one to the next; OVER: the last whole
+    template <bool OVER> __device__ __forceinline__ void set(int64_t c, int64_t apart, int64_t n) {
+        cols = n;
+#pragma unroll
+        for (int k = 0; k < N; k++) at[k] = c + k * apart < cols && OVER ? whole_vector<V>(c + k * apart, cols) : c + k * apart;
+    }
+};
+template <typename T, int V, int E> struct Share {
+    static constexpr int N = E / V;
     Piece<T, V> e[N];
-    __device__ __forceinline__ void fetch(const T *row, int64_t c, int64_t apart, int64_t cols) {
+    __device__ __forceinline__ void fetch(const T *row, const Columns<V, E> &c) {
 #pragma unroll
         for (int n = 0; n < N; n++)
-            if (c + n * apart < cols) e[n].fetch(row + c + n * apart, cols - c - n * apart);
+            if (c.at[n] < c.cols) e[n].fetch(row + c.at[n], c.cols - c.at[n]);
     }
     __device__ __forceinline__ void add_to(float (&f)[N][V]) const {
 #pragma unroll
@@ -163,39 +165,46 @@ template <typename T, int V> struct Share {
 #pragma unroll
             for (int j = 0; j < V; j++) f[n][j] += e[n].at(j);
     }
-    // scale f [+ what is there]
-    // (a table's gradient is larger than the caches, and stores past them are faster: 268 MB in 52 us, else 70)
-    template <bool ADD> static __device__ __forceinline__ void put(T *row, int64_t c, int64_t apart, int64_t cols,
-                                                                    float scale, float (&f)[N][V]) {
+    // scale f [+ what is there]; stores of a whole table go past the caches: 268 MB in 52 us, else 70; 16 MB as fast
+    // either way
+    template <bool ADD>
+    static __device__ __forceinline__ void put(T *row, const Columns<V, E> &c, float scale, float (&f)[N][V]) {
 #pragma unroll
         for (int n = 0; n < N; n++) {
-            if (c + n * apart >= cols) continue;
-            T *p = row + c + n * apart;
+            if (c.at[n] >= c.cols) continue;
+            T *p = row + c.at[n];
             Piece<T, V> old;
-            if (ADD) old.fetch(p, cols - c - n * apart);
+            if (ADD) old.fetch(p, c.cols - c.at[n]);
 #pragma unroll
             for (int j = 0; j < V; j++) f[n][j] = (ADD ? old.at(j) : 0.0f) + f[n][j] * scale;
-            Piece<T, V>::template store<!ADD>(p, cols - c - n * apart, f[n]);
+            Piece<T, V>::template store<!ADD>(p, c.cols - c.at[n], f[n]);
         }
     }
 };
 
-// Adds a share of the rows order[from, to).
-template <typename T, int V>
+// Adds a share of the rows order[from, to), FLY rows in flight.  The places of 32 rows come in one load, by 32
+// lanes of a row (all of a row's lanes are here), where it has as many: with a load for each, a run of 32 rows
+// waited 16 times, and 8191 x 2051 f16 took 48 us.
+template <typename T, int V, int E>
 __device__ __forceinline__ void add_run(const EmbedSums &s, const T *drows, int64_t stride, int64_t from, int64_t to,
-                                        int64_t c, int64_t apart, float (&f)[8 / V][V]) {
-    int64_t i = from;
-    for (; i + 4 <= to; i += 4) {  // four rows in flight
-        Share<T, V> e[4];
+                                        const Columns<V, E> &c, int log_l, float (&f)[E / V][V]) {
+    constexpr int FLY = sizeof(T) * E > 16 ? 4 : 8;
+    const int l = threadIdx.x & 31, half = threadIdx.x & 32;
+    for (int64_t base = from; base < to; base += 32) {
+        const int n = to - base < 32 ? (int)(to - base) : 32;
+        const int32_t mine = s.order[base + (l < n ? l : 0)];
+        for (int i = 0; i < n; i += FLY) {
+            Share<T, V, E> e[FLY];
 #pragma unroll
-        for (int k = 0; k < 4; k++) e[k].fetch(drows + s.order[i + k] * stride, c, apart, s.cols);
+            for (int k = 0; k < FLY; k++) {
+                if (i + k >= n) break;
+                const int32_t row = log_l >= 5 ? __shfl(mine, half + i + k) : s.order[base + i + k];
+                e[k].fetch(drows + row * stride, c);
+            }
 #pragma unroll
-        for (int k = 0; k < 4; k++) e[k].add_to(f);
-    }
-    for (; i < to; i++) {
-        Share<T, V> e;
-        e.fetch(drows + s.order[i] * stride, c, apart, s.cols);
-        e.add_to(f);
+            for (int k = 0; k < FLY; k++)
+                if (i + k < n) e[k].add_to(f);
+        }
     }
 }
 
@@ -205,69 +214,64 @@ __device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, in
     constexpr int V = JOINT<T, float>;
     const int64_t from = j * s.chunk, n = s.starts[s.vocab], to = from + s.chunk < n ? from + s.chunk : n;
     if (from >= to) return;
-    const int64_t va = s.firsts[j], vb = s.lasts[j];
+    const int64_t va = s.token_of[from], vb = s.token_of[to - 1];
     for (int k = 0; k < (va == vb ? 1 : 2); k++) {
         const int64_t v = k ? vb : va, a = s.starts[v], b = s.starts[v + 1];
         if (b - a <= s.chunk) continue;
-        for (int64_t c = (int64_t)threadIdx.x * V; c < s.cols; c += 256 * 8) {
+        for (int64_t first = blockIdx.y * 2048; first < s.cols; first += gridDim.y * 2048) {
+            Columns<V, 8> c;
+            c.template set<true>(first + threadIdx.x * V, 256 * V, s.cols);
             float f[8 / V][V] = {};
-            add_run<T, V>(s, drows, stride, a > from ? a : from, b < to ? b : to, c, 256 * V, f);
-            Share<float, V>::template put<false>(s.parts + (2 * j + k) * s.cols, c, 256 * V, s.cols, 1.0f, f);
+            add_run<T, V, 8>(s, drows, stride, a > from ? a : from, b < to ? b : to, c, 8, f);
+            Share<float, V, 8>::template put<false>(s.parts + (2 * j + k) * s.cols, c, 1.0f, f);
         }
     }
 }
 
-// The first `chunks` workgroups: parts of long runs.  The others: 2^log_l threads on TABLE_ROWS rows of the table,
-// with the first row of each run, and where those start, on their way together.
-constexpr int TABLE_ROWS = 4;
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void k_embed_table(EmbedSums s, const T *drows, int64_t stride, O *out,
-                                                     int64_t out_stride, int64_t first, int64_t chunks, int log_l) {
+// The first `chunks` workgroups: parts of long runs.  The others: 2^log_l threads for ROWS rows of the table (the
+// zeros of tokens that do not occur first, which wait for nothing), or with ADD for a place of the order, the first of
+// its token.
+//
+// Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 47 us for 335 MB (7.1 TB/s, past the
+// caches), behind 11 us of order and in front of 5 us of long runs.  E elements a thread: 16 spare rows of just over
+// 2048 columns a second turn for the rest (4000 x 8191 bf16 75 us, with 8 99), 8 are faster for narrower ones (4096 x
+// 64 19 us, with 16 22).  Two rows of the table where they are short: 8191 rows f16 into 20011 x 2051 40.5 us, with one
+// 44; 16384 rows bf16 into 32768 x 2048 f32 70.6 us, with one 66.4.
+template <typename T, typename O, bool ADD, int E, int ROWS>
+__global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, int64_t stride, O *out,
+                                                   int64_t out_stride, int64_t from, int64_t chunks, int log_l) {
     if (blockIdx.x < chunks) return sum_parts(s, drows, stride, blockIdx.x);
     constexpr int V = JOINT<T, O>;
-    const int64_t group = ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
-    const int64_t v = first + group * TABLE_ROWS, apart = (int64_t)V << log_l;
-    if (v >= s.vocab) return;
-    int32_t at[TABLE_ROWS + 1], row[TABLE_ROWS];
-#pragma unroll
-    for (int k = 0; k <= TABLE_ROWS; k++) at[k] = s.starts[v + k < s.vocab ? v + k : s.vocab];
-#pragma unroll
-    for (int k = 0; k < TABLE_ROWS; k++) {
-        const int32_t n = at[k + 1] - at[k];
-        row[k] = n && n <= s.chunk ? s.order[at[k]] : -1;
+    const int64_t group = from + ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
+    const int64_t turn = (int64_t)E << log_l;
+    int64_t v = group * ROWS;
+    if (ADD) {
+        const int64_t a = group;
+        if (a >= s.rows || a >= s.starts[s.vocab]) return;
+        v = s.token_of[a];
+        if (a && s.token_of[a - 1] == v) return;
+    } else if (v >= s.vocab) {
+        return;
     }
-    for (int64_t c = (int64_t)(threadIdx.x & ((1 << log_l) - 1)) * V; c < s.cols; c += (int64_t)8 << log_l) {
-        Share<T, V> e[TABLE_ROWS];
+    int32_t at[ROWS + 1];
 #pragma unroll
-        for (int k = 0; k < TABLE_ROWS; k++)
-            if (row[k] >= 0) e[k].fetch(drows + row[k] * stride, c, apart, s.cols);
+    for (int k = 0; k <= ROWS; k++) at[k] = s.starts[v + k < s.vocab ? v + k : s.vocab];
+    for (int64_t first = blockIdx.y * turn; first < s.cols; first += gridDim.y * turn) {
+        Columns<V, E> c;
+        c.template set<!ADD>(first + (threadIdx.x & ((1 << log_l) - 1)) * V, (int64_t)V << log_l, s.cols);
 #pragma unroll
-        for (int k = 0; k < TABLE_ROWS; k++) {
-            if (v + k >= s.vocab || at[k + 1] - at[k] > s.chunk) continue;
-            float f[8 / V][V] = {};
-            if (row[k] >= 0) {
-                e[k].add_to(f);
-                add_run<T, V>(s, drows, stride, at[k] + 1, at[k + 1], c, apart, f);
-            }
-            Share<O, V>::template put<false>(out + (v + k) * out_stride, c, apart, s.cols, s.scale, f);
+        for (int k = 0; k < ROWS; k++) {
+            float f[E / V][V] = {};
+            if (!ADD && v + k < s.vocab && at[k] == at[k + 1])
+                Share<O, V, E>::template put<ADD>(out + (v + k) * out_stride, c, 0.0f, f);
         }
-    }
-}
-
-// The same with the sums added to `out`: a place of the order for 2^log_l threads, the first of its token.
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void k_embed_add(EmbedSums s, const T *drows, int64_t stride, O *out,
-                                                   int64_t out_stride, int64_t first, int64_t chunks, int log_l) {
-    if (blockIdx.x < chunks) return sum_parts(s, drows, stride, blockIdx.x);
-    constexpr int V = JOINT<T, O>;
-    const int64_t i = first + ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
-    if (i >= s.starts[s.vocab]) return;
-    const int64_t v = s.tokens[s.order[i]], apart = (int64_t)V << log_l;
-    if (i != s.starts[v] || s.starts[v + 1] - i > s.chunk) return;
-    for (int64_t c = (int64_t)(threadIdx.x & ((1 << log_l) - 1)) * V; c < s.cols; c += (int64_t)8 << log_l) {
-        float f[8 / V][V] = {};
-        add_run<T, V>(s, drows, stride, i, s.starts[v + 1], c, apart, f);
-        Share<O, V>::template put<true>(out + v * out_stride, c, apart, s.cols, s.scale, f);
+#pragma unroll
+        for (int k = 0; k < ROWS; k++) {
+            if (at[k] == at[k + 1] || at[k + 1] - at[k] > s.chunk) continue;
+            float f[E / V][V] = {};
+            add_run<T, V, E>(s, drows, stride, at[k], at[k + 1], c, log_l, f);
+            Share<O, V, E>::template put<ADD>(out + (v + k) * out_stride, c, s.scale, f);
+        }
     }
 }
 
@@ -280,18 +284,21 @@ __global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_
     const int64_t j = blockIdx.x, n = s.starts[s.vocab], from = j * s.chunk;
     const int64_t to = from + s.chunk < n ? from + s.chunk : n;
     if (from >= to) return;
-    const int64_t v = s.lasts[j], a = s.starts[v], b = s.starts[v + 1];
+    const int64_t v = s.token_of[to - 1], a = s.starts[v], b = s.starts[v + 1];
     if (b - a <= s.chunk || a < from) return;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int64_t c = (int64_t)blockIdx.y * JOIN_COLS + l * 4, last = (b - 1) / s.chunk;
-    float f[2][4] = {};
+    float f[8] = {};
     for (int64_t k = j + wave; k <= last; k += 16) {
-        Share<float, 4> e{};
-        e.fetch(s.parts + (2 * k + (k == j && a > from)) * s.cols, c, 256, s.cols);
-        e.add_to(f);
+        const float *part = s.parts + (2 * k + (k == j && a > from)) * s.cols;
+        Piece<float, 4> e[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) e[i].fetch(part + c + i * 256, s.cols - c - i * 256);
+#pragma unroll
+        for (int i = 0; i < 8; i++) f[i] += e[i / 4].at(i % 4);
     }
 #pragma unroll
-    for (int i = 0; i < 8; i++) sh[wave][i / 4 * 256 + l * 4 + i % 4] = f[i / 4][i % 4];
+    for (int i = 0; i < 8; i++) sh[wave][i / 4 * 256 + l * 4 + i % 4] = f[i];
     __syncthreads();
     const int64_t mine = (int64_t)blockIdx.y * JOIN_COLS + threadIdx.x;
     if (threadIdx.x >= JOIN_COLS || mine >= s.cols) return;
@@ -303,10 +310,10 @@ __global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_
 
 // ------------------------------------------------------------------ launches
 
-// threads of 8 elements for a row: a power of two, at most a workgroup
-int log_lanes(int64_t cols) {
+// threads of `share` elements for a row: a power of two, at most a workgroup
+int log_lanes(int64_t cols, int share) {
     int l = 0;
-    while (l < 8 && ((int64_t)8 << l) < cols) l++;
+    while (l < 8 && ((int64_t)share << l) < cols) l++;
     return l;
 }
 template <typename F> int typed(int type, F f) {
@@ -336,7 +343,7 @@ int embed(const T *table, int64_t table_stride, const float *table_scale, size_t
     if (overlap(out, ob, table, span(vocab, table_stride, cols, size)) || overlap(out, ob, tokens, rows * 8) ||
         overlap(out, ob, table_scale, vocab * 4))
         return CKKS_EINVAL;
-    const int l = log_lanes(cols);
+    const int l = log_lanes(cols, 8);
     return typed(out_type, [&](auto ty) {
         typedef decltype(ty) O;
         return in_parts(rows, 1 << l, [&](int64_t first, int64_t n) {
@@ -351,29 +358,26 @@ int embed(const T *table, int64_t table_stride, const float *table_scale, size_t
 
 // Bins of a workgroup of k_token_order: 256 workgroups, as far as LDS has room.
 int log_bins(int64_t vocab) {
-    int b = 2;
+    int b = 0;
     while (b < 9 && ((int64_t)256 << b) < vocab) b++;
     return b;
 }
-// Rows of a chunk, as a power of two: at most 2048 chunks.
-int log_chunk_rows(int64_t rows) {
-    int l = 5;
-    while ((int64_t)2048 << l < rows) l++;
-    return l;
+// Rows of a chunk: at most 2048 chunks.
+int64_t chunk_rows(int64_t rows) {
+    int64_t c = 32;
+    while (c * 2048 < rows) c *= 2;
+    return c;
 }
 struct EmbedPlan {
-    int log_chunk;
     int64_t chunk, chunks;
-    size_t order, starts, ends, parts;  // bytes
+    size_t order, starts, parts;  // bytes
 };
 EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     EmbedPlan p;
-    p.log_chunk = log_chunk_rows(rows);
-    p.chunk = (int64_t)1 << p.log_chunk;
+    p.chunk = chunk_rows(rows);
     p.chunks = rows > p.chunk ? (rows + p.chunk - 1) / p.chunk : 0;  // without a long run none are needed
     p.order = (size_t)round_up(rows * 4, 16);
     p.starts = (size_t)round_up((vocab + 1) * 4, 16);
-    p.ends = (size_t)round_up(p.chunks * 4, 16);
     p.parts = (size_t)p.chunks * 2 * cols * 4;
     return p;
 }
@@ -408,7 +412,7 @@ extern "C" int ckks_plain_embed_grad_workspace_size(int64_t rows, int64_t vocab,
     if (!bytes) return CKKS_EINVAL;
     if (int e = check_embed(vocab, cols, rows, CKKS_PLAIN_F32)) return e;
     const EmbedPlan p = embed_plan(rows, vocab, cols);
-    *bytes = p.order + p.starts + 2 * p.ends + p.parts;
+    *bytes = 2 * p.order + p.starts + p.parts;
     return CKKS_OK;
 }
 
@@ -435,13 +439,11 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
     if (!at(ws, 16)) return CKKS_EALIGN;
     const hipStream_t s = (hipStream_t)stream;
     const EmbedPlan p = embed_plan(rows, vocab, cols);
-    const int b = log_bins(vocab), l = log_lanes(cols);
+    const int b = log_bins(vocab), share = cols > 2048 ? 16 : 8, l = log_lanes(cols, share);
     char *w = (char *)ws;
-    TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), nullptr, nullptr, p.log_chunk};
-    w += p.order + p.starts;
-    if (p.chunks) o.firsts = (int32_t *)w, o.lasts = (int32_t *)(w + p.ends);
-    const EmbedSums a{tokens, o.order, o.starts, o.firsts, o.lasts, rows, vocab, cols, p.chunk, p.chunks, scale,
-                      (float *)(w + 2 * p.ends)};
+    const TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), (int32_t *)(w + 2 * p.order)};
+    const EmbedSums a{o.order, o.token_of, o.starts, rows, vocab, cols, p.chunk, scale,
+                      (float *)(w + 2 * p.order + p.starts)};
     k_token_order<<<dim3((uint32_t)((vocab + (1 << b) - 1) >> b)), ORDER_NT, (size_t)ORDER_WAVES * 4 << b, s>>>(
         tokens, rows, vocab, b, o);
     if (int e = launched()) return e;
@@ -452,18 +454,26 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
             auto go = [&](auto addition) {
                 constexpr bool ADD = decltype(addition)::value;
                 int64_t chunks = p.chunks;  // with the first part of the rows
-                const int64_t each = ADD ? 1 : TABLE_ROWS, n = ADD ? rows : (vocab + each - 1) / each;
-                int e = in_parts(n, 1 << l, [&](int64_t first, int64_t n) {
-                    const dim3 grid((uint32_t)(((n + (256 >> l) - 1) >> (8 - l)) + chunks));
-                    if constexpr (ADD)
-                        k_embed_add<T, O><<<grid, 256, 0, s>>>(a, (const T *)drows, drows_stride, (O *)out, out_stride,
-                                                               first, chunks, l);
-                    else
-                        k_embed_table<T, O><<<grid, 256, 0, s>>>(a, (const T *)drows, drows_stride, (O *)out,
-                                                                 out_stride, first * each, chunks, l);
-                    chunks = 0;
-                    return launched();
-                });
+                // wide rows by workgroups of 2048 columns, as far as a grid goes
+                const uint32_t turns = (uint32_t)(cols > 64 * 2048 ? 64 : (cols + 2047) / 2048);
+                auto sum = [&](auto elements, auto table_rows) {
+                    constexpr int E = decltype(elements)::value, ROWS = decltype(table_rows)::value;
+                    return in_parts(ADD ? rows : (vocab + ROWS - 1) / ROWS, turns << l, [&](int64_t first, int64_t n) {
+                        k_embed_sum<T, O, ADD, E, ROWS>
+                            <<<dim3((uint32_t)(((n + (256 >> l) - 1) >> (8 - l)) + chunks), turns), 256, 0, s>>>(
+                                a, (const T *)drows, drows_stride, (O *)out, out_stride, first, chunks, l);
+                        chunks = 0;
+                        return launched();
+                    });
+                };
+                const bool two = cols * sizeof(O) < 6144;
+                int e;
+                if constexpr (ADD)
+                    e = share == 16 ? sum(Int<16>{}, Int<1>{}) : sum(Int<8>{}, Int<1>{});
+                else if constexpr (sizeof(O) == 4)  // 16 elements: rows of 8 KB at least
+                    e = share == 16 ? sum(Int<16>{}, Int<1>{}) : two ? sum(Int<8>{}, Int<2>{}) : sum(Int<8>{}, Int<1>{});
+                else  // 8 elements: rows of 4 KB at most
+                    e = share == 8 ? sum(Int<8>{}, Int<2>{}) : two ? sum(Int<16>{}, Int<2>{}) : sum(Int<16>{}, Int<1>{});
                 if (e || !p.chunks) return e;
                 k_embed_join<O, ADD><<<dim3((uint32_t)p.chunks, (uint32_t)((cols + JOIN_COLS - 1) / JOIN_COLS)), 1024,
                                        0, s>>>(a, (O *)out, out_stride);

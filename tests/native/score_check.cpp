@@ -5,6 +5,8 @@
 
 #include "hip/hip_runtime.h"
 
+#define __builtin_nontemporal_load(p) (*(p))
+#define __builtin_nontemporal_store(v, p) (*(p) = (v))
 // moves within a row of 16 lanes that the header does not have
 static Index gridDim;
 static uint32_t update_dpp(uint32_t none, uint32_t v, int ctrl, int rows) {
