@@ -85,6 +85,15 @@ def test_embed_of_8_bit_rows(T, V, D, out):
     assert plain.embed(on_gpu(t, torch.int64), r).dtype == torch.bfloat16
 
 
+@pytest.mark.parametrize("D", [2048, 2051])
+def test_embed_of_a_prompt(D):
+    """More than 64 MB, past the caches."""
+    table = rnd(5, 300, D).to(torch.bfloat16).cuda()
+    t = on_gpu(ints(6, 17000, 0, 300), torch.int64)
+    assert torch.equal(plain.embed(t, table), table[t])
+    assert torch.equal(plain.embed(t, table, 0.5, torch.float32), table[t].float() * 0.5)
+
+
 def test_embed_of_tokens_far_outside_and_none():
     table = torch.ones(10, 64, device="cuda")
     t = torch.tensor([-1, 10, -2 ** 63, 2 ** 63 - 1, 2 ** 32, 9], device="cuda")
