@@ -116,23 +116,19 @@ int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckks_plain_nor
  *   y_a = n_a cos f - n_b sin f,  y_b = n_b cos f + n_a sin f,
  *   (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved; from
  *   rotary on, y = n.
- * Element (t, h, i) of a tensor is at t token + h head + i: unit stride in a
- * head, the other two strides at least head_dim where there is more than one
- * token or head.  head_dim and rotary are even, rotary <= head_dim <=
+ * Element (t, h, i) of a tensor is at t token_stride + h head_stride + i, both
+ * strides at least head_dim where there is more than one token or head.  head_dim and rotary are even, rotary <= head_dim <=
  * CKKS_PLAIN_MAX_HEAD.  positions [tokens] and inv_freq [rotary / 2] may be
  * NULL where rotary is 0; the angle's product and its turns are held in 64
  * bits, its sine and cosine in 32.  k_heads = 0: queries alone (k and k_weight
  * NULL).  Weights have the type of q and k. */
 #define CKKS_PLAIN_MAX_HEAD 512
 typedef struct {
-    int64_t token, head;
-} ckks_plain_head_strides;
-typedef struct {
     int type; /* CKKS_PLAIN_BF16, _F16 or _F32 */
     int interleaved;
     int64_t tokens, q_heads, k_heads, head_dim, rotary;
     const void *q, *k;
-    ckks_plain_head_strides q_strides, k_strides;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
     const void *q_weight, *k_weight; /* [head_dim] */
     const int64_t *positions;
     const float *inv_freq;
@@ -141,8 +137,9 @@ typedef struct {
 
 /* q_out and k_out may be q and k themselves (the same pointer and strides);
  * elements of an output do not share memory. */
-int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, ckks_plain_head_strides q_out_strides,
-                                void *k_out, ckks_plain_head_strides k_out_strides, void *stream);
+int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, int64_t q_out_token_stride,
+                                int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
+                                int64_t k_out_head_stride, void *stream);
 
 /* Gradients, given those of the outputs (dq, dk): dq_in, dk_in of the type of
  * q; of the weights in 32 bits, each where the forward call has that operand
@@ -150,9 +147,9 @@ int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, ckks_pla
  * aligned to 16 (may be NULL where that is 0). */
 typedef struct {
     const void *dq, *dk;
-    ckks_plain_head_strides dq_strides, dk_strides;
+    int64_t dq_token_stride, dq_head_stride, dk_token_stride, dk_head_stride;
     void *dq_in, *dk_in;
-    ckks_plain_head_strides dq_in_strides, dk_in_strides;
+    int64_t dq_in_token_stride, dq_in_head_stride, dk_in_token_stride, dk_in_head_stride;
     float *q_weight, *k_weight; /* [head_dim] */
 } ckks_plain_head_grads;
 int ckks_plain_head_grad_workspace_size(const ckks_plain_heads *p, size_t *bytes);

@@ -53,25 +53,21 @@ class PlainNormGrads(C.Structure):
                 ("block_bias", C.c_void_p), ("gate", C.c_void_p)]
 
 
-class PlainHeadStrides(C.Structure):
-    """ckks_plain_head_strides (include/ckks_plain.h)."""
-    _fields_ = [("token", C.c_int64), ("head", C.c_int64)]
-
-
 class PlainHeads(C.Structure):
     """ckks_plain_heads (include/ckks_plain.h)."""
     _fields_ = [("type", C.c_int), ("interleaved", C.c_int), ("tokens", C.c_int64), ("q_heads", C.c_int64),
                 ("k_heads", C.c_int64), ("head_dim", C.c_int64), ("rotary", C.c_int64), ("q", C.c_void_p),
-                ("k", C.c_void_p), ("q_strides", PlainHeadStrides), ("k_strides", PlainHeadStrides),
-                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("positions", C.c_void_p),
+                ("k", C.c_void_p), ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("positions", C.c_void_p),
                 ("inv_freq", C.c_void_p), ("eps", C.c_float)]
 
 
 class PlainHeadGrads(C.Structure):
     """ckks_plain_head_grads (include/ckks_plain.h)."""
-    _fields_ = [("dq", C.c_void_p), ("dk", C.c_void_p), ("dq_strides", PlainHeadStrides),
-                ("dk_strides", PlainHeadStrides), ("dq_in", C.c_void_p), ("dk_in", C.c_void_p),
-                ("dq_in_strides", PlainHeadStrides), ("dk_in_strides", PlainHeadStrides), ("q_weight", C.c_void_p),
+    _fields_ = [("dq", C.c_void_p), ("dk", C.c_void_p), ("dq_token_stride", C.c_int64), ("dq_head_stride", C.c_int64),
+                ("dk_token_stride", C.c_int64), ("dk_head_stride", C.c_int64), ("dq_in", C.c_void_p),
+                ("dk_in", C.c_void_p), ("dq_in_token_stride", C.c_int64), ("dq_in_head_stride", C.c_int64),
+                ("dk_in_token_stride", C.c_int64), ("dk_in_head_stride", C.c_int64), ("q_weight", C.c_void_p),
                 ("k_weight", C.c_void_p)]
 
 
@@ -133,8 +129,8 @@ SIGNATURES = {
     "ckks_plain_norm_grad_workspace_size": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(C.c_size_t)]),
     "ckks_plain_residual_norm_grad": (C.c_int, [C.POINTER(PlainNorm), C.POINTER(PlainNormGrads), C.c_void_p,
                                                 C.c_size_t, C.c_void_p]),
-    "ckks_plain_head_norm_rotate": (C.c_int, [C.POINTER(PlainHeads), C.c_void_p, PlainHeadStrides, C.c_void_p,
-                                              PlainHeadStrides, C.c_void_p]),
+    "ckks_plain_head_norm_rotate": (C.c_int, [C.POINTER(PlainHeads), C.c_void_p, C.c_int64, C.c_int64, C.c_void_p,
+                                              C.c_int64, C.c_int64, C.c_void_p]),
     "ckks_plain_head_grad_workspace_size": (C.c_int, [C.POINTER(PlainHeads), C.POINTER(C.c_size_t)]),
     "ckks_plain_head_norm_rotate_grad": (C.c_int, [C.POINTER(PlainHeads), C.POINTER(PlainHeadGrads), C.c_void_p,
                                                    C.c_size_t, C.c_void_p]),

@@ -3,12 +3,15 @@
 
 namespace ckks_plain {
 
+struct HeadStrides {
+    int64_t token, head;
+};
 // One tensor of heads and what becomes of it.
 struct HeadSide {
     const void *x, *weight, *dy;  // dy: the gradient of the output (gradient alone)
     void *out;                    // the output, or the gradient of x
     float *part;                  // [blocks][head_dim]: the weight's gradient from each workgroup
-    ckks_plain_head_strides x_strides, dy_strides, out_strides;
+    HeadStrides x_strides, dy_strides, out_strides;
     int heads, blocks;
 };
 struct HeadArgs {
@@ -127,19 +130,26 @@ __device__ __forceinline__ void head_angles(const HeadArgs &a, int64_t first, in
     }
 }
 
-// A workgroup's tokens on one side: f(token, head, angles of the token) for each head by 2^log_l threads,
-// `step` tokens at a time.
-template <typename F>
-__device__ __forceinline__ void each_head(const HeadArgs &a, int heads, int64_t block, float2 *angles, F f) {
+// A workgroup's tokens on one side, `step` tokens at a time: for each head, by 2^log_l threads, fetch(token, head)
+// and then, with the next head's on its way, work(token, head, angles of the token).
+template <typename Fetch, typename Work>
+__device__ __forceinline__ void each_head(const HeadArgs &a, int heads, int64_t block, float2 *angles, Fetch fetch,
+                                          Work work) {
     const int64_t first = block * a.span;
     const int64_t last = first + a.span < a.tokens ? first + a.span : a.tokens;
     const int groups = 256 >> a.log_l, g = threadIdx.x >> a.log_l;
     for (int64_t t = first; t < last; t += a.step) {
         const int64_t end = t + a.step < last ? t + a.step : last;
-        __syncthreads();  // the angles before are not read any more
+        const int n = (int)(end - t) * heads;
+        if (g < n) fetch(t + g / heads, g % heads);
+        if (t != first) __syncthreads();  // the angles before are not read any more
         head_angles(a, t, end, angles);
         __syncthreads();
-        for (int i = g; i < (int)(end - t) * heads; i += groups) f(t + i / heads, i % heads, angles + i / heads * a.r);
+        for (int i = g; i < n; i += groups) {
+            const int next = i + groups;
+            work(t + i / heads, i % heads, angles + i / heads * a.r,
+                 [&] { if (next < n) fetch(t + next / heads, next % heads); });
+        }
     }
 }
 
@@ -150,13 +160,16 @@ __global__ __launch_bounds__(256) void k_head_norm_rotate(HeadArgs a) {
     const int which = blockIdx.x >= a.side[0].blocks;
     const HeadSide &s = a.side[which];
     const int l = threadIdx.x & ((1 << a.log_l) - 1);
-    H hw;
+    H hw, hx;
     if (s.weight) hw.fetch(a, (const T *)s.weight, l);
-    each_head(a, s.heads, blockIdx.x - (which ? a.side[0].blocks : 0), angles, [&](int64_t t, int h, const float2 *cs) {
-        H hx;
-        float x[K][V], y[K][V];
+    each_head(a, s.heads, blockIdx.x - (which ? a.side[0].blocks : 0), angles,
+              [&](int64_t t, int h) {
         hx.fetch(a, (const T *)s.x + t * s.x_strides.token + h * s.x_strides.head, l);
+    },
+              [&](int64_t t, int h, const float2 *cs, auto fetch_next) {
+        float x[K][V], y[K][V];
         hx.widen(a, x, y);
+        fetch_next();
         if (s.weight) {
             float w[K][V], v[K][V], sum = 0;
 #pragma unroll
@@ -181,24 +194,27 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void k_head_grad(HeadArgs a) {
     typedef Head<T, V, K> H;
     extern __shared__ float2 angles[];
+    __shared__ float sums[4][CKKS_PLAIN_MAX_HEAD];
     const int which = blockIdx.x >= a.side[0].blocks;
     const HeadSide &s = a.side[which];
     const int block = blockIdx.x - (which ? a.side[0].blocks : 0);
     const int l = threadIdx.x & ((1 << a.log_l) - 1);
     float ax[K][V] = {}, ay[K][V] = {};
-    H hw;
+    H hw, hx, hd;
     if (s.weight) hw.fetch(a, (const T *)s.weight, l);
-    each_head(a, s.heads, block, angles, [&](int64_t t, int h, const float2 *cs) {
-        H hd;
-        float p[K][V], q[K][V];
+    each_head(a, s.heads, block, angles,
+              [&](int64_t t, int h) {
         hd.fetch(a, (const T *)s.dy + t * s.dy_strides.token + h * s.dy_strides.head, l);
+        if (s.weight) hx.fetch(a, (const T *)s.x + t * s.x_strides.token + h * s.x_strides.head, l);
+    },
+              [&](int64_t t, int h, const float2 *cs, auto fetch_next) {
+        float p[K][V], q[K][V], x[K][V], y[K][V];
         hd.widen(a, p, q);
+        if (s.weight) hx.widen(a, x, y);
+        fetch_next();
         H::turn(a, cs, l, -1.0f, p, q);
         if (s.weight) {
-            H hx;
-            float x[K][V], y[K][V], w[K][V], v[K][V], sum = 0, dot = 0;
-            hx.fetch(a, (const T *)s.x + t * s.x_strides.token + h * s.x_strides.head, l);
-            hx.widen(a, x, y);
+            float w[K][V], v[K][V], sum = 0, dot = 0;
             hw.widen(a, w, v);
 #pragma unroll
             for (int k = 0; k < K; k++)
@@ -226,27 +242,26 @@ __global__ __launch_bounds__(256) void k_head_grad(HeadArgs a) {
         H::store(a, (T *)s.out + t * s.out_strides.token + h * s.out_strides.head, l, p, q);
     });
     if (!s.part) return;
-    // the groups' sums in their order: a group's in LDS at a time
-    __shared__ float sums[2 * 256];
-    const int groups = 256 >> a.log_l, g = threadIdx.x >> a.log_l;
+    // the sums of a wave's groups, in a fixed order, then of the four waves
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
     for (int k = 0; k < K; k++) {
         const int u = ((k << a.log_l) + l) * V;
+        int apart;
+        const int at = H::place(a, u, apart);
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            __syncthreads();
-            sums[threadIdx.x] = ax[k][j], sums[256 + threadIdx.x] = ay[k][j];
-            __syncthreads();
-            if (g == 0 && u < a.half) {
-                float x = 0, y = 0;
-                for (int i = 0; i < groups; i++) x += sums[(i << a.log_l) + l], y += sums[256 + (i << a.log_l) + l];
-                int apart;
-                const int at = H::place(a, u, apart);
-                float *o = s.part + (int64_t)block * 2 * a.half;
-                o[at + (a.interleaved ? 2 * j : j)] = x;
-                o[at + (a.interleaved ? 2 * j + 1 : apart + j)] = y;
+            float x = ax[k][j], y = ay[k][j];
+            for (int far = 32; far >> a.log_l; far >>= 1) x += __shfl_xor(x, far), y += __shfl_xor(y, far);
+            if ((threadIdx.x & 63) >> a.log_l == 0 && u < a.half) {
+                sums[wave][at + (a.interleaved ? 2 * j : j)] = x;
+                sums[wave][at + (a.interleaved ? 2 * j + 1 : apart + j)] = y;
             }
         }
     }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * a.half; c += 256)
+        s.part[(int64_t)block * 2 * a.half + c] = ((sums[0][c] + sums[1][c]) + sums[2][c]) + sums[3][c];
 }
 
 // out[c] = the sum of part[b][c] over b, 64 columns and a side a workgroup, 16 waves on the rows in turn.
@@ -259,8 +274,17 @@ __global__ __launch_bounds__(1024) void k_head_weight_sum(const float *part0, co
     const int c = blockIdx.x * 64 + l;
     if (!out) return;
     float v = 0;
-    if (c < dim)
-        for (int b = wave; b < n; b += 16) v += part[(int64_t)b * dim + c];
+    if (c < dim) {
+        int b = wave;
+        for (; b + 7 * 16 < n; b += 8 * 16) {  // eight rows in flight
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) w[i] = part[(int64_t)(b + i * 16) * dim + c];
+#pragma unroll
+            for (int i = 0; i < 8; i++) v += w[i];
+        }
+        for (; b < n; b += 16) v += part[(int64_t)b * dim + c];
+    }
     sh[wave][l] = v;
     __syncthreads();
     if (wave || c >= dim) return;
@@ -271,13 +295,15 @@ __global__ __launch_bounds__(1024) void k_head_weight_sum(const float *part0, co
 // ------------------------------------------------------------------ launches
 
 // first and last element of a tensor of heads, as a number of bytes from its pointer
-size_t head_span(int64_t tokens, int64_t heads, int64_t dim, const ckks_plain_head_strides &s, size_t size) {
+size_t head_span(int64_t tokens, int64_t heads, int64_t dim, const HeadStrides &s, size_t size) {
     return tokens && heads ? ((size_t)(tokens - 1) * s.token + (size_t)(heads - 1) * s.head + dim) * size : 0;
 }
-bool same(const ckks_plain_head_strides &a, const ckks_plain_head_strides &b) {
+HeadStrides q_strides(const ckks_plain_heads *p) { return {p->q_token_stride, p->q_head_stride}; }
+HeadStrides k_strides(const ckks_plain_heads *p) { return {p->k_token_stride, p->k_head_stride}; }
+bool same(const HeadStrides &a, const HeadStrides &b) {
     return a.token == b.token && a.head == b.head;
 }
-int check_side(const ckks_plain_heads *p, const void *x, int64_t heads, const ckks_plain_head_strides &s, bool output) {
+int check_side(const ckks_plain_heads *p, const void *x, int64_t heads, const HeadStrides &s, bool output) {
     if (!p->tokens || !heads) return CKKS_OK;
     if (!x || (p->tokens > 1 && s.token < p->head_dim) || (heads > 1 && s.head < p->head_dim)) return CKKS_EINVAL;
     // heads within a token, or tokens within a head
@@ -297,14 +323,14 @@ int check_heads(const ckks_plain_heads *p) {
     const size_t z = type_size(p->type);
     if (!at(p->q_weight, z) || !at(p->k_weight, z) || !at(p->positions, 8) || !at(p->inv_freq, 4)) return CKKS_EALIGN;
     if (p->tokens && p->rotary && (!p->positions || !p->inv_freq)) return CKKS_EINVAL;
-    if (int e = check_side(p, p->q, p->q_heads, p->q_strides, false)) return e;
-    return check_side(p, p->k, p->k_heads, p->k_strides, false);
+    if (int e = check_side(p, p->q, p->q_heads, q_strides(p), false)) return e;
+    return check_side(p, p->k, p->k_heads, k_strides(p), false);
 }
 // an output's range against every input of the call (which: 0 and 1 leave out q or k)
 bool heads_overlap(const ckks_plain_heads *p, const void *out, size_t bytes, int without) {
     const size_t z = type_size(p->type);
-    return (without != 0 && overlap(out, bytes, p->q, head_span(p->tokens, p->q_heads, p->head_dim, p->q_strides, z))) ||
-           (without != 1 && overlap(out, bytes, p->k, head_span(p->tokens, p->k_heads, p->head_dim, p->k_strides, z))) ||
+    return (without != 0 && overlap(out, bytes, p->q, head_span(p->tokens, p->q_heads, p->head_dim, q_strides(p), z))) ||
+           (without != 1 && overlap(out, bytes, p->k, head_span(p->tokens, p->k_heads, p->head_dim, k_strides(p), z))) ||
            overlap(out, bytes, p->q_weight, p->head_dim * z) || overlap(out, bytes, p->k_weight, p->head_dim * z) ||
            overlap(out, bytes, p->positions, p->tokens * 8) || overlap(out, bytes, p->inv_freq, p->rotary / 2 * 4);
 }
@@ -339,15 +365,24 @@ struct HeadPlan {
 };
 HeadPlan head_plan(const ckks_plain_heads *p, bool grad) {
     HeadPlan h;
+    bool wide = false;
     by_head(p, [&](auto, auto v, auto k) {
+        wide = decltype(v)::value == 8;
         const int64_t share = decltype(v)::value * decltype(k)::value;
         h.log_l = 0;
         while ((share << h.log_l) < p->head_dim / 2) h.log_l++;
         return 0;
     });
     const int64_t groups = 256 >> h.log_l;
-    h.step = (int)(p->q_heads < groups ? groups / p->q_heads : 1);
-    const int64_t most = grad ? 1024 : 1 << 22;  // workgroups of a side
+    // A step of so many tokens that all threads work out angles, and each takes a few heads behind the next's loads:
+    // 8192 tokens of 32 + 8 heads of 128 bf16 29 us in steps of four, 39 one by one.  Short ones where there are few
+    // tokens (two workgroups a unit come first), and at most 8 KB of angles.
+    const int64_t one = p->q_heads < groups ? groups / p->q_heads : 1;
+    h.step = (int)one;
+    while (h.step < 4 * one && h.step * p->rotary <= 1024 && p->tokens >= 1024 * (int64_t)h.step) h.step *= 2;
+    // The gradient's workgroups each leave a row of partial sums: as many as run at a time (with vectors of 16-bit
+    // pairs 128 registers leave room for four a unit, of both sides; other forms have fewer).
+    const int64_t most = !grad ? 1 << 22 : wide ? 512 : 1024;  // workgroups of a side
     h.span = (int)((p->tokens + most * h.step - 1) / (most * h.step) * h.step);
     if (h.span < h.step) h.span = h.step;
     h.blocks = (p->tokens + h.span - 1) / h.span;
@@ -355,8 +390,8 @@ HeadPlan head_plan(const ckks_plain_heads *p, bool grad) {
 }
 HeadArgs head_args(const ckks_plain_heads *p, const HeadPlan &h) {
     HeadArgs a{};
-    a.side[0].x = p->q, a.side[0].weight = p->q_weight, a.side[0].x_strides = p->q_strides;
-    a.side[1].x = p->k, a.side[1].weight = p->k_weight, a.side[1].x_strides = p->k_strides;
+    a.side[0].x = p->q, a.side[0].weight = p->q_weight, a.side[0].x_strides = q_strides(p);
+    a.side[1].x = p->k, a.side[1].weight = p->k_weight, a.side[1].x_strides = k_strides(p);
     a.side[0].heads = (int)p->q_heads, a.side[1].heads = (int)p->k_heads;
     a.side[0].blocks = (int)h.blocks, a.side[1].blocks = p->k_heads ? (int)h.blocks : 0;
     a.positions = p->positions, a.inv_freq = p->inv_freq, a.tokens = p->tokens;
@@ -370,9 +405,12 @@ HeadArgs head_args(const ckks_plain_heads *p, const HeadPlan &h) {
 
 using namespace ckks_plain;
 
-extern "C" int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, ckks_plain_head_strides q_out_strides,
-                                           void *k_out, ckks_plain_head_strides k_out_strides, void *stream) {
+extern "C" int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, int64_t q_out_token_stride,
+                                           int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
+                                           int64_t k_out_head_stride, void *stream) {
     if (int e = check_heads(p)) return e;
+    const HeadStrides q_out_strides{q_out_token_stride, q_out_head_stride};
+    const HeadStrides k_out_strides{k_out_token_stride, k_out_head_stride};
     if (!p->k_heads && k_out) return CKKS_EINVAL;
     if (int e = check_side(p, q_out, p->q_heads, q_out_strides, true)) return e;
     if (int e = check_side(p, k_out, p->k_heads, k_out_strides, true)) return e;
@@ -380,8 +418,8 @@ extern "C" int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_ou
     const size_t z = type_size(p->type);
     const size_t qb = head_span(p->tokens, p->q_heads, p->head_dim, q_out_strides, z);
     const size_t kb = head_span(p->tokens, p->k_heads, p->head_dim, k_out_strides, z);
-    const bool q_in_place = q_out == p->q && same(q_out_strides, p->q_strides);
-    const bool k_in_place = k_out == p->k && same(k_out_strides, p->k_strides);
+    const bool q_in_place = q_out == p->q && same(q_out_strides, q_strides(p));
+    const bool k_in_place = k_out == p->k && same(k_out_strides, k_strides(p));
     if (heads_overlap(p, q_out, qb, q_in_place ? 0 : -1) || heads_overlap(p, k_out, kb, k_in_place ? 1 : -1) ||
         overlap(q_out, qb, k_out, kb))
         return CKKS_EINVAL;
@@ -414,16 +452,19 @@ extern "C" int ckks_plain_head_norm_rotate_grad(const ckks_plain_heads *p, const
     if (!p->q_weight != !g->q_weight || !p->k_weight != !g->k_weight) return CKKS_EINVAL;
     if (!p->k_heads && (g->dk || g->dk_in)) return CKKS_EINVAL;
     if (!at(g->q_weight, 4) || !at(g->k_weight, 4)) return CKKS_EALIGN;
-    if (int e = check_side(p, g->dq, p->q_heads, g->dq_strides, false)) return e;
-    if (int e = check_side(p, g->dk, p->k_heads, g->dk_strides, false)) return e;
-    if (int e = check_side(p, g->dq_in, p->q_heads, g->dq_in_strides, true)) return e;
-    if (int e = check_side(p, g->dk_in, p->k_heads, g->dk_in_strides, true)) return e;
+    const HeadStrides dq_strides{g->dq_token_stride, g->dq_head_stride}, dk_strides{g->dk_token_stride, g->dk_head_stride};
+    const HeadStrides dq_in_strides{g->dq_in_token_stride, g->dq_in_head_stride};
+    const HeadStrides dk_in_strides{g->dk_in_token_stride, g->dk_in_head_stride};
+    if (int e = check_side(p, g->dq, p->q_heads, dq_strides, false)) return e;
+    if (int e = check_side(p, g->dk, p->k_heads, dk_strides, false)) return e;
+    if (int e = check_side(p, g->dq_in, p->q_heads, dq_in_strides, true)) return e;
+    if (int e = check_side(p, g->dk_in, p->k_heads, dk_in_strides, true)) return e;
     const size_t z = type_size(p->type);
-    const size_t dqb = head_span(p->tokens, p->q_heads, p->head_dim, g->dq_strides, z);
-    const size_t dkb = head_span(p->tokens, p->k_heads, p->head_dim, g->dk_strides, z);
+    const size_t dqb = head_span(p->tokens, p->q_heads, p->head_dim, dq_strides, z);
+    const size_t dkb = head_span(p->tokens, p->k_heads, p->head_dim, dk_strides, z);
     struct { const void *p; size_t n; } w[5] = {
-        {g->dq_in, head_span(p->tokens, p->q_heads, p->head_dim, g->dq_in_strides, z)},
-        {g->dk_in, head_span(p->tokens, p->k_heads, p->head_dim, g->dk_in_strides, z)},
+        {g->dq_in, head_span(p->tokens, p->q_heads, p->head_dim, dq_in_strides, z)},
+        {g->dk_in, head_span(p->tokens, p->k_heads, p->head_dim, dk_in_strides, z)},
         {g->q_weight, (size_t)p->head_dim * 4}, {g->k_weight, (size_t)p->head_dim * 4}, {ws, need}};
     for (int i = 0; i < 5; i++) {
         if (heads_overlap(p, w[i].p, w[i].n, -1) || overlap(w[i].p, w[i].n, g->dq, dqb) ||
@@ -436,10 +477,10 @@ extern "C" int ckks_plain_head_norm_rotate_grad(const ckks_plain_heads *p, const
     if (!at(ws, 16)) return CKKS_EALIGN;
     const HeadPlan h = head_plan(p, true);
     HeadArgs a = head_args(p, h);
-    a.side[0].dy = g->dq, a.side[0].dy_strides = g->dq_strides;
-    a.side[1].dy = g->dk, a.side[1].dy_strides = g->dk_strides;
-    a.side[0].out = g->dq_in, a.side[0].out_strides = g->dq_in_strides;
-    a.side[1].out = g->dk_in, a.side[1].out_strides = g->dk_in_strides;
+    a.side[0].dy = g->dq, a.side[0].dy_strides = dq_strides;
+    a.side[1].dy = g->dk, a.side[1].dy_strides = dk_strides;
+    a.side[0].out = g->dq_in, a.side[0].out_strides = dq_in_strides;
+    a.side[1].out = g->dk_in, a.side[1].out_strides = dk_in_strides;
     const size_t one = (size_t)round_up(h.blocks * p->head_dim * 4, 16);
     if (p->q_weight) a.side[0].part = (float *)ws;
     if (p->k_weight) a.side[1].part = (float *)((char *)ws + (p->q_weight ? one : 0));

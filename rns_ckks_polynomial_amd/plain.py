@@ -484,33 +484,31 @@ def embed_grad(drows, tokens, vocab: int, scale: float = 1.0, dtype=torch.float3
 # ------------------------------------------------------------------ heads
 
 def _heads(t, what, tokens=None, dim=None, dtype=None, device=None):
-    """(address, strides) of a tensor of heads."""
+    """(address, token stride, head stride) of a tensor of heads."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{what}: expected a device tensor [tokens, heads, head_dim]")
-    T, H, d = t.shape
-    if (tokens is not None and T != tokens) or (dim is not None and d != dim):
-        raise ValueError(f"{what}: expected [{tokens}, heads, {dim}], got {tuple(t.shape)}")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if tokens is not None:
+        T, _, d = t.shape
+        if T != tokens or d != dim:
+            raise ValueError(f"{what}: expected [{tokens}, heads, {dim}], got {tuple(t.shape)}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{what} is on {t.device}, not on {device}")
     token, head, across = t.stride()
-    if d > 1 and across != 1:
+    if across != 1 and t.shape[2] > 1:
         raise ValueError(f"{what}: expected unit stride within a head")
-    return t.data_ptr(), nat.PlainHeadStrides(token, head)
-
-
-_NO_STRIDES = nat.PlainHeadStrides(0, 0)
+    return t.data_ptr(), token, head
 
 
 def _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
     """ckks_plain_heads of the arguments."""
-    qp, qs = _heads(q, "q")
+    qp, q_token, q_head = _heads(q, "q")
     T, H, d = q.shape
     dev, dt = q.device, q.dtype
-    kp, ks, k_heads = None, _NO_STRIDES, 0
+    kp, k_token, k_head, k_heads = None, 0, 0, 0
     if k is not None:
-        kp, ks = _heads(k, "k", T, d, dt, dev)
+        kp, k_token, k_head = _heads(k, "k", T, d, dt, dev)
         k_heads = k.shape[1]
         if k_heads < 1:
             raise ValueError("k: expected at least one head")
@@ -523,24 +521,29 @@ def _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
         pp = _vector(positions, "positions", T, torch.int64, dev)
         n = _count(inv_freq, "inv_freq")
         fp, rotary = _vector(inv_freq, "inv_freq", n, torch.float32, dev), 2 * n
-    return nat.PlainHeads(_type(q, "q"), 1 if interleaved else 0, T, H, k_heads, d, rotary, qp, kp, qs, ks,
-                          _vector(q_weight, "q_weight", d, dt, dev), _vector(k_weight, "k_weight", d, dt, dev), pp, fp,
-                          eps)
+    return nat.PlainHeads(_type(q, "q"), 1 if interleaved else 0, T, H, k_heads, d, rotary, qp, kp, q_token, q_head,
+                          k_token, k_head, _vector(q_weight, "q_weight", d, dt, dev),
+                          _vector(k_weight, "k_weight", d, dt, dev), pp, fp, eps)
 
 
-def _new_heads(t):
-    """(tensor of t's shape and type, its strides)"""
-    if t is None:
-        return None, None, _NO_STRIDES
-    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return out, out.data_ptr(), nat.PlainHeadStrides(t.shape[1] * t.shape[2], t.shape[2])
+@functools.lru_cache(maxsize=4096)
+def _head_grad_workspace(ty, tokens, q_heads, k_heads, dim, rotary, q_weight, k_weight):
+    """Bytes of scratch of the gradient: it goes by sizes and by which weights there are (16: there is one)."""
+    p = nat.PlainHeads(ty, 0, tokens, q_heads, k_heads, dim, rotary, 16, 16 if k_heads else None, dim, dim, dim, dim,
+                       16 if q_weight else None, 16 if k_weight else None, 16, 16, 0.0)
+    out = C.c_size_t()
+    nat.check(nat.lib().ckks_plain_head_grad_workspace_size(C.byref(p), C.byref(out)),
+              "ckks_plain_head_grad_workspace_size")
+    return out.value
 
 
 def _head_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
     p = _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
-    q_out, qp, qs = _new_heads(q)
-    k_out, kp, ks = _new_heads(k)
-    _call("ckks_plain_head_norm_rotate", q.device, C.byref(p), qp, qs, kp, ks)
+    d = p.head_dim
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _call("ckks_plain_head_norm_rotate", q.device, C.byref(p), q_out.data_ptr(), p.q_heads * d, d,
+          None if k is None else k_out.data_ptr(), p.k_heads * d, d)
     return q_out, k_out
 
 
@@ -584,29 +587,27 @@ def head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, q_weight=None, k_we
     of the weights in float32, None where there is no such operand.  They have no gradient of their own: a second
     derivative raises."""
     p = _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
-    T, d = q.shape[0], q.shape[2]
+    T, d, dev = p.tokens, p.head_dim, q.device
     side = []
     for x, g, what in ((q, dq, "dq"), (k, dk, "dk")):
         if (x is None) != (g is None):
             raise ValueError(f"{what}: expected the gradient of each result")
         if x is None:
-            side.append((None, _NO_STRIDES))
+            side.append((None, 0, 0))
             continue
-        side.append(_heads(g, what, T, d, x.dtype, x.device))
+        side.append(_heads(g, what, T, d, x.dtype, dev))
         if g.shape[1] != x.shape[1]:
             raise ValueError(f"{what}: expected {x.shape[1]} heads, got {g.shape[1]}")
-    dq_in, qp, qs = _new_heads(q)
-    dk_in, kp, ks = _new_heads(k)
-    new = lambda v: None if v is None else torch.empty(v.shape, dtype=torch.float32, device=q.device)  # noqa: E731
-    r = HeadNormRotateGrads(dq_in, dk_in, new(q_weight), new(k_weight))
+    new = lambda v, dt: None if v is None else torch.empty(v.shape, dtype=dt, device=dev)  # noqa: E731
+    r = HeadNormRotateGrads(new(q, q.dtype), new(k, q.dtype), new(q_weight, torch.float32),
+                            new(k_weight, torch.float32))
     at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
-    g = nat.PlainHeadGrads(side[0][0], side[1][0], side[0][1], side[1][1], qp, kp, qs, ks, at(r.q_weight),
-                           at(r.k_weight))
-    size = C.c_size_t()
-    nat.check(nat.lib().ckks_plain_head_grad_workspace_size(C.byref(p), C.byref(size)),
-              "ckks_plain_head_grad_workspace_size")
-    _keep, ws, size = _scratch(size.value, q.device)
-    _call("ckks_plain_head_norm_rotate_grad", q.device, C.byref(p), C.byref(g), ws, size)
+    (dqp, dq_token, dq_head), (dkp, dk_token, dk_head) = side
+    g = nat.PlainHeadGrads(dqp, dkp, dq_token, dq_head, dk_token, dk_head, at(r.dq), at(r.dk), p.q_heads * d, d,
+                           p.k_heads * d, d, at(r.q_weight), at(r.k_weight))
+    _keep, ws, size = _scratch(_head_grad_workspace(p.type, T, p.q_heads, p.k_heads, d, p.rotary,
+                                                    q_weight is not None, k_weight is not None), dev)
+    _call("ckks_plain_head_norm_rotate_grad", dev, C.byref(p), C.byref(g), ws, size)
     operands = (q, k, dq, dk, inv_freq, q_weight, k_weight)
     if _tracked(*operands):
         some = iter(_NoGradient.apply("head_norm_rotate_grad", tuple(v for v in r if v is not None), *operands))

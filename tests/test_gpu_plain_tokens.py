@@ -310,14 +310,11 @@ def test_heads_of_other_strides():
     want, _ = plain.head_norm_rotate(q, None, at, freq)
     p = plain._head_args(q, None, at, freq, None, None, 1e-6, False)
     out = torch.full((9, 6, 66), 7.0, dtype=torch.bfloat16, device="cuda")
-    none = nat.PlainHeadStrides(0, 0)
     stream = torch.cuda.current_stream().cuda_stream
-    assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), out.data_ptr(), nat.PlainHeadStrides(66, 6 * 66), None,
-                                                 none, stream) == 0
+    assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), out.data_ptr(), 66, 6 * 66, None, 0, 0, stream) == 0
     assert torch.equal(out.transpose(0, 1)[:, :, :64], want) and out[..., 64:].eq(7).all()
     keep = x.clone()
-    assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), q.data_ptr(), nat.PlainHeadStrides(9 * 70, 70), None, none,
-                                                 stream) == 0  # in place
+    assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), q.data_ptr(), 9 * 70, 70, None, 0, 0, stream) == 0  # in place
     assert torch.equal(q, want) and torch.equal(x[..., 64:], keep[..., 64:])
 
 

@@ -64,13 +64,13 @@ def test_embed_grad_workspace():
     assert lib.ckks_plain_embed_grad_workspace_size(T, 0, D, C.byref(n)) == INV
 
 
-def strides(token, head=0):
-    return nat.PlainHeadStrides(token, head)
+def at(what, token, head):
+    return {f"{what}_token_stride": token, f"{what}_head_stride": head}
 
 
 def heads(**kw):
     f = dict(type=0, interleaved=0, tokens=T, q_heads=4, k_heads=2, head_dim=D, rotary=D, q=X, k=Y,
-             q_strides=strides(6 * D, D), k_strides=strides(6 * D, D), q_weight=W, k_weight=W + 4096, positions=G,
+             **at("q", 6 * D, D), **at("k", 6 * D, D), q_weight=W, k_weight=W + 4096, positions=G,
              inv_freq=S, eps=1e-6)
     f.update(kw)
     return nat.PlainHeads(**f)
@@ -80,44 +80,44 @@ BAD_HEADS = [
     (dict(type=3), INV), (dict(interleaved=2), INV), (dict(tokens=-1), INV), (dict(tokens=1 << 31), INV),
     (dict(q_heads=0), INV), (dict(k_heads=-1), INV), (dict(k_heads=0), INV), (dict(head_dim=0), INV),
     (dict(head_dim=63, rotary=62), UNSUP), (dict(rotary=63), UNSUP), (dict(rotary=66), INV), (dict(rotary=-2), INV),
-    (dict(head_dim=514, q_strides=strides(1 << 15, 514), k_strides=strides(1 << 15, 514)), UNSUP),
+    (dict(head_dim=514, **at("q", 1 << 15, 514), **at("k", 1 << 15, 514)), UNSUP),
     (dict(q_heads=65536), UNSUP), (dict(eps=-1.0), INV), (dict(eps=float("nan")), INV), (dict(q=None), INV),
-    (dict(k=None), INV), (dict(positions=None), INV), (dict(inv_freq=None), INV), (dict(q_strides=strides(D - 1, D)), INV),
-    (dict(k_strides=strides(6 * D, D - 1)), INV), (dict(q=X + 1), ALIGN), (dict(k=Y + 1), ALIGN),
+    (dict(k=None), INV), (dict(positions=None), INV), (dict(inv_freq=None), INV), (at("q", D - 1, D), INV),
+    (at("k", 6 * D, D - 1), INV), (dict(q=X + 1), ALIGN), (dict(k=Y + 1), ALIGN),
     (dict(q_weight=W + 1), ALIGN), (dict(positions=G + 4), ALIGN), (dict(inv_freq=S + 2), ALIGN),
 ]
-OUT = (H, strides(4 * D, D), U, strides(2 * D, D))
+OUT = (H, 4 * D, D, U, 2 * D, D)
 
 
 @pytest.mark.parametrize("kw,code", BAD_HEADS)
 def test_heads_arguments(kw, code):
     lib, p = nat.lib(), heads(**kw)
     assert lib.ckks_plain_head_norm_rotate(C.byref(p), *OUT, None) == code
-    g = nat.PlainHeadGrads(X + (1 << 27), Y + (1 << 27), strides(6 * 512, 512), strides(6 * 512, 512), H, U,
-                           strides(4 * 512, 512), strides(2 * 512, 512), Q, Q + 4096)
+    g = nat.PlainHeadGrads(X + (1 << 27), Y + (1 << 27), 6 * 512, 512, 6 * 512, 512, H, U, 4 * 512, 512, 2 * 512, 512, Q,
+                           Q + 4096)
     assert lib.ckks_plain_head_norm_rotate_grad(C.byref(p), C.byref(g), WSP, 1 << 20, None) == code
 
 
 @pytest.mark.parametrize("out,code", [
-    ((None, OUT[1], *OUT[2:]), INV), ((H, strides(D, D), *OUT[2:]), INV), ((H, strides(4 * D, D - 1), *OUT[2:]), INV),
-    ((H, strides(4 * D - 1, D), *OUT[2:]), INV), ((H + 1, *OUT[1:]), ALIGN), ((X, *OUT[1:]), INV), ((Y, *OUT[1:]), INV),
-    ((H, OUT[1], H, OUT[3]), INV), ((W, *OUT[1:]), INV), ((G, *OUT[1:]), INV), ((S, *OUT[1:]), INV),
-    ((*OUT[:2], None, OUT[3]), INV), ((*OUT[:2], Y, OUT[3]), INV), ((*OUT[:2], U + 1, OUT[3]), ALIGN),
+    ((None, *OUT[1:]), INV), ((H, D, D, *OUT[3:]), INV), ((H, 4 * D, D - 1, *OUT[3:]), INV),
+    ((H, 4 * D - 1, D, *OUT[3:]), INV), ((H + 1, *OUT[1:]), ALIGN), ((X, *OUT[1:]), INV), ((Y, *OUT[1:]), INV),
+    ((*OUT[:3], H, *OUT[4:]), INV), ((W, *OUT[1:]), INV), ((G, *OUT[1:]), INV), ((S, *OUT[1:]), INV),
+    ((*OUT[:3], None, *OUT[4:]), INV), ((*OUT[:3], Y, *OUT[4:]), INV), ((*OUT[:3], U + 1, *OUT[4:]), ALIGN),
 ])
 def test_heads_outputs(out, code):
     p = heads()
     assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), *out, None) == code
 
 
-HG = dict(dq=X + (1 << 27), dk=Y + (1 << 27), dq_strides=strides(4 * D, D), dk_strides=strides(2 * D, D), dq_in=H, dk_in=U,
-          dq_in_strides=strides(4 * D, D), dk_in_strides=strides(2 * D, D), q_weight=Q, k_weight=Q + 4096)
+HG = dict(dq=X + (1 << 27), dk=Y + (1 << 27), **at("dq", 4 * D, D), **at("dk", 2 * D, D), dq_in=H, dk_in=U,
+          **at("dq_in", 4 * D, D), **at("dk_in", 2 * D, D), q_weight=Q, k_weight=Q + 4096)
 
 
 @pytest.mark.parametrize("kw,ws,code", [
     (dict(dq=None), WSP, INV), (dict(dk=None), WSP, INV), (dict(dq_in=None), WSP, INV), (dict(q_weight=None), WSP, INV),
-    (dict(k_weight=None), WSP, INV), (dict(dq_strides=strides(1, D)), WSP, INV), (dict(dq_in=X), WSP, INV),
+    (dict(k_weight=None), WSP, INV), (at("dq", 1, D), WSP, INV), (dict(dq_in=X), WSP, INV),
     (dict(dq_in=X + (1 << 27)), WSP, INV), (dict(dk_in=H), WSP, INV), (dict(q_weight=H + 4), WSP, INV),
-    (dict(k_weight=Q + 8), WSP, INV), (dict(q_weight=Q + 2), WSP, ALIGN), (dict(dq_in_strides=strides(D, D)), WSP, INV),
+    (dict(k_weight=Q + 8), WSP, INV), (dict(q_weight=Q + 2), WSP, ALIGN), (at("dq_in", D, D), WSP, INV),
     ({}, None, WS), ({}, WSP + 4, ALIGN), ({}, H, INV), ({}, X, INV), ({}, Q, INV),
 ])
 def test_heads_grad_arguments(kw, ws, code):
@@ -194,7 +194,7 @@ def test_no_rows_is_valid():
     assert lib.ckks_plain_embed(*{**EMB, "rows": 0, "table": None, "tokens": None, "out": None}.values(), None) == 0
     assert lib.ckks_plain_embed_grad(*{**EG, "rows": 0, "add": 1}.values(), None) == 0
     p = heads(tokens=0, q=None, k=None, positions=None)
-    assert lib.ckks_plain_head_norm_rotate(C.byref(p), None, strides(0), None, strides(0), None) == 0
+    assert lib.ckks_plain_head_norm_rotate(C.byref(p), None, 0, 0, None, 0, 0, None) == 0
     assert lib.ckks_plain_token_logprobs(*{**SC, "rows": 0}.values(), None) == 0
     assert lib.ckks_plain_token_logprobs_grad(*{**SG, "rows": 0}.values(), None) == 0
 
