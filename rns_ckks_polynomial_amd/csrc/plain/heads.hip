@@ -335,20 +335,21 @@ bool heads_overlap(const ckks_plain_heads *p, const void *out, size_t bytes, int
            overlap(out, bytes, p->positions, p->tokens * 8) || overlap(out, bytes, p->inv_freq, p->rotary / 2 * 4);
 }
 
-// Pairs of a vector: as many as 16 bytes hold, where pairs that turn, and all pairs, are whole vectors.
+// Pairs of a vector: as many as 16 bytes hold, or fewer, so that pairs that turn, and all pairs, are whole vectors.
 int head_vector(const ckks_plain_heads *p) {
-    const int whole = 16 / (int)type_size(p->type);
-    const int64_t r = p->rotary / 2, half = p->head_dim / 2;
-    if (r % whole == 0 && half % whole == 0) return whole;
-    return r % 2 == 0 && half % 2 == 0 ? 2 : 1;
+    int v = 16 / (int)type_size(p->type);
+    while (v > 1 && (p->rotary / 2 % v || p->head_dim / 2 % v)) v /= 2;
+    return v;
 }
-// f(type tag, pairs of a vector, vectors of a thread)
+// f(type tag, pairs of a vector, vectors of a thread): at most 64 threads
 template <typename T, typename F> int by_head(const ckks_plain_heads *p, F f) {
     const int v = head_vector(p);
     const int64_t units = p->head_dim / 2;
-    if (v == VEC<T>) return f(T{}, Int<VEC<T>>{}, Int<1>{});  // at most 64 threads of 4 or more
     if (v == 2) return units <= 128 ? f(T{}, Int<2>{}, Int<1>{}) : f(T{}, Int<2>{}, Int<2>{});
-    return units <= 64 ? f(T{}, Int<1>{}, Int<1>{}) : units <= 128 ? f(T{}, Int<1>{}, Int<2>{}) : f(T{}, Int<1>{}, Int<4>{});
+    if (v == 1)
+        return units <= 64 ? f(T{}, Int<1>{}, Int<1>{}) : units <= 128 ? f(T{}, Int<1>{}, Int<2>{}) : f(T{}, Int<1>{}, Int<4>{});
+    if (v == 4) return f(T{}, Int<4>{}, Int<1>{});
+    return f(T{}, Int<VEC<T>>{}, Int<1>{});
 }
 template <typename F> int by_head(const ckks_plain_heads *p, F f) {
     switch (p->type) {

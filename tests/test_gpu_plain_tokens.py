@@ -235,7 +235,7 @@ def host(v):
     return None if v is None else v.cpu().numpy()
 
 
-HEADS = [(1, 1, 0, 2, 1), (3, 2, 1, 64, 32), (5, 16, 8, 128, 64), (2, 3, 1, 80, 20), (7, 5, 5, 72, 9), (4, 2, 2, 96, 48),
+HEADS = [(1, 1, 0, 2, 1), (3, 2, 2, 72, 36), (2, 1, 1, 504, 252), (3, 2, 1, 64, 32), (5, 16, 8, 128, 64), (2, 3, 1, 80, 20), (7, 5, 5, 72, 9), (4, 2, 2, 96, 48),
          (3, 1, 1, 256, 128), (2, 2, 1, 512, 256), (2, 1, 1, 510, 255), (3, 4, 2, 508, 2), (9, 12, 4, 36, 18),
          (2, 2, 2, 64, 0), (130, 3, 1, 16, 8)]
 
