@@ -74,7 +74,7 @@ template <typename T, bool MASK> struct Logits {
     }
 };
 
-constexpr int SCORE_NT = 512, GROUPS = 64, GROUP_LANES = SCORE_NT / GROUPS, CANDIDATES = 1024;
+constexpr int JOIN_NT = 512, CANDIDATES = 1024, FEW = 128;
 constexpr float LEAST = -200.0f;  // exp2 of it is 0
 
 // Sums of 2^x and of x 2^x over logits z, x = z scale - at, where `at` is near the largest z scale so far.
@@ -120,10 +120,10 @@ __device__ __forceinline__ void put_top(const ScoreArgs &a, int64_t row, int ran
     a.top_logprob[row * a.top + rank] = key ? distance(key_logit(key), largest) * inv_t - log_mass : -INFINITY;
 }
 
-struct ScoreShared {
-    uint64_t groups[GROUPS], list[CANDIDATES], bound;
-    uint32_t slots[SCORE_NT / 64], more[SCORE_NT / 64], winners[SCORE_NT], n_winners, n_readers, n;
-    float sums[2][SCORE_NT / 64];
+template <int NT> struct ScoreShared {
+    uint64_t list[CANDIDATES], bound;  // the list begins as the threads' keys
+    uint32_t slots[NT / 64], more[NT / 64], winners[NT], n_winners, n_readers, n;
+    float sums[2][NT / 64];
 };
 // What a slice of a row leaves for the whole: these and its `top` largest keys, in order.
 struct Part {
@@ -136,6 +136,46 @@ __device__ __forceinline__ int rank_in_list(const uint64_t *list, int n, uint64_
     for (int i = 0; i < n; i++) r += list[i] > key;
     return r;
 }
+__device__ __forceinline__ uint64_t other_lane(uint64_t v, int far) {
+    return (uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), far) << 32 | (uint32_t)__shfl_xor((int)v, far);
+}
+// One key a lane, falling over the wave: all of them, or (from half = 32 on) of a sequence that falls and then rises.
+__device__ __forceinline__ uint64_t sort_halves(uint64_t v, int l, int size, int half) {
+    for (; half; half >>= 1) {
+        const uint64_t w = other_lane(v, half);
+        const bool low = !(l & half), falls = !(l & size);
+        v = (low == falls) == (v > w) ? v : w;
+    }
+    return v;
+}
+__device__ __forceinline__ uint64_t sort_wave(uint64_t v, int l) {
+    for (int size = 2; size <= 64; size *= 2) v = sort_halves(v, l, size, size / 2);
+    return v;
+}
+// The largest 64 of two falling sequences, falling; `reversed`: the second from its end.
+__device__ __forceinline__ uint64_t join_waves(uint64_t v, uint64_t reversed, int l) {
+    return sort_halves(v > reversed ? v : reversed, l, 64, 32);
+}
+// The largest 64 of the list's first n, falling, at its front (behind the last: 0).  All threads; ends behind a barrier.
+// (A rank by comparison with all n costs as many reads for each: 4096 x 1000 bf16 top 64 450 us, so ...)
+template <int NT> __device__ __forceinline__ void sort_list(uint64_t *list, int n) {
+    const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
+    uint64_t v = 0;
+    for (int q = wave; q * 64 < n; q += NT / 64) {
+        uint64_t w = sort_wave(q * 64 + l < n ? list[q * 64 + l] : 0, l);
+        v = join_waves(v, other_lane(w, 63), l);
+    }
+    __syncthreads();
+    list[threadIdx.x] = v;
+    for (int s = NT / 128; s; s /= 2) {
+        __syncthreads();
+        if (wave < s) {
+            v = join_waves(v, list[(wave + s) * 64 + 63 - l], l);
+            list[wave * 64 + l] = v;
+        }
+    }
+    __syncthreads();
+}
 
 // A workgroup reads a slice of a row once; each thread keeps the sums of what it reads.  Their `at` is the
 // rounded product of its largest logit and the scale: one multiply-add gives an x, whose shift by that
@@ -147,13 +187,14 @@ __device__ __forceinline__ int rank_in_list(const uint64_t *list, int n, uint64_
 // at least one token is not below it.  The top-th largest of the keys of 64 groups of threads is a bound which
 // at least `top` tokens pass; they are all among the tokens of threads whose largest logit passes it from its
 // vector's start (`winners`, little more than `top`).  Such a thread's vector is read again, and its others where
-// the largest of them may pass too (all of them would be lines of memory: 2048 x 131072 bf16 top 20 117 us).  What
-// passes goes on a list, and a token's rank there is its place.  Where the list is too short (runs of equal logits, rows in bad order), the
-// top-th largest on it is a better bound: all that were on it below that one do not come back, so it ends.
+// the largest of them may pass too (all of them would be lines of memory: 2048 x 131072 bf16 top 20 117 us, so 107).
+// What passes goes on a list, and a token's rank there is its place.  Where the list is too short (runs of equal
+// logits, rows in bad order), the top-th largest on it is a better bound: all that were on it below that one do not
+// come back, so it ends.
 constexpr float ROOM = 0x1p20f;
-template <typename T, bool MASK, bool TOP, bool STREAM>
-__global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {
-    __shared__ ScoreShared sh;
+template <typename T, bool MASK, bool TOP, bool STREAM, int NT>
+__global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {
+    __shared__ ScoreShared<NT> sh;
     const int t = threadIdx.x;
     const int64_t row = a.first + blockIdx.x;
     const T *z = (const T *)a.logits + row * a.stride;
@@ -182,7 +223,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
         s.add(f, scale);
         s.add(g, scale);
     };
-    constexpr int STEP = SCORE_NT * 8;
+    constexpr int STEP = NT * 8;
     const int whole = (end - begin) / (2 * STEP);
     int c = begin + t * 8;
     Logits<T, MASK> p, q;
@@ -206,7 +247,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
         q.widen(c + STEP, end, g);
         take(f, c, g, c + STEP);
     }
-    const uint32_t top_bits = row_all<SCORE_NT>(best != best ? ~0u : order_bits(best), sh.slots, Larger{});
+    const uint32_t top_bits = row_all<NT>(best != best ? ~0u : order_bits(best), sh.slots, Larger{});
     float m = of_order_bits(top_bits);  // -infinity where nothing is possible
     if (top_bits != ~0u && fabsf(m * scale) < ROOM) {
         const float at = m * scale;
@@ -223,7 +264,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
             next = fmaxf(next, fminf(v, best));
             if (v > best) best = v, best_at = c;
         }
-        m = of_order_bits(row_all<SCORE_NT>(order_bits(best), sh.more, Larger{}));
+        m = of_order_bits(row_all<NT>(order_bits(best), sh.more, Larger{}));
         s.mass = s.moment = 0;
         for (int c = begin + t * 8; c < end; c += STEP) {
             float f[8];
@@ -238,7 +279,7 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
             }
         }
     }
-    row_sums<SCORE_NT>(s.mass, s.moment, sh.sums[0], sh.sums[1]);
+    row_sums<NT>(s.mass, s.moment, sh.sums[0], sh.sums[1]);
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
     if (t == 0) {
@@ -250,19 +291,16 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
     }
     if (!TOP) return;
     const uint64_t mine = best > -INFINITY ? token_key(best, best_at + 7) : 0;
-    uint64_t group = mine;
-    group = Larger{}(group, moved<0xb1, 0xf>((uint64_t)0, group));
-    group = Larger{}(group, moved<0x4e, 0xf>((uint64_t)0, group));
-    if (GROUP_LANES > 4) group = Larger{}(group, moved<0x141, 0xf>((uint64_t)0, group));
-    if (t % GROUP_LANES == 0) sh.groups[t / GROUP_LANES] = group;
+    sh.list[t] = mine;
     __syncthreads();
     if (t < 64) {
-        const uint64_t key = sh.groups[t];
+        uint64_t key = 0;  // of the threads t, t + 64, ...: short rows are in all of these groups too
+        for (int w = 0; w < NT / 64; w++) key = Larger{}(key, sh.list[w * 64 + t]);
         int rank = 0;
-        for (int i = 0; i < GROUPS; i++) rank += lane(key, i) > key;
+        for (int i = 0; i < 64; i++) rank += lane(key, i) > key;
         if (rank == a.top - 1 && key) sh.bound = key;
     }
-    const int steps = (end - begin + SCORE_NT * 8 - 1) / (SCORE_NT * 8);  // vectors of a thread
+    const int steps = (end - begin + NT * 8 - 1) / (NT * 8);  // vectors of a thread
     int n;
     for (;;) {
         __syncthreads();
@@ -285,37 +323,40 @@ __global__ __launch_bounds__(SCORE_NT) void k_token_logprobs(ScoreArgs a, int sl
             // its other vectors, if one may hold a token that passes; the front of `winners` is those to read in
             // full, the back those of one vector
             if (token_key(next, 0) >= bound) sh.winners[atomicAdd(&sh.n_readers, 1u)] = t;
-            else sh.winners[SCORE_NT - 1 - atomicAdd(&sh.n_winners, 1u)] = best_at;
+            else sh.winners[NT - 1 - atomicAdd(&sh.n_winners, 1u)] = best_at;
         }
         __syncthreads();
         const int jobs = (int)sh.n_readers * steps, ones = (int)sh.n_winners;
-        for (int j = t; j < jobs + ones; j += SCORE_NT) {
-            const int c = j < jobs ? begin + (j % steps * SCORE_NT + (int)sh.winners[j / steps]) * 8
-                                   : (int)sh.winners[SCORE_NT - 1 - (j - jobs)];
+        for (int j = t; j < jobs + ones; j += NT) {
+            const int c = j < jobs ? begin + (j % steps * NT + (int)sh.winners[j / steps]) * 8
+                                   : (int)sh.winners[NT - 1 - (j - jobs)];
             if (c < end) list_vector(c);
         }
         __syncthreads();
         n = (int)sh.n;
+        if (n <= FEW) break;
+        sort_list<NT>(sh.list, n < CANDIDATES ? n : CANDIDATES);
         if (n <= CANDIDATES) break;
-        for (int i = t; i < CANDIDATES; i += SCORE_NT)
-            if (rank_in_list(sh.list, CANDIDATES, sh.list[i]) == a.top - 1) sh.bound = sh.list[i];
-        __syncthreads();
-        if (t == 0) sh.n_winners = sh.n_readers = sh.n = 0;
+        if (t == 0) sh.bound = sh.list[a.top - 1], sh.n_winners = sh.n_readers = sh.n = 0;
     }
-    for (int i = t; i < n; i += SCORE_NT) {
-        const int rank = rank_in_list(sh.list, n, sh.list[i]);
-        if (rank < a.top) put_top(a, row, rank, sh.list[i], largest, log_mass, inv_t, keys);
+    if (n > FEW) {  // sorted
+        if (t < a.top) put_top(a, row, t, sh.list[t], largest, log_mass, inv_t, keys);
+        return;
     }
-    for (int i = n + t; i < a.top; i += SCORE_NT) put_top(a, row, i, 0, largest, log_mass, inv_t, keys);
+    if (t < n) {
+        const int rank = rank_in_list(sh.list, n, sh.list[t]);
+        if (rank < a.top) put_top(a, row, rank, sh.list[t], largest, log_mass, inv_t, keys);
+    }
+    if (t >= n && t < a.top) put_top(a, row, t, 0, largest, log_mass, inv_t, keys);
 }
 
 // A row's slices together: one workgroup a row.
 template <typename T, bool MASK>
-__global__ __launch_bounds__(SCORE_NT) void k_join_logprobs(ScoreArgs a, int slices, const Part *parts,
+__global__ __launch_bounds__(JOIN_NT) void k_join_logprobs(ScoreArgs a, int slices, const Part *parts,
                                                             const uint64_t *keys) {
     __shared__ uint64_t list[JOIN_KEYS];
-    __shared__ uint32_t slots[SCORE_NT / 64];
-    __shared__ float sums[2][SCORE_NT / 64];
+    __shared__ uint32_t slots[JOIN_NT / 64];
+    __shared__ float sums[2][JOIN_NT / 64];
     const int t = threadIdx.x;
     const int64_t row = a.first + blockIdx.x;
     const T *z = (const T *)a.logits + row * a.stride;
@@ -323,25 +364,25 @@ __global__ __launch_bounds__(SCORE_NT) void k_join_logprobs(ScoreArgs a, int sli
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
     Part p{-INFINITY, 0, 0, 0};
     if (t < slices) p = parts[row * slices + t];
-    for (int i = t; i < slices * a.top; i += SCORE_NT) list[i] = keys[row * slices * a.top + i];
-    const float m = of_order_bits(row_all<SCORE_NT>(order_bits(p.m), slots, Larger{}));
+    for (int i = t; i < slices * a.top; i += JOIN_NT) list[i] = keys[row * slices * a.top + i];
+    const float m = of_order_bits(row_all<JOIN_NT>(order_bits(p.m), slots, Larger{}));
     Mass s{0, p.mass, p.moment};
     if (p.m != m) s.shift(fmaxf((p.m - m) * scale, LEAST));  // two infinities have no distance
-    row_sums<SCORE_NT>(s.mass, s.moment, sums[0], sums[1]);
+    row_sums<JOIN_NT>(s.mass, s.moment, sums[0], sums[1]);
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
     if (t == 0) put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
     if (!a.top) return;
     // Bounds that `top` keys pass: a slice's last, and the least of the slices' keys at a place that makes `top`
     // of them together.
-    __shared__ uint64_t ends[2][SCORE_NT / 64];
+    __shared__ uint64_t ends[2][JOIN_NT / 64];
     uint64_t last = 0, least = 0;
     if (t < slices) last = list[t * a.top + a.top - 1], least = ~list[t * a.top + (a.top - 1) / slices];
-    last = row_all<SCORE_NT>(last, ends[0], Larger{});
-    least = ~row_all<SCORE_NT>(least, ends[1], Larger{});
+    last = row_all<JOIN_NT>(last, ends[0], Larger{});
+    least = ~row_all<JOIN_NT>(least, ends[1], Larger{});
     const uint64_t bound = last > least ? last : least;
     // Each slice's keys fall: a key's place among all is where it would stand in each of them.
-    for (int i = t; i < slices * a.top; i += SCORE_NT) {
+    for (int i = t; i < slices * a.top; i += JOIN_NT) {
         const uint64_t key = list[i];
         if (key < bound) continue;
         int rank = i % a.top;
@@ -520,20 +561,25 @@ extern "C" int ckks_plain_token_logprobs(int type, const void *logits, int64_t l
         const int slice = (int)round_up((vocab + slices - 1) / slices, 8);
         Part *parts = slices > 1 ? (Part *)ws : nullptr;
         uint64_t *keys = slices > 1 && top ? (uint64_t *)(parts + rows * slices) : nullptr;
-        return in_parts(rows, SCORE_NT * slices, [&](int64_t first, int64_t n) {
+        return in_parts(rows, 512 * slices, [&](int64_t first, int64_t n) {
             a.first = first;
             const dim3 grid((uint32_t)n, slices);
-            auto go = [&](auto alternatives, auto past) {
-                k_token_logprobs<T, MASK, decltype(alternatives)::value, decltype(past)::value>
-                    <<<grid, SCORE_NT, 0, (hipStream_t)stream>>>(a, slice, parts, keys);
+            auto go = [&](auto alternatives, auto past, auto threads) {
+                constexpr int NT = decltype(threads)::value;
+                k_token_logprobs<T, MASK, decltype(alternatives)::value, decltype(past)::value, NT>
+                    <<<grid, NT, 0, (hipStream_t)stream>>>(a, slice, parts, keys);
                 return launched();
             };
-            const bool past = past_caches(rows, vocab, z);
-            int e = top ? past ? go(Flag<true>{}, Flag<true>{}) : go(Flag<true>{}, Flag<false>{})
-                        : past ? go(Flag<false>{}, Flag<true>{}) : go(Flag<false>{}, Flag<false>{});
+            // 512 threads where a unit has one workgroup (1 x 262144 bf16 top 64 22 us, with 256 35; such rows are
+            // within the caches), 256 where it has several (4096 x 32768 bf16 top 20 57 us, with 512 69)
+            const bool few = n * slices <= 256;
+            const bool past = !few && past_caches(rows, vocab, z);
+            int e = few   ? top ? go(Flag<true>{}, Flag<false>{}, Int<512>{}) : go(Flag<false>{}, Flag<false>{}, Int<512>{})
+                    : top ? past ? go(Flag<true>{}, Flag<true>{}, Int<256>{}) : go(Flag<true>{}, Flag<false>{}, Int<256>{})
+                          : past ? go(Flag<false>{}, Flag<true>{}, Int<256>{}) : go(Flag<false>{}, Flag<false>{}, Int<256>{});
             if (e) return e;
             if (slices == 1) return CKKS_OK;
-            k_join_logprobs<T, MASK><<<dim3((uint32_t)n), SCORE_NT, 0, (hipStream_t)stream>>>(a, slices, parts, keys);
+            k_join_logprobs<T, MASK><<<dim3((uint32_t)n), JOIN_NT, 0, (hipStream_t)stream>>>(a, slices, parts, keys);
             return launched();
         });
     });

@@ -15,6 +15,10 @@ static uint32_t update_dpp(uint32_t none, uint32_t v, int ctrl, int rows) {
     if (from < 0) return host::update_dpp(none, v, ctrl, rows);
     return host::exchange(v, [&](const uint32_t *wave) { return wave[from]; });
 }
+static int shfl_xor(int v, int far) {
+    return (int)host::exchange((uint32_t)v, [&](const uint32_t *wave) { return wave[(threadIdx.x % host::LANES) ^ far]; });
+}
+#define __shfl_xor shfl_xor
 #undef __builtin_amdgcn_update_dpp
 #define __builtin_amdgcn_update_dpp(none, v, ctrl, rows, banks, bound) \
     ((int)update_dpp((uint32_t)(none), (uint32_t)(v), ctrl, rows))
@@ -53,14 +57,12 @@ static void check(const char *what, int vocab, int top, int slices, bool masked,
         blockIdx = {0, y, 0};
         Part *p = slices > 1 ? parts.get() : nullptr;
         uint64_t *k = slices > 1 ? keys.get() : nullptr;
-        done = host::run(SCORE_NT, 20000000, [&] {
-            masked ? k_token_logprobs<float, true, true, false>(a, slice, p, k)
-                   : k_token_logprobs<float, false, true, false>(a, slice, p, k);
-        });
+        done = masked ? host::run(512, 20000000, [&] { k_token_logprobs<float, true, true, false, 512>(a, slice, p, k); })
+                      : host::run(256, 20000000, [&] { k_token_logprobs<float, false, true, false, 256>(a, slice, p, k); });
     }
     blockIdx = {0, 0, 0};
     if (slices > 1 && done)
-        done = host::run(SCORE_NT, 20000000, [&] { k_join_logprobs<float, true>(a, slices, parts.get(), keys.get()); });
+        done = host::run(JOIN_NT, 20000000, [&] { k_join_logprobs<float, true>(a, slices, parts.get(), keys.get()); });
     int bad = !done;
     for (int i = 0; i < top && !bad; i++) bad = tops[i] != (i < (int)want.size() ? want[i] : -1);
     double mass = 0;
@@ -76,7 +78,7 @@ int main() {
     auto rising = [](int i, int) { return i * 1e-3f; };
     auto falling = [](int i, int) { return -i * 1e-3f; };
     // what one group of threads reads is large, and rises: all of it passes the first bound
-    auto group = [](int i, int n) { return i / 8 % 512 < 8 ? 10 + i * 1e-4f : -i * 1e-4f; };
+    auto group = [](int i, int n) { return i / 8 % 256 < 8 ? 10 + i * 1e-4f : -i * 1e-4f; };
     auto lanes = [](int i, int n) { return i / 8 % 8 == 3 ? 10 + i * 1e-4f : -INFINITY; };
     auto few = [](int i, int n) { return i % 1000 == 7 ? 1.0f : -INFINITY; };
     auto none = [](int, int) { return (float)NAN; };
