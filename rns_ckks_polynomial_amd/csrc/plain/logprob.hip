@@ -27,16 +27,25 @@ __device__ __forceinline__ float distance(float z, float largest) { return z == 
 
 constexpr int MAX_SLICES = 32, JOIN_KEYS = MAX_SLICES * CKKS_PLAIN_MAX_TOP;
 
+// A row's given token: its logit (NaN where it is not possible), or none.  Asked for before the row is read: at the
+// end, two loads one after the other took a third of the time between the last logit and the results.
+struct Given {
+    bool there;
+    float logit;
+};
 template <typename T, bool MASK>
-__device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const T *z, const uint8_t *allowed,
-                                          float largest, float log_mass, float mean, float inv_t) {
+__device__ __forceinline__ Given given_token(const ScoreArgs &a, int64_t row, const T *z, const uint8_t *allowed) {
     const int64_t token = a.tokens[row];
-    float lp = 0;
-    if (token >= 0 && token < a.vocab) {
-        const float v = to_f32(z[token]);
-        lp = v > -INFINITY && (!MASK || allowed[token]) ? distance(v, largest) * inv_t - log_mass : -INFINITY;
-    }
-    a.logprob[row] = lp;
+    Given g{token >= 0 && token < a.vocab, NAN};
+    if (g.there) g.logit = to_f32(z[token]);
+    if (MASK && g.there && !allowed[token]) g.logit = NAN;
+    return g;
+}
+__device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const Given &g, float largest, float log_mass,
+                                          float mean, float inv_t) {
+    a.logprob[row] = !g.there                ? 0.0f
+                     : g.logit > -INFINITY ? distance(g.logit, largest) * inv_t - log_mass
+                                             : -INFINITY;
     a.entropy[row] = log_mass > -INFINITY ? log_mass - LN2 * mean : 0.0f;  // mean: of the distances, in powers of two
     a.largest[row] = largest;
     a.log_mass[row] = log_mass;
@@ -122,7 +131,7 @@ __device__ __forceinline__ void put_top(const ScoreArgs &a, int64_t row, int ran
 
 template <int NT> struct ScoreShared {
     uint64_t list[CANDIDATES], bound;  // the list begins as the threads' keys
-    uint32_t slots[NT / 64], more[NT / 64], winners[NT], n_winners, n_readers, n;
+    uint32_t slots[NT / 64], more[NT / 64], ranks[64], winners[NT], n_winners, n_readers, n;
     float sums[2][NT / 64];
 };
 // What a slice of a row leaves for the whole: these and its `top` largest keys, in order.
@@ -199,6 +208,8 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, P
     const int64_t row = a.first + blockIdx.x;
     const T *z = (const T *)a.logits + row * a.stride;
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
+    Given given{};
+    if (!parts) given = given_token<T, MASK>(a, row, z, allowed);
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
     const int begin = blockIdx.y * slice, end = begin + slice < a.vocab ? begin + slice : a.vocab;
     Mass s{-ROOM, 0, 0};
@@ -206,6 +217,7 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, P
     int best_at = 0;
     float next = -INFINITY;  // the largest of the other vectors
     if (t == 0) sh.bound = 1, sh.n_winners = sh.n_readers = sh.n = 0;
+    if (t < 64) sh.ranks[t] = 0;
     // two vectors at a time, the next two on their way
     auto take = [&](const float (&f)[8], int c, const float (&g)[8], int d) {
         const float v = largest_of(f), w = largest_of(g);
@@ -286,20 +298,20 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, P
         if (parts) {
             parts[row * gridDim.y + blockIdx.y] = Part{largest, s.mass, s.moment, 0};
         } else {
-            put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
+            put_score(a, row, given, largest, log_mass, s.moment / s.mass, inv_t);
         }
     }
     if (!TOP) return;
     const uint64_t mine = best > -INFINITY ? token_key(best, best_at + 7) : 0;
     sh.list[t] = mine;
     __syncthreads();
-    if (t < 64) {
-        uint64_t key = 0;  // of the threads t, t + 64, ...: short rows are in all of these groups too
-        for (int w = 0; w < NT / 64; w++) key = Larger{}(key, sh.list[w * 64 + t]);
-        int rank = 0;
-        for (int i = 0; i < 64; i++) rank += lane(key, i) > key;
-        if (rank == a.top - 1 && key) sh.bound = key;
-    }
+    uint64_t key = 0;  // of the threads l, l + 64, ...: short rows are in all of these groups too
+    for (int w = 0; w < NT / 64; w++) key = Larger{}(key, sh.list[w * 64 + (t & 63)]);
+    uint32_t larger = 0;  // a part of the other groups for each wave
+    for (int i = t >> 6; i < 64; i += NT / 64) larger += lane(key, i) > key;
+    atomicAdd(&sh.ranks[t & 63], larger);
+    __syncthreads();
+    if (t < 64 && sh.ranks[t] == (uint32_t)a.top - 1 && key) sh.bound = key;
     const int steps = (end - begin + NT * 8 - 1) / (NT * 8);  // vectors of a thread
     int n;
     for (;;) {
@@ -362,6 +374,7 @@ __global__ __launch_bounds__(JOIN_NT) void k_join_logprobs(ScoreArgs a, int slic
     const T *z = (const T *)a.logits + row * a.stride;
     const uint8_t *allowed = MASK ? a.allowed + row * a.allowed_stride : nullptr;
     const float inv_t = inverse_temperature(a.temperature, row), scale = inv_t * LOG2E;
+    const Given given = given_token<T, MASK>(a, row, z, allowed);
     Part p{-INFINITY, 0, 0, 0};
     if (t < slices) p = parts[row * slices + t];
     for (int i = t; i < slices * a.top; i += JOIN_NT) list[i] = keys[row * slices * a.top + i];
@@ -371,7 +384,7 @@ __global__ __launch_bounds__(JOIN_NT) void k_join_logprobs(ScoreArgs a, int slic
     row_sums<JOIN_NT>(s.mass, s.moment, sums[0], sums[1]);
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
-    if (t == 0) put_score<T, MASK>(a, row, z, allowed, largest, log_mass, s.moment / s.mass, inv_t);
+    if (t == 0) put_score(a, row, given, largest, log_mass, s.moment / s.mass, inv_t);
     if (!a.top) return;
     // Bounds that `top` keys pass: a slice's last, and the least of the slices' keys at a place that makes `top`
     // of them together.
@@ -570,13 +583,15 @@ extern "C" int ckks_plain_token_logprobs(int type, const void *logits, int64_t l
                     <<<grid, NT, 0, (hipStream_t)stream>>>(a, slice, parts, keys);
                 return launched();
             };
-            // 512 threads where a unit has one workgroup (1 x 262144 bf16 top 64 22 us, with 256 35; such rows are
-            // within the caches), 256 where it has several (4096 x 32768 bf16 top 20 57 us, with 512 69)
-            const bool few = n * slices <= 256;
-            const bool past = !few && past_caches(rows, vocab, z);
-            int e = few   ? top ? go(Flag<true>{}, Flag<false>{}, Int<512>{}) : go(Flag<false>{}, Flag<false>{}, Int<512>{})
-                    : top ? past ? go(Flag<true>{}, Flag<true>{}, Int<256>{}) : go(Flag<true>{}, Flag<false>{}, Int<256>{})
-                          : past ? go(Flag<false>{}, Flag<true>{}, Int<256>{}) : go(Flag<false>{}, Flag<false>{}, Int<256>{});
+            // 512 threads where a unit has one workgroup (1 x 262144 bf16 top 64 22 us, with 256 35) and for long rows
+            // (2048 x 131072 bf16 top 20 94 us, with 256 99), 256 for others (4096 x 32768 top 20 56 us, with 512 58;
+            // 4096 x 4001 top 5 22 us, with 512 32)
+            auto go2 = [&](auto alternatives, auto past) {
+                return n * slices <= 256 || slice > 65536 ? go(alternatives, past, Int<512>{}) : go(alternatives, past, Int<256>{});
+            };
+            const bool past = past_caches(rows, vocab, z);
+            int e = top ? past ? go2(Flag<true>{}, Flag<true>{}) : go2(Flag<true>{}, Flag<false>{})
+                        : past ? go2(Flag<false>{}, Flag<true>{}) : go2(Flag<false>{}, Flag<false>{});
             if (e) return e;
             if (slices == 1) return CKKS_OK;
             k_join_logprobs<T, MASK><<<dim3((uint32_t)n), JOIN_NT, 0, (hipStream_t)stream>>>(a, slices, parts, keys);
