@@ -8,6 +8,7 @@ oracle: decryption is host-side here) and, on the GPU again, in clear,
   residual stream + block output, final norm, 8-bit rows  (residual_norm_i8)
   product with the 8-bit vocabulary weights               (matmul_i8)
   temperature, top-k, top-p and a draw                    (sample)
+  entropy and the likeliest alternatives of each draw     (token_logprobs)
 
 Run from the repository's root: python examples/next_token.py
 """
@@ -88,8 +89,9 @@ def main():
     h, rows = plain.residual_norm_i8(dev(x, torch.float32), dev(y, torch.float32), norm)
     logits = plain.matmul_i8(rows, weights, dtype=torch.float32)
     token, logprob = plain.sample(logits, gumbel, each(0.8), top_k=each(40, torch.int32), top_p=each(0.95))
+    scores = plain.token_logprobs(logits, token, top=3, temperature=each(0.8))
     return {"y_error": float(np.abs(y - x * diagonal).max()), "logits": logits, "token": token, "logprob": logprob,
-            "clear_logits": _clear_logits(x, x * diagonal, norm, weights)}
+            "scores": scores, "clear_logits": _clear_logits(x, x * diagonal, norm, weights)}
 
 
 def _clear_logits(x, y, norm, weights):
@@ -105,4 +107,6 @@ if __name__ == "__main__":
     print(f"decrypted block output within {r['y_error']:.1e} of the clear one")
     print(f"logits within {off.max():.3f} of the clear ones (their deviation is {r['clear_logits'].std():.2f})")
     for t in range(TOKENS):
-        print(f"sequence {t}: token {int(r['token'][t])}, log probability {float(r['logprob'][t]):.3f}")
+        others = ", ".join(f"{int(v)} ({float(p):.2f})" for v, p in zip(r["scores"].top_token[t], r["scores"].top_logprob[t]))
+        print(f"sequence {t}: token {int(r['token'][t])}, log probability {float(r['logprob'][t]):.3f}; "
+              f"entropy {float(r['scores'].entropy[t]):.2f}, likeliest: {others}")

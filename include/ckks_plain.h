@@ -136,7 +136,9 @@ typedef struct {
 } ckks_plain_heads;
 
 /* q_out and k_out may be q and k themselves (the same pointer and strides);
- * elements of an output do not share memory. */
+ * elements of an output do not share memory.  Tensors of one token stride whose
+ * tokens lie beside each other (parts of a joint projection's rows) do not
+ * overlap, here and in the gradient. */
 int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_out, int64_t q_out_token_stride,
                                 int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
                                 int64_t k_out_head_stride, void *stream);

@@ -326,13 +326,32 @@ int check_heads(const ckks_plain_heads *p) {
     if (int e = check_side(p, p->q, p->q_heads, q_strides(p), false)) return e;
     return check_side(p, p->k, p->k_heads, k_strides(p), false);
 }
-// an output's range against every input of the call (which: 0 and 1 leave out q or k)
-bool heads_overlap(const ckks_plain_heads *p, const void *out, size_t bytes, int without) {
+// A tensor of heads of a call.
+struct Heads {
+    const void *p;
+    int64_t heads;
+    HeadStrides s;
+};
+// Whether two share memory: their ranges, unless each token of one lies between two tokens of the other (parts of
+// the rows of a joint projection).
+bool share(const ckks_plain_heads *p, const Heads &a, const Heads &b) {
     const size_t z = type_size(p->type);
-    return (without != 0 && overlap(out, bytes, p->q, head_span(p->tokens, p->q_heads, p->head_dim, q_strides(p), z))) ||
-           (without != 1 && overlap(out, bytes, p->k, head_span(p->tokens, p->k_heads, p->head_dim, k_strides(p), z))) ||
-           overlap(out, bytes, p->q_weight, p->head_dim * z) || overlap(out, bytes, p->k_weight, p->head_dim * z) ||
-           overlap(out, bytes, p->positions, p->tokens * 8) || overlap(out, bytes, p->inv_freq, p->rotary / 2 * 4);
+    if (!overlap(a.p, head_span(p->tokens, a.heads, p->head_dim, a.s, z), b.p,
+                 head_span(p->tokens, b.heads, p->head_dim, b.s, z)))
+        return false;
+    const int64_t each = a.s.token, bytes = (const char *)b.p - (const char *)a.p;
+    if (p->tokens < 2 || each != b.s.token || bytes % (int64_t)z) return true;
+    const int64_t off = (bytes / (int64_t)z % each + each) % each;
+    return off < (a.heads - 1) * a.s.head + p->head_dim || off + (b.heads - 1) * b.s.head + p->head_dim > each;
+}
+// An output against every input of the call but itself (in place).
+bool heads_overlap(const ckks_plain_heads *p, const Heads &out) {
+    const Heads in[2] = {{p->q, p->q_heads, q_strides(p)}, {p->k, p->k_heads, k_strides(p)}};
+    for (const Heads &h : in)
+        if (!(h.p == out.p && h.heads == out.heads && same(h.s, out.s)) && share(p, out, h)) return true;
+    const size_t z = type_size(p->type), bytes = head_span(p->tokens, out.heads, p->head_dim, out.s, z);
+    return overlap(out.p, bytes, p->q_weight, p->head_dim * z) || overlap(out.p, bytes, p->k_weight, p->head_dim * z) ||
+           overlap(out.p, bytes, p->positions, p->tokens * 8) || overlap(out.p, bytes, p->inv_freq, p->rotary / 2 * 4);
 }
 
 // Pairs of a vector: as many as 16 bytes hold, or fewer, so that pairs that turn, and all pairs, are whole vectors.
@@ -416,13 +435,9 @@ extern "C" int ckks_plain_head_norm_rotate(const ckks_plain_heads *p, void *q_ou
     if (int e = check_side(p, q_out, p->q_heads, q_out_strides, true)) return e;
     if (int e = check_side(p, k_out, p->k_heads, k_out_strides, true)) return e;
     if (p->tokens == 0) return CKKS_OK;
-    const size_t z = type_size(p->type);
-    const size_t qb = head_span(p->tokens, p->q_heads, p->head_dim, q_out_strides, z);
-    const size_t kb = head_span(p->tokens, p->k_heads, p->head_dim, k_out_strides, z);
-    const bool q_in_place = q_out == p->q && same(q_out_strides, q_strides(p));
-    const bool k_in_place = k_out == p->k && same(k_out_strides, k_strides(p));
-    if (heads_overlap(p, q_out, qb, q_in_place ? 0 : -1) || heads_overlap(p, k_out, kb, k_in_place ? 1 : -1) ||
-        overlap(q_out, qb, k_out, kb))
+    const Heads q{q_out, p->q_heads, q_out_strides}, k{k_out, p->k_heads, k_out_strides};
+    // in place is for the tensor itself: queries over the keys are not
+    if (heads_overlap(p, q) || heads_overlap(p, k) || share(p, q, k) || (q_out && q_out == p->k) || (k_out && k_out == p->q))
         return CKKS_EINVAL;
     const HeadPlan h = head_plan(p, false);
     HeadArgs a = head_args(p, h);
@@ -460,17 +475,29 @@ extern "C" int ckks_plain_head_norm_rotate_grad(const ckks_plain_heads *p, const
     if (int e = check_side(p, g->dk, p->k_heads, dk_strides, false)) return e;
     if (int e = check_side(p, g->dq_in, p->q_heads, dq_in_strides, true)) return e;
     if (int e = check_side(p, g->dk_in, p->k_heads, dk_in_strides, true)) return e;
-    const size_t z = type_size(p->type);
-    const size_t dqb = head_span(p->tokens, p->q_heads, p->head_dim, dq_strides, z);
-    const size_t dkb = head_span(p->tokens, p->k_heads, p->head_dim, dk_strides, z);
-    struct { const void *p; size_t n; } w[5] = {
-        {g->dq_in, head_span(p->tokens, p->q_heads, p->head_dim, dq_in_strides, z)},
-        {g->dk_in, head_span(p->tokens, p->k_heads, p->head_dim, dk_in_strides, z)},
-        {g->q_weight, (size_t)p->head_dim * 4}, {g->k_weight, (size_t)p->head_dim * 4}, {ws, need}};
-    for (int i = 0; i < 5; i++) {
-        if (heads_overlap(p, w[i].p, w[i].n, -1) || overlap(w[i].p, w[i].n, g->dq, dqb) ||
-            overlap(w[i].p, w[i].n, g->dk, dkb))
-            return CKKS_EINVAL;
+    const Heads in[4] = {{p->q, p->q_heads, q_strides(p)}, {p->k, p->k_heads, k_strides(p)},
+                         {g->dq, p->q_heads, dq_strides}, {g->dk, p->k_heads, dk_strides}};
+    const Heads out[2] = {{g->dq_in, p->q_heads, dq_in_strides}, {g->dk_in, p->k_heads, dk_in_strides}};
+    const size_t z = type_size(p->type), row = p->head_dim * z;
+    auto bytes = [&](const Heads &h) { return head_span(p->tokens, h.heads, p->head_dim, h.s, z); };
+    struct { const void *p; size_t n; } w[3] = {{g->q_weight, (size_t)p->head_dim * 4}, {g->k_weight, (size_t)p->head_dim * 4},
+                                                {ws, need}},
+                                        v[4] = {{p->q_weight, row}, {p->k_weight, row}, {p->positions, (size_t)p->tokens * 8},
+                                                {p->inv_freq, (size_t)p->rotary / 2 * 4}};
+    for (const Heads &o : out) {
+        for (const Heads &i : in)
+            if (share(p, o, i)) return CKKS_EINVAL;
+        for (const auto &i : v)
+            if (overlap(o.p, bytes(o), i.p, i.n)) return CKKS_EINVAL;
+    }
+    if (share(p, out[0], out[1])) return CKKS_EINVAL;
+    for (int i = 0; i < 3; i++) {
+        for (const Heads &h : in)
+            if (overlap(w[i].p, w[i].n, h.p, bytes(h))) return CKKS_EINVAL;
+        for (const Heads &h : out)
+            if (overlap(w[i].p, w[i].n, h.p, bytes(h))) return CKKS_EINVAL;
+        for (const auto &x : v)
+            if (overlap(w[i].p, w[i].n, x.p, x.n)) return CKKS_EINVAL;
         for (int j = 0; j < i; j++)
             if (overlap(w[i].p, w[i].n, w[j].p, w[j].n)) return CKKS_EINVAL;
     }

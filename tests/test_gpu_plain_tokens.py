@@ -318,6 +318,21 @@ def test_heads_of_other_strides():
     assert torch.equal(q, want) and torch.equal(x[..., 64:], keep[..., 64:])
 
 
+def test_heads_in_place_in_joint_rows():
+    """Queries and keys of a joint projection over themselves: values between them stay."""
+    T, Q, K, d = 9, 4, 2, 64
+    joint = rnd(53, T, (Q + 2 * K) * d).to(torch.bfloat16).cuda()
+    q, k, v = (joint[:, a * d:b * d].view(T, b - a, d) for a, b in ((0, Q), (Q, Q + K), (Q + K, Q + 2 * K)))
+    pos, freq = torch.arange(T, device="cuda") * 5, torch.tensor([1.0, 0.3], device="cuda")
+    w = (1 + 0.1 * rnd(54, d)).to(torch.bfloat16).cuda()
+    want, old = plain.head_norm_rotate(q, k, pos, freq, w, w), v.clone()
+    p = plain._head_args(q, k, pos, freq, w, w, 1e-6, False)
+    s = joint.stride(0)
+    assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), q.data_ptr(), s, d, k.data_ptr(), s, d,
+                                                 torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, old)
+
+
 def test_heads_that_are_zero_or_not_finite():
     q, k, pos, freq, qw, kw = head_inputs(61, 4, 3, 1, 64, 32, "f32")
     q, k = q.clone(), k.clone()

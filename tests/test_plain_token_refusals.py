@@ -109,6 +109,29 @@ def test_heads_outputs(out, code):
     assert nat.lib().ckks_plain_head_norm_rotate(C.byref(p), *out, None) == code
 
 
+def test_heads_beside_each_other_in_rows():
+    """Parts of joint rows are apart where no element is shared, and not where one is (no tokens: nothing is launched;
+    the pairs of ranges are looked at for two tokens and more, so by way of an error behind them: a workspace)."""
+    lib = nat.lib()
+    row = 8 * D * 2  # bytes of a token of 4 + 2 + 2 heads
+    joint = dict(q=X, k=X + 4 * D * 2, **at("q", 8 * D, D), **at("k", 8 * D, D))
+    p = heads(**joint)
+    def grad(dq_in, dk_in, token=8 * D, **kw):
+        g = nat.PlainHeadGrads(**{**HG, "dq_in": dq_in, "dk_in": dk_in, **at("dq_in", token, D), **at("dk_in", token, D), **kw})
+        return lib.ckks_plain_head_norm_rotate_grad(C.byref(p), C.byref(g), None, 0, None)
+    assert grad(H, H + 4 * D * 2) == WS                      # apart
+    assert grad(H + 4 * D * 2, H) == WS                      # the other way round
+    assert grad(H + 5 * D * 2, H) == INV                     # the queries' heads reach into the next token's keys
+    assert grad(H, H + 3 * D * 2) == INV                     # the last query head is the first key
+    assert grad(H, H + 7 * D * 2) == INV                     # the second key is the next token's first query
+    assert grad(H, H + 4 * D * 2 + 5 * row) == WS            # rows further on
+    assert grad(H + 5 * row, H + 4 * D * 2) == WS
+    assert grad(X + 6 * D * 2, U) == INV                     # over the next token's queries
+    # forward, into the values' place and over the other tensor
+    call = lambda q, k: lib.ckks_plain_head_norm_rotate(C.byref(p), q, 8 * D, D, k, 8 * D, D, None)  # noqa: E731
+    assert call(X, X) == INV and call(X + 4 * D * 2, U) == INV and call(H, X) == INV and call(X, X + 2 * D * 2) == INV
+
+
 HG = dict(dq=X + (1 << 27), dk=Y + (1 << 27), **at("dq", 4 * D, D), **at("dk", 2 * D, D), dq_in=H, dk_in=U,
           **at("dq_in", 4 * D, D), **at("dk_in", 2 * D, D), q_weight=Q, k_weight=Q + 4096)
 
