@@ -117,11 +117,12 @@ int ckks_plain_residual_norm_grad(const ckks_plain_norm *p, const ckks_plain_nor
  *   (a, b) = (i, i + rotary / 2), or (2 i, 2 i + 1) if interleaved; from
  *   rotary on, y = n.
  * Element (t, h, i) of a tensor is at t token_stride + h head_stride + i, both
- * strides at least head_dim where there is more than one token or head.  head_dim and rotary are even, rotary <= head_dim <=
- * CKKS_PLAIN_MAX_HEAD.  positions [tokens] and inv_freq [rotary / 2] may be
- * NULL where rotary is 0; the angle's product and its turns are held in 64
- * bits, its sine and cosine in 32.  k_heads = 0: queries alone (k and k_weight
- * NULL).  Weights have the type of q and k. */
+ * strides at least head_dim where there is more than one token or head.
+ * head_dim and rotary are even, rotary <= head_dim <= CKKS_PLAIN_MAX_HEAD.
+ * positions [tokens] and inv_freq [rotary / 2] may be NULL where rotary is 0;
+ * the angle's product and its turns are held in 64 bits, its sine and cosine
+ * in 32.  k_heads = 0: queries alone (k and k_weight NULL).  Weights have the
+ * type of q and k. */
 #define CKKS_PLAIN_MAX_HEAD 512
 typedef struct {
     int type; /* CKKS_PLAIN_BF16, _F16 or _F32 */

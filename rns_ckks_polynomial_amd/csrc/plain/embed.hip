@@ -4,8 +4,8 @@
 namespace ckks_plain {
 
 // Elements of a vector of types T and O: 16 bytes of the wider, so that neighbouring lanes' accesses join to
-// whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction: the table's
-// gradient in f32 97 us, so ...).
+// whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction: the gradient of
+// 16384 rows bf16 into 32768 x 2048 f32 119 us, so 67).
 template <typename T, typename O> constexpr int JOINT = 16 / (int)(sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
 
 // out[t] = scale table[tokens[t]], 2^log_l threads a row, the rest of 256 threads on other rows.  Bound by memory:
@@ -51,7 +51,8 @@ constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 // A workgroup has 2^log_bins tokens of the vocabulary and reads all rows' tokens itself, so nothing is joined
 // between workgroups and one launch does: wave w counts those of its part of the rows, and after a sum over
 // waves and bins puts its rows where they belong, in order.  The tokens of up to HELD * 64 rows a wave stay in
-// registers in between.
+// registers in between.  Latency: 16384 tokens of 32768 10 us, 8191 of 20011 8 us, about 3 us of them until the tokens
+// are there and 4 in the second pass, where the rows of a wave that belong here take turns.
 constexpr int HELD = 16;
 constexpr uint32_t NONE = ~0u;
 struct TokenOrder {
@@ -235,8 +236,8 @@ __device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, in
 // zeros of tokens that do not occur first, which wait for nothing), or with ADD for a place of the order, the first of
 // its token.
 //
-// Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 47 us for 335 MB (7.1 TB/s, past the
-// caches), behind 11 us of order and in front of 5 us of long runs.  E elements a thread: 16 spare rows of just over
+// Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 52 us for 335 MB (6.5 TB/s, past the
+// caches), behind 10 us of order and in front of 6 us of long runs.  E elements a thread: 16 spare rows of just over
 // 2048 columns a second turn for the rest (4000 x 8191 bf16 75 us, with 8 99), 8 are faster for narrower ones (4096 x
 // 64 19 us, with 16 22).  Two rows of the table where they are short: 8191 rows f16 into 20011 x 2051 40.5 us, with one
 // 44; 16384 rows bf16 into 32768 x 2048 f32 70.6 us, with one 66.4.
@@ -278,19 +279,19 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, 
     }
 }
 
-// The long run that starts in chunk blockIdx.x, if there is one: 512 columns (blockIdx.y), 16 waves on its
-// parts in turn, then their sums in order.
+// The long run that starts in chunk blockIdx.y, if there is one: 512 columns (blockIdx.x), 16 waves on its
+// parts in turn, then their sums in order.  Latency, 4.6 to 6 us: a launch, and four loads that wait for each other.
 constexpr int JOIN_COLS = 512;
 template <typename O, bool ADD>
 __global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_t out_stride) {
     __shared__ float sh[16][JOIN_COLS];
-    const int64_t j = blockIdx.x, n = s.starts[s.vocab], from = j * s.chunk;
+    const int64_t j = blockIdx.y, n = s.starts[s.vocab], from = j * s.chunk;
     const int64_t to = from + s.chunk < n ? from + s.chunk : n;
     if (from >= to) return;
     const int64_t v = s.token_of[to - 1], a = s.starts[v], b = s.starts[v + 1];
     if (b - a <= s.chunk || a < from) return;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.y * JOIN_COLS + l * 4, last = (b - 1) / s.chunk;
+    const int64_t c = (int64_t)blockIdx.x * JOIN_COLS + l * 4, last = (b - 1) / s.chunk;
     float f[8] = {};
     for (int64_t k = j + wave; k <= last; k += 16) {
         const float *part = s.parts + (2 * k + (k == j && a > from)) * s.cols;
@@ -303,7 +304,7 @@ __global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_
 #pragma unroll
     for (int i = 0; i < 8; i++) sh[wave][i / 4 * 256 + l * 4 + i % 4] = f[i];
     __syncthreads();
-    const int64_t mine = (int64_t)blockIdx.y * JOIN_COLS + threadIdx.x;
+    const int64_t mine = (int64_t)blockIdx.x * JOIN_COLS + threadIdx.x;
     if (threadIdx.x >= JOIN_COLS || mine >= s.cols) return;
     float sum = 0;
     for (int w = 0; w < 16; w++) sum += sh[w][threadIdx.x];
@@ -481,7 +482,8 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
                 else  // 8 elements: rows of 4 KB at most
                     e = share == 8 ? sum(Int<8>{}, Int<2>{}) : two ? sum(Int<16>{}, Int<2>{}) : sum(Int<16>{}, Int<1>{});
                 if (e || !p.chunks) return e;
-                k_embed_join<O, ADD><<<dim3((uint32_t)p.chunks, (uint32_t)((cols + JOIN_COLS - 1) / JOIN_COLS)), 1024,
+                // chunks, at most 2048, as the dimension of few
+                k_embed_join<O, ADD><<<dim3((uint32_t)((cols + JOIN_COLS - 1) / JOIN_COLS), (uint32_t)p.chunks), 1024,
                                        0, s>>>(a, (O *)out, out_stride);
                 return launched();
             };

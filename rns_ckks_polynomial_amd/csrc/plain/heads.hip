@@ -153,6 +153,9 @@ __device__ __forceinline__ void each_head(const HeadArgs &a, int heads, int64_t 
     }
 }
 
+// A head is read once, into registers, and its sum goes over its own lanes: no barrier but those around the angles, which
+// all heads of a token share.  Bound by memory: 8192 tokens of 32 + 8 heads of 128 bf16 34.5 us for 168 MB that no cache
+// has (4.9 TB/s, as a copy).  Four tokens 3.5 us: latency.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void k_head_norm_rotate(HeadArgs a) {
     typedef Head<T, V, K> H;
@@ -189,7 +192,8 @@ __global__ __launch_bounds__(256) void k_head_norm_rotate(HeadArgs a) {
 }
 
 // dn: dy turned back.  With a weight: dx = r (a - hat mean(a hat)), a = dn weight, hat = x r; the weight's
-// sum of dn hat over a workgroup's heads leaves as one row of partial sums.
+// sum of dn hat over a workgroup's heads leaves as one row of partial sums.  Bound by memory: 8192 tokens of 32 + 8 heads
+// of 128 bf16 56 us for 252 MB (4.5 TB/s), and 4.6 us for the sums of the partial sums.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void k_head_grad(HeadArgs a) {
     typedef Head<T, V, K> H;
@@ -395,13 +399,14 @@ HeadPlan head_plan(const ckks_plain_heads *p, bool grad) {
     });
     const int64_t groups = 256 >> h.log_l;
     // A step of so many tokens that all threads work out angles, and each takes a few heads behind the next's loads:
-    // 8192 tokens of 32 + 8 heads of 128 bf16 29 us in steps of four, 39 one by one.  Short ones where there are few
-    // tokens (two workgroups a unit come first), and at most 8 KB of angles.
+    // 8192 tokens of 32 + 8 heads of 128 bf16 in a loop 29 us in steps of four, 39 one by one (gradient 54 and 62).
+    // Short ones where there are few tokens (two workgroups a unit come first), and at most 8 KB of angles.
     const int64_t one = p->q_heads < groups ? groups / p->q_heads : 1;
     h.step = (int)one;
     while (h.step < 4 * one && h.step * p->rotary <= 1024 && p->tokens >= 1024 * (int64_t)h.step) h.step *= 2;
     // The gradient's workgroups each leave a row of partial sums: as many as run at a time (with vectors of 16-bit
-    // pairs 128 registers leave room for four a unit, of both sides; other forms have fewer).
+    // pairs the registers leave room for four a unit, of both sides: that gradient 54 us, with 256 a side 68, with
+    // 1024 55; other forms have fewer registers).
     const int64_t most = !grad ? 1 << 22 : wide ? 512 : 1024;  // workgroups of a side
     h.span = (int)((p->tokens + most * h.step - 1) / (most * h.step) * h.step);
     if (h.span < h.step) h.span = h.step;

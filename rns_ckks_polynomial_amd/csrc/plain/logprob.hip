@@ -136,7 +136,7 @@ template <int NT> struct ScoreShared {
 };
 // What a slice of a row leaves for the whole: these and its `top` largest keys, in order.
 struct Part {
-    float m, mass, moment, unused;
+    float m, mass, moment, unused;  // 16 bytes: the keys behind the parts are aligned
 };
 
 // The rank of a key of sh.list: how many of its first n are larger.
@@ -166,7 +166,7 @@ __device__ __forceinline__ uint64_t join_waves(uint64_t v, uint64_t reversed, in
     return sort_halves(v > reversed ? v : reversed, l, 64, 32);
 }
 // The largest 64 of the list's first n, falling, at its front (behind the last: 0).  All threads; ends behind a barrier.
-// (A rank by comparison with all n costs as many reads for each: 4096 x 1000 bf16 top 64 450 us, so ...)
+// (A rank by comparison with all n costs as many reads for each: 4096 x 1000 bf16 top 64 450 us, so 34.)
 template <int NT> __device__ __forceinline__ void sort_list(uint64_t *list, int n) {
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     uint64_t v = 0;
@@ -196,10 +196,17 @@ template <int NT> __device__ __forceinline__ void sort_list(uint64_t *list, int 
 // at least one token is not below it.  The top-th largest of the keys of 64 groups of threads is a bound which
 // at least `top` tokens pass; they are all among the tokens of threads whose largest logit passes it from its
 // vector's start (`winners`, little more than `top`).  Such a thread's vector is read again, and its others where
-// the largest of them may pass too (all of them would be lines of memory: 2048 x 131072 bf16 top 20 117 us, so 107).
+// the largest of them may pass too (all of them would be lines of memory: 2048 x 131072 bf16 top 20 120 us, so 96).
 // What passes goes on a list, and a token's rank there is its place.  Where the list is too short (runs of equal
 // logits, rows in bad order), the top-th largest on it is a better bound: all that were on it below that one do not
 // come back, so it ends.
+//
+// 2048 x 131072 bf16 top 20 takes 96 us in a loop, 100 on logits that no cache has (5.6 and 5.4 TB/s; reading alone
+// reaches 6.1): memory, with the vector units busy for 70 % of it, and 5 us of choosing at the rows' ends.  Without
+// alternatives 4096 x 32768 bf16 49 us (5.5 TB/s).  Few rows are latency: 4 x 32768 f32 top 5 7.5 us, 333 x 50021 f16
+// top 20 under a mask 21.5 us for 50 MB.  The next two vectors are on their way while two are added; four or six on
+// their way were no faster (2048 x 131072 95 and 97 us, 333 x 50021 15.6 and 15.9 instead of 15.0, 1000 x 16384 9.0 and
+// 9.1 instead of 8.4).
 constexpr float ROOM = 0x1p20f;
 template <typename T, bool MASK, bool TOP, bool STREAM, int NT>
 __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {
@@ -427,7 +434,8 @@ struct ScoreGradArgs {
 // A piece of a row for a workgroup, GRAD_EACH vectors a thread.  With lp = ln 2 x, x = z A - B,
 //   dz = p (c0 + c1 x) + [token] dlogprob / temperature,  p = 2^x,
 // of which a row's constants are worked out first (B in 64 bits; what its rounding to 32 leaves is in c0 and c1).
-// Where they have no room, x comes from distances as above.
+// Where they have no room, x comes from distances as above.  Bound by memory: 4096 x 32768 bf16 88 us for 537 MB (6.1
+// TB/s, past the caches); 333 x 50021 f16 under a mask 18 us for 83 MB, in rows that start at odd elements.
 constexpr int GRAD_EACH = 4, GRAD_PIECE = 256 * 8 * GRAD_EACH;
 template <typename T, bool MASK, bool STREAM>
 __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, int64_t last, uint32_t pieces) {
@@ -498,12 +506,13 @@ int check_score(int64_t rows, int64_t vocab) {
     if (rows < 0 || rows >= (int64_t)1 << 31 || vocab < 1) return CKKS_EINVAL;
     return vocab > (int64_t)1 << 24 ? CKKS_EUNSUPPORTED : CKKS_OK;
 }
-// Logits that the last-level cache (256 MB) does not hold beside their gradient go past the caches: 4096 x 32768
-// bf16 with its gradient 130 us, so, else 141 to 149; 512 x 32768 f32 43 us, else 41.
+// Logits that the last-level cache (256 MB) does not hold beside their gradient go past the caches (log probabilities
+// and gradient: 4096 x 32768 bf16 132 us, else 152; 1024 x 131072 134, else 152); others do not (512 x 32768 f32 40 us,
+// past the caches 42; 333 x 50021 f16 under a mask 34, past them 38).
 bool past_caches(int64_t rows, int64_t vocab, size_t size) { return rows * vocab * (int64_t)size > (int64_t)128 << 20; }
 // Slices of a row: a workgroup for each compute unit where there are few rows, none of less than 32768 logits
-// (16 x 131072 bf16 top 20: 13.7 us with four slices, 15.0 with one, 19.3 with 16; 4 x 32768 f32 top 5: 8.1 us, with
-// four 10.9; 200 x 131072: 15.5 us, with two 19.9).
+// (16 x 131072 bf16 top 20: 13.7 us with four slices, 15.0 with one, 19.3 with 16; 4 x 32768 f32 top 5: 7.5 us, with
+// four about 11; 200 x 131072: 15.5 us, with two 19.9).
 int64_t score_slices(int64_t rows, int64_t vocab) {
     const int64_t most = vocab / 32768, want = rows ? 256 / rows : 1;
     const int64_t n = want < most ? want : most;
@@ -584,8 +593,8 @@ extern "C" int ckks_plain_token_logprobs(int type, const void *logits, int64_t l
                 return launched();
             };
             // 512 threads where a unit has one workgroup (1 x 262144 bf16 top 64 22 us, with 256 35) and for long rows
-            // (2048 x 131072 bf16 top 20 94 us, with 256 99), 256 for others (4096 x 32768 top 20 56 us, with 512 58;
-            // 4096 x 4001 top 5 22 us, with 512 32)
+            // (2048 x 131072 bf16 top 20 96 us, with 256 99), 256 for others (512 x 32768 top 5 11 us, with 512 12;
+            // 1000 x 32768 top 20 17.7 us, with 512 20.8; 4096 x 4001 top 5 22 us, with 512 32)
             auto go2 = [&](auto alternatives, auto past) {
                 return n * slices <= 256 || slice > 65536 ? go(alternatives, past, Int<512>{}) : go(alternatives, past, Int<256>{});
             };

@@ -185,6 +185,14 @@ def test_embed_grad_of_many_tokens(kind):
     check_embed_grad(70001, 140001, 8, "f32", "f32", kind)
 
 
+def test_embed_grad_of_the_widest_rows():
+    """A long run of rows of more than 65536 * 512 columns; sums of small integers are exact."""
+    D = 65536 * 512 + 5
+    d = (torch.arange(D, dtype=torch.int32, device="cuda") % 5)[None] + torch.arange(33, dtype=torch.int32, device="cuda")[:, None]
+    got = plain.embed_grad(d.half(), torch.ones(33, dtype=torch.int64, device="cuda"), 2)
+    assert not got[0].any() and torch.equal(got[1].int(), d.sum(0, dtype=torch.int32))
+
+
 def test_embed_grad_does_not_mix_what_is_not_finite():
     T, V, D = 600, 20, 64
     t = on_gpu(tokens_of("uniform", T, V), torch.int64)
@@ -595,6 +603,19 @@ def test_token_logprobs_agree_with_sample():
     assert (r.logprob[ok] - logprob[ok]).abs().max() < 2 * (V / 256 + 224) * EPS
     greedy = ~(t > 0) & ok
     assert greedy.any() and torch.equal(r.top_token[greedy, 0], token[greedy])
+
+
+def test_the_examples_scores():
+    """examples/next_token.py: the draws' log probabilities from both operators, and the likeliest in front."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import next_token
+    r = next_token.main()
+    s = r["scores"]
+    assert (s.logprob - r["logprob"]).abs().max() < 2 * (next_token.VOCAB / 256 + 224) * EPS  # as above
+    assert torch.equal(s.top_token[:, 0], r["logits"].argmax(1)) and (s.top_logprob.diff(dim=1) <= 0).all()
+    assert (s.entropy > 0).all() and (s.logprob <= s.top_logprob[:, 0]).all()
 
 
 def test_token_logprobs_grad_against_differences():
