@@ -5,7 +5,7 @@ namespace ckks_plain {
 
 // Elements of a vector of types T and O: 16 bytes of the wider, so that neighbouring lanes' accesses join to
 // whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction: the gradient of
-// 16384 rows bf16 into 32768 x 2048 f32 119 us, so 67).
+// 16384 rows bf16 into 32768 x 2048 f32 119 us where this took 67).
 template <typename T, typename O> constexpr int JOINT = 16 / (int)(sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
 
 // out[t] = scale table[tokens[t]], 2^log_l threads a row, the rest of 256 threads on other rows.  Bound by memory:
@@ -49,11 +49,12 @@ constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 // places; starts[v]: how many of them have a token below v (v <= vocab).
 //
 // A workgroup has 2^log_bins tokens of the vocabulary and reads all rows' tokens itself, so nothing is joined
-// between workgroups and one launch does: wave w counts those of its part of the rows, and after a sum over
-// waves and bins puts its rows where they belong, in order.  The tokens of up to HELD * 64 rows a wave stay in
-// registers in between.  Latency: 16384 tokens of 32768 10 us, 8191 of 20011 8 us, about 3 us of them until the tokens
-// are there and 4 in the second pass, where the rows of a wave that belong here take turns.
-constexpr int HELD = 16;
+// between workgroups and one launch does: wave w counts those of its part of the rows and lists its own (up to
+// LISTED of them; where there are more, the part is read again), and after a sum over waves and bins puts its rows
+// where they belong, in order.  Latency: 16384 tokens of 32768 8.5 us, 8191 of 20011 6.3 us (a launch, the tokens at four
+// loads a turn, five barriers).  It is short code on purpose: with all of a wave's tokens in registers, and so a copy of
+// the loops' bodies for each, 9.9 and 7.9 us, most of the difference to fetch the instructions.
+constexpr int FETCHED = 4, LISTED = 512;
 constexpr uint32_t NONE = ~0u;
 struct TokenOrder {
     int32_t *order, *token_of, *starts;
@@ -62,30 +63,42 @@ __device__ __forceinline__ uint32_t token_at(const int64_t *tokens, int64_t i, i
     const int64_t v = i < last ? tokens[i] : -1;
     return v >= 0 && v < vocab ? (uint32_t)v : NONE;
 }
+// a lane's place among the lanes of a mask
+__device__ __forceinline__ uint32_t place_in(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
 __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens, int64_t rows, int64_t vocab,
                                                           int log_bins, TokenOrder o) {
     extern __shared__ uint32_t places[];  // [wave][bin]: counts, then the next place
+    __shared__ uint32_t listed[ORDER_WAVES][LISTED];  // rows of the wave's part
+    __shared__ uint16_t listed_bin[ORDER_WAVES][LISTED];
     __shared__ uint32_t buf[ORDER_WAVES], sums[ORDER_WAVES], ends[ORDER_WAVES];
     const uint32_t bins = 1u << log_bins, wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     const uint32_t low = blockIdx.x << log_bins;
     const int64_t part = (rows + ORDER_NT - 1) / ORDER_NT * 64;
     const int64_t first = wave * part, last = first + part < rows ? first + part : rows;
-    const int64_t step = HELD * 64;
     uint32_t *mine = places + (wave << log_bins);
     for (uint32_t i = threadIdx.x; i < ORDER_WAVES << log_bins; i += ORDER_NT) places[i] = 0;
     __syncthreads();
-    uint32_t below = 0, all = 0, v[HELD];
-    auto fetch = [&](int64_t from) {
+    uint32_t below = 0, all = 0, found = 0;
+    for (int64_t i = first; i < last; i += FETCHED * 64) {
+        uint32_t v[FETCHED];
 #pragma unroll
-        for (int k = 0; k < HELD; k++) v[k] = token_at(tokens, from + k * 64 + l, last, vocab);
-    };
-    for (int64_t i = first; i < last; i += step) {
-        fetch(i);
+        for (int k = 0; k < FETCHED; k++) v[k] = token_at(tokens, i + k * 64 + l, last, vocab);
 #pragma unroll
-        for (int k = 0; k < HELD; k++) {
+        for (int k = 0; k < FETCHED; k++) {
             below += v[k] < low;
             all += v[k] != NONE;
-            if (v[k] - low < bins) atomicAdd(&mine[v[k] - low], 1u);
+            const uint32_t bin = v[k] - low;
+            const bool in = bin < bins;  // not NONE: low + bins is at most 2^24 + 2^9
+            const uint64_t mask = __ballot(in);
+            if (!mask) continue;
+            if (in) {
+                const uint32_t at = found + place_in(mask);
+                atomicAdd(&mine[bin], 1u);
+                if (at < LISTED) listed[wave][at] = (uint32_t)(i + k * 64 + l), listed_bin[wave][at] = (uint16_t)bin;
+            }
+            found += (uint32_t)__popcll(mask);
         }
     }
     below = row_all<ORDER_NT>(below, buf, Sum{});  // its barrier ends the counting
@@ -109,26 +122,34 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
         }
     }
     __syncthreads();
-    for (int64_t i = first; i < last; i += step) {
-        if (part > step) fetch(i);
-#pragma unroll
-        for (int k = 0; k < HELD; k++) {
-            const uint32_t bin = v[k] - low;
-            const bool in = bin < bins;  // NONE: low + bins is at most 2^24 + 2^9
-            for (uint64_t left = __ballot(in); left;) {  // one token of the wave's at a time
-                const int leader = __ffsll((unsigned long long)left) - 1;
-                const uint32_t b = lane(bin, leader), place = mine[b];
-                const uint64_t same = __ballot(in && bin == b);
-                if (in && bin == b) {
-                    const uint32_t to = place + __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32),
-                                                                          __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
-                    o.order[to] = (int32_t)(i + k * 64 + l);
-                    o.token_of[to] = (int32_t)v[k];
-                }
-                if (l == (uint32_t)leader) mine[b] = place + (uint32_t)__popcll(same);
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's other lanes read it next
-                left &= ~same;
-            }
+    // up to 64 rows of the wave at a time: a lane goes behind the lanes before it that have its token
+    auto put = [&](bool in, uint32_t bin, int64_t row) {
+        const uint32_t place = in ? mine[bin] : 0;
+        uint64_t same = __ballot(in);
+        if (!same) return;
+        for (int bit = 0; bit < log_bins; bit++) {
+            const uint64_t ones = __ballot(bin >> bit & 1);
+            same &= bin >> bit & 1 ? ones : ~ones;
+        }
+        if (in) {
+            const uint32_t before = place_in(same);
+            o.order[place + before] = (int32_t)row;
+            o.token_of[place + before] = (int32_t)(low + bin);
+            if (before == 0) mine[bin] = place + (uint32_t)__popcll(same);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's other lanes read them next
+    };
+    if (found <= LISTED) {
+        for (uint32_t i = 0; i < found; i += 64) {
+            const bool in = i + l < found;
+            put(in, in ? listed_bin[wave][i + l] : 0, in ? listed[wave][i + l] : 0);
+        }
+    } else {
+        uint32_t next = token_at(tokens, first + l, last, vocab);
+        for (int64_t i = first; i < last; i += 64) {
+            const uint32_t bin = next - low;
+            next = token_at(tokens, i + 64 + l, last, vocab);
+            put(bin < bins, bin, i + l);
         }
     }
 }
@@ -136,12 +157,14 @@ __global__ __launch_bounds__(ORDER_NT) void k_token_order(const int64_t *tokens,
 // What the sums go by: order and starts above; a run is the rows of one token, in order.  Runs of more
 // than `chunk` rows are cut where a multiple of it falls: a chunk's part of such a run is summed into
 // parts[2 chunk] if the run holds the chunk's first place, else into parts[2 chunk + 1] (it is long, so
-// it holds the first or the last), and k_embed_join adds up the parts.
+// it holds the first or the last), and k_embed_join adds up the parts.  runs[chunk]: the token whose long run begins
+// there, or -1.
 struct EmbedSums {
     const int32_t *order, *token_of, *starts;
     int64_t rows, vocab, cols, chunk;
     float scale;
     float *parts;
+    int32_t *runs;
 };
 
 // A thread's share of a row, E elements: the columns of its vectors of V.
@@ -169,7 +192,7 @@ template <typename T, int V, int E> struct Share {
 #pragma unroll
             for (int j = 0; j < V; j++) f[n][j] += e[n].at(j);
     }
-    // scale f [+ what is there]; stores of a whole table go past the caches: 268 MB in 52 us, else 70; 16 MB as fast
+    // scale f [+ what is there]; stores of a whole table go past the caches: 268 MB in 48 us, else 66 (with what it reads); 16 MB as fast
     // either way
     template <bool ADD>
     static __device__ __forceinline__ void put(T *row, const Columns<V, E> &c, float scale, float (&f)[N][V]) {
@@ -217,8 +240,16 @@ template <typename T>
 __device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, int64_t stride, int64_t j) {
     constexpr int V = JOINT<T, float>;
     const int64_t from = j * s.chunk, n = s.starts[s.vocab], to = from + s.chunk < n ? from + s.chunk : n;
-    if (from >= to) return;
+    const bool first_columns = blockIdx.y == 0 && threadIdx.x == 0;
+    if (from >= to) {
+        if (first_columns) s.runs[j] = -1;
+        return;
+    }
     const int64_t va = s.token_of[from], vb = s.token_of[to - 1];
+    if (first_columns) {
+        const int64_t a = s.starts[vb], b = s.starts[vb + 1];
+        s.runs[j] = b - a > s.chunk && a >= from ? (int32_t)vb : -1;
+    }
     for (int k = 0; k < (va == vb ? 1 : 2); k++) {
         const int64_t v = k ? vb : va, a = s.starts[v], b = s.starts[v + 1];
         if (b - a <= s.chunk) continue;
@@ -236,11 +267,12 @@ __device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, in
 // zeros of tokens that do not occur first, which wait for nothing), or with ADD for a place of the order, the first of
 // its token.
 //
-// Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 52 us for 335 MB (6.5 TB/s, past the
-// caches), behind 10 us of order and in front of 6 us of long runs.  E elements a thread: 16 spare rows of just over
-// 2048 columns a second turn for the rest (4000 x 8191 bf16 75 us, with 8 99), 8 are faster for narrower ones (4096 x
-// 64 19 us, with 16 22).  Two rows of the table where they are short: 8191 rows f16 into 20011 x 2051 40.5 us, with one
-// 44; 16384 rows bf16 into 32768 x 2048 f32 70.6 us, with one 66.4.
+// Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 48 us for 335 MB (6.9 TB/s, past the
+// caches), behind 8.5 us of order and in front of 6.7 us of long runs.  E elements a thread: 16 spare rows of just over
+// 2048 columns a second turn for the rest (8191 rows f16 into 20011 x 2051 35.6 us, with 8 42.5), 8 are faster for
+// narrower ones (4096 into 32768 x 64 f32 15.2 us, with 16 16.9; 16384 into 32768 x 2048 f32 63, with 16 70).  Two rows
+// of the table where they are short: 8191 rows f16 into 20011 x 2051 35.6 us, with one 40.6; 8192 bf16 into 32768 x 1024
+// 28.1, with one 29.6; 16384 bf16 into 32768 x 2048 f32 71.0 us, with one 63.2.
 template <typename T, typename O, bool ADD, int E, int ROWS>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, int64_t stride, O *out,
                                                    int64_t out_stride, int64_t from, int64_t chunks, int log_l) {
@@ -279,35 +311,43 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, 
     }
 }
 
-// The long run that starts in chunk blockIdx.y, if there is one: 512 columns (blockIdx.x), 16 waves on its
-// parts in turn, then their sums in order.  Latency, 4.6 to 6 us: a launch, and four loads that wait for each other.
+// The long run that begins in chunk blockIdx.y, if there is one: 512 columns (blockIdx.x), eight waves on its
+// parts in turn, then their sums in order.  Latency, 4.1 to 6.7 us: a launch and three loads that wait for each other,
+// and the parts of the longest run (with 16 waves, and each workgroup to find out whether a run begins, 10 us).
 constexpr int JOIN_COLS = 512;
 template <typename O, bool ADD>
-__global__ __launch_bounds__(1024) void k_embed_join(EmbedSums s, O *out, int64_t out_stride) {
-    __shared__ float sh[16][JOIN_COLS];
-    const int64_t j = blockIdx.y, n = s.starts[s.vocab], from = j * s.chunk;
-    const int64_t to = from + s.chunk < n ? from + s.chunk : n;
-    if (from >= to) return;
-    const int64_t v = s.token_of[to - 1], a = s.starts[v], b = s.starts[v + 1];
-    if (b - a <= s.chunk || a < from) return;
+__global__ __launch_bounds__(JOIN_COLS) void k_embed_join(EmbedSums s, O *out, int64_t out_stride) {
+    constexpr int WAVES = JOIN_COLS / 64;
+    __shared__ float sh[WAVES][JOIN_COLS];
+    const int64_t j = blockIdx.y, v = s.runs[j];
+    if (v < 0) return;
+    const int64_t a = s.starts[v], b = s.starts[v + 1], from = j * s.chunk;
     const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
     const int64_t c = (int64_t)blockIdx.x * JOIN_COLS + l * 4, last = (b - 1) / s.chunk;
     float f[8] = {};
-    for (int64_t k = j + wave; k <= last; k += 16) {
-        const float *part = s.parts + (2 * k + (k == j && a > from)) * s.cols;
-        Piece<float, 4> e[2];
+    for (int64_t k = j + wave; k <= last; k += 2 * WAVES) {
+        Piece<float, 4> e[2][2];
 #pragma unroll
-        for (int i = 0; i < 2; i++) e[i].fetch(part + c + i * 256, s.cols - c - i * 256);
+        for (int p = 0; p < 2; p++) {
+            const int64_t q = k + p * WAVES;
+            const float *part = s.parts + (2 * q + (q == j && a > from)) * s.cols;
+            if (q <= last)
 #pragma unroll
-        for (int i = 0; i < 8; i++) f[i] += e[i / 4].at(i % 4);
+                for (int i = 0; i < 2; i++) e[p][i].fetch(part + c + i * 256, s.cols - c - i * 256);
+        }
+#pragma unroll
+        for (int p = 0; p < 2; p++)
+            if (k + p * WAVES <= last)
+#pragma unroll
+                for (int i = 0; i < 8; i++) f[i] += e[p][i / 4].at(i % 4);
     }
 #pragma unroll
     for (int i = 0; i < 8; i++) sh[wave][i / 4 * 256 + l * 4 + i % 4] = f[i];
     __syncthreads();
     const int64_t mine = (int64_t)blockIdx.x * JOIN_COLS + threadIdx.x;
-    if (threadIdx.x >= JOIN_COLS || mine >= s.cols) return;
+    if (mine >= s.cols) return;
     float sum = 0;
-    for (int w = 0; w < 16; w++) sum += sh[w][threadIdx.x];
+    for (int w = 0; w < WAVES; w++) sum += sh[w][threadIdx.x];
     O *p = out + v * out_stride + mine;
     *p = from_f32<O>((ADD ? to_f32(*p) : 0.0f) + sum * s.scale);
 }
@@ -369,15 +409,17 @@ int log_bins(int64_t vocab) {
     while (b < 9 && ((int64_t)256 << b) < vocab) b++;
     return b;
 }
-// Rows of a chunk: at most 2048 chunks.
+// Rows of a chunk: at most 2048 chunks.  Long runs are read by as many workgroups as they have chunks, and their parts
+// by fewer: 500 rows f16 into 4001 x 1001 f32 in chunks of 8 13.2 us, of 16 15.0, of 32 16.4; 4000 rows bf16 into
+// 1000 x 4096 24.3, 22.4 and 26.2 us; 16384 into 1000 x 512 f32 31.5, 27.7 and 31.4 us (before runs[] took 1 to 2 off).
 int64_t chunk_rows(int64_t rows) {
-    int64_t c = 32;
+    int64_t c = rows <= 2048 ? 8 : 16;
     while (c * 2048 < rows) c *= 2;
     return c;
 }
 struct EmbedPlan {
     int64_t chunk, chunks;
-    size_t order, starts, parts;  // bytes
+    size_t order, starts, runs, parts;  // bytes
 };
 EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     EmbedPlan p;
@@ -385,6 +427,7 @@ EmbedPlan embed_plan(int64_t rows, int64_t vocab, int64_t cols) {
     p.chunks = rows > p.chunk ? (rows + p.chunk - 1) / p.chunk : 0;  // without a long run none are needed
     p.order = (size_t)round_up(rows * 4, 16);
     p.starts = (size_t)round_up((vocab + 1) * 4, 16);
+    p.runs = (size_t)round_up(p.chunks * 4, 16);
     p.parts = (size_t)p.chunks * 2 * cols * 4;
     return p;
 }
@@ -419,7 +462,7 @@ extern "C" int ckks_plain_embed_grad_workspace_size(int64_t rows, int64_t vocab,
     if (!bytes) return CKKS_EINVAL;
     if (int e = check_embed(vocab, cols, rows, CKKS_PLAIN_F32)) return e;
     const EmbedPlan p = embed_plan(rows, vocab, cols);
-    *bytes = 2 * p.order + p.starts + p.parts;
+    *bytes = 2 * p.order + p.starts + p.runs + p.parts;
     return CKKS_OK;
 }
 
@@ -450,7 +493,7 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
     char *w = (char *)ws;
     const TokenOrder o{(int32_t *)w, (int32_t *)(w + p.order), (int32_t *)(w + 2 * p.order)};
     const EmbedSums a{o.order, o.token_of, o.starts, rows, vocab, cols, p.chunk, scale,
-                      (float *)(w + 2 * p.order + p.starts)};
+                      (float *)(w + 2 * p.order + p.starts + p.runs), (int32_t *)(w + 2 * p.order + p.starts)};
     k_token_order<<<dim3((uint32_t)((vocab + (1 << b) - 1) >> b)), ORDER_NT, (size_t)ORDER_WAVES * 4 << b, s>>>(
         tokens, rows, vocab, b, o);
     if (int e = launched()) return e;
@@ -483,7 +526,7 @@ extern "C" int ckks_plain_embed_grad(int type, const void *drows, int64_t drows_
                     e = share == 8 ? sum(Int<8>{}, Int<2>{}) : two ? sum(Int<16>{}, Int<2>{}) : sum(Int<16>{}, Int<1>{});
                 if (e || !p.chunks) return e;
                 // chunks, at most 2048, as the dimension of few
-                k_embed_join<O, ADD><<<dim3((uint32_t)((cols + JOIN_COLS - 1) / JOIN_COLS), (uint32_t)p.chunks), 1024,
+                k_embed_join<O, ADD><<<dim3((uint32_t)((cols + JOIN_COLS - 1) / JOIN_COLS), (uint32_t)p.chunks), JOIN_COLS,
                                        0, s>>>(a, (O *)out, out_stride);
                 return launched();
             };

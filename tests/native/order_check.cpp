@@ -1,5 +1,5 @@
 // The order of tokens (k_token_order, csrc/plain/embed.hip), device code on the host, against a stable sort: all
-// tokens, one token, none, more rows than stay in registers.
+// tokens, one token, none, more rows than a wave lists.
 #include <algorithm>
 
 #include "hip/hip_runtime.h"
@@ -7,7 +7,7 @@ static Index gridDim;
 #define __shfl(v, l) (v)  // of kernels that are not run here
 #define __builtin_nontemporal_load(p) (*(p))
 #define __builtin_nontemporal_store(v, p) (*(p) = (v))
-#define __builtin_amdgcn_fence(order, scope)  // one thread at a time
+#define __builtin_amdgcn_fence(order, scope) host::ballot(true)  // the wave meets
 #include "device.inc"
 
 using namespace ckks_plain;
