@@ -1,7 +1,7 @@
 """MI355X-native RNS-CKKS arithmetic core (HIP kernels behind a C ABI).
 
 `Context` (in .api) binds the C library; `plain` binds its plaintext-side
-operators (norms, 8-bit products, sampling); `synth` generates seeded inputs.
+operators (embedding, norms, heads, 8-bit products, sampling, log probabilities); `synth` generates seeded inputs.
 The bindings are imported lazily so CPU-only tools can use `synth` without
 torch or the HIP library.
 """
