@@ -202,12 +202,11 @@ template <int NT> __device__ __forceinline__ void sort_list(uint64_t *list, int 
 // come back, so it ends.
 //
 // 2048 x 131072 bf16 top 20 takes 96 us in a loop, 100 on logits that no cache has (5.6 and 5.4 TB/s; reading alone
-// reaches 6.1): memory, with the vector units busy for most of it (an instruction or two less in 16
-// logits changes nothing), and 5 us of choosing at the rows' ends.  Without
-// alternatives 4096 x 32768 bf16 49 us (5.5 TB/s).  Few rows are latency: 4 x 32768 f32 top 5 7.5 us, 333 x 50021 f16
-// top 20 under a mask 21.5 us for 50 MB.  The next two vectors are on their way while two are added; four or six on
-// their way were no faster (2048 x 131072 95 and 97 us, 333 x 50021 15.6 and 15.9 instead of 15.0, 1000 x 16384 9.0 and
-// 9.1 instead of 8.4).
+// reaches 6.1): memory, with the vector units busy for most of it (two of the 124 vector instructions for 16 logits
+// less change nothing), and 5 us of choosing at the rows' ends.  Without alternatives 4096 x 32768 bf16 50 us
+// (5.4 TB/s).  Few rows are latency: 4 x 32768 f32 top 5 7.5 us, 333 x 50021 f16 top 20 under a mask 21.5 us for 50 MB.
+// The next two vectors are on their way while two are added; four or six were no faster (2048 x 131072 95 and 97 us,
+// 333 x 50021 15.6 and 15.9 instead of 15.0, 1000 x 16384 9.0 and 9.1 instead of 8.4).
 constexpr float ROOM = 0x1p20f;
 template <typename T, bool MASK, bool TOP, bool STREAM, int NT>
 __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, Part *parts, uint64_t *keys) {

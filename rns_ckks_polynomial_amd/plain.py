@@ -405,7 +405,7 @@ def _embed(tokens, table, scale, dtype):
         raise ValueError(f"dtype: expected bfloat16, float16 or float32, got {dtype}")
     dev, T = t.device, _count(tokens, "tokens")
     tp = _vector(tokens, "tokens", T, torch.int64, dev)
-    out = torch.empty((T, D), dtype=dtype, device=dev)
+    out = t.new_empty((T, D), dtype=dtype)
     if is_i8:
         _call("ckks_plain_embed_i8", dev, t.data_ptr(), stride, table.scale.data_ptr(), V, D, tp, T, scale,
               TYPES[dtype], out.data_ptr(), D)
@@ -540,8 +540,8 @@ def _head_grad_workspace(ty, tokens, q_heads, k_heads, dim, rotary, q_weight, k_
 def _head_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
     p = _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved)
     d = p.head_dim
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    q_out = q.new_empty(q.shape)
+    k_out = None if k is None else k.new_empty(k.shape)
     _call("ckks_plain_head_norm_rotate", q.device, C.byref(p), q_out.data_ptr(), p.q_heads * d, d,
           None if k is None else k_out.data_ptr(), p.k_heads * d, d)
     return q_out, k_out
@@ -598,7 +598,7 @@ def head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, q_weight=None, k_we
         side.append(_heads(g, what, T, d, x.dtype, dev))
         if g.shape[1] != x.shape[1]:
             raise ValueError(f"{what}: expected {x.shape[1]} heads, got {g.shape[1]}")
-    new = lambda v, dt: None if v is None else torch.empty(v.shape, dtype=dt, device=dev)  # noqa: E731
+    new = lambda v, dt: None if v is None else v.new_empty(v.shape, dtype=dt)  # noqa: E731
     r = HeadNormRotateGrads(new(q, q.dtype), new(k, q.dtype), new(q_weight, torch.float32),
                             new(k_weight, torch.float32))
     at = lambda v: None if v is None else v.data_ptr()  # noqa: E731
@@ -636,7 +636,7 @@ def _score(logits, tokens, top, temperature, allowed, apart=False):
     args = _score_args(logits, tokens, temperature, allowed)
     B, V = logits.shape
     dev = logits.device
-    new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+    new = lambda dt, *shape: logits.new_empty(shape, dtype=dt)  # noqa: E731
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top: expected 0 to {MAX_TOP}, got {top}")
     f32 = torch.float32
