@@ -153,7 +153,7 @@ def _prepare_heads(g, c):
     length = max(1, T // 3)
     start = (_rand(g, 4).double() * (c["far"] + 1)).long()
     at = torch.arange(T, device="cuda")
-    s["positions"] = start[(at // length).clamp(max=3)] + at % length  # (the rest of three equal parts has the fourth)
+    s["positions"] = start[at // length] + at % length
     r = c["rotary"] // 2
     s["inv_freq"] = (BASE ** (-torch.arange(r, device="cuda", dtype=torch.float64) / r)).float()
     if c["backward"]:
