@@ -434,7 +434,8 @@ struct ScoreGradArgs {
 // A piece of a row for a workgroup, GRAD_EACH vectors a thread.  With lp = ln 2 x, x = z A - B,
 //   dz = p (c0 + c1 x) + [token] dlogprob / temperature,  p = 2^x,
 // of which a row's constants are worked out first (B in 64 bits; what its rounding to 32 leaves is in c0 and c1).
-// Where they have no room, x comes from distances as above.  Bound by memory: 4096 x 32768 bf16 88 us for 537 MB (6.1
+// Where they have no room, x comes from distances as above, and 1 / temperature is multiplied last: at 1e-38 it leaves the
+// range of 32 bits with a term of 4, where p is 1 and the terms' sum 0.  Bound by memory: 4096 x 32768 bf16 88 us for 537 MB (6.1
 // TB/s, past the caches); 333 x 50021 f16 under a mask 18 us for 83 MB, in rows that start at odd elements.
 constexpr int GRAD_EACH = 4, GRAD_PIECE = 256 * 8 * GRAD_EACH;
 template <typename T, bool MASK, bool STREAM>
@@ -462,8 +463,9 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
         if (c + 8 <= a.vocab) v[j].template fetch<STREAM>(z, allowed, c);
         else if (c < a.vocab) v[j].fetch(z, allowed, c, a.vocab);
     }
-    const float c0 = k * (dl + dh * (h - LN2 * off)), c1 = k * dh * LN2;
-    const bool room = fabsf(b) < ROOM && fabsf(c0) < INFINITY && fabsf(c1) < INFINITY;
+    const float c0 = k * (dl + dh * (h - LN2 * off)), c1 = k * dh * LN2, given = dl * inv_t;
+    // nothing below overflows, not even for x = LEAST, whose p is 0 (NaN: no)
+    const bool room = fabsf(b) < ROOM && fabsf(c0) + fabsf(LEAST * c1) + fabsf(given) < 0x1p126f;
 #pragma unroll
     for (int j = 0; j < GRAD_EACH; j++) {
         const int c = begin + j * 2048;
@@ -476,18 +478,20 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
                 const float x = fmaxf(__builtin_fmaf(f[i], scale, -b), LEAST);
                 f[i] = __builtin_amdgcn_exp2f(x) * __builtin_fmaf(c1, x, c0);
             }
+            if ((uint64_t)(token - c) < 8) {
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (c + i == token) f[i] += given;
+            }
         } else {
+            // the terms cancel before 1 / temperature comes to them
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 const float lp = fmaxf(distance(f[i], m) * inv_t - log_mass, LEAST);
-                const float e = __builtin_amdgcn_exp2f(lp * LOG2E);  // 0 at the bound
-                f[i] = f[i] > -INFINITY ? -e * (dl + dh * (lp + h)) * inv_t : 0.0f;
+                const float e = f[i] > -INFINITY ? __builtin_amdgcn_exp2f(lp * LOG2E) : 0.0f;  // 0 at the bound
+                const float g = e > 0.0f ? -e * (dl + dh * (lp + h)) : 0.0f;
+                f[i] = (c + i == token ? g + dl : g) * inv_t;
             }
-        }
-        if ((uint64_t)(token - c) < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (c + i == token) f[i] += dl * inv_t;
         }
         Piece<T, 8>::template store<STREAM>(out + c, a.vocab - c, f);
     }

@@ -1,0 +1,47 @@
+"""Embedding, heads and log probabilities (include/ckks_plain.h) where numbers,
+layouts and uses are at the edge of what the calls take, against their
+definitions in 64 bits (plain_token_ref).  Bounds as in test_gpu_plain_tokens."""
+import numpy as np
+import pytest
+
+from gpu_util import require_gpu, say, torch
+from rns_ckks_polynomial_amd import plain
+from test_gpu_plain import TYPE, rnd
+from test_gpu_plain_tokens import check_score, ints, on_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+# ------------------------------------------------------------------ log probabilities
+
+@pytest.mark.parametrize("ty", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("temperature", [1e-45, 1e-38, 1e-37, 1e-36])
+def test_gradient_at_tiny_temperatures(ty, temperature):
+    """Rows whose largest logit is far above the others: p is 0 and 1, and the gradient 0, whatever 1 / temperature
+    times its terms would be; and rows whose others are near it."""
+    V = 5003
+    z = -(1 + torch.rand(4, V, generator=torch.Generator().manual_seed(3)))
+    at = torch.tensor([0, 17, V - 1, 2500])
+    z[torch.arange(4), at] = torch.tensor([0.0, 0.0, 3.0, -0.5])
+    z, tok = z.to(TYPE[ty]).cuda(), torch.where(torch.arange(4) == 2, 5, at).cuda()
+    t = torch.full((4,), temperature, device="cuda")
+    r = plain.token_logprobs(z, tok, 0, t)
+    for dl in (None, 4.0, 50.0):
+        for dh in (None, 1.0, -30.0):
+            say(f"tiny {ty} {temperature} {dl} {dh}")
+            each = lambda v: None if v is None else torch.full((4,), v, device="cuda")  # noqa: E731
+            d = plain.token_logprobs_grad(z, tok, r, each(dl), each(dh), t)
+            want = torch.zeros(4, V, dtype=torch.float64)
+            if dl is not None:  # the third row's given token has p = 0, its largest p = 1
+                want[2, 5], want[2, V - 1] = dl / max(temperature, 2.0 ** -127), -dl / max(temperature, 2.0 ** -127)
+            # 1 / temperature and the product are rounded once each, then to the type; +-: infinite where it has no room
+            low, high = ((want * (1 + s * 2.0 ** -22)).float().to(TYPE[ty]) for s in (-1, 1))
+            d = d.cpu()
+            assert ((d >= torch.minimum(low, high)) & (d <= torch.maximum(low, high))).all()
+    near_ones = (rnd(5, 4, 300) * 2 * temperature).float().cuda()
+    check_score(near_ones, ints(6, 4, 0, 300), 3, t)
