@@ -22,8 +22,15 @@ __device__ __forceinline__ float inverse_temperature(const float *temperature, i
     const float t = temperature ? temperature[row] : 1.0f;
     return t > 0.0f ? fminf(1.0f / t, 0x1p127f) : 1.0f;
 }
-// The distance of a logit to the largest, 0 also where both are infinite.
-__device__ __forceinline__ float distance(float z, float largest) { return z == largest ? 0.0f : z - largest; }
+// (z - largest) factor: 0 where both are infinite; -infinity below an infinite largest logit (and of -infinity and NaN),
+// also where the factor is 0, that of an infinite temperature; by its two parts where the distance of finite logits
+// leaves the range of 32 bits, as its quotient by a large temperature need not.
+__device__ __forceinline__ float distance_times(float z, float largest, float factor) {
+    const float d = z - largest;
+    if (z == largest) return 0.0f;
+    if (d > -INFINITY) return d * factor;
+    return z > -INFINITY && largest < INFINITY ? z * factor - largest * factor : -INFINITY;
+}
 
 constexpr int MAX_SLICES = 32, JOIN_KEYS = MAX_SLICES * CKKS_PLAIN_MAX_TOP;
 
@@ -44,7 +51,7 @@ __device__ __forceinline__ Given given_token(const ScoreArgs &a, int64_t row, co
 __device__ __forceinline__ void put_score(const ScoreArgs &a, int64_t row, const Given &g, float largest, float log_mass,
                                           float mean, float inv_t) {
     a.logprob[row] = !g.there                ? 0.0f
-                     : g.logit > -INFINITY ? distance(g.logit, largest) * inv_t - log_mass
+                     : g.logit > -INFINITY ? distance_times(g.logit, largest, inv_t) - log_mass
                                              : -INFINITY;
     a.entropy[row] = log_mass > -INFINITY ? log_mass - LN2 * mean : 0.0f;  // mean: of the distances, in powers of two
     a.largest[row] = largest;
@@ -126,7 +133,7 @@ __device__ __forceinline__ void put_top(const ScoreArgs &a, int64_t row, int ran
         return;
     }
     a.top_token[row * a.top + rank] = key ? (int64_t)(uint32_t)~(uint32_t)key : -1;
-    a.top_logprob[row * a.top + rank] = key ? distance(key_logit(key), largest) * inv_t - log_mass : -INFINITY;
+    a.top_logprob[row * a.top + rank] = key ? distance_times(key_logit(key), largest, inv_t) - log_mass : -INFINITY;
 }
 
 template <int NT> struct ScoreShared {
@@ -291,7 +298,7 @@ __global__ __launch_bounds__(NT) void k_token_logprobs(ScoreArgs a, int slice, P
             p.widen(c, end, f);
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float x = fmaxf(distance(f[i], m) * scale, LEAST);
+                const float x = fmaxf(distance_times(f[i], m, scale), LEAST);
                 const float e = f[i] > -INFINITY ? __builtin_amdgcn_exp2f(x) : 0.0f;
                 s.mass += e;
                 s.moment += e * x;
@@ -387,7 +394,7 @@ __global__ __launch_bounds__(JOIN_NT) void k_join_logprobs(ScoreArgs a, int slic
     for (int i = t; i < slices * a.top; i += JOIN_NT) list[i] = keys[row * slices * a.top + i];
     const float m = of_order_bits(row_all<JOIN_NT>(order_bits(p.m), slots, Larger{}));
     Mass s{0, p.mass, p.moment};
-    if (p.m != m) s.shift(fmaxf((p.m - m) * scale, LEAST));  // two infinities have no distance
+    s.shift(fmaxf(distance_times(p.m, m, scale), LEAST));
     row_sums<JOIN_NT>(s.mass, s.moment, sums[0], sums[1]);
     const bool some = s.mass > 0;
     const float log_mass = some ? logf(s.mass) : -INFINITY, largest = some ? m : -INFINITY;
@@ -487,7 +494,7 @@ __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, in
             // the terms cancel before 1 / temperature comes to them
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                const float lp = fmaxf(distance(f[i], m) * inv_t - log_mass, LEAST);
+                const float lp = fmaxf(distance_times(f[i], m, inv_t) - log_mass, LEAST);
                 const float e = f[i] > -INFINITY ? __builtin_amdgcn_exp2f(lp * LOG2E) : 0.0f;  // 0 at the bound
                 const float g = e > 0.0f ? -e * (dl + dh * (lp + h)) : 0.0f;
                 f[i] = (c + i == token ? g + dl : g) * inv_t;

@@ -6,7 +6,7 @@ import pytest
 
 from gpu_util import require_gpu, say, torch
 from rns_ckks_polynomial_amd import plain
-from test_gpu_plain import TYPE, rnd
+from test_gpu_plain import EPS, TYPE, rnd
 from test_gpu_plain_tokens import check_score, ints, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +45,31 @@ def test_gradient_at_tiny_temperatures(ty, temperature):
             assert ((d >= torch.minimum(low, high)) & (d <= torch.maximum(low, high))).all()
     near_ones = (rnd(5, 4, 300) * 2 * temperature).float().cuda()
     check_score(near_ones, ints(6, 4, 0, 300), 3, t)
+
+
+@pytest.mark.parametrize("B,V", [(5, 300), (5, 70001)])
+def test_distances_past_32_bits_and_infinite_temperatures(B, V):
+    """Logits over the whole range at temperatures of its size, beside a NaN, and infinite ones at an infinite
+    temperature; in slices too."""
+    z = ((rnd(31, B, V).clamp(-3, 3)) * 1.1e38).float()
+    z[1, V // 2] = float("nan")
+    z[2, :V // 2], z[2, V // 2:] = 3e38, -3e38
+    z[3, 7] = float("inf")
+    z[4, 7] = z[4, V - 1] = float("inf")
+    for t in (1e38, 3.4e38, float("inf")):
+        say(f"distances {B}x{V} at {t}")
+        r = plain.token_logprobs(z.cuda(), torch.tensor([0, 1, V - 1, 8, 7], device="cuda"), 4,
+                                 torch.full((B,), t, device="cuda"))
+        x = (z.double() - z.double().nan_to_num(-np.inf, np.inf).amax(1, keepdim=True)) / t
+        x[3:] = -np.inf  # an infinite logit outweighs the finite ones
+        x[3, 7] = x[4, 7] = x[4, V - 1] = 0
+        x[x.isnan()] = -np.inf
+        lp = torch.log_softmax(x, 1)
+        bound = (V / 256 + 64 + 4 * 6 + 4 * np.log(V) + 4 * 24) * EPS  # |x| <= 6 / 1.1, and of log probabilities 24
+        given = lp[torch.arange(B), torch.tensor([0, 1, V - 1, 8, 7])]
+        for got, want in ((r.logprob, given), (r.log_mass, -lp.amax(1)), (r.top_logprob, lp.topk(4).values)):
+            got = got.cpu().double()
+            assert torch.equal(got == -np.inf, want == -np.inf)
+            assert ((got - want).abs()[want > -np.inf] <= bound).all()
+        entropy = -(lp.exp() * lp).nan_to_num(0).sum(1)
+        assert ((r.entropy.cpu().double() - entropy).abs() <= bound * (1 + 2 * 6 + np.log(V))).all()
