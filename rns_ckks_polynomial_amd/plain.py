@@ -632,7 +632,7 @@ def _score_args(logits, tokens, temperature, allowed):
             None if allowed is None else allowed.data_ptr(), a_stride, B, V)
 
 
-def _score(logits, tokens, top, temperature, allowed, apart=False):
+def _score(logits, tokens, top, temperature, allowed):
     args = _score_args(logits, tokens, temperature, allowed)
     B, V = logits.shape
     dev = logits.device
@@ -640,9 +640,8 @@ def _score(logits, tokens, top, temperature, allowed, apart=False):
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top: expected 0 to {MAX_TOP}, got {top}")
     f32 = torch.float32
-    # four allocations instead of six; what autograd follows stays apart, as it would not let one of several views be written
-    rows = [new(f32, B) for _ in range(4)] if apart else new(f32, 4, B).unbind(0)
-    r = TokenLogprobs(rows[0], rows[1], new(torch.int64, B, top), new(f32, B, top), rows[2], rows[3])
+    # an allocation for each: views of one would share a version, and a write to one be taken for a write to all
+    r = TokenLogprobs(new(f32, B), new(f32, B), new(torch.int64, B, top), new(f32, B, top), new(f32, B), new(f32, B))
     _keep, ws, size = _scratch(_workspace("ckks_plain_token_logprobs_workspace_size", B, V, top), dev)
     _call("ckks_plain_token_logprobs", dev, *args, top, r.logprob.data_ptr(), r.entropy.data_ptr(),
           r.largest.data_ptr(), r.log_mass.data_ptr(), r.top_token.data_ptr() if top else None,
@@ -654,7 +653,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top, temperature, allowed):
         ctx.set_materialize_grads(False)
-        r = _score(logits, tokens, top, temperature, allowed, True)
+        r = _score(logits, tokens, top, temperature, allowed)
         ctx.save_for_backward(logits, tokens, temperature, allowed, *r)
         ctx.mark_non_differentiable(r.top_token)
         return tuple(r)

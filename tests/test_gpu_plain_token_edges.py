@@ -73,3 +73,28 @@ def test_distances_past_32_bits_and_infinite_temperatures(B, V):
             assert ((got - want).abs()[want > -np.inf] <= bound).all()
         entropy = -(lp.exp() * lp).nan_to_num(0).sum(1)
         assert ((r.entropy.cpu().double() - entropy).abs() <= bound * (1 + 2 * 6 + np.log(V))).all()
+
+
+# ------------------------------------------------------------------ results and what autograd keeps of them
+
+def some_scores(requires_grad=False):
+    z = (rnd(41, 6, 700) * 2).float().cuda().requires_grad_(requires_grad)
+    return z, on_gpu(ints(42, 6, -1, 700), torch.int64)
+
+
+def test_results_are_tensors_of_their_own():
+    """Writing to one result leaves what autograd holds of the others, and may be followed by it."""
+    z, tok = some_scores()
+    r = plain.token_logprobs(z, tok, 3)
+    assert len({v.untyped_storage().data_ptr() for v in r}) == len(r) and not any(v._is_view() for v in r)
+    w = torch.full((6,), 0.5, device="cuda", requires_grad=True)
+    loss = (w * r.logprob).sum()
+    kept = [v.clone() for v in r]
+    r.entropy.add_(1)
+    r.log_mass.zero_()
+    loss.backward()
+    assert torch.equal(w.grad, kept[0])
+    w.grad = None
+    r.largest.mul_(w)
+    r.largest.sum().backward()
+    assert torch.equal(w.grad, kept[4]) and torch.equal(r.logprob, kept[0])
