@@ -654,7 +654,7 @@ class _TokenLogprobs(torch.autograd.Function):
     def forward(ctx, logits, tokens, top, temperature, allowed):
         ctx.set_materialize_grads(False)
         r = _score(logits, tokens, top, temperature, allowed)
-        ctx.save_for_backward(logits, tokens, temperature, allowed, *r)
+        ctx.save_for_backward(logits, tokens, temperature, allowed, r.entropy, r.largest, r.log_mass)
         ctx.mark_non_differentiable(r.top_token)
         return tuple(r)
 
@@ -664,9 +664,10 @@ class _TokenLogprobs(torch.autograd.Function):
             raise RuntimeError("token_logprobs has no gradient of the temperature")
         if any(g is not None for g in others):
             raise RuntimeError("token_logprobs has a gradient of logprob and entropy alone")
-        logits, tokens, temperature, allowed, *r = ctx.saved_tensors
+        logits, tokens, temperature, allowed, entropy, largest, log_mass = ctx.saved_tensors
+        scores = TokenLogprobs(None, entropy, None, None, largest, log_mass)
         whole = lambda g: None if g is None else g.contiguous()  # noqa: E731
-        return token_logprobs_grad(logits, tokens, TokenLogprobs(*r), whole(dlogprob), whole(dentropy), temperature,
+        return token_logprobs_grad(logits, tokens, scores, whole(dlogprob), whole(dentropy), temperature,
                                    allowed), None, None, None, None
 
 

@@ -98,3 +98,15 @@ def test_results_are_tensors_of_their_own():
     r.largest.mul_(w)
     r.largest.sum().backward()
     assert torch.equal(w.grad, kept[4]) and torch.equal(r.logprob, kept[0])
+
+
+def test_results_that_the_gradient_does_not_need_may_be_written():
+    z, tok = some_scores(True)
+    want, = torch.autograd.grad(plain.token_logprobs(z, tok, 3).logprob.neg().sum(), z)
+    r = plain.token_logprobs(z, tok, 3)
+    loss = r.logprob.neg_().sum()
+    r.top_token.clamp_(min=0)
+    with torch.no_grad():
+        r.top_logprob.clamp_(min=-100)
+    loss.backward()
+    assert torch.equal(z.grad, want)
