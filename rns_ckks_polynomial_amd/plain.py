@@ -501,6 +501,12 @@ def _heads(t, what, tokens=None, dim=None, dtype=None, device=None):
     return t.data_ptr(), token, head
 
 
+def _heads_apart(t):
+    """Whether the strides are what the kernels take: one within a head, and heads that share no memory."""
+    (T, H, d), (token, head, across) = t.shape, t.stride()
+    return across == 1 and (T < 2 or token >= d) and (H < 2 or head >= d)
+
+
 def _head_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved):
     """ckks_plain_heads of the arguments."""
     qp, q_token, q_head = _heads(q, "q")
@@ -560,8 +566,7 @@ class _HeadNormRotate(torch.autograd.Function):
         if ctx.needs_input_grad[3]:
             raise RuntimeError("head_norm_rotate has no gradient of inv_freq")
         eps, interleaved = ctx.rest
-        unit = lambda v: v if v is None or v.stride(-1) == 1 else v.contiguous()  # noqa: E731
-        dq, dk = (v if v is None or min(v.stride()) else v.contiguous() for v in (unit(dq), unit(dk)))
+        dq, dk = (v if v is None or _heads_apart(v) else v.contiguous() for v in (dq, dk))
         g = head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, qw, kw, eps, interleaved)
         like = lambda v, p: None if p is None else v.to(p.dtype)  # noqa: E731
         return g.dq, g.dk, None, None, like(g.q_weight, qw), like(g.k_weight, kw), None, None
