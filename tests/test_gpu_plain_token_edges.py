@@ -116,7 +116,7 @@ def test_heads_take_a_gradient_of_any_strides():
     """Rows of a gradient that share memory, as a window over a sequence gives them."""
     q, k = (rnd(43 + i, 7, 3, 64).to(torch.bfloat16).cuda().requires_grad_() for i in range(2))
     pos, freq = torch.arange(7, device="cuda"), torch.tensor([1.0, 0.3, 0.01], device="cuda")
-    flat = rnd(45, 4096).to(torch.bfloat16).cuda()
+    flat = rnd(45, 8192).to(torch.bfloat16).cuda()
     for strides in ((8, 64, 1), (192, 16, 1), (0, 64, 1), (1, 64, 64), (7, 5, 3)):
         say(f"gradient of strides {strides}")
         g = torch.as_strided(flat, (7, 3, 64), strides)
