@@ -4,10 +4,11 @@ definitions in 64 bits (plain_token_ref).  Bounds as in test_gpu_plain_tokens.""
 import numpy as np
 import pytest
 
+import plain_token_ref as ref
 from gpu_util import require_gpu, say, torch
 from rns_ckks_polynomial_amd import plain
-from test_gpu_plain import EPS, TYPE, rnd
-from test_gpu_plain_tokens import check_score, ints, on_gpu
+from test_gpu_plain import EPS, TYPE, f64, rnd
+from test_gpu_plain_tokens import check_embed_grad, check_score, head_inputs, host, ints, near, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -123,3 +124,45 @@ def test_heads_take_a_gradient_of_any_strides():
         want = plain.head_norm_rotate_grad(q.detach(), k.detach(), g.contiguous(), g.contiguous(), pos, freq)
         got = torch.autograd.grad(plain.head_norm_rotate(q, k, pos, freq), (q, k), (g, g))
         assert torch.equal(got[0], want.dq) and torch.equal(got[1], want.dk)
+
+
+# ------------------------------------------------------------------ sizes that take another form of a kernel
+
+@pytest.mark.parametrize("T,Q,K,d,r,ty,interleaved,norm", [
+    (4101, 32, 8, 128, 64, "bf16", False, True),   # 12 tokens a workgroup, four at a time; the last has 9
+    (4101, 17, 2, 128, 48, "f32", True, True),     # 8, four at a time; the last has 5
+    (5500, 6, 2, 64, 32, "f16", False, True),      # 20, ten at a time; the last has 20
+    (5503, 6, 2, 64, 20, "bf16", True, True),      # the same; the last has 3
+    (4101, 9, 40, 128, 64, "bf16", False, False),  # more heads of keys than of queries, no norm
+])
+def test_heads_gradient_of_workgroups_with_several_steps(T, Q, K, d, r, ty, interleaved, norm):
+    """A workgroup's angles replaced between its steps, the next step's head fetched before, and the weights' sums
+    carried over them.  A weight's sum adds up in a thread at most 60 terms (tokens times heads over groups of
+    threads), 6 between lanes and 4 between waves, and of at most 1024 workgroups' 64 and 16: under 160 roundings, and
+    each term is off by 96 eps as the gradient's are."""
+    say(f"gradient of {T} x {Q} + {K} heads of {d} {ty}")
+    q, k, pos, freq, qw, kw = head_inputs(71, T, Q, K, d, r, ty, norm)
+    dq, dk = rnd(72, *q.shape).to(q.dtype).cuda(), rnd(73, *k.shape).to(k.dtype).cuda()
+    got = plain.head_norm_rotate(q, k, pos, freq, qw, kw, 1e-6, interleaved)
+    g = plain.head_norm_rotate_grad(q, k, dq, dk, pos, freq, qw, kw, 1e-6, interleaved)
+    e = float(np.float32(1e-6))
+    for x, w, y, dy, dx, dw in ((q, qw, got[0], dq, g.dq, g.q_weight), (k, kw, got[1], dk, g.dk, g.k_weight)):
+        want, size = ref.heads(f64(x), f64(w), host(pos), host(freq), e, interleaved)
+        near(y, want, 32 * EPS * size, "forward")
+        a, asize, b, bsize = ref.heads_grad(f64(x), f64(dy), f64(w), host(pos), host(freq), e, interleaved)
+        near(dx, a, 96 * EPS * asize, "gradient")
+        if norm:
+            near(dw, b, 256 * EPS * bsize, "weight")
+    again = plain.head_norm_rotate_grad(q, k, dq, dk, pos, freq, qw, kw, 1e-6, interleaved)
+    assert all(a is b or torch.equal(a, b) for a, b in zip(g, again))
+
+
+@pytest.mark.parametrize("D", [1, 3, 7, 9, 2051, 2500, 3333, 4099, 9001])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kind", ["text", "two", "one"])
+def test_new_tables_gradient(D, out, kind):
+    """Rows narrower than a vector and wider than 2048 columns in every type of the table, an odd number of rows of it
+    (the last without a neighbour), tokens that do not occur, and runs of more rows than a chunk."""
+    say(f"new table {D} {out} {kind}")
+    check_embed_grad(151, 51, D, "bf16", out, kind, pad=3)
+    check_embed_grad(67, 33, D, "f32", out, kind)
