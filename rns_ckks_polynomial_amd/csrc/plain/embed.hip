@@ -280,6 +280,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, 
     constexpr int V = JOINT<T, O>;
     const int64_t group = from + ((blockIdx.x - chunks) << (8 - log_l)) + (threadIdx.x >> log_l);
     const int64_t turn = (int64_t)E << log_l;
+    if (blockIdx.y * turn >= s.cols) return;  // the grid's columns go by pieces of 2048, those of the chunks
     int64_t v = group * ROWS;
     if (ADD) {
         const int64_t a = group;
