@@ -567,9 +567,16 @@ class _HeadNormRotate(torch.autograd.Function):
             raise RuntimeError("head_norm_rotate has no gradient of inv_freq")
         eps, interleaved = ctx.rest
         dq, dk = (v if v is None or _heads_apart(v) else v.contiguous() for v in (dq, dk))
-        g = head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, qw, kw, eps, interleaved)
+        q_needed, k_needed = (any(ctx.needs_input_grad[i] for i in side) for side in ((0, 4), (1, 5)))
         like = lambda v, p: None if p is None else v.to(p.dtype)  # noqa: E731
-        return g.dq, g.dk, None, None, like(g.q_weight, qw), like(g.k_weight, kw), None, None
+        if q_needed and k_needed:
+            g = head_norm_rotate_grad(q, k, dq, dk, positions, inv_freq, qw, kw, eps, interleaved)
+            return g.dq, g.dk, None, None, like(g.q_weight, qw), like(g.k_weight, kw), None, None
+        if q_needed:  # of one side alone
+            g = head_norm_rotate_grad(q, None, dq, None, positions, inv_freq, qw, None, eps, interleaved)
+            return g.dq, None, None, None, like(g.q_weight, qw), None, None, None
+        g = head_norm_rotate_grad(k, None, dk, None, positions, inv_freq, kw, None, eps, interleaved)
+        return None, g.dq, None, None, None, like(g.q_weight, kw), None, None
 
 
 def head_norm_rotate(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6,

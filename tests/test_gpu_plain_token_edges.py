@@ -126,6 +126,35 @@ def test_heads_take_a_gradient_of_any_strides():
         assert torch.equal(got[0], want.dq) and torch.equal(got[1], want.dk)
 
 
+def test_heads_gradient_of_what_is_asked_for(monkeypatch):
+    """Backward works on the queries or the keys alone where the other side is frozen, with the same results."""
+    q, k, pos, freq, qw, kw = head_inputs(46, 40, 6, 2, 64, 32, "bf16")
+    dq, dk = rnd(47, *q.shape).to(q.dtype).cuda(), rnd(48, *k.shape).to(k.dtype).cuda()
+    whole = plain.head_norm_rotate_grad(q, k, dq, dk, pos, freq, qw, kw)
+    heads, call = [], plain._call
+
+    def record(name, device, p, *args):
+        if name == "ckks_plain_head_norm_rotate_grad":
+            heads.append((p._obj.q_heads, p._obj.k_heads))
+        return call(name, device, p, *args)
+
+    monkeypatch.setattr(plain, "_call", record)
+    for frozen, worked in (((), (6, 2)), ((1, 3), (6, 0)), ((0, 2), (2, 0)), ((1,), (6, 2)), ((1, 2, 3), (6, 0)), ((0, 1, 2), (2, 0))):
+        leaves = [v.detach().clone().requires_grad_(i not in frozen) for i, v in enumerate((q, k, qw, kw))]
+        heads.clear()
+        torch.autograd.backward(plain.head_norm_rotate(leaves[0], leaves[1], pos, freq, leaves[2], leaves[3]), (dq, dk))
+        assert heads == [worked], frozen
+        for i, (v, want) in enumerate(zip(leaves, whole)):
+            if i in frozen:
+                assert v.grad is None
+            elif i < 2:
+                assert torch.equal(v.grad, want)
+            else:  # the terms may be added in another order: the bound of several steps, below
+                x, dy = ((q, dq), (k, dk))[i - 2]
+                _, _, b, bsize = ref.heads_grad(f64(x), f64(dy), f64((qw, kw)[i - 2]), host(pos), host(freq), 1e-6, False)
+                near(v.grad, b, 256 * EPS * bsize, "weight")
+
+
 # ------------------------------------------------------------------ sizes that take another form of a kernel
 
 @pytest.mark.parametrize("T,Q,K,d,r,ty,interleaved,norm", [
