@@ -4,8 +4,8 @@
 namespace ckks_plain {
 
 // Elements of a vector of types T and O: 16 bytes of the wider, so that neighbouring lanes' accesses join to
-// whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction: the gradient of
-// 16384 rows bf16 into 32768 x 2048 f32 119 us where this took 67).
+// whole lines on both sides (with 32 bytes a lane of the wider type, half a line an instruction, the gradient of
+// 16384 rows bf16 into 32768 x 2048 f32 took 119 us in its first form; 62 now).
 template <typename T, typename O> constexpr int JOINT = 16 / (int)(sizeof(T) > sizeof(O) ? sizeof(T) : sizeof(O));
 
 // out[t] = scale table[tokens[t]], 2^log_l threads a row, the rest of 256 threads on other rows.  Bound by memory:
@@ -51,8 +51,10 @@ constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 // A workgroup has 2^log_bins tokens of the vocabulary and reads all rows' tokens itself, so nothing is joined
 // between workgroups and one launch does: wave w counts those of its part of the rows and lists its own (up to
 // LISTED of them; where there are more, the part is read again), and after a sum over waves and bins puts its rows
-// where they belong, in order.  Latency: 16384 tokens of 32768 8.5 us, 8191 of 20011 6.3 us (a launch, the tokens at four
-// loads a turn, five barriers).  It is short code on purpose: with all of a wave's tokens in registers, and so a copy of
+// where they belong, in order.  Latency: 16384 tokens of 32768 8.2 us, 8191 of 20011 6.3 us (a launch, the tokens at four
+// loads a turn, five barriers).  A workgroup has at most 512 tokens of the vocabulary, so beyond 131072 of them there are
+// more workgroups and each still reads all rows' tokens: 16384 rows into 2^20 47 us, into 2^24 630; 131072 rows into 2^17
+// 27 us, into 2^24 2500 (an order joined between workgroups would read them once).  It is short code on purpose: with all of a wave's tokens in registers, and so a copy of
 // the loops' bodies for each, 9.9 and 7.9 us, most of the difference to fetch the instructions.
 constexpr int FETCHED = 4, LISTED = 512;
 constexpr uint32_t NONE = ~0u;
@@ -268,11 +270,12 @@ __device__ __forceinline__ void sum_parts(const EmbedSums &s, const T *drows, in
 // its token.
 //
 // Bound by memory, most of it stores: 16384 rows bf16 into 32768 x 2048 f32 48 us for 335 MB (6.9 TB/s, past the
-// caches), behind 8.5 us of order and in front of 6.7 us of long runs.  E elements a thread: 16 spare rows of just over
-// 2048 columns a second turn for the rest (8191 rows f16 into 20011 x 2051 35.6 us, with 8 42.5), 8 are faster for
-// narrower ones (4096 into 32768 x 64 f32 15.2 us, with 16 16.9; 16384 into 32768 x 2048 f32 63, with 16 70).  Two rows
-// of the table where they are short: 8191 rows f16 into 20011 x 2051 35.6 us, with one 40.6; 8192 bf16 into 32768 x 1024
-// 28.1, with one 29.6; 16384 bf16 into 32768 x 2048 f32 71.0 us, with one 63.2.
+// caches), behind 8.2 us of order and in front of 6.6 us of long runs; added to such a table 44 us for 156 MB (3.5 TB/s:
+// each row of it waits for its places, its rows and what is there).  E elements a thread: 16 spare rows of just over
+// 2048 columns a second turn for the rest (8191 rows f16, none of them padding, into 20011 x 2051 36.1 us, with 8 43.0), 8
+// are faster for narrower ones (4096 into 32768 x 64 f32 15.3 us, with 16 17.2; 16384 into 32768 x 2048 f32 62.8, with 16
+// 71.3).  Two rows of the table where they are short: 8191 rows f16 into 20011 x 2051 36.1 us, with one 39.9; 16384 bf16
+// into 32768 x 2048 f32 70.1 us, with one 62.8; between them (8192 bf16 into 32768 x 1024 f32 36.6 and 36.1) it is the same.
 template <typename T, typename O, bool ADD, int E, int ROWS>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, int64_t stride, O *out,
                                                    int64_t out_stride, int64_t from, int64_t chunks, int log_l) {
@@ -314,7 +317,8 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, 
 
 // The long run that begins in chunk blockIdx.y, if there is one: 512 columns (blockIdx.x), eight waves on its
 // parts in turn, then their sums in order.  Latency, 4.1 to 6.7 us: a launch and three loads that wait for each other,
-// and the parts of the longest run (with 16 waves, and each workgroup to find out whether a run begins, 10 us).
+// and the parts of the longest run (with 16 waves, and each workgroup to find out whether a run begins, 10 us).  Of rows of
+// fewer than 512 columns a part of the lanes has one: 32768 rows of 64 columns into 1000 12 us, of 16 lanes a wave.
 constexpr int JOIN_COLS = 512;
 template <typename O, bool ADD>
 __global__ __launch_bounds__(JOIN_COLS) void k_embed_join(EmbedSums s, O *out, int64_t out_stride) {
@@ -410,9 +414,9 @@ int log_bins(int64_t vocab) {
     while (b < 9 && ((int64_t)256 << b) < vocab) b++;
     return b;
 }
-// Rows of a chunk: at most 2048 chunks.  Long runs are read by as many workgroups as they have chunks, and their parts
-// by fewer: 500 rows f16 into 4001 x 1001 f32 in chunks of 8 13.2 us, of 16 15.0, of 32 16.4; 4000 rows bf16 into
-// 1000 x 4096 24.3, 22.4 and 26.2 us; 16384 into 1000 x 512 f32 31.5, 27.7 and 31.4 us (before runs[] took 1 to 2 off).
+// Rows of a chunk: at most 2048 chunks, so 64 at 131072 rows and more beyond.  Long runs are read by as many workgroups
+// as they have chunks, and their parts by fewer: 500 rows f16 into 4001 x 1001 f32 in chunks of 8 13.4 us, of 16 14.6, of
+// 32 18.2; 4000 rows bf16 into 1000 x 4096 f32 22.1, 22.7 and 29.1 us; 16384 f32 into 1000 x 512 33.9, 29.2 and 31.7 us.
 int64_t chunk_rows(int64_t rows) {
     int64_t c = rows <= 2048 ? 8 : 16;
     while (c * 2048 < rows) c *= 2;

@@ -604,8 +604,11 @@ extern "C" int ckks_plain_token_logprobs(int type, const void *logits, int64_t l
                 return launched();
             };
             // 512 threads where a unit has one workgroup (1 x 262144 bf16 top 64 22 us, with 256 35) and for long rows
-            // (2048 x 131072 bf16 top 20 96 us, with 256 99), 256 for others (512 x 32768 top 5 11 us, with 512 12;
-            // 1000 x 32768 top 20 17.7 us, with 512 20.8; 4096 x 4001 top 5 22 us, with 512 32)
+            // (2048 x 131072 bf16 top 20 96 us, with 256 99), 256 for others (512 x 32768 f16 top 20 11.9 us, with 512
+            // 12.8; 600 x 65536 21.2 and 22.6; 900 x 65536 28.5 and 34.2; 2048 x 65536 55.5 and 55.5; 4096 x 4001 top 5 22
+            // and 32).  The rule goes by length alone: between a row a unit and four, long rows without a mask would be
+            // faster with 256 (600 x 131072 35.9, with 512 37.8; 900 45.8 and 53.5), masked ones with 512 (333 x 50021
+            // 20.9, with 512 19.8; 300 x 65536 22.3 and 21.8; 600 x 131072 53.0 and 49.6).
             auto go2 = [&](auto alternatives, auto past) {
                 return n * slices <= 256 || slice > 65536 ? go(alternatives, past, Int<512>{}) : go(alternatives, past, Int<256>{});
             };

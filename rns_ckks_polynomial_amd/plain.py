@@ -583,8 +583,9 @@ def head_norm_rotate(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
                      interleaved: bool = False):
     """(q, k) [T, heads, d], each head normalised (x / sqrt(mean x^2 + eps) weight) and then rotated by position
     (ckks_plain_head_norm_rotate): pair i of its dimensions, (i, i + r) or (2 i, 2 i + 1) if interleaved, turns by
-    positions[t] inv_freq[i]; dimensions from 2 r on stay.  q, k: heads of any strides with unit stride within a head
-    (views of a joint projection, say), k may be None.  positions: int64 [T]; inv_freq: float32 [r], 2 r <= d; both
+    positions[t] inv_freq[i]; dimensions from 2 r on stay.  q, k: unit stride within a head, heads and tokens at least a
+    head apart (views of a joint projection, heads before tokens; an expanded tensor has to be copied), k may be None.
+    The results' gradients may have any strides.  positions: int64 [T]; inv_freq: float32 [r], 2 r <= d; both
     None: no rotation.  q_weight, k_weight: [d], of the type of q; None: no norm.  d is even, at most MAX_HEAD.
     Differentiable once through torch.autograd (gradients of weights are summed in 32 bits, then rounded to their
     type; a second derivative raises, as does one by inv_freq)."""
