@@ -54,8 +54,10 @@ constexpr int ORDER_NT = 1024, ORDER_WAVES = ORDER_NT / 64;
 // where they belong, in order.  Latency: 16384 tokens of 32768 8.2 us, 8191 of 20011 6.3 us (a launch, the tokens at four
 // loads a turn, five barriers).  A workgroup has at most 512 tokens of the vocabulary, so beyond 131072 of them there are
 // more workgroups and each still reads all rows' tokens: 16384 rows into 2^20 47 us, into 2^24 630; 131072 rows into 2^17
-// 27 us, into 2^24 2500 (an order joined between workgroups would read them once).  It is short code on purpose: with all of a wave's tokens in registers, and so a copy of
-// the loops' bodies for each, 9.9 and 7.9 us, most of the difference to fetch the instructions.
+// 27 us, into 2^24 2500 (an order joined between workgroups would read them once).
+//
+// It is short code on purpose: with all of a wave's tokens in registers, and so a copy of the loops' bodies for each, 9.9
+// and 7.9 us, most of the difference to fetch the instructions.
 constexpr int FETCHED = 4, LISTED = 512;
 constexpr uint32_t NONE = ~0u;
 struct TokenOrder {
@@ -317,8 +319,8 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbedSums s, const T *drows, 
 
 // The long run that begins in chunk blockIdx.y, if there is one: 512 columns (blockIdx.x), eight waves on its
 // parts in turn, then their sums in order.  Latency, 4.1 to 6.7 us: a launch and three loads that wait for each other,
-// and the parts of the longest run (with 16 waves, and each workgroup to find out whether a run begins, 10 us).  Of rows of
-// fewer than 512 columns a part of the lanes has one: 32768 rows of 64 columns into 1000 12 us, of 16 lanes a wave.
+// and the parts of the longest run (with 16 waves, and each workgroup to find out whether a run begins, 10 us).  Rows of
+// fewer than 512 columns leave lanes idle: 32768 rows of 64 into 1000 take it 12 us, with 16 lanes of a wave at work.
 constexpr int JOIN_COLS = 512;
 template <typename O, bool ADD>
 __global__ __launch_bounds__(JOIN_COLS) void k_embed_join(EmbedSums s, O *out, int64_t out_stride) {

@@ -402,8 +402,8 @@ HeadPlan head_plan(const ckks_plain_heads *p, bool grad) {
     // 8192 tokens of 32 + 8 heads of 128 bf16 in a loop 29 us in steps of four, 39 one by one (gradient 54 and 62).
     // The first step is as many tokens as it takes to give each group of threads a head of the queries (with one head of
     // 64, 64 tokens and 16 KB of angles, the most); it doubles to at most four times that while 512 workgroups a side
-    // remain and the angles stay within 8 KB.  Where keys have more heads than queries their side takes as many tokens a step and
-    // so more turns: 8192 tokens of 1 + 32 heads of 128 43 us, of 32 + 1 27; of 8 + 32 32 us, of 32 + 8 29.
+    // remain and the angles stay within 8 KB.  Where keys have more heads than queries, their side takes as many tokens
+    // a step and so more turns: 8192 tokens of 1 + 32 heads of 128 43 us, of 32 + 1 27; of 8 + 32 32 us, of 32 + 8 29.
     const int64_t one = p->q_heads < groups ? groups / p->q_heads : 1;
     h.step = (int)one;
     while (h.step < 4 * one && h.step * p->rotary <= 1024 && p->tokens >= 1024 * (int64_t)h.step) h.step *= 2;

@@ -441,9 +441,10 @@ struct ScoreGradArgs {
 // A piece of a row for a workgroup, GRAD_EACH vectors a thread.  With lp = ln 2 x, x = z A - B,
 //   dz = p (c0 + c1 x) + [token] dlogprob / temperature,  p = 2^x,
 // of which a row's constants are worked out first (B in 64 bits; what its rounding to 32 leaves is in c0 and c1).
-// Where they have no room, x comes from distances as above, and 1 / temperature is multiplied last: at 1e-38 it leaves the
-// range of 32 bits with a term of 4, where p is 1 and the terms' sum 0.  Bound by memory: 4096 x 32768 bf16 88 us for 537 MB (6.1
-// TB/s, past the caches); 333 x 50021 f16 under a mask 18 us for 83 MB, in rows that start at odd elements.
+// Where they have no room, x comes from distances as above, and 1 / temperature is multiplied last: at 1e-38 it leaves
+// the range of 32 bits with a term of 4, where p is 1 and the terms' sum 0.
+// Bound by memory: 4096 x 32768 bf16 88 us for 537 MB (6.1 TB/s, past the caches); 333 x 50021 f16 under a mask 18 us
+// for 83 MB, in rows that start at odd elements.
 constexpr int GRAD_EACH = 4, GRAD_PIECE = 256 * 8 * GRAD_EACH;
 template <typename T, bool MASK, bool STREAM>
 __global__ __launch_bounds__(256) void k_token_logprobs_grad(ScoreGradArgs a, int64_t last, uint32_t pieces) {
